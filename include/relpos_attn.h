@@ -3,7 +3,10 @@
  * library (librelpos_attn.so): the forward pass (also over right-padded
  * batches), the T5 cached decode and the T5, Shaw, DeBERTa and ALiBi
  * backward passes (relpos_t5_attn_bwd, relpos_shaw_attn_bwd,
- * relpos_deberta_attn_bwd, relpos_alibi_attn_bwd, at the end of this header).
+ * relpos_deberta_attn_bwd, relpos_alibi_attn_bwd), and what serving from a
+ * paged key/value cache takes: rotary positions (relpos_rotary), appending to
+ * the cache (relpos_paged_append) and decoding over it (relpos_paged_decode),
+ * at the end of this header.
  *
  * One forward call computes multi-head attention whose logits carry a relative-
  * position term that is formed inside the kernel and never written to
@@ -67,9 +70,10 @@ extern "C" {
 #define RELPOS_ALIBI 3
 #define RELPOS_TXL 4
 
-/* element types of Q, K, V and out */
+/* element types of Q, K, V and out; of a paged cache: BF16 or E4M3 */
 #define RELPOS_BF16 0
 #define RELPOS_FP32 1
+#define RELPOS_E4M3 2
 
 /* return codes */
 #define RELPOS_OK 0
@@ -79,6 +83,8 @@ extern "C" {
 #define RELPOS_ERR_DEVICE_TIMEOUT (-4) /* a kernel gave up on a bounded wait */
 #define RELPOS_ERR_SCRATCH_LIMIT (-5)  /* request needs more than the fixed scratch of
                                           relpos_t5_decode_noalloc */
+#define RELPOS_ERR_PAGE (-6)           /* a kernel met a length, a row range or a page number
+                                          outside the paged cache and skipped it */
 
 /*
  * relpos_attn_fwd -- attention forward with an in-kernel relative term.
@@ -186,8 +192,9 @@ int relpos_index_ids(int mode, int n, int rel_first, int num_buckets, int rel_pa
 /*
  * relpos_check_status -- synchronize `stream` and report whether any kernel
  * of this library hit a bounded-wait limit since the last check
- * (RELPOS_ERR_DEVICE_TIMEOUT), or a CUDA error (RELPOS_ERR_CUDA). Clears the
- * recorded device status. Blocking.
+ * (RELPOS_ERR_DEVICE_TIMEOUT) or met a page number or length outside its paged
+ * cache (RELPOS_ERR_PAGE), whichever came first, or a CUDA error
+ * (RELPOS_ERR_CUDA). Clears the recorded device status. Blocking.
  */
 int relpos_check_status(void* stream);
 
@@ -403,6 +410,205 @@ int relpos_deberta_attn_bwd(const void* Q, const void* K, const void* V, const v
                             const void* Pk, const void* Pq, int B, int H, int Lq, int Lk, int d, int k,
                             int causal, int q_offset, void* dQ, void* dK, void* dV, void* dPk, void* dPq,
                             void* stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Rotary positions ("Relative Position Embeddings, in depth", section "ALiBi
+ * and RoPE: the two endpoints": queries and keys are turned by their position
+ * before attention, so that their product depends on the offset alone). The
+ * page names the scheme without formulas; the reading here is the usual one.
+ *
+ * The first rot_dim dimensions of a head form rot_dim / 2 pairs. Pair m at
+ * position p is turned by the angle p w_m and scaled by the plan's amplitude a:
+ *   (x1, x2) -> a (x1 cos - x2 sin, x1 sin + x2 cos)
+ * RELPOS_ROTARY_HALF         x1 = x[m],  x2 = x[m + rot_dim / 2]
+ * RELPOS_ROTARY_INTERLEAVED  x1 = x[2m], x2 = x[2m + 1]
+ * The dimensions from rot_dim on pass unchanged.
+ *
+ * Frequencies: w_m = base^(-2m / rot_dim), a = 1, and for contexts longer than
+ * the trained one
+ *   RELPOS_ROTARY_LINEAR  w_m / factor (position interpolation)
+ *   RELPOS_ROTARY_NTK     the base times factor^(rot_dim / (rot_dim - 2))
+ *   RELPOS_ROTARY_YARN    by parts: with r_m = original_len w_m / 2 pi turns
+ *                         over the trained length and g = (r_m - slow_turns) /
+ *                         (fast_turns - slow_turns) clipped to [0, 1], w_m
+ *                         becomes (1 - g) w_m / factor + g w_m; a = 0.1
+ *                         ln(factor) + 1 (Peng et al., "YaRN: Efficient Context
+ *                         Window Extension of Large Language Models")
+ */
+#define RELPOS_ROTARY_HALF 0
+#define RELPOS_ROTARY_INTERLEAVED 1
+
+#define RELPOS_ROTARY_PLAIN 0
+#define RELPOS_ROTARY_LINEAR 1
+#define RELPOS_ROTARY_NTK 2
+#define RELPOS_ROTARY_YARN 3
+
+#define RELPOS_ROTARY_MAX_DIM 256
+
+/* A host-side plan, filled by relpos_rotary_plan_init and passed to the calls
+   below by pointer (its contents are copied into the launch). */
+typedef struct RelposRotaryPlan {
+  int rot_dim;
+  int layout;
+  double amplitude;
+  unsigned long long turns[RELPOS_ROTARY_MAX_DIM / 2]; /* w_m / 2 pi, in 2^-64 of a turn */
+} RelposRotaryPlan;
+
+/* One tensor of a relpos_rotary call: x and out [B, H, L, d] with the given
+   strides in elements (the d values of a row are contiguous). */
+typedef struct RelposRotaryTensor {
+  const void* x;
+  void* out;
+  long long x_batch, x_head, x_row;
+  long long out_batch, out_head, out_row;
+  int H;
+} RelposRotaryTensor;
+
+/*
+ * relpos_rotary_plan_init -- fill a plan (host only, nothing is launched).
+ *
+ *   rot_dim       even, 2 .. RELPOS_ROTARY_MAX_DIM (NTK: at least 4).
+ *   layout        RELPOS_ROTARY_HALF or RELPOS_ROTARY_INTERLEAVED.
+ *   base          > 1.
+ *   scaling       RELPOS_ROTARY_PLAIN, _LINEAR, _NTK or _YARN.
+ *   factor        >= 1 (ignored by PLAIN).
+ *   original_len  > 0, fast_turns > slow_turns >= 0: YARN only.
+ */
+int relpos_rotary_plan_init(RelposRotaryPlan* plan, int rot_dim, int layout, double base, int scaling,
+                            double factor, double original_len, double fast_turns, double slow_turns);
+
+/*
+ * relpos_rotary -- turn one or two tensors (queries and keys) by position, in
+ * one launch.
+ *
+ *   dtype       RELPOS_BF16 or RELPOS_FP32: element type of every x and out.
+ *               Computed in fp32, rounded once.
+ *   inverse     0, or 1 to turn by the opposite angle with the same amplitude:
+ *               the gradient of the call with inverse = 0 (x the gradient of
+ *               its output).
+ *   tensors     host array of `ntensors` (1 or 2) descriptions. out may be x
+ *               itself (with x's strides); otherwise nothing may overlap.
+ *   B, L, d     batch, rows and head dimension (even, >= the plan's rot_dim);
+ *               an empty size makes the call a no-op.
+ *   positions   device, int32: row l of batch element b is at
+ *               positions[b * pos_stride + l] (pos_stride 0: one row of
+ *               positions for the whole batch). Any int32 values; angles are
+ *               exact modulo a full turn. Null: position offset + l.
+ * Sizes and strides that allow 16- or 8-byte accesses (rot_dim and d
+ * multiples of 16 or 8, rows that start on such a boundary) run with them,
+ * others element by element. Asynchronous on `stream`, no scratch.
+ */
+int relpos_rotary(const RelposRotaryPlan* plan, int dtype, int inverse, const RelposRotaryTensor* tensors,
+                  int ntensors, int B, int L, int d, const int* positions, long long pos_stride, int offset,
+                  void* stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Paged key/value cache ("Relative Position Embeddings, in depth", section
+ * "Kernels and the KV cache"; the pages treat one contiguous cache, the pages
+ * of memory are this library's reading). A pool of num_pages pages holds `page`
+ * tokens of every key/value head each; a sequence owns a list of pages (its row
+ * of the block table) and the token at position j lies in slot j mod page of
+ * its page number j / page.
+ *
+ *   k, v             device, [num_pages, H, page, d], 16-byte aligned: bf16, or
+ *                    e4m3 codes (1 byte).
+ *   k_scale, v_scale device, fp32 [num_pages, H] (E4M3 only): a stored value is
+ *                    its code times its page's and head's scale.
+ *   d                64 or 128; page 32, 64 or 128 (RELPOS_ERR_UNSUPPORTED
+ *                    otherwise). Host struct, copied into each launch.
+ *
+ * Block tables are device int32 [B, max_pages] with table_stride elements
+ * between rows; lens is device int32 [B]: the tokens of each sequence, those
+ * of the current step included. The kernels check lengths and page numbers
+ * against the cache, skip what lies outside it and report it through
+ * relpos_check_status() as RELPOS_ERR_PAGE; table entries beyond a sequence's
+ * last page are never read.
+ */
+typedef struct RelposPagedCache {
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  int num_pages, H, page, d;
+  int dtype;
+} RelposPagedCache;
+
+/* strides in elements of a [B, H, L, d] tensor (batch unused for ragged rows) */
+typedef struct RelposRowStrides {
+  long long batch, head, row;
+} RelposRowStrides;
+
+/*
+ * relpos_paged_append -- write each sequence's newest tokens into its pages.
+ * Sequence b with n_b new tokens and lens[b] tokens in all gets them at
+ * positions lens[b] - n_b .. lens[b] - 1.
+ *
+ *   plan        null: keys are stored as they are; otherwise turned at their
+ *               positions (rot_dim <= d and a multiple of 16,
+ *               RELPOS_ERR_UNSUPPORTED otherwise).
+ *   K, V        device, bf16 rows of d contiguous values with the given
+ *               strides. cu_new null: n new tokens of every sequence, row i of
+ *               head h of sequence b at b * batch + h * head + i * row. Else
+ *               ragged: cu_new is device int32 [B + 1], ascending from >= 0,
+ *               n_b = cu_new[b + 1] - cu_new[b], and row i of sequence b is row
+ *               cu_new[b] + i of the `rows` rows. Rows behind the last
+ *               sequence are not read.
+ *   lens        an entry <= 0, or without new tokens, is skipped (an unused
+ *               entry of a padded batch).
+ *
+ * BF16 caches: the turned keys and the values, rounded once. E4M3 caches: a
+ * page's scale for a head becomes the smallest power of two (within 2^-120 ..
+ * 2^120) that holds the largest new magnitude in 448 times it, for turned keys
+ * sqrt(2) * amplitude times that magnitude, which holds them at any angle; it
+ * never becomes smaller than it was while the page is being filled (a page
+ * whose first token is written starts afresh), and when it grows the codes
+ * already in the page are rounded to it. Codes are the correctly rounded ones
+ * (nearest, ties to even; a value next to a border is decided in 64 bits). An
+ * infinity takes the largest scale and saturates, NaN stays NaN and has no
+ * share in the scale.
+ *
+ * Slots outside the new tokens keep their bytes unless their page's scale
+ * grows. Pages written by one call must not be shared by two of its
+ * sequences, nor written or read by another stream meanwhile. Appending the
+ * same tokens again writes the same bytes. Asynchronous on `stream`, no
+ * scratch.
+ */
+int relpos_paged_append(const RelposPagedCache* cache, const RelposRotaryPlan* plan, const void* K, const void* V,
+                        const RelposRowStrides* k_strides, const RelposRowStrides* v_strides, const int* cu_new,
+                        int rows, int n, int B, const int* block_table, long long table_stride, int max_pages,
+                        const int* lens, void* stream);
+
+/*
+ * relpos_paged_decode -- attention of each sequence's newest Lq rows over its
+ * cached tokens, their own included (append them first).
+ *   logit = q . k * scale + bias,  out = softmax(logit) v
+ * Query row i of sequence b sits at position lens[b] - Lq + i and sees the
+ * keys up to that position; a row before the sequence's start is zero. Head hq
+ * of the Hq query heads reads key/value head hq / (Hq / H); Hq must be a
+ * multiple of the cache's H.
+ *
+ *   bias_mode   RELPOS_NO_BIAS; RELPOS_T5: bias device fp32 [num_buckets, Hq],
+ *               causal buckets (num_buckets and max_distance as for
+ *               relpos_attn_fwd); RELPOS_ALIBI: bias device fp32 [Hq], the
+ *               slopes, -slope |offset| is added.
+ *   Q, out      device, bf16 [B, Hq, Lq, d] with the given strides in elements
+ *               (rows of d contiguous values; out rows 2-byte aligned).
+ *   Lq          0 .. 8 rows (RELPOS_ERR_UNSUPPORTED beyond).
+ *   scale       softmax scale, finite; 0 takes 1 / sqrt(d).
+ * Keys and values in masked or unused slots have no effect, whatever they
+ * hold. The cache is read once for up to 16 rows (query heads of a group times
+ * Lq) and again for each further 16. Scratch: at most about 17 MB for partial results of
+ * sequences that several blocks share, from cudaMallocAsync on `stream`, freed
+ * with cudaFreeAsync before the call returns. Results do not depend on what
+ * else runs. Asynchronous on `stream`.
+ */
+#define RELPOS_NO_BIAS (-1)
+int relpos_paged_decode(const RelposPagedCache* cache, const void* Q, const RelposRowStrides* q_strides, int B,
+                        int Hq, int Lq, const int* block_table, long long table_stride, int max_pages,
+                        const int* lens, int bias_mode, const void* bias, int num_buckets, int max_distance,
+                        float scale, void* out, const RelposRowStrides* out_strides, void* stream);
 
 #ifdef __cplusplus
 }

@@ -121,6 +121,9 @@ bool make_tmap_acc(CUtensorMap* m, const void* base, int L, int BH) {
 
 }  // namespace
 
+int* device_status() { return status_ptr(); }
+int device_sms() { return num_sms(); }
+
 // Thresholds of the T5 log buckets: thr[q] is the smallest distance n whose
 // bucket within a half is >= exact + q + 1, found by evaluating the pages'
 // formula exact + int(log(n / exact) / log(max_distance / exact) * (S - exact))
@@ -237,6 +240,7 @@ extern "C" const char* relpos_strerror(int code) {
     case RELPOS_ERR_CUDA: return "CUDA error";
     case RELPOS_ERR_DEVICE_TIMEOUT: return "device-side bounded wait timed out";
     case RELPOS_ERR_SCRATCH_LIMIT: return "request exceeds the fixed scratch of the no-allocation decode";
+    case RELPOS_ERR_PAGE: return "length, row range or page number outside the paged cache";
     default: return "unknown error";
   }
 }
@@ -276,7 +280,7 @@ extern "C" int relpos_check_status(void* stream) {
     const int zero = 0;
     if (cudaMemcpy(sp, &zero, sizeof(int), cudaMemcpyHostToDevice) != cudaSuccess)
       return RELPOS_ERR_CUDA;
-    return RELPOS_ERR_DEVICE_TIMEOUT;
+    return v == RELPOS_ERR_PAGE ? RELPOS_ERR_PAGE : RELPOS_ERR_DEVICE_TIMEOUT;
   }
   return RELPOS_OK;
 }

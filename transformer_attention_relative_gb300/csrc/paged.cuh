@@ -1,0 +1,87 @@
+// paged.cuh -- device helpers of the paged key/value cache: bf16 and e4m3
+// vectors as the append kernel reads, scales and writes them.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include <cstdint>
+
+#include "ptx.cuh"
+
+namespace relpos {
+
+// 8 bf16 values from a pointer that is only 2-byte aligned
+RP_DEVI uint4 load8_unaligned(const __nv_bfloat16* p) {
+  const unsigned short* u = reinterpret_cast<const unsigned short*>(p);
+  uint32_t w[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) w[e] = u[2 * e] | static_cast<uint32_t>(u[2 * e + 1]) << 16;
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+RP_DEVI void unpack8(const uint4& u, float (&f)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    f[2 * e] = __uint_as_float(w[e] << 16);
+    f[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+  }
+}
+
+// The largest magnitude among 8 bf16 values, as the bits of a bf16; NaN counts
+// as nothing.
+RP_DEVI uint32_t absmax_bf16(const uint4& u) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  uint32_t m = 0;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const uint32_t lo = w[e] & 0x7fffu, hi = (w[e] >> 16) & 0x7fffu;
+    m = max(m, lo > 0x7f80u ? 0u : lo);
+    m = max(m, hi > 0x7f80u ? 0u : hi);
+  }
+  return m;
+}
+
+// 8 values times inv (a power of two) as e4m3 codes, rounded to nearest even,
+// saturating at 448
+RP_DEVI uint2 codes8(const float (&f)[8], float inv) {
+  uint32_t c[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    c[e] = __nv_cvt_float2_to_fp8x2(make_float2(f[2 * e] * inv, f[2 * e + 1] * inv), __NV_SATFINITE, __NV_E4M3);
+  return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+}
+
+RP_DEVI uint2 moved8(const uint2& u, float ratio) {
+  uint32_t w[2] = {u.x, u.y};
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    uint32_t out = 0;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const __half2_raw r =
+          __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>((w[e] >> (16 * h)) & 0xffffu), __NV_E4M3);
+      const float2 f = __half22float2(__half2(r));
+      const uint32_t c =
+          __nv_cvt_float2_to_fp8x2(make_float2(f.x * ratio, f.y * ratio), __NV_SATFINITE, __NV_E4M3);
+      out |= c << (16 * h);
+    }
+    w[e] = out;
+  }
+  return make_uint2(w[0], w[1]);
+}
+
+// The codes of one unit of a token (dims d1 .. d1 + 7 and d2 .. d2 + 7) to
+// another scale; ratio = old scale / new scale.
+RP_DEVI void move_codes(uint8_t* row, int d1, int d2, float ratio) {
+  if (ratio == 1.f) return;
+  uint2* a = reinterpret_cast<uint2*>(row + d1);
+  uint2* b = reinterpret_cast<uint2*>(row + d2);
+  const uint2 u = *a, v = *b;
+  *a = moved8(u, ratio);
+  *b = moved8(v, ratio);
+}
+
+}  // namespace relpos
