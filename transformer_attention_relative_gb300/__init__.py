@@ -457,235 +457,6 @@ def deberta_attention_backward(Q, K, V, dO, Pk, Pq, *, k: int = 256, causal: boo
     return dQ, dK, dV, dPk, dPq
 
 
-# ---------------------------------------------------------------- rotary positions
-
-class RotaryPlan:
-    """Frequencies and layout of rotary positions, made once and passed to each call.
-
-    ``rot_dim`` dimensions of a head are turned, as pairs of its halves (``layout="half"``) or of neighbours
-    (``"interleaved"``). ``scaling`` stretches the positions for contexts longer than the trained one: ``"linear"``,
-    ``"ntk"``, or ``"yarn"`` with ``original_len`` trained positions (see ``relpos_rotary_plan_init`` in the C header).
-    """
-
-    def __init__(self, rot_dim: int, *, layout: str = "half", base: float = 10000.0, scaling: str = "none",
-                 factor: float = 1.0, original_len: float = 0.0, fast_turns: float = 32.0, slow_turns: float = 1.0):
-        if layout not in ROTARY_LAYOUTS:
-            raise ValueError(f"layout must be one of {sorted(ROTARY_LAYOUTS)}")
-        if scaling not in ROTARY_SCALINGS:
-            raise ValueError(f"scaling must be one of {sorted(ROTARY_SCALINGS)}")
-        self._c = _RotaryPlan()
-        self.rot_dim = rot_dim
-        rc = relpos_rotary_plan_init(ctypes.byref(self._c), rot_dim, ROTARY_LAYOUTS[layout], base,
-                                     ROTARY_SCALINGS[scaling], factor, original_len, fast_turns, slow_turns)
-        if rc != RELPOS_OK:
-            raise RelposError(rc, "relpos_rotary_plan_init")
-        self._ref = ctypes.byref(self._c)
-
-
-def _check_device(device, *tensors):
-    """The library launches on the current device: every tensor has to be there."""
-    import torch
-    if device.type != "cuda":
-        raise ValueError("tensors must be CUDA tensors")
-    if device.index != torch.cuda.current_device():
-        raise ValueError("tensors must be on the current CUDA device")
-    for t in tensors:
-        if t is not None and t.device != device:
-            raise ValueError("tensors must be on one device")
-
-
-def _rotate(Q, plan, K, positions, offset, out, stream, inverse, what):
-    import torch
-    if Q.dtype == torch.bfloat16:
-        dtype = RELPOS_BF16
-    elif Q.dtype == torch.float32:
-        dtype = RELPOS_FP32
-    else:
-        raise TypeError(f"unsupported dtype {Q.dtype}")
-    B, _, L, d = Q.shape
-    xs = (Q,) if K is None else (Q, K)
-    if out is None:
-        outs = tuple(torch.empty_like(x) for x in xs)
-    else:
-        outs = (out,) if K is None else tuple(out)
-        if len(outs) != len(xs):
-            raise ValueError("out must hold one tensor for each input")
-    _check_device(Q.device, *xs, *outs, positions)
-    desc = (_RotaryTensor * len(xs))()
-    for e, x, y in zip(desc, xs, outs):
-        if x.dtype != Q.dtype or y.dtype != Q.dtype:
-            raise TypeError("Q, K and out must have one dtype")
-        H = x.shape[1]
-        if x.shape != (B, H, L, d) or y.shape != x.shape:
-            raise ValueError("Q and K must agree but for their heads, and out with them")
-        xs_, ys_ = x.stride(), y.stride()
-        if d > 1 and (xs_[3] != 1 or ys_[3] != 1):
-            raise ValueError("the last dimension must be contiguous")
-        e.x, e.out, e.H = x.data_ptr(), y.data_ptr(), H
-        e.x_batch, e.x_head, e.x_row = xs_[0], xs_[1], xs_[2]
-        e.out_batch, e.out_head, e.out_row = ys_[0], ys_[1], ys_[2]
-    ptr, stride = None, 0
-    if positions is not None:
-        if positions.dtype != torch.int32:
-            raise TypeError("positions must be int32")
-        if positions.shape != (B, L) and positions.shape != (L,):
-            raise ValueError("positions must be [L] or [B, L]")
-        if L > 1 and positions.stride(-1) != 1:
-            raise ValueError("positions must be contiguous along a sequence")
-        ptr = positions.data_ptr()
-        stride = positions.stride(0) if positions.dim() == 2 else 0
-    rc = relpos_rotary(plan._ref, dtype, inverse, desc, len(xs), B, L, d, ptr, stride, offset, _stream(stream))
-    if rc != RELPOS_OK:
-        raise RelposError(rc, what)
-    return outs[0] if K is None else outs
-
-
-def rotary(Q, plan, K=None, *, positions=None, offset: int = 0, out=None, stream=None):
-    """Turn queries (and keys, in the same launch) by their positions; returns ``out``, a pair when K is given.
-
-    Q [B,Hq,L,d] and K [B,Hk,L,d] are bf16 or fp32 with any strides but a contiguous last dimension; a [T,H,d]
-    tensor of ragged rows goes in as ``x.transpose(0, 1)[None]`` with its tokens' positions. ``positions``: int32
-    [L] or [B,L]; without it row l is at ``offset + l``. ``out`` is allocated like the inputs when not given, and
-    may be the inputs themselves.
-    """
-    return _rotate(Q, plan, K, positions, offset, out, stream, 0, "relpos_rotary")
-
-
-def rotary_backward(dQ, plan, dK=None, *, positions=None, offset: int = 0, out=None, stream=None):
-    """Gradients of ``rotary`` with respect to its inputs, from those of its outputs (arguments as ``rotary``)."""
-    return _rotate(dQ, plan, dK, positions, offset, out, stream, 1, "relpos_rotary")
-
-
-# ---------------------------------------------------------------- paged key/value cache
-
-class PagedCache:
-    """A pool of pages for keys and values, ``k`` and ``v`` [num_pages, H, page, d]: bf16, or float8_e4m3fn with fp32
-    ``k_scale`` and ``v_scale`` [num_pages, H] (a value is its code times its page's and head's scale)."""
-
-    def __init__(self, k, v, k_scale=None, v_scale=None):
-        import torch
-        if k.dtype not in (torch.bfloat16, torch.float8_e4m3fn) or v.dtype != k.dtype:
-            raise TypeError("k and v must both be bfloat16 or both float8_e4m3fn")
-        if k.dim() != 4 or v.shape != k.shape:
-            raise ValueError("k and v must be [num_pages, H, page, d]")
-        eight = k.dtype == torch.float8_e4m3fn
-        if eight != (k_scale is not None) or eight != (v_scale is not None):
-            raise ValueError("k_scale and v_scale come with a float8_e4m3fn cache, and only with one")
-        for s in (k_scale, v_scale):
-            if s is not None and (s.dtype != torch.float32 or s.shape != k.shape[:2]):
-                raise TypeError("scales must be fp32 [num_pages, H]")
-        for t in (k, v, k_scale, v_scale):
-            if t is not None and not t.is_contiguous():
-                raise ValueError("the cache's tensors must be contiguous")
-        _check_device(k.device, v, k_scale, v_scale)
-        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        self.num_pages, self.heads, self.page_size, self.head_dim = k.shape
-        self.device = k.device
-        self._c = _PagedCache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if eight else None,
-                              v_scale.data_ptr() if eight else None, *k.shape,
-                              RELPOS_E4M3 if eight else RELPOS_BF16)
-        self._ref = ctypes.byref(self._c)
-
-    @classmethod
-    def empty(cls, num_pages: int, heads: int, head_dim: int, *, page_size: int = 64, dtype=None, device="cuda"):
-        """A cache of its own memory; ``dtype`` bfloat16 (default) or float8_e4m3fn."""
-        import torch
-        dtype = dtype or torch.bfloat16
-        shape = (num_pages, heads, page_size, head_dim)
-        k, v = (torch.zeros(shape, dtype=torch.uint8 if dtype == torch.float8_e4m3fn else dtype, device=device)
-                for _ in range(2))
-        if dtype != torch.float8_e4m3fn:
-            return cls(k, v)
-        return cls(k.view(dtype), v.view(dtype), *(torch.ones(shape[:2], device=device) for _ in range(2)))
-
-
-def _check_table(cache, block_table, lens, B):
-    import torch
-    if block_table.dtype != torch.int32 or lens.dtype != torch.int32:
-        raise TypeError("block_table and lens must be int32")
-    if block_table.dim() != 2 or block_table.shape[0] != B or lens.shape != (B,):
-        raise ValueError("block_table must be [B, max_pages] and lens [B]")
-    if (block_table.shape[1] > 1 and block_table.stride(1) != 1) or (B > 1 and lens.stride(0) != 1):
-        raise ValueError("block_table rows and lens must be contiguous")
-    _check_device(cache.device, block_table, lens)
-
-
-def paged_append(cache, K, V, block_table, lens, *, cu_new=None, plan=None, stream=None):
-    """Run ``relpos_paged_append``: write each sequence's newest tokens into its pages, keys turned by ``plan``.
-
-    K, V bf16, contiguous along d: [B,H,n,d] with n new tokens of every sequence, or ragged rows [T,H,d] with
-    ``cu_new`` (int32 [B+1], first row of each sequence). block_table int32 [B, max_pages]; lens int32 [B], the
-    tokens of each sequence with the new ones.
-    """
-    import torch
-    if K.dtype != torch.bfloat16 or V.dtype != torch.bfloat16:
-        raise TypeError("K and V must be bf16")
-    if V.shape != K.shape or K.dim() != (4 if cu_new is None else 3):
-        raise ValueError("K and V must be [B,H,n,d], or [T,H,d] with cu_new")
-    if K.shape[1] != cache.heads or K.shape[-1] != cache.head_dim:
-        raise ValueError("K and V must have the cache's heads and head dimension")
-    if K.stride(-1) != 1 or V.stride(-1) != 1:
-        raise ValueError("the last dimension must be contiguous")
-    sk, sv = K.stride(), V.stride()
-    if cu_new is None:
-        B, n, rows = K.shape[0], K.shape[2], 0
-        ks, vs = _RowStrides(sk[0], sk[1], sk[2]), _RowStrides(sv[0], sv[1], sv[2])
-    else:
-        if cu_new.dtype != torch.int32 or cu_new.dim() != 1 or cu_new.shape[0] < 1:
-            raise TypeError("cu_new must be int32 [B + 1]")
-        if not cu_new.is_contiguous():
-            raise ValueError("cu_new must be contiguous")
-        B, n, rows = cu_new.shape[0] - 1, 0, K.shape[0]
-        ks, vs = _RowStrides(0, sk[1], sk[0]), _RowStrides(0, sv[1], sv[0])
-    _check_table(cache, block_table, lens, B)
-    _check_device(cache.device, K, V, cu_new)
-    rc = relpos_paged_append(cache._ref, None if plan is None else plan._ref, K.data_ptr(), V.data_ptr(),
-                             ctypes.byref(ks), ctypes.byref(vs), None if cu_new is None else cu_new.data_ptr(), rows,
-                             n, B, block_table.data_ptr(), block_table.stride(0), block_table.shape[1],
-                             lens.data_ptr(), _stream(stream))
-    if rc != RELPOS_OK:
-        raise RelposError(rc, "relpos_paged_append")
-
-
-def paged_decode(Q, cache, block_table, lens, *, bias=None, mode=None, num_buckets: int = 32,
-                 max_distance: int = 128, scale: float = 0.0, out=None, stream=None):
-    """Run ``relpos_paged_decode``: attention of each sequence's newest rows over its cached tokens; returns ``out``.
-
-    Q bf16 [B,Hq,Lq,d] (Lq <= 8; Hq a multiple of the cache's heads), any strides but a contiguous last dimension;
-    its rows are the last Lq of the lens[b] tokens. ``mode``: None (no bias), ``MODE_T5`` with bias fp32
-    [num_buckets, Hq] (causal buckets) or ``MODE_ALIBI`` with the slopes fp32 [Hq]. ``scale`` 0 takes 1/sqrt(d).
-    """
-    import torch
-    if Q.dtype != torch.bfloat16 or (out is not None and out.dtype != torch.bfloat16):
-        raise TypeError("Q and out must be bf16")
-    B, Hq, Lq, d = Q.shape
-    if d != cache.head_dim:
-        raise ValueError("Q must have the cache's head dimension")
-    if out is None:
-        out = torch.empty_like(Q)
-    elif out.shape != Q.shape:
-        raise ValueError("out must have Q's shape")
-    sq, so = Q.stride(), out.stride()
-    if sq[3] != 1 or so[3] != 1:
-        raise ValueError("the last dimension must be contiguous")
-    _check_table(cache, block_table, lens, B)
-    _check_device(cache.device, Q, out, bias)
-    if mode is None:
-        if bias is not None:
-            raise ValueError("a bias needs its mode")
-        mode, ptr = RELPOS_NO_BIAS, None
-    else:
-        if mode not in (MODE_T5, MODE_ALIBI):
-            raise ValueError("mode must be None, MODE_T5 or MODE_ALIBI")
-        if bias is None or bias.dtype != torch.float32 or not bias.is_contiguous():
-            raise TypeError("bias must be a contiguous fp32 tensor")
-        if bias.shape != ((num_buckets, Hq) if mode == MODE_T5 else (Hq,)):
-            raise ValueError("bias must be [num_buckets, Hq] for MODE_T5, [Hq] for MODE_ALIBI")
-        ptr = bias.data_ptr()
-    rc = relpos_paged_decode(cache._ref, Q.data_ptr(), ctypes.byref(_RowStrides(sq[0], sq[1], sq[2])), B, Hq, Lq,
-                             block_table.data_ptr(), block_table.stride(0), block_table.shape[1], lens.data_ptr(),
-                             mode, ptr, num_buckets, max_distance, scale, out.data_ptr(),
-                             ctypes.byref(_RowStrides(so[0], so[1], so[2])), _stream(stream))
-    if rc != RELPOS_OK:
-        raise RelposError(rc, "relpos_paged_decode")
-    return out
+# rotary positions and the paged key/value cache
+from .serving import (PagedCache, RotaryPlan, paged_append, paged_decode, rotary,  # noqa: E402,F401
+                      rotary_backward)

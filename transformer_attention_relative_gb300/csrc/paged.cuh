@@ -12,6 +12,10 @@
 
 namespace relpos {
 
+// two fp32 operations in one instruction
+RP_DEVI float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+RP_DEVI float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+
 // 8 bf16 values from a pointer that is only 2-byte aligned
 RP_DEVI uint4 load8_unaligned(const __nv_bfloat16* p) {
   const unsigned short* u = reinterpret_cast<const unsigned short*>(p);
@@ -30,16 +34,22 @@ RP_DEVI void unpack8(const uint4& u, float (&f)[8]) {
   }
 }
 
-// The largest magnitude among 8 bf16 values, as the bits of a bf16; NaN counts
-// as nothing.
-RP_DEVI uint32_t absmax_bf16(const uint4& u) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+// The largest magnitude among 16 bf16 values, as the bits of a bf16: they
+// order like the magnitudes, infinity last. NaN counts as nothing.
+RP_DEVI uint32_t absmax_bf16(const uint4& u, const uint4& v) {
+  const uint32_t w[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
   uint32_t m = 0;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const uint32_t lo = w[e] & 0x7fffu, hi = (w[e] >> 16) & 0x7fffu;
-    m = max(m, lo > 0x7f80u ? 0u : lo);
-    m = max(m, hi > 0x7f80u ? 0u : hi);
+  for (int e = 0; e < 8; ++e) m = __vmaxu2(m, w[e] & 0x7fff7fffu);
+  m = max(m & 0xffffu, m >> 16);
+  if (m > 0x7f80u) {  // a NaN among them
+    m = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const uint32_t lo = w[e] & 0x7fffu, hi = (w[e] >> 16) & 0x7fffu;
+      m = max(m, lo > 0x7f80u ? 0u : lo);
+      m = max(m, hi > 0x7f80u ? 0u : hi);
+    }
   }
   return m;
 }

@@ -31,8 +31,7 @@
 namespace relpos {
 namespace {
 
-constexpr int kAppThreads = 256;
-constexpr int kAppSlots = 4;  // 16-element units of a key and a value that a thread holds
+constexpr int kAppMaxGroup = 64;  // heads of a block at most
 
 struct AppendParams {
   RelposRotaryPlan plan;  // rot_dim 0: no rotation
@@ -49,17 +48,16 @@ struct AppendParams {
   const int* lens;
   int log_page, log_units;  // page and d / 16, powers of two
   int group;              // heads of a block
-  double reach;           // largest rotated magnitude over the largest one
+  int exp_k[2], exp_v[2]; // scale_exponents of keys and values
   int* status;
 };
 
-// The smallest power of two s with amax * reach <= 448 s, clamped to
-// 2^-120 .. 2^120: the exponent comes from the bits of the quotient.
-RP_DEVI float scale_for(float amax, double reach) {
-  if (!(amax > 0.f)) return __int_as_float((127 - 120) << 23);
-  const unsigned long long r = __double_as_longlong(static_cast<double>(amax) * reach / 448.0);
-  int e = static_cast<int>((r >> 52) & 0x7ff) - 1023;  // floor(log2)
-  if (r & 0xfffffffffffffull) ++e;
+// The scale of a largest magnitude (bf16 bits without the sign): the smallest
+// power of two s with magnitude * reach <= 448 s. For a magnitude m 2^k with
+// 7 bits after the point its exponent is k + ex[0], one more from the
+// mantissa ex[1] on; clamped to -120 .. 120.
+RP_DEVI float scale_for(uint32_t bits, const int (&ex)[2]) {
+  int e = static_cast<int>(bits >> 7) - 127 + ex[0] + (static_cast<int>(bits & 127u) >= ex[1]);
   e = min(120, max(-120, e));
   return __int_as_float((e + 127) << 23);
 }
@@ -91,15 +89,19 @@ __device__ __noinline__ uint32_t rotated_codes_exact(float x1, float x2, unsigne
   return e4m3_of((u * c - v * s) * a) | (e4m3_of((u * s + v * c) * a) << 8);
 }
 
-// Blocks of 256 threads take one page that gets new tokens and `group` heads;
-// a thread holds up to four 16-element units of the keys and of the values in
-// registers, all loads in flight at once, so both the page's largest value
-// and its codes come from one read.
-template <bool FP8>
-__global__ void __launch_bounds__(kAppThreads) relpos_paged_append_kernel(const __grid_constant__ AppendParams p) {
-  __shared__ int amax_s[8][2];
-  __shared__ float inv_s[8][2];
-  __shared__ float move_s[8][2];
+// A block takes one page that gets new tokens and `group` heads of it. Its
+// items are the heads' new tokens in units of 16 elements, a thread holding
+// UNITS of them (keys and values, all loads in flight at once) in registers,
+// so that a page's largest value and its codes come from one read; heads
+// follow one another, as many at a time as the block has threads for, the next
+// ones' loads ahead of the present ones' arithmetic. Sines and cosines are
+// formed once for the block, in shared memory: [4][slots * units] float4, the
+// two sines, then the two cosines, of pairs 2 j and 2 j + 1 of a unit in plane j.
+template <bool FP8, bool INTERLEAVED, int THREADS, int UNITS>
+__global__ void __launch_bounds__(THREADS, UNITS == 1 ? 768 / THREADS : 1) relpos_paged_append_kernel(const __grid_constant__ AppendParams p) {
+  extern __shared__ float4 turn_s[];
+  __shared__ int amax_s[2][kAppMaxGroup];
+  __shared__ float had_s[2][kAppMaxGroup];
   griddep_launch_dependents();
   griddep_wait();
   const int tid = threadIdx.x, lane = tid & 31;
@@ -137,184 +139,278 @@ __global__ void __launch_bounds__(kAppThreads) relpos_paged_append_kernel(const 
     if (tid == 0) atomicCAS(p.status, 0, RELPOS_ERR_PAGE);
     return;
   }
-  const int page = 1 << p.log_page;
-  const int t_lo = max(start - pg * page, 0), t_hi = min(len - pg * page, page);  // new slots of the page
+  const int page = 1 << p.log_page, page0 = pg << p.log_page;
+  const int t_lo = max(start - page0, 0), t_hi = min(len - page0, page);  // new slots of the page
   const int h0 = blockIdx.y * p.group;
   const int nheads = min(p.group, p.cache.H - h0);
   const int d = p.cache.d;
-  const int log_items = p.log_page + p.log_units;  // units of one head's page
   const int rot_units = p.plan.rot_dim >> 4;
-  const bool interleaved = p.plan.layout == RELPOS_ROTARY_INTERLEAVED;
+  const size_t page_rows = static_cast<size_t>(page_id) * p.cache.H + h0;
 
-  // dims of a unit: 8 pairs of the rotation, or 16 neighbouring values
-  auto dims = [&](int unit, int& d1, int& d2) {
-    if (unit < rot_units && !interleaved) {
+  // items of a head: its new tokens, rounded up to a power of two, by units
+  const int log_tok = 32 - __clz(t_hi - t_lo - 1);
+  const int log_items = log_tok + p.log_units;
+  constexpr int kSpan = THREADS * UNITS;
+  const int step_heads = max(1, kSpan >> log_items);
+  // unit i of the thread: item tid + i * THREADS of the block's span
+  auto place = [&](int i, int& hs, int& slot, int& unit, int& d1, int& d2) {
+    const int item = i * THREADS + tid;
+    hs = item >> log_items;
+    slot = t_lo + ((item >> p.log_units) & ((1 << log_tok) - 1));
+    unit = item & ((1 << p.log_units) - 1);
+    if (unit < rot_units && !INTERLEAVED) {  // 8 pairs of the rotation's halves
       d1 = unit * 8;
       d2 = (p.plan.rot_dim >> 1) + d1;
-    } else {
+    } else {  // 16 neighbours
       d1 = unit * 16;
       d2 = d1 + 8;
     }
   };
-
-  uint4 kr[kAppSlots][2], vr[kAppSlots][2];
-  bool live[kAppSlots];
+  const long long k_base = (p.cu ? (row0 - static_cast<long long>(start - page0)) * p.k_row
+                                 : b * p.k_batch - (start - page0) * p.k_row) + h0 * p.k_head;
+  const long long v_base = (p.cu ? (row0 - static_cast<long long>(start - page0)) * p.v_row
+                                 : b * p.v_batch - (start - page0) * p.v_row) + h0 * p.v_head;
+  uint4 kr[UNITS][2], vr[UNITS][2];
+  const __nv_bfloat16 *kp[UNITS], *vp[UNITS];  // the next head's row of each unit
 #pragma unroll
-  for (int i = 0; i < kAppSlots; ++i) {
-    const int item = i * kAppThreads + tid;
-    const int hs = item >> log_items;
-    const int slot = (item >> p.log_units) & (page - 1);
-    const int unit = item & ((1 << p.log_units) - 1);
-    live[i] = hs < nheads && slot >= t_lo && slot < t_hi;
-    kr[i][0] = kr[i][1] = vr[i][0] = vr[i][1] = make_uint4(0, 0, 0, 0);
-    if (live[i]) {
-      const long long r = pg * page + slot - start;  // new row of the sequence
-      const long long kb = p.cu ? (row0 + r) * p.k_row : b * p.k_batch + r * p.k_row;
-      const long long vb = p.cu ? (row0 + r) * p.v_row : b * p.v_batch + r * p.v_row;
-      const __nv_bfloat16* kp = p.K + kb + (h0 + hs) * p.k_head;
-      const __nv_bfloat16* vp = p.V + vb + (h0 + hs) * p.v_head;
-      int d1, d2;
-      dims(unit, d1, d2);
-      if (p.vec) {
-        kr[i][0] = *reinterpret_cast<const uint4*>(kp + d1);
-        kr[i][1] = *reinterpret_cast<const uint4*>(kp + d2);
-        vr[i][0] = *reinterpret_cast<const uint4*>(vp + d1);
-        vr[i][1] = *reinterpret_cast<const uint4*>(vp + d2);
-      } else {
-        kr[i][0] = load8_unaligned(kp + d1);
-        kr[i][1] = load8_unaligned(kp + d2);
-        vr[i][0] = load8_unaligned(vp + d1);
-        vr[i][1] = load8_unaligned(vp + d2);
-      }
-    }
+  for (int i = 0; i < UNITS; ++i) {
+    int hs, slot, unit, d1, d2;
+    place(i, hs, slot, unit, d1, d2);
+    kp[i] = p.K + k_base + slot * p.k_row + hs * p.k_head + d1;
+    vp[i] = p.V + v_base + slot * p.v_row + hs * p.v_head + d1;
   }
-
-  const size_t page_rows = static_cast<size_t>(page_id) * p.cache.H;
-  if constexpr (FP8) {
-    float* const scales[2] = {p.cache.k_scale, p.cache.v_scale};
-    // thread 2 h + w looks after head h's scale of the keys (w = 0) or values
-    const bool keeper = tid < 2 * nheads;
-    float had = 0.f;
-    if (keeper) {
-      amax_s[tid >> 1][tid & 1] = 0;
-      if (t_lo > 0) had = scales[tid & 1][page_rows + h0 + (tid >> 1)];
-    }
-    __syncthreads();
+  auto load = [&](int head) {
 #pragma unroll
-    for (int i = 0; i < kAppSlots; ++i) {
-      const int hs = (i * kAppThreads + tid) >> log_items;  // the same for the whole warp
-      if (hs >= nheads) break;
-      // magnitudes of bf16 order like their bits; infinities and NaN: an
-      // infinity takes the largest scale, NaN has no magnitude
-      uint32_t mk = max(absmax_bf16(kr[i][0]), absmax_bf16(kr[i][1]));
-      uint32_t mv = max(absmax_bf16(vr[i][0]), absmax_bf16(vr[i][1]));
-      mk = __reduce_max_sync(0xffffffffu, mk);
-      mv = __reduce_max_sync(0xffffffffu, mv);
-      if (lane == 0) {
-        if (mk) atomicMax(&amax_s[hs][0], static_cast<int>(mk << 16));
-        if (mv) atomicMax(&amax_s[hs][1], static_cast<int>(mv << 16));
-      }
-    }
-    __syncthreads();
-    if (keeper) {
-      const float want =
-          scale_for(__int_as_float(amax_s[tid >> 1][tid & 1]), (tid & 1) ? 1.0 : p.reach);
-      const float now = t_lo > 0 ? fmaxf(want, had) : want;
-      move_s[tid >> 1][tid & 1] = t_lo > 0 ? had / now : 1.f;
-      inv_s[tid >> 1][tid & 1] = 1.f / now;
-      if (t_lo == 0 || now != had) scales[tid & 1][page_rows + h0 + (tid >> 1)] = now;
-    }
-    __syncthreads();
-  }
-
-  const float amplitude = static_cast<float>(p.plan.amplitude);
-  float s[8], c[8];
-#pragma unroll
-  for (int i = 0; i < kAppSlots; ++i) {
-    const int item = i * kAppThreads + tid;
-    const int hs = item >> log_items;
-    if (hs >= nheads) break;
-    const int slot = (item >> p.log_units) & (page - 1);
-    const int unit = item & ((1 << p.log_units) - 1);
-    int d1, d2;
-    dims(unit, d1, d2);
-    const size_t at = ((page_rows + h0 + hs) * page + slot) * d;
-    if constexpr (FP8) {
-      if (slot < t_lo) {  // codes that were there, to the page's new scale
-        move_codes(static_cast<uint8_t*>(p.cache.k) + at, d1, d2, move_s[hs][0]);
-        move_codes(static_cast<uint8_t*>(p.cache.v) + at, d1, d2, move_s[hs][1]);
-      }
-    }
-    if (!live[i]) continue;
-    const bool turns = unit < rot_units;
-    const int pos = pg * page + slot;
-    // threads keep their unit and slot from head to head when a head's page
-    // has at most 256 units
-    if (turns && (i == 0 || log_items > 8)) {
-#pragma unroll
-      for (int m = 0; m < 8; ++m) {
-        rotary_sincos(p.plan.turns[8 * unit + m], pos, s[m], c[m]);
-        s[m] *= amplitude;
-        c[m] *= amplitude;
-      }
-    }
-    float x1[8], x2[8];
-    unpack8(kr[i][0], x1);
-    unpack8(kr[i][1], x2);
-    if constexpr (!FP8) {
-      __nv_bfloat16* ko = static_cast<__nv_bfloat16*>(p.cache.k) + at;
-      __nv_bfloat16* vo = static_cast<__nv_bfloat16*>(p.cache.v) + at;
-      if (turns) {
-        rotate_unit<8>(x1, x2, s, c, interleaved);
-        store_vec<8>(ko + d1, x1);
-        store_vec<8>(ko + d2, x2);
-      } else {
-        *reinterpret_cast<uint4*>(ko + d1) = kr[i][0];
-        *reinterpret_cast<uint4*>(ko + d2) = kr[i][1];
-      }
-      *reinterpret_cast<uint4*>(vo + d1) = vr[i][0];
-      *reinterpret_cast<uint4*>(vo + d2) = vr[i][1];
-    } else {
-      uint8_t* ko = static_cast<uint8_t*>(p.cache.k) + at;
-      uint8_t* vo = static_cast<uint8_t*>(p.cache.v) + at;
-      const float ik = inv_s[hs][0], iv = inv_s[hs][1];
-      uint2 o1, o2;
-      if (turns) {
-        uint32_t code[8];  // of pair m: first member's code, second's in the next byte
-#pragma unroll
-        for (int m = 0; m < 8; ++m) {
-          const float a = interleaved ? (m < 4 ? x1[2 * (m & 3)] : x2[2 * (m & 3)]) : x1[m];
-          const float q = interleaved ? (m < 4 ? x1[2 * (m & 3) + 1] : x2[2 * (m & 3) + 1]) : x2[m];
-          float y1, y2;
-          rotate_pair(a, q, s[m], c[m], y1, y2);
-          // the fp32 rotation is off by less than 2^-21 (|a| + |q|) amplitude:
-          // where both ends of that round to one code it is the right one
-          const float off = (fabsf(a) + fabsf(q)) * (4.76837158e-07f * amplitude);
-          code[m] = e4m3x2((y1 - off) * ik, (y2 - off) * ik);
-          if (code[m] != e4m3x2((y1 + off) * ik, (y2 + off) * ik))
-            code[m] = rotated_codes_exact(a, q, p.plan.turns[8 * unit + m], pos, p.plan.amplitude, ik);
-        }
-        if (interleaved) {
-          o1 = make_uint2(code[0] | code[1] << 16, code[2] | code[3] << 16);
-          o2 = make_uint2(code[4] | code[5] << 16, code[6] | code[7] << 16);
+    for (int i = 0; i < UNITS; ++i) {
+      int hs, slot, unit, d1, d2;
+      place(i, hs, slot, unit, d1, d2);
+      kr[i][0] = kr[i][1] = vr[i][0] = vr[i][1] = make_uint4(0, 0, 0, 0);
+      if (hs < step_heads && head + hs < nheads && slot < t_hi) {
+        if (p.vec) {
+          kr[i][0] = *reinterpret_cast<const uint4*>(kp[i]);
+          kr[i][1] = *reinterpret_cast<const uint4*>(kp[i] + d2 - d1);
+          vr[i][0] = *reinterpret_cast<const uint4*>(vp[i]);
+          vr[i][1] = *reinterpret_cast<const uint4*>(vp[i] + d2 - d1);
         } else {
-          const uint32_t a0 = __byte_perm(code[0], code[1], 0x5140), a1 = __byte_perm(code[2], code[3], 0x5140);
-          const uint32_t a2 = __byte_perm(code[4], code[5], 0x5140), a3 = __byte_perm(code[6], code[7], 0x5140);
-          o1 = make_uint2(__byte_perm(a0, a1, 0x5410), __byte_perm(a2, a3, 0x5410));
-          o2 = make_uint2(__byte_perm(a0, a1, 0x7632), __byte_perm(a2, a3, 0x7632));
+          kr[i][0] = load8_unaligned(kp[i]);
+          kr[i][1] = load8_unaligned(kp[i] + d2 - d1);
+          vr[i][0] = load8_unaligned(vp[i]);
+          vr[i][1] = load8_unaligned(vp[i] + d2 - d1);
         }
-      } else {
-        o1 = codes8(x1, ik);
-        o2 = codes8(x2, ik);
       }
-      *reinterpret_cast<uint2*>(ko + d1) = o1;
-      *reinterpret_cast<uint2*>(ko + d2) = o2;
-      unpack8(vr[i][0], x1);
-      unpack8(vr[i][1], x2);
-      *reinterpret_cast<uint2*>(vo + d1) = codes8(x1, iv);
-      *reinterpret_cast<uint2*>(vo + d2) = codes8(x2, iv);
+      kp[i] += step_heads * p.k_head;
+      vp[i] += step_heads * p.v_head;
+    }
+  };
+  load(0);
+
+  if constexpr (FP8) {
+    for (int i = tid; i < 2 * nheads; i += THREADS) {
+      const int w = i >= nheads, h = i - w * nheads;
+      amax_s[w][h] = 0;
+      had_s[w][h] = t_lo > 0 ? (w ? p.cache.v_scale : p.cache.k_scale)[page_rows + h] : 0.f;
     }
   }
+  const float amplitude = static_cast<float>(p.plan.amplitude);
+  const int planes = (t_hi - t_lo) << p.log_units;  // float4 of a plane
+  {
+    // a warp at one pair of frequencies (their loads are uniform), its lanes
+    // at the tokens
+    for (int m = 2 * (tid >> 5); m < p.plan.rot_dim >> 1; m += THREADS / 16) {
+      const unsigned long long w0 = p.plan.turns[m], w1 = p.plan.turns[m + 1];
+      for (int tok = lane; tok < t_hi - t_lo; tok += 32) {
+        float4 f;
+        rotary_sincos(w0, page0 + t_lo + tok, f.x, f.y);
+        rotary_sincos(w1, page0 + t_lo + tok, f.z, f.w);
+        f.x *= amplitude, f.y *= amplitude, f.z *= amplitude, f.w *= amplitude;
+        f = make_float4(f.x, f.z, f.y, f.w);
+        turn_s[((m >> 1) & 3) * planes + (tok << p.log_units) + (m >> 3)] = f;
+      }
+    }
+  }
+  __syncthreads();
+
+  for (int head = 0; head < nheads; head += step_heads) {
+    if constexpr (FP8) {
+#pragma unroll
+      for (int i = 0; i < UNITS; ++i) {
+        int hs, slot, unit, d1, d2;
+        place(i, hs, slot, unit, d1, d2);
+        uint32_t both = absmax_bf16(kr[i][0], kr[i][1]) << 16 | absmax_bf16(vr[i][0], vr[i][1]);
+        if (log_items >= 5) {  // the warp has one head
+          both = __reduce_max_sync(0xffffffffu, both >> 16) << 16 | __reduce_max_sync(0xffffffffu, both & 0xffffu);
+        } else {
+#pragma unroll
+          for (int o = 8; o > 0; o >>= 1) {  // lanes of one head
+            const uint32_t other = __shfl_xor_sync(0xffffffffu, both, o);
+            if (o < (1 << log_items)) both = __vmaxu2(both, other);
+          }
+        }
+        if ((lane & ((1 << log_items) - 1)) == 0 && head + hs < nheads && hs < step_heads) {
+          if (both >> 16) atomicMax(&amax_s[0][head + hs], static_cast<int>(both >> 16));
+          if (both & 0xffffu) atomicMax(&amax_s[1][head + hs], static_cast<int>(both & 0xffffu));
+        }
+      }
+      __syncthreads();
+      // each head's scales, and the codes that are in the page to a larger one
+      const int heads_now = min(step_heads, nheads - head);
+      for (int i = tid; i < 2 * heads_now; i += THREADS) {
+        const int w = i >= heads_now, h = head + i - w * heads_now;
+        const float want = w ? scale_for(amax_s[1][h], p.exp_v) : scale_for(amax_s[0][h], p.exp_k);
+        const float now = t_lo > 0 ? fmaxf(want, had_s[w][h]) : want;
+        if (t_lo == 0 || now != had_s[w][h]) (w ? p.cache.v_scale : p.cache.k_scale)[page_rows + h] = now;
+      }
+      if (t_lo > 0) {
+        for (int w = 0; w < 2; ++w) {
+          uint8_t* base = static_cast<uint8_t*>(w ? p.cache.v : p.cache.k);
+          for (int h = head; h < head + heads_now; ++h) {
+            const float want = w ? scale_for(amax_s[1][h], p.exp_v) : scale_for(amax_s[0][h], p.exp_k);
+            const float had = had_s[w][h], now = fmaxf(want, had);
+            if (now == had) continue;
+            uint2* row = reinterpret_cast<uint2*>(base + ((page_rows + h) << p.log_page) * d);
+            for (int i = tid; i < t_lo * d / 8; i += THREADS) row[i] = moved8(row[i], had / now);
+          }
+        }
+      }
+    }
+
+    uint4 kc[UNITS][2], vc[UNITS][2];
+#pragma unroll
+    for (int i = 0; i < UNITS; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) kc[i][j] = kr[i][j], vc[i][j] = vr[i][j];
+    if (head + step_heads < nheads) load(head + step_heads);
+
+#pragma unroll
+    for (int i = 0; i < UNITS; ++i) {
+      int hs, slot, unit, d1, d2;
+      place(i, hs, slot, unit, d1, d2);
+      if (hs >= step_heads || head + hs >= nheads || slot >= t_hi) continue;
+      const int h = head + hs;
+      const size_t at = (((page_rows + h) << p.log_page) + slot) * d;
+      const bool turns = unit < rot_units;
+      float s[8], c[8];
+      if (turns) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float4 f = turn_s[j * planes + ((slot - t_lo) << p.log_units) + unit];
+          s[2 * j] = f.x, s[2 * j + 1] = f.y, c[2 * j] = f.z, c[2 * j + 1] = f.w;
+        }
+      }
+      float x1[8], x2[8];
+      unpack8(kc[i][0], x1);
+      unpack8(kc[i][1], x2);
+      if constexpr (!FP8) {
+        __nv_bfloat16* ko = static_cast<__nv_bfloat16*>(p.cache.k) + at;
+        __nv_bfloat16* vo = static_cast<__nv_bfloat16*>(p.cache.v) + at;
+        if (turns) {
+          rotate_unit<8>(x1, x2, s, c, INTERLEAVED);
+          store_vec<8>(ko + d1, x1);
+          store_vec<8>(ko + d2, x2);
+        } else {
+          *reinterpret_cast<uint4*>(ko + d1) = kc[i][0];
+          *reinterpret_cast<uint4*>(ko + d2) = kc[i][1];
+        }
+        *reinterpret_cast<uint4*>(vo + d1) = vc[i][0];
+        *reinterpret_cast<uint4*>(vo + d2) = vc[i][1];
+      } else {
+        uint8_t* ko = static_cast<uint8_t*>(p.cache.k) + at;
+        uint8_t* vo = static_cast<uint8_t*>(p.cache.v) + at;
+        const float want_k = scale_for(amax_s[0][h], p.exp_k), want_v = scale_for(amax_s[1][h], p.exp_v);
+        float ik = __int_as_float((254 << 23) - __float_as_int(want_k));  // of a power of two: exact
+        float iv = __int_as_float((254 << 23) - __float_as_int(want_v));
+        if (t_lo > 0) {  // the page's scale so far may be any number
+          ik = 1.f / fmaxf(want_k, had_s[0][h]);
+          iv = 1.f / fmaxf(want_v, had_s[1][h]);
+        }
+        uint2 o1, o2;
+        // The fp32 rotation is off by less than 2^-22 (|a| + |q|): sine and
+        // cosine by 2^-23, two products and a sum by 2^-24 each; by twice that
+        // times the amplitude where there is one; by nothing at position 0,
+        // where many values do lie on a border.
+        const float slack =
+            ik * (amplitude != 1.f ? 4.76837158e-07f * amplitude : page0 + slot ? 2.38418579e-07f : 0.f);
+        uint32_t doubt = 0;  // pairs whose codes the fp32 rotation leaves open
+        if (turns) {
+          uint32_t code[8];  // of pair m: first member's code, second's in the next byte
+          const float2 scale2 = make_float2(ik, ik);
+#pragma unroll
+          for (int m = 0; m < 8; m += 2) {  // two pairs at a time in packed fp32
+            float2 a, q;
+            if (INTERLEAVED) {
+              const float(&x)[8] = m < 4 ? x1 : x2;
+              const int e = 2 * (m & 3);
+              a = make_float2(x[e], x[e + 2]);
+              q = make_float2(x[e + 1], x[e + 3]);
+            } else {
+              a = make_float2(x1[m], x1[m + 1]);
+              q = make_float2(x2[m], x2[m + 1]);
+            }
+            const float2 sm = make_float2(s[m], s[m + 1]), cm = make_float2(c[m], c[m + 1]);
+            const float2 y1 = fma2(a, cm, mul2(q, make_float2(-sm.x, -sm.y))), y2 = fma2(a, sm, mul2(q, cm));
+            // where both ends of the rotation's error bound round to one
+            // code it is the right one
+            const float2 off = make_float2((fabsf(a.x) + fabsf(q.x)) * slack, (fabsf(a.y) + fabsf(q.y)) * slack);
+            const float2 neg = make_float2(-off.x, -off.y);
+            const float2 l1 = fma2(y1, scale2, neg), l2 = fma2(y2, scale2, neg);
+            const float2 u1 = fma2(y1, scale2, off), u2 = fma2(y2, scale2, off);
+            code[m] = e4m3x2(l1.x, l2.x);
+            code[m + 1] = e4m3x2(l1.y, l2.y);
+            if (code[m] != e4m3x2(u1.x, u2.x)) doubt |= 1u << m;
+            if (code[m + 1] != e4m3x2(u1.y, u2.y)) doubt |= 2u << m;
+          }
+          if (INTERLEAVED) {
+            o1 = make_uint2(code[0] | code[1] << 16, code[2] | code[3] << 16);
+            o2 = make_uint2(code[4] | code[5] << 16, code[6] | code[7] << 16);
+          } else {
+            const uint32_t a0 = __byte_perm(code[0], code[1], 0x5140), a1 = __byte_perm(code[2], code[3], 0x5140);
+            const uint32_t a2 = __byte_perm(code[4], code[5], 0x5140), a3 = __byte_perm(code[6], code[7], 0x5140);
+            o1 = make_uint2(__byte_perm(a0, a1, 0x5410), __byte_perm(a2, a3, 0x5410));
+            o2 = make_uint2(__byte_perm(a0, a1, 0x7632), __byte_perm(a2, a3, 0x7632));
+          }
+        } else {
+          o1 = codes8(x1, ik);
+          o2 = codes8(x2, ik);
+        }
+        *reinterpret_cast<uint2*>(ko + d1) = o1;
+        *reinterpret_cast<uint2*>(ko + d2) = o2;
+        unpack8(vc[i][0], x1);
+        unpack8(vc[i][1], x2);
+        *reinterpret_cast<uint2*>(vo + d1) = codes8(x1, iv);
+        *reinterpret_cast<uint2*>(vo + d2) = codes8(x2, iv);
+        const __nv_bfloat16* row = p.K + k_base + slot * p.k_row + h * p.k_head;
+        while (doubt) {
+          const int m = __ffs(doubt) - 1;
+          doubt &= doubt - 1;
+          const int e1 = INTERLEAVED ? d1 + 2 * m : d1 + m, e2 = INTERLEAVED ? e1 + 1 : d2 + m;
+          const uint32_t both = rotated_codes_exact(__bfloat162float(row[e1]), __bfloat162float(row[e2]),
+                                                    p.plan.turns[8 * unit + m], page0 + slot, p.plan.amplitude, ik);
+          ko[e1] = static_cast<uint8_t>(both);
+          ko[e2] = static_cast<uint8_t>(both >> 8);
+        }
+      }
+    }
+  }
+}
+
+// {e0, threshold}: see scale_for. The quotient is formed as its definition
+// says, magnitude times reach over 448 in 64 bits, for every 7-bit mantissa.
+void scale_exponents(double reach, int (&ex)[2]) {
+  auto exponent = [&](int m) {  // smallest e with (1 + m / 128) reach / 448 <= 2^e
+    int e;
+    return std::frexp((1.0 + m / 128.0) * reach / 448.0, &e) == 0.5 ? e - 1 : e;
+  };
+  ex[0] = exponent(0);
+  ex[1] = 0;
+  while (ex[1] < 128 && exponent(ex[1]) == ex[0]) ++ex[1];
+}
+
+template <bool FP8, bool INTERLEAVED>
+void (*append_kernel(int threads, int units))(AppendParams) {
+  if (units == 2) return relpos_paged_append_kernel<FP8, INTERLEAVED, 512, 2>;
+  if (threads == 512) return relpos_paged_append_kernel<FP8, INTERLEAVED, 512, 1>;
+  if (threads == 256) return relpos_paged_append_kernel<FP8, INTERLEAVED, 256, 1>;
+  return relpos_paged_append_kernel<FP8, INTERLEAVED, 128, 1>;
 }
 
 }  // namespace
@@ -380,22 +476,40 @@ extern "C" int relpos_paged_append(const RelposPagedCache* cache, const RelposRo
   p.lens = lens;
   p.log_page = cache->page == 32 ? 5 : cache->page == 64 ? 6 : 7;
   p.log_units = cache->d == 64 ? 2 : 3;
-  p.group = (kAppThreads * kAppSlots) >> (p.log_page + p.log_units);  // 8 .. 1 heads
-  p.reach = plan ? 1.4142135623730951 * plan->amplitude : 1.0;
+  scale_exponents(plan ? 1.4142135623730951 * plan->amplitude : 1.0, p.exp_k);
+  scale_exponents(1.0, p.exp_v);
   p.status = device_status();
-  if (!p.status) return RELPOS_ERR_CUDA;
+  const int sms = device_sms();
+  if (!p.status || sms <= 0) return RELPOS_ERR_CUDA;
+  // a thread for each 16-element unit of a head's page, two units from 1024 on
+  const int items = 1 << (p.log_page + p.log_units);
+  const int threads = std::min(items, 512), units = items / threads;
+  const long long pages = (total >> p.log_page) + 2 * static_cast<long long>(B);
+  // heads of a block: as few as fill the GPU's SMs, since a block walks them
+  const long long groups = std::min<long long>(
+      cache->H, std::max<long long>((cache->H + kAppMaxGroup - 1) / kAppMaxGroup, (4 * sms + pages - 1) / pages));
+  p.group = static_cast<int>((cache->H + groups - 1) / groups);
+  const bool inter = p.plan.layout == RELPOS_ROTARY_INTERLEAVED;
+  const auto kernel = cache->dtype == RELPOS_E4M3
+                          ? (inter ? append_kernel<true, true>(threads, units) : append_kernel<true, false>(threads, units))
+                          : (inter ? append_kernel<false, true>(threads, units) : append_kernel<false, false>(threads, units));
+  const int smem = p.plan.rot_dim ? 64 * items : 0;
+  if (smem > 48 * 1024 &&
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
+    cudaGetLastError();
+    return RELPOS_ERR_CUDA;
+  }
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((total >> p.log_page) + 2 * static_cast<long long>(B)),
-                     (cache->H + p.group - 1) / p.group);
-  cfg.blockDim = dim3(kAppThreads);
+  cfg.gridDim = dim3(static_cast<unsigned>(pages), (cache->H + p.group - 1) / p.group);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = static_cast<cudaStream_t>(stream);
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cache->dtype == RELPOS_E4M3 ? cudaLaunchKernelEx(&cfg, relpos_paged_append_kernel<true>, p)
-                                                    : cudaLaunchKernelEx(&cfg, relpos_paged_append_kernel<false>, p);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p);
   if (e != cudaSuccess) {
     cudaGetLastError();
     return RELPOS_ERR_CUDA;

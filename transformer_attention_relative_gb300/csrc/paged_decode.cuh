@@ -1,0 +1,992 @@
+// paged_decode.cuh -- the kernels of attention of a few new rows over a paged
+// key/value cache, bf16 or e4m3 with a scale for each page and head ("Relative
+// Position Embeddings, in depth", section "Kernels and the KV cache"), with no
+// bias, the T5 bucket bias or ALiBi, and grouped heads.
+//
+//   out_r = sum_j p_rj v_j / sum_j p_rj,  p_rj = exp(scale q_r . k_j + bias_rj - m_r)
+//
+// The cache is streamed once, about one product per byte and row, so the kernel
+// is built around keeping loads in flight: each warp has its own ring of tiles
+// in shared memory, filled by asynchronous copies. The products of the up to 32
+// rows that share a key/value head (query heads of the group times new rows)
+// run on the tensor cores' m16n8k16 form, whose operands come straight out of
+// the streamed tile.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cfloat>
+#include <cstdint>
+#include <type_traits>
+#include <utility>
+
+#include "../../include/relpos_attn.h"
+#include "ptx.cuh"
+#include "relpos_common.cuh"
+#include "relpos_internal.h"
+
+namespace relpos {
+
+constexpr int kPdWarps = 4;
+constexpr int kPdThreads = 32 * kPdWarps;
+constexpr int kPdMaxRows = 32;  // rows of a unit at most
+constexpr int kPdMinTiles = 4;  // fewest tiles of a block's share: one for each warp
+constexpr int kPdBuckets = 1024;  // distances whose T5 bucket is looked up
+// The weights p are kept as 2^(logit - off) for a row offset `off` that starts
+// below every logit and moves up only when a logit comes more than kPdMost above
+// it, to kPdShift below the largest: most tiles then need no maximum across the
+// warp and no rescaling. Weights stay below 2^14, so that fp16 ones (8-bit
+// caches) keep 11 bits down to 2^-20 of the offset's logit and vanish below 2^-30.
+constexpr float kPdShift = 6.f, kPdMost = 14.f;
+
+struct PagedDecodeParams {
+  const uint8_t* k;
+  const uint8_t* v;
+  const float* k_scale;
+  const float* v_scale;
+  int num_pages, Hkv, log_page;
+  const __nv_bfloat16* Q;
+  long long q_batch, q_head, q_row;
+  int q_vec, o_vec;  // rows of Q and of out are 16-byte aligned
+  __nv_bfloat16* out;
+  long long o_batch, o_head, o_row;
+  const int* table;
+  long long table_stride;
+  int max_len;  // tokens that the block table's row can name
+  const int* lens;
+  int B, Hq, Lq, G;  // G: query heads of a key/value head
+  int rows;          // rows of a unit (a multiple of 8)
+  int rt;            // units that the G * Lq rows of a key/value head take
+  const float* bias;
+  int mode;          // RELPOS_NO_BIAS, RELPOS_T5 or RELPOS_ALIBI
+  int t5_R;
+  T5Index t5;
+  float scale_log2;
+  float* part_o;   // [blocks][2][rows][d] partial outputs
+  float* part_ml;  // [blocks][2][rows][2] their offsets and sums
+  int blocks;
+  int* status;
+};
+
+// A variant's kernels, tile size and shared memory; one translation unit each
+// for the head dimensions and types. `rows8`: 8-row groups of a unit.
+struct PagedDecodeVariant {
+  void (*decode)(PagedDecodeParams);
+  void (*combine)(PagedDecodeParams);
+  int tile, smem;
+};
+PagedDecodeVariant paged_decode_e4m3_64(int rows8);
+PagedDecodeVariant paged_decode_e4m3_128(int rows8);
+PagedDecodeVariant paged_decode_bf16_64(int rows8);
+PagedDecodeVariant paged_decode_bf16_128(int rows8);
+
+namespace {
+
+// A unit is one sequence, key/value head and up to 32 rows; units follow one
+// another in that order, each with the sequence's key tiles. A block takes an
+// equal share of the tiles of all units, whatever the lengths, and its warps
+// every fourth tile of it.
+
+RP_DEVI int seq_tiles(const PagedDecodeParams& p, int b, int KT) {
+  const int len = __ldcg(p.lens + b);
+  return (min(max(len, 0), p.max_len) + KT - 1) / KT;
+}
+
+// Key tiles of the units before sequence `upto` and of all units, summed by a
+// warp. (Lengths are read past the L1 cache: the combine kernel looks at them
+// before it waits for this one.)
+RP_DEVI void count_tiles(const PagedDecodeParams& p, int upto, int KT, int lane, int& before, int& total) {
+  int sum = 0, part = 0;
+  for (int i = lane; i < p.B; i += 32) {
+    const int nt = seq_tiles(p, i, KT);
+    sum += nt;
+    part += i < upto ? nt : 0;
+  }
+  before = __reduce_add_sync(0xffffffffu, part) * p.Hkv * p.rt;
+  total = __reduce_add_sync(0xffffffffu, sum) * p.Hkv * p.rt;
+}
+
+RP_DEVI int share_of(int total, int blocks) { return max((total + blocks - 1) / blocks, kPdMinTiles); }
+
+// Place in the sequence of tiles: sequence and its length, unit of it, tile of
+// the unit.
+struct Cursor {
+  int b, u, t, nt, len;
+  int h;             // key/value head of the unit
+  const int* pages;  // the sequence's row of the block table
+  template <int KT>
+  RP_DEVI void enter(const PagedDecodeParams& p) {  // the first sequence from b on that has tiles
+    nt = len = 0;
+    for (; b < p.B; ++b) {
+      len = min(max(__ldcg(p.lens + b), 0), p.max_len);
+      nt = (len + KT - 1) / KT;
+      pages = p.table + b * p.table_stride;
+      if (nt) return;
+    }
+  }
+  template <int KT>
+  RP_DEVI void forward(const PagedDecodeParams& p, int by) {
+    t += by;
+    while (t >= nt && b < p.B) {
+      t -= nt;
+      if (++u == p.Hkv * p.rt) {
+        u = 0;
+        ++b;
+        enter<KT>(p);
+      }
+      h = u / p.rt;
+    }
+  }
+};
+
+// This block's share x0 .. x1 - 1 of all tiles, and the cursor at x0;
+// warp-uniform. The first 32 sequences' lengths are loaded once.
+template <int KT>
+RP_DEVI Cursor locate(const PagedDecodeParams& p, int lane, int& x0, int& x1) {
+  const int per = p.Hkv * p.rt;
+  auto length = [&](int b) { return b < p.B ? min(max(__ldcg(p.lens + b), 0), p.max_len) : 0; };
+  const int len0 = length(lane);
+  int sum = (len0 + KT - 1) / KT;
+  for (int b = lane + 32; b < p.B; b += 32) sum += (length(b) + KT - 1) / KT;
+  const int total = __reduce_add_sync(0xffffffffu, sum) * per;
+  const int share = share_of(total, p.blocks);
+  x0 = min(static_cast<int>(blockIdx.x) * share, total);
+  x1 = min(x0 + share, total);
+  Cursor c{p.B, 0, 0, 0, 0, 0, p.table};
+  if (x0 == x1) return c;
+  int before = 0;
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
+    const int len = b0 ? length(b0 + lane) : len0;
+    const int nt = (len + KT - 1) / KT;
+    int upto = nt;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += y;
+    }
+    // the first sequence whose tiles end behind x0
+    const unsigned past = __ballot_sync(0xffffffffu, (before + upto) * per > x0);
+    if (past) {
+      const int l = __ffs(past) - 1;
+      const int rest = x0 - (before + __shfl_sync(0xffffffffu, upto - nt, l)) * per;
+      c.b = b0 + l;
+      c.len = __shfl_sync(0xffffffffu, len, l);
+      c.nt = __shfl_sync(0xffffffffu, nt, l);
+      c.pages = p.table + c.b * p.table_stride;
+      c.u = rest / c.nt;
+      c.t = rest - c.u * c.nt;
+      c.h = c.u / p.rt;
+      return c;
+    }
+    before += __shfl_sync(0xffffffffu, upto, 31);
+  }
+  return c;
+}
+
+template <int DST, int SRC>
+RP_DEVI void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0 + %2], [%1 + %3], 16;" ::"r"(dst), "l"(src), "n"(DST), "n"(SRC) : "memory");
+}
+// `bytes` (16 or 0) are copied, the rest is zero
+template <int DST, int SRC>
+RP_DEVI void cp_async16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0 + %2], [%1 + %3], 16, %4;" ::"r"(dst), "l"(src), "n"(DST), "n"(SRC),
+               "r"(bytes)
+               : "memory");
+}
+RP_DEVI void cp_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+RP_DEVI void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+RP_DEVI void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+RP_DEVI uint4 lds128(uint32_t a) {
+  uint4 u;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "r"(a) : "memory");
+  return u;
+}
+RP_DEVI uint2 lds64(uint32_t a) {
+  uint2 u;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(u.x), "=r"(u.y) : "r"(a) : "memory");
+  return u;
+}
+RP_DEVI float lds32f(uint32_t a) {
+  float f;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f) : "r"(a) : "memory");
+  return f;
+}
+
+// two e4m3 codes to two fp16 values (exact), from the low or high half of w
+RP_DEVI uint32_t half2_lo(uint32_t w) {
+  uint32_t h;
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t}" : "=r"(h) : "r"(w));
+  return h;
+}
+RP_DEVI uint32_t half2_hi(uint32_t w) {
+  uint32_t h;
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, b;\n\t}" : "=r"(h) : "r"(w));
+  return h;
+}
+
+template <bool F16>
+RP_DEVI void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (F16) {
+    asm(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  } else {
+    asm(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  }
+}
+
+// an 8 x 8 matrix of 16-bit values, transposed across the warp
+RP_DEVI uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+RP_DEVI uint32_t pack_half2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+RP_DEVI uint32_t pack_bf2(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Shapes of a variant: head dimension, cache type, 8-row groups of a unit, keys
+// of a tile, ring stages. A tile divides a page, so it has one page number and
+// one pair of scales.
+template <int D, bool FP8, int NQ, int KT, int STAGES>
+struct Shape {
+  static constexpr int kRows = 8 * NQ;
+  static constexpr int kRowBytes = D * (FP8 ? 1 : 2);
+  static constexpr int kChunks = kRowBytes / 16;       // 16-byte chunks of a key's row
+  static constexpr int kTileBytes = KT * kRowBytes;    // of the keys, and of the values
+  static constexpr int kStageBytes = 2 * kTileBytes + 16;  // and the two scales
+  static constexpr int kRingBytes = STAGES * kStageBytes;  // of a warp
+  static constexpr int kSmem = kPdWarps * kRingBytes + 2 * kRows * D * 4 + kPdWarps * kRows * 2 * 4;
+  static constexpr int kIters = KT * kChunks / 32;     // 16-byte copies of a lane, of each of K and V
+};
+
+// Chunk c of row r lies at chunk c ^ f(r) of its row in shared memory. A
+// quarter-warp reads the keys by 4 chunks of rows 2i, 2i + 1, the values by 2
+// chunks of rows 2t + o for t = 0..3; with this f both meet 8 different groups
+// of banks (rows of 64 bytes, two to a bank line, need only the row pair's
+// index).
+template <int CHUNKS>
+RP_DEVI constexpr int swizzle(int r) {
+  return CHUNKS == 4 ? (r >> 1) & 3 : (((r >> 1) & 3) << 1) ^ ((r & 1) << 2);
+}
+
+template <int... I, typename F>
+RP_DEVI void for_each(std::integer_sequence<int, I...>, F&& f) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+
+// log2 units, a finite value staying finite (a table may hold the type's lowest)
+RP_DEVI float to_log2(float x) {
+  return fabsf(x) <= FLT_MAX ? fminf(fmaxf(x * kLog2e, -FLT_MAX), FLT_MAX) : x;
+}
+
+// The products are formed the other way round, keys and output dimensions as
+// the rows of the matrix instruction (16) and query rows as its columns (8):
+// one query row of one head, the common case, then wastes 7 of 8 columns
+// instead of 15 of 16 rows, and everything that is done per score or per output
+// value halves. K's rows are the A operand as they lie in memory; V^T's A
+// operand is V's words of two keys interleaved; p^T, the B operand, is the
+// scores' tile transposed across the warp (movmatrix). 8-bit keys and values
+// become fp16, exactly (the e4m3 form of the instruction takes more
+// instructions here: 510 a tile against 453).
+template <int D, bool FP8, int NQ, int KT, int STAGES>
+__global__ void __launch_bounds__(kPdThreads, NQ * D <= 64 ? 4 : NQ * D <= 128 ? 3 : 2)
+    relpos_paged_decode_kernel(const __grid_constant__ PagedDecodeParams p) {
+  using S = Shape<D, FP8, NQ, KT, STAGES>;
+  constexpr int MT = KT / 16;   // 16-key tiles of the scores, 16-key steps of v^T p^T
+  constexpr int KS = D / 16;    // 16-dim steps of k . q, 16-dim tiles of the output
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ uint8_t bucket_s[kPdBuckets];  // T5 buckets of the first distances
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int g = lane >> 2, t = lane & 3;
+  const uint32_t ring = smem_u32(smem) + warp * S::kRingBytes;
+  float* const out_s = reinterpret_cast<float*>(smem + kPdWarps * S::kRingBytes);
+  float* const ml_s = out_s + 2 * S::kRows * D;
+
+  griddep_wait();
+  griddep_launch_dependents();
+  int x0, x1;
+  Cursor pc = locate<KT>(p, lane, x0, x1);
+  if (x0 >= x1) return;
+
+  // ---- producer: this warp's tiles x0 + warp, x0 + warp + 4, ... into its ring
+  Cursor cc = pc;
+  pc.forward<KT>(p, warp);
+  int px = x0 + warp;
+  auto page_of = [&](const Cursor& c) { return __ldg(c.pages + ((c.t * KT) >> p.log_page)); };
+  int next_page = px < x1 ? page_of(pc) : 0;  // a step ahead: its load does not delay the copies
+  const int r0 = lane / S::kChunks, ch = lane % S::kChunks;
+  const uint32_t dst0 = r0 * S::kRowBytes + ((ch ^ swizzle<S::kChunks>(r0)) << 4);
+  constexpr int kStep = 32 / S::kChunks;  // rows between a lane's copies
+  const uint32_t page_bytes = S::kRowBytes << p.log_page;
+  const uint8_t *k_lane = p.k + lane * 16, *v_lane = p.v + lane * 16;
+  auto produce = [&](int stage) {
+    if (px < x1) {
+      const int key0 = pc.t * KT;
+      int valid = pc.len - key0;
+      uint32_t page = next_page;
+      if (page >= static_cast<uint32_t>(p.num_pages)) {  // zeros in its place, and the error on record
+        if (lane == 0) atomicCAS(p.status, 0, RELPOS_ERR_PAGE);
+        page = 0;
+        valid = 0;
+      }
+      const uint32_t ph = page * p.Hkv + pc.h;  // (page, head) pairs of a pool are fewer than 2^31
+      const size_t at = static_cast<size_t>(ph) * page_bytes + (key0 & ((1 << p.log_page) - 1)) * S::kRowBytes;
+      const uint32_t base = ring + stage * S::kStageBytes;
+      const uint8_t *kp = k_lane + at, *vp = v_lane + at;
+      // row r0 + i kStep goes to dst0 ^ (f(i kStep) << 4) + 512 i: two bases
+      const uint32_t even = base + dst0, odd = base + (dst0 ^ (swizzle<S::kChunks>(kStep) << 4));
+      auto copy = [&](auto index, auto full) {
+        constexpr int i = decltype(index)::value;
+        constexpr uint32_t x = swizzle<S::kChunks>(i * kStep) << 4;
+        const uint32_t dst = x == 0 ? even : x == (swizzle<S::kChunks>(kStep) << 4) ? odd : base + (dst0 ^ x);
+        if constexpr (decltype(full)::value) {
+          cp_async16<i * 512, i * 512>(dst, kp);
+          cp_async16<S::kTileBytes + i * 512, i * 512>(dst, vp);
+        } else {  // zeros behind the sequence's end
+          const int bytes = r0 + i * kStep < valid ? 16 : 0;
+          cp_async16<i * 512, i * 512>(dst, kp, bytes);
+          cp_async16<S::kTileBytes + i * 512, i * 512>(dst, vp, bytes);
+        }
+      };
+      if (valid >= KT)
+        for_each(std::make_integer_sequence<int, S::kIters>{}, [&](auto i) { copy(i, std::true_type{}); });
+      else
+        for_each(std::make_integer_sequence<int, S::kIters>{}, [&](auto i) { copy(i, std::false_type{}); });
+      if constexpr (FP8) {
+        if (lane < 2) cp_async4(base + 2 * S::kTileBytes + lane * 4, (lane ? p.v_scale : p.k_scale) + ph);
+      }
+      px += kPdWarps;
+      if (px < x1) {
+        pc.forward<KT>(p, kPdWarps);
+        next_page = page_of(pc);
+      }
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < STAGES - 1; ++i) produce(i);
+  if (p.mode == RELPOS_T5) {
+    for (int i = threadIdx.x; i < min(p.t5_R, kPdBuckets); i += kPdThreads)
+      bucket_s[i] = static_cast<uint8_t>(t5_bucket_dev(-i, p.t5));
+    __syncthreads();
+  }
+
+  // ---- consumer: the block's units one after another
+  constexpr int KC = FP8 ? D / 64 : D / 32;  // chunks that a lane reads of a key's row
+  uint32_t k_off[KC], v_off[2];
+#pragma unroll
+  for (int j = 0; j < KC; ++j) k_off[j] = g * S::kRowBytes + (((t + 4 * j) ^ swizzle<S::kChunks>(g)) << 4);
+#pragma unroll
+  for (int o = 0; o < 2; ++o) {
+    const int row = 2 * t + o;
+    if constexpr (FP8 && D == 64)
+      v_off[o] = row * S::kRowBytes + (((g >> 1) ^ swizzle<S::kChunks>(row)) << 4) + (g & 1) * 8;
+    else
+      v_off[o] = row * S::kRowBytes + ((g ^ swizzle<S::kChunks>(row)) << 4);
+  }
+
+  // the first of the 4 dims that a lane holds of q and of a key for step s
+  auto dim_of = [&](int s) { return FP8 ? 16 * (t + 4 * (s / 4)) + 4 * (s % 4) : 8 * (t + 4 * (s / 2)) + 4 * (s % 2); };
+
+  int stage = 0;
+  int x = x0;
+  while (x < x1) {
+    const int xe = min(x1, x + cc.nt - cc.t);  // the unit's tiles in this block
+    const int len = cc.len;
+    if (threadIdx.x == 0 && __ldcg(p.lens + cc.b) > p.max_len) atomicCAS(p.status, 0, RELPOS_ERR_PAGE);
+    const int h = cc.h, row0 = (cc.u - h * p.rt) * S::kRows;
+    const int rows = min(p.G * p.Lq - row0, S::kRows);
+
+    // row 8 n + g of the unit as the B operand of k . q
+    uint32_t q[NQ][KS][2];
+    // this lane's score columns, rows 8 n + 2 t and + 1: scale of the products,
+    // last key seen, constant and slope of the bias
+    float qs[NQ][2], add[NQ][2], slope[NQ][2];
+    int vis[NQ][2];
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+      const int r = row0 + 8 * n + g;
+      const int i = r / p.G, hq = h * p.G + r - i * p.G;
+      const bool real = 8 * n + g < rows;
+      const __nv_bfloat16* qp = p.Q + cc.b * p.q_batch + hq * p.q_head + i * p.q_row;
+      float f[KS][4];
+#pragma unroll
+      for (int s = 0; s < KS; ++s) f[s][0] = f[s][1] = f[s][2] = f[s][3] = 0.f;
+      if (real && p.q_vec) {
+#pragma unroll
+        for (int s = 0; s < KS; s += 2) {
+          const uint4 u = __ldg(reinterpret_cast<const uint4*>(qp + dim_of(s)));
+          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+          for (int m = 0; m < 4; ++m) {
+            f[s + m / 2][2 * (m & 1)] = __uint_as_float(w[m] << 16);
+            f[s + m / 2][2 * (m & 1) + 1] = __uint_as_float(w[m] & 0xffff0000u);
+          }
+        }
+      } else if (real) {
+#pragma unroll
+        for (int s = 0; s < KS; ++s)
+#pragma unroll
+          for (int m = 0; m < 4; ++m) f[s][m] = __bfloat162float(qp[dim_of(s) + m]);
+      }
+      float up = p.scale_log2;
+      if constexpr (FP8) {
+        // to fp16 by way of a power of two that brings the row's largest
+        // value into [1, 2): exact but for values below 2^-14 of it
+        float big = 0.f;
+#pragma unroll
+        for (int s = 0; s < KS; ++s)
+#pragma unroll
+          for (int m = 0; m < 4; ++m) big = fmaxf(big, fabsf(f[s][m]));
+        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+        const int ex = min(126, max(-126, static_cast<int>(__float_as_uint(big) >> 23) - 127));
+        const float down = __int_as_float((127 - ex) << 23);
+        up *= __int_as_float((127 + ex) << 23);
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+          q[n][s][0] = pack_half2(f[s][0] * down, f[s][1] * down);
+          q[n][s][1] = pack_half2(f[s][2] * down, f[s][3] * down);
+        }
+      } else {
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+          q[n][s][0] = pack_bf2(f[s][0], f[s][1]);
+          q[n][s][1] = pack_bf2(f[s][2], f[s][3]);
+        }
+      }
+      int last = -1;
+      float far = 0.f, sl = 0.f;
+      if (real) {
+        last = len - p.Lq + i;
+        if (p.mode == RELPOS_ALIBI) sl = __ldg(p.bias + hq) * kLog2e;
+        if (p.mode == RELPOS_T5) far = to_log2(__ldg(p.bias + (p.t5.slots - 1) * p.Hq + hq));
+      }
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {  // from the lanes of row 8 n + 2 t + c
+        const int from = 4 * (2 * t + c);
+        qs[n][c] = __shfl_sync(0xffffffffu, up, from);
+        vis[n][c] = __shfl_sync(0xffffffffu, last, from);
+        add[n][c] = __shfl_sync(0xffffffffu, far, from);
+        slope[n][c] = __shfl_sync(0xffffffffu, sl, from);
+      }
+    }
+    const int vis_first = len - p.Lq + row0 / p.G;  // last key that every row sees
+    float off[NQ][2], l_run[NQ][2], o[NQ][KS][4];
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+      off[n][0] = off[n][1] = 0.f;
+      l_run[n][0] = l_run[n][1] = 0.f;
+#pragma unroll
+      for (int j = 0; j < KS; ++j) o[n][j][0] = o[n][j][1] = o[n][j][2] = o[n][j][3] = 0.f;
+    }
+
+    // this warp's tiles of the unit: x + k with (x - x0 + k) mod 4 = warp
+    for (int y = x + ((warp - (x - x0)) & (kPdWarps - 1)); y < xe; y += kPdWarps) {
+      cp_async_wait<STAGES - 2>();
+      __syncwarp();
+      produce(stage == 0 ? STAGES - 1 : stage - 1);
+      const uint32_t ks = ring + stage * S::kStageBytes, vs = ks + S::kTileBytes;
+      if (++stage == STAGES) stage = 0;
+      const int key0 = (cc.t + y - x) * KT;
+
+      // scores: lane (g, t) holds keys 16 i + g (+ 8) and rows 8 n + 2 t, + 1
+      float sc[NQ][MT][4];
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) sc[n][i][0] = sc[n][i][1] = sc[n][i][2] = sc[n][i][3] = 0.f;
+#pragma unroll
+        for (int j = 0; j < KC; ++j) {
+          const uint4 u = lds128(ks + k_off[j] + 16 * i * S::kRowBytes);
+          const uint4 w = lds128(ks + k_off[j] + (16 * i + 8) * S::kRowBytes);
+          const uint32_t a[4] = {u.x, u.y, u.z, u.w}, b[4] = {w.x, w.y, w.z, w.w};
+          if constexpr (FP8) {
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+              const uint32_t f[4] = {half2_lo(a[s]), half2_lo(b[s]), half2_hi(a[s]), half2_hi(b[s])};
+#pragma unroll
+              for (int n = 0; n < NQ; ++n) mma16816<true>(sc[n][i], f, q[n][4 * j + s][0], q[n][4 * j + s][1]);
+            }
+          } else {
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+              const uint32_t f[4] = {a[2 * s], b[2 * s], a[2 * s + 1], b[2 * s + 1]};
+#pragma unroll
+              for (int n = 0; n < NQ; ++n) mma16816<false>(sc[n][i], f, q[n][2 * j + s][0], q[n][2 * j + s][1]);
+            }
+          }
+        }
+      }
+      float k_scale = 1.f, v_scale = 1.f;
+      if constexpr (FP8) {
+        k_scale = lds32f(vs + S::kTileBytes);
+        v_scale = lds32f(vs + S::kTileBytes + 4);
+      }
+      const bool edge = key0 + KT - 1 > vis_first;  // some row does not see every key
+      const bool near = p.mode == RELPOS_T5 && vis_first - (key0 + KT - 1) < p.t5_R;
+      // logit of row 8 n + 2 t + c and key 16 i + 8 e + g, less its row's offset
+      auto logits = [&](float (&z)[NQ][MT][4]) {
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) {
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const float cs = qs[n][c] * k_scale;
+            const int back0 = vis[n][c] - key0 - g;  // to key 16 i + 8 e: less 16 i + 8 e
+            if (near) {
+              const int hq = h * p.G + (row0 + 8 * n + 2 * t + c) % p.G;
+#pragma unroll
+              for (int i = 0; i < MT; ++i) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  const int back = back0 - 16 * i - 8 * e;
+                  int bucket = p.t5.slots - 1;
+                  if (back < p.t5_R) bucket = back < kPdBuckets ? bucket_s[max(back, 0)] : t5_bucket_dev(-back, p.t5);
+                  z[n][i][2 * e + c] =
+                      fmaf(sc[n][i][2 * e + c], cs, to_log2(__ldg(p.bias + bucket * p.Hq + hq))) - off[n][c];
+                }
+              }
+            } else if (p.mode != RELPOS_ALIBI) {
+              // bias and offset in one constant; a bias of the type's lowest
+              // values, beside which a product has no bits, takes it away
+              const float base = add[n][c] - off[n][c], cf = fabsf(add[n][c]) < 1e30f ? cs : 0.f;
+#pragma unroll
+              for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) z[n][i][2 * e + c] = fmaf(sc[n][i][2 * e + c], cf, base);
+            } else {
+              const float back_f = static_cast<float>(back0);
+#pragma unroll
+              for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                  z[n][i][2 * e + c] =
+                      fmaf(sc[n][i][2 * e + c], cs, fmaf(-slope[n][c], back_f - (16 * i + 8 * e), -off[n][c]));
+            }
+            if (edge) {
+#pragma unroll
+              for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                  if (back0 < 16 * i + 8 * e) z[n][i][2 * e + c] = -INFINITY;
+            }
+          }
+        }
+      };
+      // Offsets move by the logits themselves (less an offset far below them
+      // these have no bits left): the rows concerned take offset 0 and the
+      // logits are formed anew. At the warp's first tile of the unit that is
+      // where they stand.
+      float z[NQ][MT][4], was[NQ][2];
+      bool moves[NQ][2], settle = y < x + kPdWarps;
+#pragma unroll
+      for (int n = 0; n < NQ; ++n) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          was[n][c] = -FLT_MAX;
+          moves[n][c] = true;
+        }
+      }
+      auto largest = [&](int n, int c) {
+        float top = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < MT; ++i) top = fmaxf(top, fmaxf(z[n][i][c], z[n][i][2 + c]));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+        return fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+      };
+      while (true) {
+        logits(z);
+        if (settle) break;
+        bool above = false;
+#pragma unroll
+        for (int n = 0; n < NQ; ++n)
+#pragma unroll
+          for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) above |= z[n][i][e] > kPdMost;
+        if (!__any_sync(0xffffffffu, above)) break;
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) {
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            was[n][c] = off[n][c];
+            moves[n][c] = largest(n, c) > kPdMost;
+            if (moves[n][c]) off[n][c] = 0.f;
+          }
+        }
+        settle = true;
+      }
+      if (settle) {
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) {
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const float top = fmaxf(largest(n, c) - kPdShift, -FLT_MAX);  // a row may see no key
+            if (moves[n][c]) {
+              off[n][c] = top;
+              const float down = ex2_approx(was[n][c] - top);
+              l_run[n][c] *= down;
+#pragma unroll
+              for (int i = 0; i < MT; ++i) z[n][i][c] -= top, z[n][i][2 + c] -= top;
+#pragma unroll
+              for (int j = 0; j < KS; ++j) o[n][j][c] *= down, o[n][j][2 + c] *= down;
+            }
+          }
+        }
+      }
+#pragma unroll
+      for (int n = 0; n < NQ; ++n) {
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            sc[n][i][e] = ex2_approx(z[n][i][e]);
+            l_run[n][e & 1] += sc[n][i][e];
+          }
+        }
+      }
+
+      // o^T += v^T p^T, for the rows and the keys of one query position (ONE)
+      // or all
+      auto add_values = [&](auto one, int last) {
+        constexpr bool ONE = decltype(one)::value;
+        uint32_t ph[NQ][MT][2];
+        [[maybe_unused]] uint32_t pl[FP8 ? 1 : NQ][MT][2];
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) {
+          const bool mine[2] = {!ONE || vis[n][0] == last, !ONE || vis[n][1] == last};
+#pragma unroll
+          for (int i = 0; i < MT; ++i) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float a = mine[0] ? sc[n][i][2 * e] : 0.f, c = mine[1] ? sc[n][i][2 * e + 1] : 0.f;
+              if constexpr (FP8) {
+                // 11 bits of a weight: its rounding (2^-12) is far below the
+                // output's (2^-9)
+                ph[n][i][e] = transpose8(pack_half2(a, c));
+              } else {
+                // bf16 alone would round the weights as coarsely as the
+                // output: a second part carries the next 8 bits
+                const uint32_t hi = pack_bf2(a, c);
+                ph[n][i][e] = transpose8(hi);
+                pl[n][i][e] =
+                    transpose8(pack_bf2(a - __uint_as_float(hi << 16), c - __uint_as_float(hi & 0xffff0000u)));
+              }
+            }
+          }
+        }
+        // value rows of the lane: 16 i + 8 e + 2 t + o
+        auto row_words = [&](int i, int e, int oo, int half, uint32_t (&w)[4]) {
+          const uint32_t a = vs + v_off[oo] + (16 * i + 8 * e) * S::kRowBytes + half * 128;
+          if constexpr (FP8 && D == 64) {
+            const uint2 u = lds64(a);
+            w[0] = u.x, w[1] = u.y, w[2] = w[3] = 0;
+          } else {
+            const uint4 u = lds128(a);
+            w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+          }
+          if (ONE && key0 + 16 * i + 8 * e + 2 * t + oo > last) w[0] = w[1] = w[2] = w[3] = 0;
+        };
+        if constexpr (FP8) {
+          uint32_t r[MT][2][2][4];
+#pragma unroll
+          for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+              for (int oo = 0; oo < 2; ++oo) row_words(i, e, oo, 0, r[i][e][oo]);
+#pragma unroll
+          for (int w = 0; w < D / 32; ++w) {  // words of 4 dims that a lane holds of a row
+            float acc[NQ][2][4];
+#pragma unroll
+            for (int n = 0; n < NQ; ++n)
+#pragma unroll
+              for (int j = 0; j < 2; ++j) acc[n][j][0] = acc[n][j][1] = acc[n][j][2] = acc[n][j][3] = 0.f;
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                const uint32_t a = __byte_perm(r[i][0][0][w], r[i][0][1][w], j ? 0x7362 : 0x5140);
+                const uint32_t b = __byte_perm(r[i][1][0][w], r[i][1][1][w], j ? 0x7362 : 0x5140);
+                const uint32_t f[4] = {half2_lo(a), half2_hi(a), half2_lo(b), half2_hi(b)};
+#pragma unroll
+                for (int n = 0; n < NQ; ++n) mma16816<true>(acc[n][j], f, ph[n][i][0], ph[n][i][1]);
+              }
+            }
+#pragma unroll
+            for (int n = 0; n < NQ; ++n)
+#pragma unroll
+              for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  if (!ONE || vis[n][e & 1] == last)
+                    o[n][2 * w + j][e] = fmaf(acc[n][j][e], v_scale, o[n][2 * w + j][e]);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < MT; ++i) {
+#pragma unroll
+            for (int half = 0; half < D / 64; ++half) {
+              uint32_t r[2][2][4];
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int oo = 0; oo < 2; ++oo) row_words(i, e, oo, half, r[e][oo]);
+#pragma unroll
+              for (int w = 0; w < 4; ++w) {
+                const uint32_t f[4] = {
+                    __byte_perm(r[0][0][w], r[0][1][w], 0x5410), __byte_perm(r[0][0][w], r[0][1][w], 0x7632),
+                    __byte_perm(r[1][0][w], r[1][1][w], 0x5410), __byte_perm(r[1][0][w], r[1][1][w], 0x7632)};
+#pragma unroll
+                for (int n = 0; n < NQ; ++n) {
+                  float(&d)[4] = o[n][4 * half + w];
+                  const float was[4] = {d[0], d[1], d[2], d[3]};
+                  mma16816<false>(d, f, ph[n][i][0], ph[n][i][1]);
+                  mma16816<false>(d, f, pl[n][i][0], pl[n][i][1]);
+                  if (ONE) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) d[e] = vis[n][e & 1] == last ? d[e] : was[e];
+                  }
+                }
+              }
+            }
+          }
+        }
+      };
+      // Where rows of one tile see different keys and a value that some of
+      // them do not see is not finite (0 times it is NaN), the rows of each
+      // query position go alone, with the values that they do not see as
+      // zeros.
+      bool foul = false;
+      if (edge && p.Lq > 1) {
+#pragma unroll
+        for (int i = lane; i < KT * S::kChunks; i += 32) {
+          const uint4 u = lds128(vs + 16 * i);
+          if (key0 + i / S::kChunks > vis_first) {
+            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+              foul |= FP8 ? __vcmpeq4(w[m] & 0x7f7f7f7fu, 0x7f7f7f7fu) != 0
+                          : __vcmpeq2(w[m] & 0x7f807f80u, 0x7f807f80u) != 0;
+          }
+        }
+        foul = __any_sync(0xffffffffu, foul);
+      }
+      if (foul) {
+        for (int i = 0; i < p.Lq; ++i) add_values(std::true_type{}, len - p.Lq + i);
+      } else {
+        add_values(std::false_type{}, 0);
+      }
+    }
+
+    // ---- the four warps' parts of the unit, joined in a fixed order: 2 into 0
+    // and 3 into 1, then 1 into 0
+    const int tiles = xe - x, skew = (x - x0) & (kPdWarps - 1);
+    float m[NQ][2], l[NQ][2], f[NQ][2];
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        if (((warp - skew) & (kPdWarps - 1)) >= tiles) off[n][c] = -FLT_MAX;  // a warp without tiles
+        l_run[n][c] += __shfl_xor_sync(0xffffffffu, l_run[n][c], 4);
+        l_run[n][c] += __shfl_xor_sync(0xffffffffu, l_run[n][c], 8);
+        l_run[n][c] += __shfl_xor_sync(0xffffffffu, l_run[n][c], 16);
+        if (g == 0) {
+          float* ml = ml_s + (warp * S::kRows + 8 * n + 2 * t + c) * 2;
+          ml[0] = off[n][c];
+          ml[1] = l_run[n][c];
+        }
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const float2* ml = reinterpret_cast<const float2*>(ml_s) + 8 * n + 2 * t + c;
+        m[n][c] = -FLT_MAX;
+#pragma unroll
+        for (int w = 0; w < kPdWarps; ++w) m[n][c] = fmaxf(m[n][c], ml[w * S::kRows].x);
+        l[n][c] = 0.f;
+#pragma unroll
+        for (int w = 0; w < kPdWarps; ++w)
+          l[n][c] = fmaf(ex2_approx(ml[w * S::kRows].x - m[n][c]), ml[w * S::kRows].y, l[n][c]);
+        f[n][c] = ex2_approx(off[n][c] - m[n][c]);
+#pragma unroll
+        for (int j = 0; j < KS; ++j) o[n][j][c] *= f[n][c], o[n][j][2 + c] *= f[n][c];
+      }
+    }
+    // a lane's values of a row: 16 bytes at a time, lane after lane
+    auto give = [&](float* to) {
+#pragma unroll
+      for (int n = 0; n < NQ; ++n)
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+          if (8 * n + 2 * t + c < rows)
+#pragma unroll
+            for (int j = 0; j < KS; j += 2)
+              reinterpret_cast<float4*>(to)[((n * 2 + c) * (KS / 2) + j / 2) * 32 + lane] =
+                  make_float4(o[n][j][c], o[n][j][2 + c], o[n][j + 1][c], o[n][j + 1][2 + c]);
+    };
+    auto take = [&](const float* from) {
+#pragma unroll
+      for (int n = 0; n < NQ; ++n)
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+          if (8 * n + 2 * t + c < rows)
+#pragma unroll
+            for (int j = 0; j < KS; j += 2) {
+              const float4 v = reinterpret_cast<const float4*>(from)[((n * 2 + c) * (KS / 2) + j / 2) * 32 + lane];
+              o[n][j][c] += v.x, o[n][j][2 + c] += v.y, o[n][j + 1][c] += v.z, o[n][j + 1][2 + c] += v.w;
+            }
+    };
+    if (warp >= 2) give(out_s + (warp - 2) * S::kRows * D);
+    __syncthreads();
+    if (warp < 2) take(out_s + warp * S::kRows * D);
+    if (warp == 1) give(out_s + S::kRows * D);
+    __syncthreads();
+    if (warp == 0) {
+      take(out_s + S::kRows * D);
+      const bool whole = cc.t == 0 && tiles == cc.nt;
+      const int slot = 2 * blockIdx.x + (cc.t == 0 ? 1 : 0);
+#pragma unroll
+      for (int n = 0; n < NQ; ++n) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int r = 8 * n + 2 * t + c;
+          if (r >= rows) continue;
+          float inv = 1.f;
+          __nv_bfloat16* op = nullptr;
+          float* pp = p.part_o + (static_cast<size_t>(slot) * S::kRows + r) * D;
+          if (whole) {
+            inv = l[n][c] == 0.f ? 0.f : 1.f / l[n][c];
+            const int qi = (row0 + r) / p.G;
+            const int hq = h * p.G + (row0 + r) - qi * p.G;
+            op = p.out + cc.b * p.o_batch + hq * p.o_head + qi * p.o_row;
+          } else if (g == 0) {
+            *reinterpret_cast<float2*>(p.part_ml + (static_cast<size_t>(slot) * S::kRows + r) * 2) =
+                make_float2(m[n][c], l[n][c]);
+          }
+          // 8 neighbouring dims at a time: the lane's dims as the values were read
+#pragma unroll
+          for (int j = 0; j < KS; j += 4) {
+            const int dim = FP8 ? 2 * KS * g + 2 * j : 16 * j + 8 * g;
+            if (whole) {
+              uint32_t w[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) w[i] = pack_bf2(o[n][j + i][c] * inv, o[n][j + i][2 + c] * inv);
+              if (p.o_vec) {
+                *reinterpret_cast<uint4*>(op + dim) = make_uint4(w[0], w[1], w[2], w[3]);
+              } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  op[dim + 2 * i] = __ushort_as_bfloat16(static_cast<unsigned short>(w[i]));
+                  op[dim + 2 * i + 1] = __ushort_as_bfloat16(static_cast<unsigned short>(w[i] >> 16));
+                }
+              }
+            } else {
+              *reinterpret_cast<float4*>(pp + dim) =
+                  make_float4(o[n][j][c], o[n][j][2 + c], o[n][j + 1][c], o[n][j + 1][2 + c]);
+              *reinterpret_cast<float4*>(pp + dim + 4) =
+                  make_float4(o[n][j + 2][c], o[n][j + 2][2 + c], o[n][j + 3][c], o[n][j + 3][2 + c]);
+            }
+          }
+        }
+      }
+    }
+    // the next unit writes ml_s and the two buffers only behind barriers that
+    // warp 0 reaches after this
+    cc.forward<KT>(p, xe - x);
+    x = xe;
+  }
+  cp_async_wait<0>();
+}
+
+// One block for each unit and row: units that several blocks shared, joined in
+// block order; units without keys, zero.
+template <int D, int KT>
+__global__ void __launch_bounds__(kPdThreads) relpos_paged_combine_kernel(const __grid_constant__ PagedDecodeParams p) {
+  constexpr int LANES = D / 4, PARTS = kPdThreads / LANES;
+  __shared__ float red[PARTS][D + 4];
+  __shared__ float2 ml_s[PARTS];
+  griddep_launch_dependents();
+  const int per = p.Hkv * p.rt;
+  const int b = blockIdx.x / per, u = blockIdx.x - b * per;
+  const int h = u / p.rt, row = (u - h * p.rt) * p.rows + blockIdx.y;
+  const int lane = threadIdx.x & 31;
+  int before, total;
+  count_tiles(p, b, KT, lane, before, total);
+  const int nt = seq_tiles(p, b, KT);
+  const int share = share_of(total, p.blocks);
+  const int xs = before + u * nt, xe = xs + nt;
+  const int c0 = xs / share, c1 = nt ? (xe - 1) / share : c0 - 1;
+  // the lengths above were there before the decode kernel let this one start;
+  // its partial results are there from here on
+  griddep_wait();
+  if (c1 == c0 || row >= p.G * p.Lq) return;  // one block had the whole unit
+  const int d4 = threadIdx.x % LANES, part = threadIdx.x / LANES;
+  // each of the PARTS lanes of a value joins its blocks' parts as they come
+  float m = -FLT_MAX, l = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int c = c0 + part; c <= c1; c += PARTS) {
+    const size_t slot = (2 * static_cast<size_t>(c) + (c * share <= xs ? 1 : 0)) * p.rows + blockIdx.y;
+    const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * slot);
+    const float4 v = *reinterpret_cast<const float4*>(p.part_o + slot * D + 4 * d4);
+    const float top = fmaxf(m, ml.x), w = ex2_approx(ml.x - top), down = ex2_approx(m - top);
+    m = top;
+    l = fmaf(w, ml.y, l * down);
+    acc.x = fmaf(w, v.x, acc.x * down);
+    acc.y = fmaf(w, v.y, acc.y * down);
+    acc.z = fmaf(w, v.z, acc.z * down);
+    acc.w = fmaf(w, v.w, acc.w * down);
+  }
+  *reinterpret_cast<float4*>(&red[part][4 * d4]) = acc;
+  if (d4 == 0) ml_s[part] = make_float2(m, l);
+  __syncthreads();
+  if (threadIdx.x < D) {
+    float a = 0.f, s = 0.f, top = -FLT_MAX;
+#pragma unroll
+    for (int i = 0; i < PARTS; ++i) top = fmaxf(top, ml_s[i].x);
+#pragma unroll
+    for (int i = 0; i < PARTS; ++i) {
+      const float w = ex2_approx(ml_s[i].x - top);
+      a = fmaf(w, red[i][threadIdx.x], a);
+      s = fmaf(w, ml_s[i].y, s);
+    }
+    const int qi = row / p.G, hq = h * p.G + row - qi * p.G;
+    p.out[b * p.o_batch + hq * p.o_head + qi * p.o_row + threadIdx.x] =
+        __float2bfloat16_rn(s == 0.f ? 0.f : a / s);
+  }
+}
+
+template <int D, bool FP8, int NQ, int KT, int STAGES>
+PagedDecodeVariant paged_decode_variant() {
+  return {relpos_paged_decode_kernel<D, FP8, NQ, KT, STAGES>, relpos_paged_combine_kernel<D, KT>, KT,
+          Shape<D, FP8, NQ, KT, STAGES>::kSmem};
+}
+
+}  // namespace
+}  // namespace relpos
