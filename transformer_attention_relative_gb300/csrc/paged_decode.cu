@@ -110,12 +110,13 @@ extern "C" int relpos_paged_decode(const RelposPagedCache* cache, const void* Q,
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const size_t slots = static_cast<size_t>(p.blocks) * 2 * p.rows;
   float* scratch = nullptr;
-  if (cudaMallocAsync(&scratch, slots * (cache->d + 2) * sizeof(float), s) != cudaSuccess) {
+  if (cudaMallocAsync(&scratch, slots * (cache->d + 2) * sizeof(float) + p.blocks * 2 * sizeof(int4), s) != cudaSuccess) {
     cudaGetLastError();
     return RELPOS_ERR_CUDA;
   }
   p.part_o = scratch;
   p.part_ml = scratch + slots * cache->d;
+  p.ends = reinterpret_cast<int4*>(p.part_ml + slots * 2);  // slots is a multiple of 16
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -127,7 +128,6 @@ extern "C" int relpos_paged_decode(const RelposPagedCache* cache, const void* Q,
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   bool ok = cudaLaunchKernelEx(&cfg, v.decode, p) == cudaSuccess;
-  cfg.gridDim = dim3(static_cast<unsigned>(units), std::min(G * Lq, p.rows));
   cfg.dynamicSmemBytes = 0;
   ok = ok && cudaLaunchKernelEx(&cfg, v.combine, p) == cudaSuccess;
   ok = cudaFreeAsync(scratch, s) == cudaSuccess && ok;

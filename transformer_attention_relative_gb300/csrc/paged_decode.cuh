@@ -33,7 +33,6 @@ constexpr int kPdWarps = 4;
 constexpr int kPdThreads = 32 * kPdWarps;
 constexpr int kPdMaxRows = 32;  // rows of a unit at most
 constexpr int kPdMinTiles = 4;  // fewest tiles of a block's share: one for each warp
-constexpr int kPdBuckets = 1024;  // distances whose T5 bucket is looked up
 // The weights p are kept as 2^(logit - off) for a row offset `off` that starts
 // below every logit and moves up only when a logit comes more than kPdMost above
 // it, to kPdShift below the largest: most tiles then need no maximum across the
@@ -66,6 +65,7 @@ struct PagedDecodeParams {
   float scale_log2;
   float* part_o;   // [blocks][2][rows][d] partial outputs
   float* part_ml;  // [blocks][2][rows][2] their offsets and sums
+  int4* ends;      // [blocks][2] what a slot holds: first block and number of blocks of its unit (0: nothing), sequence, unit
   int blocks;
   int* status;
 };
@@ -89,27 +89,6 @@ namespace {
 // equal share of the tiles of all units, whatever the lengths, and its warps
 // every fourth tile of it.
 
-RP_DEVI int seq_tiles(const PagedDecodeParams& p, int b, int KT) {
-  const int len = __ldcg(p.lens + b);
-  return (min(max(len, 0), p.max_len) + KT - 1) / KT;
-}
-
-// Key tiles of the units before sequence `upto` and of all units, summed by a
-// warp. (Lengths are read past the L1 cache: the combine kernel looks at them
-// before it waits for this one.)
-RP_DEVI void count_tiles(const PagedDecodeParams& p, int upto, int KT, int lane, int& before, int& total) {
-  int sum = 0, part = 0;
-  for (int i = lane; i < p.B; i += 32) {
-    const int nt = seq_tiles(p, i, KT);
-    sum += nt;
-    part += i < upto ? nt : 0;
-  }
-  before = __reduce_add_sync(0xffffffffu, part) * p.Hkv * p.rt;
-  total = __reduce_add_sync(0xffffffffu, sum) * p.Hkv * p.rt;
-}
-
-RP_DEVI int share_of(int total, int blocks) { return max((total + blocks - 1) / blocks, kPdMinTiles); }
-
 // Place in the sequence of tiles: sequence and its length, unit of it, tile of
 // the unit.
 struct Cursor {
@@ -120,7 +99,7 @@ struct Cursor {
   RP_DEVI void enter(const PagedDecodeParams& p) {  // the first sequence from b on that has tiles
     nt = len = 0;
     for (; b < p.B; ++b) {
-      len = min(max(__ldcg(p.lens + b), 0), p.max_len);
+      len = min(max(__ldg(p.lens + b), 0), p.max_len);
       nt = (len + KT - 1) / KT;
       pages = p.table + b * p.table_stride;
       if (nt) return;
@@ -141,24 +120,31 @@ struct Cursor {
   }
 };
 
-// This block's share x0 .. x1 - 1 of all tiles, and the cursor at x0;
-// warp-uniform. The first 32 sequences' lengths are loaded once.
+RP_DEVI int seq_len(const PagedDecodeParams& p, int b) {
+  return b < p.B ? min(max(__ldg(p.lens + b), 0), p.max_len) : 0;
+}
+
+// This block's share x0 .. x1 - 1 of all tiles; warp-uniform. len0 are the
+// lengths of the first 32 sequences, a lane each.
 template <int KT>
-RP_DEVI Cursor locate(const PagedDecodeParams& p, int lane, int& x0, int& x1) {
-  const int per = p.Hkv * p.rt;
-  auto length = [&](int b) { return b < p.B ? min(max(__ldcg(p.lens + b), 0), p.max_len) : 0; };
-  const int len0 = length(lane);
+RP_DEVI int share_of(const PagedDecodeParams& p, int lane, int len0, int& x0, int& x1) {
   int sum = (len0 + KT - 1) / KT;
-  for (int b = lane + 32; b < p.B; b += 32) sum += (length(b) + KT - 1) / KT;
-  const int total = __reduce_add_sync(0xffffffffu, sum) * per;
-  const int share = share_of(total, p.blocks);
+  for (int b = lane + 32; b < p.B; b += 32) sum += (seq_len(p, b) + KT - 1) / KT;
+  const int total = __reduce_add_sync(0xffffffffu, sum) * p.Hkv * p.rt;
+  const int share = max((total + p.blocks - 1) / p.blocks, kPdMinTiles);
   x0 = min(static_cast<int>(blockIdx.x) * share, total);
   x1 = min(x0 + share, total);
+  return share;
+}
+
+// The cursor at tile x0 of all, which has to exist; warp-uniform.
+template <int KT>
+RP_DEVI Cursor locate(const PagedDecodeParams& p, int lane, int len0, int x0) {
+  const int per = p.Hkv * p.rt;
   Cursor c{p.B, 0, 0, 0, 0, 0, p.table};
-  if (x0 == x1) return c;
   int before = 0;
   for (int b0 = 0; b0 < p.B; b0 += 32) {
-    const int len = b0 ? length(b0 + lane) : len0;
+    const int len = b0 ? seq_len(p, b0 + lane) : len0;
     const int nt = (len + KT - 1) / KT;
     int upto = nt;
 #pragma unroll
@@ -316,7 +302,6 @@ __global__ void __launch_bounds__(kPdThreads, NQ * D <= 64 ? 4 : NQ * D <= 128 ?
   constexpr int MT = KT / 16;   // 16-key tiles of the scores, 16-key steps of v^T p^T
   constexpr int KS = D / 16;    // 16-dim steps of k . q, 16-dim tiles of the output
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ uint8_t bucket_s[kPdBuckets];  // T5 buckets of the first distances
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
   const uint32_t ring = smem_u32(smem) + warp * S::kRingBytes;
@@ -326,8 +311,11 @@ __global__ void __launch_bounds__(kPdThreads, NQ * D <= 64 ? 4 : NQ * D <= 128 ?
   griddep_wait();
   griddep_launch_dependents();
   int x0, x1;
-  Cursor pc = locate<KT>(p, lane, x0, x1);
+  const int len0 = seq_len(p, lane);
+  const int share = share_of<KT>(p, lane, len0, x0, x1);
+  if (threadIdx.x == 0) p.ends[2 * blockIdx.x] = p.ends[2 * blockIdx.x + 1] = make_int4(0, 0, 0, 0);
   if (x0 >= x1) return;
+  Cursor pc = locate<KT>(p, lane, len0, x0);
 
   // ---- producer: this warp's tiles x0 + warp, x0 + warp + 4, ... into its ring
   Cursor cc = pc;
@@ -384,13 +372,8 @@ __global__ void __launch_bounds__(kPdThreads, NQ * D <= 64 ? 4 : NQ * D <= 128 ?
     }
     cp_async_commit();
   };
-#pragma unroll
+#pragma unroll 1
   for (int i = 0; i < STAGES - 1; ++i) produce(i);
-  if (p.mode == RELPOS_T5) {
-    for (int i = threadIdx.x; i < min(p.t5_R, kPdBuckets); i += kPdThreads)
-      bucket_s[i] = static_cast<uint8_t>(t5_bucket_dev(-i, p.t5));
-    __syncthreads();
-  }
 
   // ---- consumer: the block's units one after another
   constexpr int KC = FP8 ? D / 64 : D / 32;  // chunks that a lane reads of a key's row
@@ -414,9 +397,22 @@ __global__ void __launch_bounds__(kPdThreads, NQ * D <= 64 ? 4 : NQ * D <= 128 ?
   while (x < x1) {
     const int xe = min(x1, x + cc.nt - cc.t);  // the unit's tiles in this block
     const int len = cc.len;
-    if (threadIdx.x == 0 && __ldcg(p.lens + cc.b) > p.max_len) atomicCAS(p.status, 0, RELPOS_ERR_PAGE);
+    if (threadIdx.x == 0 && __ldg(p.lens + cc.b) > p.max_len) atomicCAS(p.status, 0, RELPOS_ERR_PAGE);
     const int h = cc.h, row0 = (cc.u - h * p.rt) * S::kRows;
     const int rows = min(p.G * p.Lq - row0, S::kRows);
+
+    // T5: the biases of the distances below the last bucket's, for each head
+    // of the group, in the joining buffers (free while tiles are read)
+    const int lut_len = p.t5_R + 1;
+    const bool lut = p.mode == RELPOS_T5 && p.G * static_cast<long long>(lut_len) <= 2 * S::kRows * D &&
+                     len - p.Lq - (cc.t + xe - x) * KT + 1 < p.t5_R;
+    if (lut) {
+      for (int i = threadIdx.x; i < p.G * lut_len; i += kPdThreads) {
+        const int hl = i / lut_len;
+        out_s[i] = to_log2(__ldg(p.bias + t5_bucket_dev(hl * lut_len - i, p.t5) * p.Hq + h * p.G + hl));
+      }
+      __syncthreads();
+    }
 
     // row 8 n + g of the unit as the B operand of k . q
     uint32_t q[NQ][KS][2];
@@ -546,6 +542,15 @@ __global__ void __launch_bounds__(kPdThreads, NQ * D <= 64 ? 4 : NQ * D <= 128 ?
       }
       const bool edge = key0 + KT - 1 > vis_first;  // some row does not see every key
       const bool near = p.mode == RELPOS_T5 && vis_first - (key0 + KT - 1) < p.t5_R;
+      float slow[NQ * MT * 4];  // biases, where a table of them does not fit
+      if (near && !lut) {
+#pragma unroll 1
+        for (int i = 0; i < NQ * MT * 4; ++i) {
+          const int r = row0 + 8 * (i / (4 * MT)) + 2 * t + i / (2 * MT) % 2, qi = r / p.G;
+          const int back = len - p.Lq + qi - (key0 + 16 * (i / 2 % MT) + 8 * (i % 2) + g);
+          slow[i] = to_log2(__ldg(p.bias + t5_bucket_dev(-min(max(back, 0), p.t5_R), p.t5) * p.Hq + h * p.G + r - qi * p.G));
+        }
+      }
       // logit of row 8 n + 2 t + c and key 16 i + 8 e + g, less its row's offset
       auto logits = [&](float (&z)[NQ][MT][4]) {
 #pragma unroll
@@ -554,19 +559,20 @@ __global__ void __launch_bounds__(kPdThreads, NQ * D <= 64 ? 4 : NQ * D <= 128 ?
           for (int c = 0; c < 2; ++c) {
             const float cs = qs[n][c] * k_scale;
             const int back0 = vis[n][c] - key0 - g;  // to key 16 i + 8 e: less 16 i + 8 e
-            if (near) {
-              const int hq = h * p.G + (row0 + 8 * n + 2 * t + c) % p.G;
+            if (near && lut) {
+              const float* biases = out_s + (row0 + 8 * n + 2 * t + c) % p.G * lut_len;
 #pragma unroll
-              for (int i = 0; i < MT; ++i) {
+              for (int i = 0; i < MT; ++i)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                  const int back = back0 - 16 * i - 8 * e;
-                  int bucket = p.t5.slots - 1;
-                  if (back < p.t5_R) bucket = back < kPdBuckets ? bucket_s[max(back, 0)] : t5_bucket_dev(-back, p.t5);
-                  z[n][i][2 * e + c] =
-                      fmaf(sc[n][i][2 * e + c], cs, to_log2(__ldg(p.bias + bucket * p.Hq + hq))) - off[n][c];
-                }
-              }
+                for (int e = 0; e < 2; ++e)
+                  z[n][i][2 * e + c] = fmaf(sc[n][i][2 * e + c], cs,
+                                            biases[min(max(back0 - 16 * i - 8 * e, 0), p.t5_R)]) - off[n][c];
+            } else if (near) {
+#pragma unroll
+              for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                  z[n][i][2 * e + c] = fmaf(sc[n][i][2 * e + c], cs, slow[((n * 2 + c) * MT + i) * 2 + e]) - off[n][c];
             } else if (p.mode != RELPOS_ALIBI) {
               // bias and offset in one constant; a bias of the type's lowest
               // values, beside which a product has no bits, takes it away
@@ -804,7 +810,6 @@ __global__ void __launch_bounds__(kPdThreads, NQ * D <= 64 ? 4 : NQ * D <= 128 ?
     // ---- the four warps' parts of the unit, joined in a fixed order: 2 into 0
     // and 3 into 1, then 1 into 0
     const int tiles = xe - x, skew = (x - x0) & (kPdWarps - 1);
-    float m[NQ][2], l[NQ][2], f[NQ][2];
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
 #pragma unroll
@@ -826,16 +831,12 @@ __global__ void __launch_bounds__(kPdThreads, NQ * D <= 64 ? 4 : NQ * D <= 128 ?
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         const float2* ml = reinterpret_cast<const float2*>(ml_s) + 8 * n + 2 * t + c;
-        m[n][c] = -FLT_MAX;
+        float top = -FLT_MAX;
 #pragma unroll
-        for (int w = 0; w < kPdWarps; ++w) m[n][c] = fmaxf(m[n][c], ml[w * S::kRows].x);
-        l[n][c] = 0.f;
+        for (int w = 0; w < kPdWarps; ++w) top = fmaxf(top, ml[w * S::kRows].x);
+        const float down = ex2_approx(off[n][c] - top);
 #pragma unroll
-        for (int w = 0; w < kPdWarps; ++w)
-          l[n][c] = fmaf(ex2_approx(ml[w * S::kRows].x - m[n][c]), ml[w * S::kRows].y, l[n][c]);
-        f[n][c] = ex2_approx(off[n][c] - m[n][c]);
-#pragma unroll
-        for (int j = 0; j < KS; ++j) o[n][j][c] *= f[n][c], o[n][j][2 + c] *= f[n][c];
+        for (int j = 0; j < KS; ++j) o[n][j][c] *= down, o[n][j][2 + c] *= down;
       }
     }
     // a lane's values of a row: 16 bytes at a time, lane after lane
@@ -867,124 +868,149 @@ __global__ void __launch_bounds__(kPdThreads, NQ * D <= 64 ? 4 : NQ * D <= 128 ?
     if (warp < 2) take(out_s + warp * S::kRows * D);
     if (warp == 1) give(out_s + S::kRows * D);
     __syncthreads();
-    if (warp == 0) {
+    if (warp == 0) {  // and the rows in order
       take(out_s + S::kRows * D);
-      const bool whole = cc.t == 0 && tiles == cc.nt;
-      const int slot = 2 * blockIdx.x + (cc.t == 0 ? 1 : 0);
 #pragma unroll
       for (int n = 0; n < NQ; ++n) {
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          const int r = 8 * n + 2 * t + c;
-          if (r >= rows) continue;
-          float inv = 1.f;
-          __nv_bfloat16* op = nullptr;
-          float* pp = p.part_o + (static_cast<size_t>(slot) * S::kRows + r) * D;
-          if (whole) {
-            inv = l[n][c] == 0.f ? 0.f : 1.f / l[n][c];
-            const int qi = (row0 + r) / p.G;
-            const int hq = h * p.G + (row0 + r) - qi * p.G;
-            op = p.out + cc.b * p.o_batch + hq * p.o_head + qi * p.o_row;
-          } else if (g == 0) {
-            *reinterpret_cast<float2*>(p.part_ml + (static_cast<size_t>(slot) * S::kRows + r) * 2) =
-                make_float2(m[n][c], l[n][c]);
-          }
-          // 8 neighbouring dims at a time: the lane's dims as the values were read
+          if (8 * n + 2 * t + c >= rows) continue;
+          float4* row = reinterpret_cast<float4*>(out_s + (8 * n + 2 * t + c) * D);
 #pragma unroll
-          for (int j = 0; j < KS; j += 4) {
-            const int dim = FP8 ? 2 * KS * g + 2 * j : 16 * j + 8 * g;
-            if (whole) {
-              uint32_t w[4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i) w[i] = pack_bf2(o[n][j + i][c] * inv, o[n][j + i][2 + c] * inv);
-              if (p.o_vec) {
-                *reinterpret_cast<uint4*>(op + dim) = make_uint4(w[0], w[1], w[2], w[3]);
-              } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  op[dim + 2 * i] = __ushort_as_bfloat16(static_cast<unsigned short>(w[i]));
-                  op[dim + 2 * i + 1] = __ushort_as_bfloat16(static_cast<unsigned short>(w[i] >> 16));
-                }
-              }
-            } else {
-              *reinterpret_cast<float4*>(pp + dim) =
-                  make_float4(o[n][j][c], o[n][j][2 + c], o[n][j + 1][c], o[n][j + 1][2 + c]);
-              *reinterpret_cast<float4*>(pp + dim + 4) =
-                  make_float4(o[n][j + 2][c], o[n][j + 2][2 + c], o[n][j + 3][c], o[n][j + 3][2 + c]);
-            }
+          for (int j = 0; j < KS; j += 2) {  // the lane's dims as the values were read
+            const int dim = FP8 ? 2 * KS * g + 2 * j : (j / 4) * 64 + 8 * g + 2 * (j % 4);
+            row[dim / 4] = make_float4(o[n][j][c], o[n][j][2 + c], o[n][j + 1][c], o[n][j + 1][2 + c]);
           }
         }
       }
     }
-    // the next unit writes ml_s and the two buffers only behind barriers that
-    // warp 0 reaches after this
+    __syncthreads();
+    const bool whole = cc.t == 0 && tiles == cc.nt;
+    const int slot = 2 * blockIdx.x + (cc.t == 0 ? 1 : 0);
+    if (!whole && threadIdx.x == 0) {  // the same thread wrote the zeros before
+      const int xs = x - cc.t, c0 = xs / share;
+      p.ends[slot] = make_int4(c0, (xs + cc.nt - 1) / share - c0 + 1, cc.b, cc.u);
+    }
+#pragma unroll 1
+    for (int i = threadIdx.x; i < rows * (D / 8); i += kPdThreads) {
+      const int r = i / (D / 8), dim = 8 * (i % (D / 8));
+      const float2* ml = reinterpret_cast<const float2*>(ml_s) + r;
+      float top = -FLT_MAX, sum = 0.f;
+#pragma unroll
+      for (int w = 0; w < kPdWarps; ++w) top = fmaxf(top, ml[w * S::kRows].x);
+#pragma unroll
+      for (int w = 0; w < kPdWarps; ++w) sum = fmaf(ex2_approx(ml[w * S::kRows].x - top), ml[w * S::kRows].y, sum);
+      const float4* v = reinterpret_cast<const float4*>(out_s + r * D + dim);
+      float4 a = v[0], b = v[1];
+      if (whole) {
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        const uint32_t w[4] = {pack_bf2(a.x * inv, a.y * inv), pack_bf2(a.z * inv, a.w * inv),
+                               pack_bf2(b.x * inv, b.y * inv), pack_bf2(b.z * inv, b.w * inv)};
+        const int qi = (row0 + r) / p.G;
+        const int hq = h * p.G + (row0 + r) - qi * p.G;
+        __nv_bfloat16* op = p.out + cc.b * p.o_batch + hq * p.o_head + qi * p.o_row + dim;
+        if (p.o_vec) {
+          *reinterpret_cast<uint4*>(op) = make_uint4(w[0], w[1], w[2], w[3]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            op[2 * e] = __ushort_as_bfloat16(static_cast<unsigned short>(w[e]));
+            op[2 * e + 1] = __ushort_as_bfloat16(static_cast<unsigned short>(w[e] >> 16));
+          }
+        }
+      } else {
+        const size_t at = static_cast<size_t>(slot) * S::kRows + r;
+        float4* to = reinterpret_cast<float4*>(p.part_o + at * D + dim);
+        to[0] = a;
+        to[1] = b;
+        if (dim == 0) *reinterpret_cast<float2*>(p.part_ml + 2 * at) = make_float2(top, sum);
+      }
+    }
+    __syncthreads();  // ml_s and the buffers are free again
     cc.forward<KT>(p, xe - x);
     x = xe;
   }
   cp_async_wait<0>();
 }
 
-// One block for each unit and row: units that several blocks shared, joined in
-// block order; units without keys, zero.
-template <int D, int KT>
+// Joins the parts of the units that several blocks shared, in block order, and
+// writes the zeros of empty sequences. Each of the k blocks of such a unit takes
+// a k-th of its output, so that every block reads about one unit's worth of
+// parts for either end of its share, however many blocks a unit has; half of
+// its threads for each end. What a slot holds the decode kernel has noted, so
+// that nothing is searched for here: these blocks mostly start when that
+// kernel's leave their SM.
+template <int D>
 __global__ void __launch_bounds__(kPdThreads) relpos_paged_combine_kernel(const __grid_constant__ PagedDecodeParams p) {
-  constexpr int LANES = D / 4, PARTS = kPdThreads / LANES;
-  __shared__ float red[PARTS][D + 4];
-  __shared__ float2 ml_s[PARTS];
   griddep_launch_dependents();
-  const int per = p.Hkv * p.rt;
-  const int b = blockIdx.x / per, u = blockIdx.x - b * per;
-  const int h = u / p.rt, row = (u - h * p.rt) * p.rows + blockIdx.y;
-  const int lane = threadIdx.x & 31;
-  int before, total;
-  count_tiles(p, b, KT, lane, before, total);
-  const int nt = seq_tiles(p, b, KT);
-  const int share = share_of(total, p.blocks);
-  const int xs = before + u * nt, xe = xs + nt;
-  const int c0 = xs / share, c1 = nt ? (xe - 1) / share : c0 - 1;
-  // the lengths above were there before the decode kernel let this one start;
-  // its partial results are there from here on
   griddep_wait();
-  if (c1 == c0 || row >= p.G * p.Lq) return;  // one block had the whole unit
-  const int d4 = threadIdx.x % LANES, part = threadIdx.x / LANES;
-  // each of the PARTS lanes of a value joins its blocks' parts as they come
-  float m = -FLT_MAX, l = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int c = c0 + part; c <= c1; c += PARTS) {
-    const size_t slot = (2 * static_cast<size_t>(c) + (c * share <= xs ? 1 : 0)) * p.rows + blockIdx.y;
-    const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * slot);
-    const float4 v = *reinterpret_cast<const float4*>(p.part_o + slot * D + 4 * d4);
-    const float top = fmaxf(m, ml.x), w = ex2_approx(ml.x - top), down = ex2_approx(m - top);
-    m = top;
-    l = fmaf(w, ml.y, l * down);
-    acc.x = fmaf(w, v.x, acc.x * down);
-    acc.y = fmaf(w, v.y, acc.y * down);
-    acc.z = fmaf(w, v.z, acc.z * down);
-    acc.w = fmaf(w, v.w, acc.w * down);
-  }
-  *reinterpret_cast<float4*>(&red[part][4 * d4]) = acc;
-  if (d4 == 0) ml_s[part] = make_float2(m, l);
-  __syncthreads();
-  if (threadIdx.x < D) {
-    float a = 0.f, s = 0.f, top = -FLT_MAX;
-#pragma unroll
-    for (int i = 0; i < PARTS; ++i) top = fmaxf(top, ml_s[i].x);
-#pragma unroll
-    for (int i = 0; i < PARTS; ++i) {
-      const float w = ex2_approx(ml_s[i].x - top);
-      a = fmaf(w, red[i][threadIdx.x], a);
-      s = fmaf(w, ml_s[i].y, s);
+  constexpr int kHalf = kPdThreads / 2;
+  const int end = threadIdx.x / kHalf, tid = threadIdx.x % kHalf;
+  const int4 what = __ldcg(p.ends + 2 * blockIdx.x + end);
+  const int c0 = what.x, k = what.y, b = what.z, u = what.w;
+  for (int i = blockIdx.x; i < p.B; i += gridDim.x) {
+    if (__ldg(p.lens + i) > 0) continue;
+    for (int j = threadIdx.x; j < p.Hq * p.Lq * D; j += kPdThreads) {
+      const int r = j / D;
+      p.out[i * p.o_batch + r / p.Lq * p.o_head + r % p.Lq * p.o_row + j % D] = __float2bfloat16_rn(0.f);
     }
-    const int qi = row / p.G, hq = h * p.G + row - qi * p.G;
-    p.out[b * p.o_batch + hq * p.o_head + qi * p.o_row + threadIdx.x] =
-        __float2bfloat16_rn(s == 0.f ? 0.f : a / s);
+  }
+  if (k == 0) return;
+  const int h = u / p.rt, row0 = (u - h * p.rt) * p.rows, rows = min(p.G * p.Lq - row0, p.rows);
+  // this block's columns (4 dims of a row) of the unit's rows * D / 4
+  const int me = blockIdx.x - c0, cols = rows * (D / 4);
+  const int first = cols * me / k, count = cols * (me + 1) / k - first;
+  int lanes = 1;  // that share a column, a power of two
+  while (lanes < 32 && lanes < k && 2 * lanes * count <= kHalf) lanes *= 2;
+  const int part = tid & (lanes - 1);
+  for (int i0 = 0; i0 < count; i0 += kHalf / lanes) {  // whole warps take part
+    const int i = i0 + tid / lanes;
+    const int col = first + min(i, count - 1), r = col / (D / 4), d4 = col % (D / 4);
+    float m = -FLT_MAX, l = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto join = [&](float m2, float l2, const float4& v) {
+      const float top = fmaxf(m, m2), w = ex2_approx(m2 - top), down = ex2_approx(m - top);
+      m = top;
+      l = fmaf(w, l2, l * down);
+      acc.x = fmaf(w, v.x, acc.x * down);
+      acc.y = fmaf(w, v.y, acc.y * down);
+      acc.z = fmaf(w, v.z, acc.z * down);
+      acc.w = fmaf(w, v.w, acc.w * down);
+    };
+#pragma unroll 4
+    for (int j = part; j < k; j += lanes) {
+      // the unit begins in its first block's second slot
+      const size_t at = (2 * static_cast<size_t>(c0 + j) + (j == 0 ? 1 : 0)) * p.rows + r;
+      const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml + 2 * at));
+      join(ml.x, ml.y, __ldcg(reinterpret_cast<const float4*>(p.part_o + at * D + 4 * d4)));
+    }
+    for (int o = 1; o < lanes; o *= 2) {
+      const float m2 = __shfl_xor_sync(0xffffffffu, m, o), l2 = __shfl_xor_sync(0xffffffffu, l, o);
+      const float4 v = make_float4(__shfl_xor_sync(0xffffffffu, acc.x, o), __shfl_xor_sync(0xffffffffu, acc.y, o),
+                                   __shfl_xor_sync(0xffffffffu, acc.z, o), __shfl_xor_sync(0xffffffffu, acc.w, o));
+      join(m2, l2, v);
+    }
+    if (i < count && part == 0) {
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const int qi = (row0 + r) / p.G, hq = h * p.G + (row0 + r) - qi * p.G;
+      __nv_bfloat16* op = p.out + b * p.o_batch + hq * p.o_head + qi * p.o_row + 4 * d4;
+      const uint32_t w[2] = {pack_bf2(acc.x * inv, acc.y * inv), pack_bf2(acc.z * inv, acc.w * inv)};
+      if (p.o_vec) {
+        *reinterpret_cast<uint2*>(op) = make_uint2(w[0], w[1]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          op[2 * e] = __ushort_as_bfloat16(static_cast<unsigned short>(w[e]));
+          op[2 * e + 1] = __ushort_as_bfloat16(static_cast<unsigned short>(w[e] >> 16));
+        }
+      }
+    }
   }
 }
 
 template <int D, bool FP8, int NQ, int KT, int STAGES>
 PagedDecodeVariant paged_decode_variant() {
-  return {relpos_paged_decode_kernel<D, FP8, NQ, KT, STAGES>, relpos_paged_combine_kernel<D, KT>, KT,
+  return {relpos_paged_decode_kernel<D, FP8, NQ, KT, STAGES>, relpos_paged_combine_kernel<D>, KT,
           Shape<D, FP8, NQ, KT, STAGES>::kSmem};
 }
 

@@ -7,8 +7,8 @@ namespace relpos {
 
 PagedDecodeVariant paged_decode_e4m3_128(int rows8) {
   switch (rows8) {
-    case 1: return paged_decode_variant<128, true, 1, 32, 3>();
-    default: return paged_decode_variant<128, true, 2, 32, 3>();
+    case 1: return paged_decode_variant<128, true, 1, 32, 2>();
+    default: return paged_decode_variant<128, true, 2, 32, 2>();
   }
 }
 

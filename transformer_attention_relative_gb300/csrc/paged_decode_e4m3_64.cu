@@ -7,10 +7,10 @@ namespace relpos {
 
 PagedDecodeVariant paged_decode_e4m3_64(int rows8) {
   switch (rows8) {
-    case 1: return paged_decode_variant<64, true, 1, 32, 3>();
-    case 2: return paged_decode_variant<64, true, 2, 32, 3>();
-    case 3: return paged_decode_variant<64, true, 3, 32, 3>();
-    default: return paged_decode_variant<64, true, 4, 32, 3>();
+    case 1: return paged_decode_variant<64, true, 1, 32, 2>();
+    case 2: return paged_decode_variant<64, true, 2, 32, 2>();
+    case 3: return paged_decode_variant<64, true, 3, 32, 2>();
+    default: return paged_decode_variant<64, true, 4, 32, 2>();
   }
 }
 
