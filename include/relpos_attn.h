@@ -598,10 +598,12 @@ int relpos_paged_append(const RelposPagedCache* cache, const RelposRotaryPlan* p
  *   Lq          0 .. 8 rows (RELPOS_ERR_UNSUPPORTED beyond).
  *   scale       softmax scale, finite; 0 takes 1 / sqrt(d).
  * Keys and values in masked or unused slots have no effect, whatever they
- * hold. The cache is read once for up to 16 rows (query heads of a group times
- * Lq) and again for each further 16. Scratch: at most about 17 MB for partial results of
- * sequences that several blocks share, from cudaMallocAsync on `stream`, freed
- * with cudaFreeAsync before the call returns. Results do not depend on what
+ * hold. The cache is read once for up to 8 or 16 rows (query heads of a group
+ * times Lq) and again, mostly from L2, for each further 8 or 16. Scratch: up to
+ * about 8 MB for partial results of sequences that several blocks share, from
+ * cudaMallocAsync on `stream`, freed with cudaFreeAsync before the call
+ * returns; none where the block table holds at most 16 tiles (256 tokens for
+ * bf16 with d = 128, 512 otherwise). Results do not depend on what
  * else runs. Asynchronous on `stream`.
  */
 #define RELPOS_NO_BIAS (-1)

@@ -101,7 +101,8 @@ template <bool FP8, bool INTERLEAVED, int THREADS, int UNITS>
 __global__ void __launch_bounds__(THREADS, UNITS == 1 ? 768 / THREADS : 1) relpos_paged_append_kernel(const __grid_constant__ AppendParams p) {
   extern __shared__ float4 turn_s[];
   __shared__ int amax_s[2][kAppMaxGroup];
-  __shared__ float had_s[2][kAppMaxGroup];
+  __shared__ float had_s[2][kAppMaxGroup];      // scales so far (0 for a page taken anew)
+  __shared__ float had_inv_s[2][kAppMaxGroup];  // and 1 over them
   griddep_launch_dependents();
   griddep_wait();
   const int tid = threadIdx.x, lane = tid & 31;
@@ -208,7 +209,9 @@ __global__ void __launch_bounds__(THREADS, UNITS == 1 ? 768 / THREADS : 1) relpo
     for (int i = tid; i < 2 * nheads; i += THREADS) {
       const int w = i >= nheads, h = i - w * nheads;
       amax_s[w][h] = 0;
-      had_s[w][h] = t_lo > 0 ? (w ? p.cache.v_scale : p.cache.k_scale)[page_rows + h] : 0.f;
+      const float had = t_lo > 0 ? (w ? p.cache.v_scale : p.cache.k_scale)[page_rows + h] : 0.f;
+      had_s[w][h] = had;
+      had_inv_s[w][h] = 1.f / had;
     }
   }
   const float amplitude = static_cast<float>(p.plan.amplitude);
@@ -317,12 +320,11 @@ __global__ void __launch_bounds__(THREADS, UNITS == 1 ? 768 / THREADS : 1) relpo
         uint8_t* ko = static_cast<uint8_t*>(p.cache.k) + at;
         uint8_t* vo = static_cast<uint8_t*>(p.cache.v) + at;
         const float want_k = scale_for(amax_s[0][h], p.exp_k), want_v = scale_for(amax_s[1][h], p.exp_v);
-        float ik = __int_as_float((254 << 23) - __float_as_int(want_k));  // of a power of two: exact
-        float iv = __int_as_float((254 << 23) - __float_as_int(want_v));
-        if (t_lo > 0) {  // the page's scale so far may be any number
-          ik = 1.f / fmaxf(want_k, had_s[0][h]);
-          iv = 1.f / fmaxf(want_v, had_s[1][h]);
-        }
+        // 1 over the scale: exact from a power of two's bits, but the page's
+        // scale so far may be any number
+        const bool same_k = want_k <= had_s[0][h], same_v = want_v <= had_s[1][h];
+        const float ik = same_k ? had_inv_s[0][h] : __int_as_float((254 << 23) - __float_as_int(want_k));
+        const float iv = same_v ? had_inv_s[1][h] : __int_as_float((254 << 23) - __float_as_int(want_v));
         uint2 o1, o2;
         // The fp32 rotation is off by less than 2^-22 (|a| + |q|): sine and
         // cosine by 2^-23, two products and a sum by 2^-24 each; by twice that
@@ -487,7 +489,7 @@ extern "C" int relpos_paged_append(const RelposPagedCache* cache, const RelposRo
   const long long pages = (total >> p.log_page) + 2 * static_cast<long long>(B);
   // heads of a block: as few as fill the GPU's SMs, since a block walks them
   const long long groups = std::min<long long>(
-      cache->H, std::max<long long>((cache->H + kAppMaxGroup - 1) / kAppMaxGroup, (4 * sms + pages - 1) / pages));
+      cache->H, std::max<long long>((cache->H + kAppMaxGroup - 1) / kAppMaxGroup, (2 * sms + pages - 1) / pages));
   p.group = static_cast<int>((cache->H + groups - 1) / groups);
   const bool inter = p.plan.layout == RELPOS_ROTARY_INTERLEAVED;
   const auto kernel = cache->dtype == RELPOS_E4M3

@@ -7,6 +7,8 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <mutex>
+#include <vector>
 
 #include "../../include/relpos_attn.h"
 #include "paged_decode.cuh"
@@ -15,13 +17,34 @@
 namespace relpos {
 namespace {
 
-// 8-row groups that a unit holds at most: the output accumulators and the
-// query rows of one stay in registers (d = 128: 32 + 16 registers a group)
-int max_rows8(int d) { return d == 64 ? 4 : 2; }
-
 PagedDecodeVariant variant_of(int d, int dtype, int rows8) {
   if (dtype == RELPOS_E4M3) return d == 64 ? paged_decode_e4m3_64(rows8) : paged_decode_e4m3_128(rows8);
   return d == 64 ? paged_decode_bf16_64(rows8) : paged_decode_bf16_128(rows8);
+}
+
+// Blocks of a variant's decode kernel that an SM of the current device holds,
+// asked once for each variant and device (with the shared memory allowed for
+// its launches); 0 on failure.
+int resident_blocks(const PagedDecodeVariant& v) {
+  struct Known {
+    void (*kernel)(PagedDecodeParams);
+    int dev, blocks;
+  };
+  static std::mutex mu;
+  static std::vector<Known> known;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  std::lock_guard<std::mutex> lk(mu);
+  for (const Known& k : known)
+    if (k.kernel == v.decode && k.dev == dev) return k.blocks;
+  int n = 0;
+  if (cudaFuncSetAttribute(v.decode, cudaFuncAttributeMaxDynamicSharedMemorySize, v.smem) != cudaSuccess ||
+      cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, v.decode, kPdThreads, v.smem) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  known.push_back({v.decode, dev, n});
+  return n;
 }
 
 }  // namespace
@@ -55,17 +78,32 @@ extern "C" int relpos_paged_decode(const RelposPagedCache* cache, const void* Q,
   if (B > 1 && table_stride < max_pages) return RELPOS_ERR_INVALID_ARG;
   const int G = Hq / cache->H;
   if (G > 65535) return RELPOS_ERR_UNSUPPORTED;
-  // rows of a unit: all of a key/value head's if they fit, in groups of 8
-  const int groups = (G * Lq + 7) / 8;
-  const int rt = (groups + max_rows8(cache->d) - 1) / max_rows8(cache->d);
-  const int rows8 = (groups + rt - 1) / rt;
   const long long capacity = static_cast<long long>(max_pages) * cache->page;
   if (capacity > (1 << 28)) return RELPOS_ERR_UNSUPPORTED;
-  const PagedDecodeVariant v = variant_of(cache->d, cache->dtype, rows8);
-  const long long units = static_cast<long long>(B) * cache->H * rt;
-  const long long most = units * ((capacity + v.tile - 1) / v.tile);  // tiles, with every page in use
-  if (units > 0x7fffffffll || most > 0x7fffffffll) return RELPOS_ERR_UNSUPPORTED;
+  PagedDecodeVariant v = variant_of(cache->d, cache->dtype, 1);
+  int rt = (G * Lq + 7) / 8;
+  long long units = static_cast<long long>(B) * cache->H * rt;
+  const long long tiles = (capacity + v.tile - 1) / v.tile;  // of a unit, with every page in use
+  if (units > 0x7fffffffll || units * tiles > 0x7fffffffll) return RELPOS_ERR_UNSUPPORTED;
   if (static_cast<long long>(cache->num_pages) * cache->H > 0x7fffffffll) return RELPOS_ERR_UNSUPPORTED;
+  const int sms = device_sms();
+  if (sms <= 0) return RELPOS_ERR_CUDA;
+  // Rows of a unit: 8, or 16 where a key/value head has more than 8 and the
+  // batch is large. 16 rows read each tile once instead of twice but keep a
+  // third fewer warps on an SM and take longer a tile: 4 heads x 16 sequences x
+  // 16 rows in bf16, d = 64, 26 against 32 us at 4096 tokens (9 tiles a warp
+  // with 8 rows), 92 against 83 at 16384 (36 tiles); 24 and 32 rows lose to both.
+  int occ = resident_blocks(v);
+  if (occ < 1) return RELPOS_ERR_CUDA;
+  const bool wide = rt > 1 && units * tiles > 16ll * kPdWarps * occ * sms;
+  if (wide) {
+    v = variant_of(cache->d, cache->dtype, 2);
+    rt = (rt + 1) / 2;
+    units = static_cast<long long>(B) * cache->H * rt;
+    occ = resident_blocks(v);
+    if (occ < 1) return RELPOS_ERR_CUDA;
+  }
+  const long long most = units * tiles;
 
   PagedDecodeParams p;
   std::memset(&p, 0, sizeof(p));
@@ -86,7 +124,7 @@ extern "C" int relpos_paged_decode(const RelposPagedCache* cache, const void* Q,
   p.table_stride = table_stride;
   p.max_len = static_cast<int>(capacity);
   p.lens = lens;
-  p.B = B, p.Hq = Hq, p.Lq = Lq, p.G = G, p.rows = 8 * rows8, p.rt = rt;
+  p.B = B, p.Hq = Hq, p.Lq = Lq, p.G = G, p.rows = wide ? 16 : 8, p.rt = rt;
   p.bias = static_cast<const float*>(bias);
   p.mode = bias_mode;
   if (bias_mode == RELPOS_T5) {
@@ -95,28 +133,25 @@ extern "C" int relpos_paged_decode(const RelposPagedCache* cache, const void* Q,
   }
   p.scale_log2 = (scale != 0.f ? scale : 1.0f / std::sqrt(static_cast<float>(cache->d))) * kLog2e;
   p.status = device_status();
-  const int sms = device_sms();
-  if (!p.status || sms <= 0) return RELPOS_ERR_CUDA;
-  if (cudaFuncSetAttribute(v.decode, cudaFuncAttributeMaxDynamicSharedMemorySize, v.smem) != cudaSuccess) {
-    cudaGetLastError();
-    return RELPOS_ERR_CUDA;
-  }
-  int occ = 0;
-  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, v.decode, kPdThreads, v.smem) != cudaSuccess || occ < 1) {
-    cudaGetLastError();
-    return RELPOS_ERR_CUDA;
-  }
-  p.blocks = static_cast<int>(std::min<long long>(static_cast<long long>(occ) * sms, (most + kPdMinTiles - 1) / kPdMinTiles));
+  if (!p.status) return RELPOS_ERR_CUDA;
+  // Sequences of up to 16 tiles at most (four of a warp) have a block for each
+  // unit and no second launch: 4.9 against 6.7 us for 113 tokens of 16 heads.
+  p.direct = tiles <= 4 * kPdMinTiles;
+  p.blocks = static_cast<int>(
+      p.direct ? units : std::min<long long>(static_cast<long long>(occ) * sms, (most + kPdMinTiles - 1) / kPdMinTiles));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const size_t slots = static_cast<size_t>(p.blocks) * 2 * p.rows;
   float* scratch = nullptr;
-  if (cudaMallocAsync(&scratch, slots * (cache->d + 2) * sizeof(float) + p.blocks * 2 * sizeof(int4), s) != cudaSuccess) {
-    cudaGetLastError();
-    return RELPOS_ERR_CUDA;
+  if (!p.direct) {
+    const size_t slots = static_cast<size_t>(p.blocks) * 2 * p.rows;  // a multiple of 16
+    if (cudaMallocAsync(&scratch, slots * (cache->d + 2) * sizeof(float) + p.blocks * 2 * sizeof(int4), s) !=
+        cudaSuccess) {
+      cudaGetLastError();
+      return RELPOS_ERR_CUDA;
+    }
+    p.part_o = scratch;
+    p.part_ml = scratch + slots * cache->d;
+    p.ends = reinterpret_cast<int4*>(p.part_ml + slots * 2);
   }
-  p.part_o = scratch;
-  p.part_ml = scratch + slots * cache->d;
-  p.ends = reinterpret_cast<int4*>(p.part_ml + slots * 2);  // slots is a multiple of 16
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -128,9 +163,11 @@ extern "C" int relpos_paged_decode(const RelposPagedCache* cache, const void* Q,
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   bool ok = cudaLaunchKernelEx(&cfg, v.decode, p) == cudaSuccess;
-  cfg.dynamicSmemBytes = 0;
-  ok = ok && cudaLaunchKernelEx(&cfg, v.combine, p) == cudaSuccess;
-  ok = cudaFreeAsync(scratch, s) == cudaSuccess && ok;
+  if (!p.direct) {
+    cfg.dynamicSmemBytes = 0;
+    ok = ok && cudaLaunchKernelEx(&cfg, v.combine, p) == cudaSuccess;
+    ok = cudaFreeAsync(scratch, s) == cudaSuccess && ok;
+  }
   if (!ok) {
     cudaGetLastError();
     return RELPOS_ERR_CUDA;

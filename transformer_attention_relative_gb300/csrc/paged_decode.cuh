@@ -7,7 +7,7 @@
 //
 // The cache is streamed once, about one product per byte and row, so the kernel
 // is built around keeping loads in flight: each warp has its own ring of tiles
-// in shared memory, filled by asynchronous copies. The products of the up to 32
+// in shared memory, filled by asynchronous copies. The products of the up to 16
 // rows that share a key/value head (query heads of the group times new rows)
 // run on the tensor cores' m16n8k16 form, whose operands come straight out of
 // the streamed tile.
@@ -31,7 +31,6 @@ namespace relpos {
 
 constexpr int kPdWarps = 4;
 constexpr int kPdThreads = 32 * kPdWarps;
-constexpr int kPdMaxRows = 32;  // rows of a unit at most
 constexpr int kPdMinTiles = 4;  // fewest tiles of a block's share: one for each warp
 // The weights p are kept as 2^(logit - off) for a row offset `off` that starts
 // below every logit and moves up only when a logit comes more than kPdMost above
@@ -67,6 +66,7 @@ struct PagedDecodeParams {
   float* part_ml;  // [blocks][2][rows][2] their offsets and sums
   int4* ends;      // [blocks][2] what a slot holds: first block and number of blocks of its unit (0: nothing), sequence, unit
   int blocks;
+  int direct;      // a block for each unit: nothing to combine
   int* status;
 };
 
@@ -84,7 +84,7 @@ PagedDecodeVariant paged_decode_bf16_128(int rows8);
 
 namespace {
 
-// A unit is one sequence, key/value head and up to 32 rows; units follow one
+// A unit is one sequence, key/value head and up to 16 rows; units follow one
 // another in that order, each with the sequence's key tiles. A block takes an
 // equal share of the tiles of all units, whatever the lengths, and its warps
 // every fourth tile of it.
@@ -309,13 +309,36 @@ __global__ void __launch_bounds__(kPdThreads, NQ * D <= 64 ? 4 : NQ * D <= 128 ?
   float* const ml_s = out_s + 2 * S::kRows * D;
 
   griddep_wait();
-  griddep_launch_dependents();
   int x0, x1;
-  const int len0 = seq_len(p, lane);
-  const int share = share_of<KT>(p, lane, len0, x0, x1);
-  if (threadIdx.x == 0) p.ends[2 * blockIdx.x] = p.ends[2 * blockIdx.x + 1] = make_int4(0, 0, 0, 0);
-  if (x0 >= x1) return;
-  Cursor pc = locate<KT>(p, lane, len0, x0);
+  int share = 0;
+  Cursor pc;
+  if (p.direct) {
+    const int per = p.Hkv * p.rt;
+    pc.b = blockIdx.x / per;
+    pc.u = blockIdx.x - pc.b * per;
+    pc.t = 0;
+    pc.len = seq_len(p, pc.b);
+    pc.nt = (pc.len + KT - 1) / KT;
+    pc.h = pc.u / p.rt;
+    pc.pages = p.table + pc.b * p.table_stride;
+    x0 = 0;
+    x1 = pc.nt;
+    if (x1 == 0) {  // no key is seen: zero rows
+      const int row0 = (pc.u - pc.h * p.rt) * S::kRows;
+      for (int i = threadIdx.x; i < min(p.G * p.Lq - row0, S::kRows) * D; i += kPdThreads) {
+        const int r = row0 + i / D, qi = r / p.G;
+        p.out[pc.b * p.o_batch + (pc.h * p.G + r - qi * p.G) * p.o_head + qi * p.o_row + i % D] =
+            __float2bfloat16_rn(0.f);
+      }
+      return;
+    }
+  } else {
+    const int len0 = seq_len(p, lane);
+    share = share_of<KT>(p, lane, len0, x0, x1);
+    if (threadIdx.x == 0) p.ends[2 * blockIdx.x] = p.ends[2 * blockIdx.x + 1] = make_int4(0, 0, 0, 0);
+    if (x0 >= x1) return;
+    pc = locate<KT>(p, lane, len0, x0);
+  }
 
   // ---- producer: this warp's tiles x0 + warp, x0 + warp + 4, ... into its ring
   Cursor cc = pc;

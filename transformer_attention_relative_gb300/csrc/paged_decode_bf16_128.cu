@@ -1,15 +1,13 @@
 // paged_decode_bf16_128.cu -- variants of the paged decode kernel for bf16 caches of
-// head dimension 128.
+// head dimension 128. Two ring stages: three took 1 to 5 percent longer (fewer
+// blocks of an SM, the same bytes in flight).
 
 #include "paged_decode.cuh"
 
 namespace relpos {
 
 PagedDecodeVariant paged_decode_bf16_128(int rows8) {
-  switch (rows8) {
-    case 1: return paged_decode_variant<128, false, 1, 16, 2>();
-    default: return paged_decode_variant<128, false, 2, 16, 2>();
-  }
+  return rows8 == 1 ? paged_decode_variant<128, false, 1, 16, 2>() : paged_decode_variant<128, false, 2, 16, 2>();
 }
 
 }  // namespace relpos

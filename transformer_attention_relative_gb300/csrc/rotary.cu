@@ -203,7 +203,9 @@ extern "C" int relpos_rotary(const RelposRotaryPlan* plan, int dtype, int invers
   if (sms <= 0) return RELPOS_ERR_CUDA;
   // heads a thread walks: as many as leave every SM its fill of threads, since
   // the sines and cosines (about 25 instructions each) are shared among them
-  const long long want = std::max<long long>(1, static_cast<long long>(sms) * 2048 / n);
+  // (1024 threads an SM, 52 registers each; 4 x 2048 tokens of 32 heads: 11.8 us
+  // against 12.7 with twice and 14.6 with four times as many)
+  const long long want = (static_cast<long long>(sms) * 1024 + n - 1) / n;
   const int groups = static_cast<int>(std::min<long long>(want, heads));
   p.group = (heads + groups - 1) / groups;
   const int threads = static_cast<int>(std::min<long long>(kRotThreads, (n + 31) / 32 * 32));

@@ -9,6 +9,7 @@ made.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -20,8 +21,16 @@ _DTYPES = {torch.bfloat16: RELPOS_BF16, torch.float32: RELPOS_FP32}
 _byref = ctypes.byref
 _device = torch._C._cuda_getDevice
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_empty_like = torch.empty_like
+_int32, _bf16 = torch.int32, torch.bfloat16
 _Pair = _RotaryTensor * 2
 _entries = None
+
+
+@functools.lru_cache(maxsize=1024)
+def _strides(batch, head, row):
+    """A stride triple as the C entry points take it (read only)."""
+    return _byref(_RowStrides(batch, head, row))
 
 
 def _lib():
@@ -67,34 +76,42 @@ class RotaryPlan:
         self._ref = _byref(self._c)
 
 
+def _row_of(x, y, B, L, d):
+    """(x, out, strides of both, heads) as the C entry point takes them."""
+    b, H, l, e = x.shape
+    if b != B or l != L or e != d:
+        raise ValueError("Q and K must agree but for their heads")
+    x0, x1, x2, x3 = x.stride()
+    y0, y1, y2, y3 = y.stride()
+    if (x3 != 1 or y3 != 1) and d > 1:
+        raise ValueError("the last dimension must be contiguous")
+    return x.data_ptr(), y.data_ptr(), x0, x1, x2, y0, y1, y2, H
+
+
 def _rotate(Q, plan, K, positions, offset, out, stream, inverse, what):
     dtype = _DTYPES.get(Q.dtype)
     if dtype is None:
         raise TypeError(f"unsupported dtype {Q.dtype}")
+    if K is not None and K.dtype != Q.dtype:
+        raise TypeError("Q, K and out must have one dtype")
     B, _, L, d = Q.shape
-    if K is None:
-        ins, outs = (Q,), (torch.empty_like(Q) if out is None else out,)
-    else:
-        ins, outs = (Q, K), ((torch.empty_like(Q), torch.empty_like(K)) if out is None else tuple(out))
-        if len(outs) != 2:
-            raise ValueError("out must hold one tensor for each input")
     index = Q.get_device()
-    _check_device(index, K, positions, *outs)
-    desc = []
-    for x, y in zip(ins, outs):
-        if x.dtype != Q.dtype or y.dtype != Q.dtype:
-            raise TypeError("Q, K and out must have one dtype")
-        b, H, l, e = x.shape
-        if b != B or l != L or e != d or y.shape != x.shape:
-            raise ValueError("Q and K must agree but for their heads, and out with them")
-        x0, x1, x2, x3 = x.stride()
-        y0, y1, y2, y3 = y.stride()
-        if (x3 != 1 or y3 != 1) and d > 1:
-            raise ValueError("the last dimension must be contiguous")
-        desc.append((x.data_ptr(), y.data_ptr(), x0, x1, x2, y0, y1, y2, H))
+    _check_device(index, K, positions)
+    if out is None:
+        outs = (_empty_like(Q),) if K is None else (_empty_like(Q), _empty_like(K))
+    else:
+        ins, outs = ((Q,), (out,)) if K is None else ((Q, K), tuple(out))
+        if len(outs) != len(ins):
+            raise ValueError("out must hold one tensor for each input")
+        _check_device(index, *outs)
+        for x, y in zip(ins, outs):
+            if y.dtype != Q.dtype:
+                raise TypeError("Q, K and out must have one dtype")
+            if y.shape != x.shape:
+                raise ValueError("out must have its input's shape")
     ptr, step = None, 0
     if positions is not None:
-        if positions.dtype != torch.int32:
+        if positions.dtype != _int32:
             raise TypeError("positions must be int32")
         shape = positions.shape
         if shape != (B, L) and shape != (L,):
@@ -104,7 +121,11 @@ def _rotate(Q, plan, K, positions, offset, out, stream, inverse, what):
         ptr = positions.data_ptr()
         if len(shape) == 2:
             step = positions.stride(0)
-    rc = _lib()[0](plan._ref, dtype, inverse, _Pair(*desc), len(desc), B, L, d, ptr, step, offset,
+    if K is None:
+        n, desc = 1, _Pair(_row_of(Q, outs[0], B, L, d))
+    else:
+        n, desc = 2, _Pair(_row_of(Q, outs[0], B, L, d), _row_of(K, outs[1], B, L, d))
+    rc = _lib()[0](plan._ref, dtype, inverse, desc, n, B, L, d, ptr, step, offset,
                    _raw_stream(index) if stream is None else stream.cuda_stream)
     if rc != RELPOS_OK:
         raise RelposError(rc, what)
@@ -167,7 +188,7 @@ class PagedCache:
 
 def _check_table(block_table, lens, B):
     """(stride between rows, pages of a row) of a block table."""
-    if block_table.dtype != torch.int32 or lens.dtype != torch.int32:
+    if block_table.dtype != _int32 or lens.dtype != _int32:
         raise TypeError("block_table and lens must be int32")
     shape = block_table.shape
     if len(shape) != 2 or shape[0] != B or lens.shape != (B,):
@@ -185,7 +206,7 @@ def paged_append(cache, K, V, block_table, lens, *, cu_new=None, plan=None, stre
     ``cu_new`` (int32 [B+1], first row of each sequence). block_table int32 [B, max_pages]; lens int32 [B], the
     tokens of each sequence with the new ones.
     """
-    if K.dtype != torch.bfloat16 or V.dtype != torch.bfloat16:
+    if K.dtype != _bf16 or V.dtype != _bf16:
         raise TypeError("K and V must be bf16")
     shape = K.shape
     if V.shape != shape or len(shape) != (4 if cu_new is None else 3):
@@ -197,18 +218,18 @@ def paged_append(cache, K, V, block_table, lens, *, cu_new=None, plan=None, stre
         raise ValueError("the last dimension must be contiguous")
     if cu_new is None:
         B, n, rows, cu = shape[0], shape[2], 0, None
-        ks, vs = _RowStrides(sk[0], sk[1], sk[2]), _RowStrides(sv[0], sv[1], sv[2])
+        ks, vs = _strides(sk[0], sk[1], sk[2]), _strides(sv[0], sv[1], sv[2])
     else:
         if cu_new.dtype != torch.int32 or cu_new.dim() != 1 or cu_new.shape[0] < 1:
             raise TypeError("cu_new must be int32 [B + 1]")
         if not cu_new.is_contiguous():
             raise ValueError("cu_new must be contiguous")
         B, n, rows, cu = cu_new.shape[0] - 1, 0, shape[0], cu_new.data_ptr()
-        ks, vs = _RowStrides(0, sk[1], sk[0]), _RowStrides(0, sv[1], sv[0])
+        ks, vs = _strides(0, sk[1], sk[0]), _strides(0, sv[1], sv[0])
     step, pages = _check_table(block_table, lens, B)
     index = cache._index
     _check_device(index, K, V, cu_new, block_table, lens)
-    rc = _lib()[1](cache._ref, None if plan is None else plan._ref, K.data_ptr(), V.data_ptr(), _byref(ks), _byref(vs),
+    rc = _lib()[1](cache._ref, None if plan is None else plan._ref, K.data_ptr(), V.data_ptr(), ks, vs,
                    cu, rows, n, B, block_table.data_ptr(), step, pages, lens.data_ptr(),
                    _raw_stream(index) if stream is None else stream.cuda_stream)
     if rc != RELPOS_OK:
@@ -223,13 +244,13 @@ def paged_decode(Q, cache, block_table, lens, *, bias=None, mode=None, num_bucke
     its rows are the last Lq of the lens[b] tokens. ``mode``: None (no bias), ``MODE_T5`` with bias fp32
     [num_buckets, Hq] (causal buckets) or ``MODE_ALIBI`` with the slopes fp32 [Hq]. ``scale`` 0 takes 1/sqrt(d).
     """
-    if Q.dtype != torch.bfloat16 or (out is not None and out.dtype != torch.bfloat16):
+    if Q.dtype != _bf16 or (out is not None and out.dtype != _bf16):
         raise TypeError("Q and out must be bf16")
     B, Hq, Lq, d = Q.shape
     if d != cache.head_dim:
         raise ValueError("Q must have the cache's head dimension")
     if out is None:
-        out = torch.empty_like(Q)
+        out = _empty_like(Q)
     elif out.shape != Q.shape:
         raise ValueError("out must have Q's shape")
     q0, q1, q2, q3 = Q.stride()
@@ -251,9 +272,9 @@ def paged_decode(Q, cache, block_table, lens, *, bias=None, mode=None, num_bucke
         if bias.shape != ((num_buckets, Hq) if mode == MODE_T5 else (Hq,)):
             raise ValueError("bias must be [num_buckets, Hq] for MODE_T5, [Hq] for MODE_ALIBI")
         ptr = bias.data_ptr()
-    rc = _lib()[2](cache._ref, Q.data_ptr(), _byref(_RowStrides(q0, q1, q2)), B, Hq, Lq, block_table.data_ptr(), step,
+    rc = _lib()[2](cache._ref, Q.data_ptr(), _strides(q0, q1, q2), B, Hq, Lq, block_table.data_ptr(), step,
                    pages, lens.data_ptr(), mode, ptr, num_buckets, max_distance, scale, out.data_ptr(),
-                   _byref(_RowStrides(o0, o1, o2)), _raw_stream(index) if stream is None else stream.cuda_stream)
+                   _strides(o0, o1, o2), _raw_stream(index) if stream is None else stream.cuda_stream)
     if rc != RELPOS_OK:
         raise RelposError(rc, "relpos_paged_decode")
     return out
