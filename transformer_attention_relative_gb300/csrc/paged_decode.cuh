@@ -512,6 +512,10 @@ __global__ void __launch_bounds__(kPdThreads, NQ * D <= 64 ? 4 : NQ * D <= 128 ?
       }
     }
     const int vis_first = len - p.Lq + row0 / p.G;  // last key that every row sees
+    bool odd = false;  // a constant bias beside which a product has no bits
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) odd |= !(fabsf(add[n][0]) < 1e30f && fabsf(add[n][1]) < 1e30f);
+    odd = __any_sync(0xffffffffu, odd);
     float off[NQ][2], l_run[NQ][2], o[NQ][KS][4];
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
@@ -565,6 +569,32 @@ __global__ void __launch_bounds__(kPdThreads, NQ * D <= 64 ? 4 : NQ * D <= 128 ?
       }
       const bool edge = key0 + KT - 1 > vis_first;  // some row does not see every key
       const bool near = p.mode == RELPOS_T5 && vis_first - (key0 + KT - 1) < p.t5_R;
+      // The common tile: every row sees it, its biases are linear in the key's
+      // position, and no logit passes its row's offset by too much.
+      float z[NQ][MT][4];
+      bool above = edge || near || odd || y < x + kPdWarps;
+      if (!above) {
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) {
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const float cs = qs[n][c] * k_scale;
+            const float base =
+                fmaf(-slope[n][c], static_cast<float>(vis[n][c] - key0 - g), add[n][c] - off[n][c]);
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                z[n][i][2 * e + c] = fmaf(sc[n][i][2 * e + c], cs, fmaf(slope[n][c], 16 * i + 8 * e, base));
+          }
+#pragma unroll
+          for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) above |= z[n][i][e] > kPdMost;
+        }
+        above = __any_sync(0xffffffffu, above);
+      }
+      if (above) {
       float slow[NQ * MT * 4];  // biases, where a table of them does not fit
       if (near && !lut) {
 #pragma unroll 1
@@ -627,7 +657,7 @@ __global__ void __launch_bounds__(kPdThreads, NQ * D <= 64 ? 4 : NQ * D <= 128 ?
       // these have no bits left): the rows concerned take offset 0 and the
       // logits are formed anew. At the warp's first tile of the unit that is
       // where they stand.
-      float z[NQ][MT][4], was[NQ][2];
+      float was[NQ][2];
       bool moves[NQ][2], settle = y < x + kPdWarps;
 #pragma unroll
       for (int n = 0; n < NQ; ++n) {
@@ -648,7 +678,7 @@ __global__ void __launch_bounds__(kPdThreads, NQ * D <= 64 ? 4 : NQ * D <= 128 ?
       while (true) {
         logits(z);
         if (settle) break;
-        bool above = false;
+        above = false;
 #pragma unroll
         for (int n = 0; n < NQ; ++n)
 #pragma unroll
@@ -684,6 +714,7 @@ __global__ void __launch_bounds__(kPdThreads, NQ * D <= 64 ? 4 : NQ * D <= 128 ?
             }
           }
         }
+      }
       }
 #pragma unroll
       for (int n = 0; n < NQ; ++n) {
