@@ -199,6 +199,20 @@ def test_far_scales(scale_exp):
     _check(_gpu(cache, q2, table, lens, bias, "none"), *_ref(cache, q2, table, lens, bias, "none"), True)
 
 
+def test_pages_of_very_different_scales():
+    """Values whose pages differ in scale by far more than a weight's bits, in
+    both directions, a page of scale zero and one of negative scale."""
+    for d in (64, 128):
+        cache, q, table, lens, bias = _case([700, 130], 4, 2, 1, d, 32, E4, "none", 23)
+        g = torch.Generator().manual_seed(24)
+        for s in (cache.v_scale,):
+            s.copy_(torch.exp2(torch.randint(-60, 30, s.shape, generator=g).float()).cuda())
+            s[table[0, 3], 0] = 0.0
+            s[table[0, 5], 1] *= -1.0
+            s[table[1, 0]] = 2.0 ** -40
+        _check(_gpu(cache, q, table, lens, bias, "none"), *_ref(cache, q, table, lens, bias, "none"), True)
+
+
 def test_strides_and_out():
     cache, q, table, lens, bias = _case([100, 9], 4, 2, 2, 64, 32, E4, "none", 15)
     want = _gpu(cache, q, table, lens, bias, "none")

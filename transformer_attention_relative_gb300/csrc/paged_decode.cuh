@@ -32,12 +32,14 @@ namespace relpos {
 constexpr int kPdWarps = 4;
 constexpr int kPdThreads = 32 * kPdWarps;
 constexpr int kPdMinTiles = 4;  // fewest tiles of a block's share: one for each warp
+constexpr int kPdUnitCost = 8;  // what a unit costs a block beside its tiles, in tiles
 // The weights p are kept as 2^(logit - off) for a row offset `off` that starts
 // below every logit and moves up only when a logit comes more than kPdMost above
 // it, to kPdShift below the largest: most tiles then need no maximum across the
-// warp and no rescaling. Weights stay below 2^14, so that fp16 ones (8-bit
-// caches) keep 11 bits down to 2^-20 of the offset's logit and vanish below 2^-30.
-constexpr float kPdShift = 6.f, kPdMost = 14.f;
+// warp and no rescaling. Weights stay below 2^13, so that fp16 ones (8-bit
+// caches, up to 4 times larger by their page's scale) keep 11 bits down to 2^-19
+// of the offset's logit and vanish below 2^-29.
+constexpr float kPdShift = 5.f, kPdMost = 13.f;
 
 struct PagedDecodeParams {
   const uint8_t* k;
@@ -86,8 +88,8 @@ namespace {
 
 // A unit is one sequence, key/value head and up to 16 rows; units follow one
 // another in that order, each with the sequence's key tiles. A block takes an
-// equal share of the tiles of all units, whatever the lengths, and its warps
-// every fourth tile of it.
+// equal share of all units' work, whatever the lengths, and its warps every
+// fourth tile of it.
 
 // Place in the sequence of tiles: sequence and its length, unit of it, tile of
 // the unit.
@@ -124,50 +126,66 @@ RP_DEVI int seq_len(const PagedDecodeParams& p, int b) {
   return b < p.B ? min(max(__ldg(p.lens + b), 0), p.max_len) : 0;
 }
 
-// This block's share x0 .. x1 - 1 of all tiles; warp-uniform. len0 are the
-// lengths of the first 32 sequences, a lane each.
+// A block's share of the work. A unit counts its tiles and kPdUnitCost more, for
+// what a block spends on each unit that it touches (its query rows, its first
+// logits, the joining of its warps); equal shares of that sum end closer together
+// than equal shares of the tiles. len0 are the lengths of the first 32
+// sequences, a lane each; all of this is warp-uniform.
+
+// Cost of a sequence's unit
 template <int KT>
-RP_DEVI int share_of(const PagedDecodeParams& p, int lane, int len0, int& x0, int& x1) {
-  int sum = (len0 + KT - 1) / KT;
-  for (int b = lane + 32; b < p.B; b += 32) sum += (seq_len(p, b) + KT - 1) / KT;
-  const int total = __reduce_add_sync(0xffffffffu, sum) * p.Hkv * p.rt;
-  const int share = max((total + p.blocks - 1) / p.blocks, kPdMinTiles);
-  x0 = min(static_cast<int>(blockIdx.x) * share, total);
-  x1 = min(x0 + share, total);
-  return share;
+RP_DEVI int unit_cost(int len) {
+  return len > 0 ? (len + KT - 1) / KT + kPdUnitCost : 0;
 }
 
-// The cursor at tile x0 of all, which has to exist; warp-uniform.
 template <int KT>
-RP_DEVI Cursor locate(const PagedDecodeParams& p, int lane, int len0, int x0) {
+RP_DEVI int total_cost(const PagedDecodeParams& p, int lane, int len0) {
+  int sum = unit_cost<KT>(len0);
+  for (int b = lane + 32; b < p.B; b += 32) sum += unit_cost<KT>(seq_len(p, b));
+  return __reduce_add_sync(0xffffffffu, sum) * p.Hkv * p.rt;
+}
+
+// The cursor at the first tile at or behind cost x of all units (behind the last
+// one: sequence p.B), the cost at which its unit starts and the number of tiles
+// before it.
+template <int KT>
+RP_DEVI Cursor locate(const PagedDecodeParams& p, int lane, int len0, int x, int& unit_at, int& before) {
   const int per = p.Hkv * p.rt;
   Cursor c{p.B, 0, 0, 0, 0, 0, p.table};
-  int before = 0;
+  int cost = 0, seqs = 0;  // of the sequences looked at, a unit each
   for (int b0 = 0; b0 < p.B; b0 += 32) {
     const int len = b0 ? seq_len(p, b0 + lane) : len0;
-    const int nt = (len + KT - 1) / KT;
-    int upto = nt;
+    const int mine = unit_cost<KT>(len);
+    const unsigned some = __ballot_sync(0xffffffffu, mine > 0);
+    int upto = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int y = __shfl_up_sync(0xffffffffu, upto, o);
       if (lane >= o) upto += y;
     }
-    // the first sequence whose tiles end behind x0
-    const unsigned past = __ballot_sync(0xffffffffu, (before + upto) * per > x0);
+    // the first sequence whose units end behind x
+    const unsigned past = __ballot_sync(0xffffffffu, (cost + upto) * per > x);
     if (past) {
       const int l = __ffs(past) - 1;
-      const int rest = x0 - (before + __shfl_sync(0xffffffffu, upto - nt, l)) * per;
+      const int unit = __shfl_sync(0xffffffffu, mine, l);
+      cost += __shfl_sync(0xffffffffu, upto, l) - unit;
+      seqs += __popc(some & ((1u << l) - 1));
       c.b = b0 + l;
       c.len = __shfl_sync(0xffffffffu, len, l);
-      c.nt = __shfl_sync(0xffffffffu, nt, l);
+      c.nt = unit - kPdUnitCost;
       c.pages = p.table + c.b * p.table_stride;
-      c.u = rest / c.nt;
-      c.t = rest - c.u * c.nt;
+      c.u = (x - cost * per) / unit;
+      unit_at = cost * per + c.u * unit;
+      c.t = max(x - unit_at - kPdUnitCost, 0);
       c.h = c.u / p.rt;
+      before = (cost - seqs * kPdUnitCost) * per + c.u * c.nt + c.t;
       return c;
     }
-    before += __shfl_sync(0xffffffffu, upto, 31);
+    cost += __shfl_sync(0xffffffffu, upto, 31);
+    seqs += __popc(some);
   }
+  unit_at = cost * per;
+  before = (cost - seqs * kPdUnitCost) * per;
   return c;
 }
 
@@ -309,8 +327,8 @@ __global__ void __launch_bounds__(kPdThreads, NQ * D <= 64 ? 4 : NQ * D <= 128 ?
   float* const ml_s = out_s + 2 * S::kRows * D;
 
   griddep_wait();
-  int x0, x1;
-  int share = 0;
+  int tiles;             // of this block
+  int size = 0, at = 0;  // cost of a block's share, and that at which the present unit starts
   Cursor pc;
   if (p.direct) {
     const int per = p.Hkv * p.rt;
@@ -318,12 +336,10 @@ __global__ void __launch_bounds__(kPdThreads, NQ * D <= 64 ? 4 : NQ * D <= 128 ?
     pc.u = blockIdx.x - pc.b * per;
     pc.t = 0;
     pc.len = seq_len(p, pc.b);
-    pc.nt = (pc.len + KT - 1) / KT;
+    pc.nt = tiles = (pc.len + KT - 1) / KT;
     pc.h = pc.u / p.rt;
     pc.pages = p.table + pc.b * p.table_stride;
-    x0 = 0;
-    x1 = pc.nt;
-    if (x1 == 0) {  // no key is seen: zero rows
+    if (tiles == 0) {  // no key is seen: zero rows
       const int row0 = (pc.u - pc.h * p.rt) * S::kRows;
       for (int i = threadIdx.x; i < min(p.G * p.Lq - row0, S::kRows) * D; i += kPdThreads) {
         const int r = row0 + i / D, qi = r / p.G;
@@ -334,25 +350,30 @@ __global__ void __launch_bounds__(kPdThreads, NQ * D <= 64 ? 4 : NQ * D <= 128 ?
     }
   } else {
     const int len0 = seq_len(p, lane);
-    share = share_of<KT>(p, lane, len0, x0, x1);
+    const int total = total_cost<KT>(p, lane, len0);
+    size = max((total + p.blocks - 1) / p.blocks, kPdMinTiles + kPdUnitCost);
     if (threadIdx.x == 0) p.ends[2 * blockIdx.x] = p.ends[2 * blockIdx.x + 1] = make_int4(0, 0, 0, 0);
-    if (x0 >= x1) return;
-    pc = locate<KT>(p, lane, len0, x0);
+    const int begin = min(static_cast<int>(blockIdx.x) * size, total);
+    if (begin == total) return;
+    int first, last, unused;
+    locate<KT>(p, lane, len0, min(begin + size, total), unused, last);
+    pc = locate<KT>(p, lane, len0, begin, at, first);
+    tiles = last - first;
   }
 
-  // ---- producer: this warp's tiles x0 + warp, x0 + warp + 4, ... into its ring
+  // ---- producer: this warp's tiles, warp, warp + 4, ... of the block's, into its ring
   Cursor cc = pc;
   pc.forward<KT>(p, warp);
-  int px = x0 + warp;
+  int px = warp;
   auto page_of = [&](const Cursor& c) { return __ldg(c.pages + ((c.t * KT) >> p.log_page)); };
-  int next_page = px < x1 ? page_of(pc) : 0;  // a step ahead: its load does not delay the copies
+  int next_page = px < tiles ? page_of(pc) : 0;  // a step ahead: its load does not delay the copies
   const int r0 = lane / S::kChunks, ch = lane % S::kChunks;
   const uint32_t dst0 = r0 * S::kRowBytes + ((ch ^ swizzle<S::kChunks>(r0)) << 4);
   constexpr int kStep = 32 / S::kChunks;  // rows between a lane's copies
   const uint32_t page_bytes = S::kRowBytes << p.log_page;
   const uint8_t *k_lane = p.k + lane * 16, *v_lane = p.v + lane * 16;
   auto produce = [&](int stage) {
-    if (px < x1) {
+    if (px < tiles) {
       const int key0 = pc.t * KT;
       int valid = pc.len - key0;
       uint32_t page = next_page;
@@ -388,7 +409,7 @@ __global__ void __launch_bounds__(kPdThreads, NQ * D <= 64 ? 4 : NQ * D <= 128 ?
         if (lane < 2) cp_async4(base + 2 * S::kTileBytes + lane * 4, (lane ? p.v_scale : p.k_scale) + ph);
       }
       px += kPdWarps;
-      if (px < x1) {
+      if (px < tiles) {
         pc.forward<KT>(p, kPdWarps);
         next_page = page_of(pc);
       }
@@ -416,9 +437,9 @@ __global__ void __launch_bounds__(kPdThreads, NQ * D <= 64 ? 4 : NQ * D <= 128 ?
   auto dim_of = [&](int s) { return FP8 ? 16 * (t + 4 * (s / 4)) + 4 * (s % 4) : 8 * (t + 4 * (s / 2)) + 4 * (s % 2); };
 
   int stage = 0;
-  int x = x0;
-  while (x < x1) {
-    const int xe = min(x1, x + cc.nt - cc.t);  // the unit's tiles in this block
+  int x = 0;
+  while (x < tiles) {
+    const int xe = min(tiles, x + cc.nt - cc.t);  // the unit's tiles in this block
     const int len = cc.len;
     if (threadIdx.x == 0 && __ldg(p.lens + cc.b) > p.max_len) atomicCAS(p.status, 0, RELPOS_ERR_PAGE);
     const int h = cc.h, row0 = (cc.u - h * p.rt) * S::kRows;
@@ -516,6 +537,9 @@ __global__ void __launch_bounds__(kPdThreads, NQ * D <= 64 ? 4 : NQ * D <= 128 ?
 #pragma unroll
     for (int n = 0; n < NQ; ++n) odd |= !(fabsf(add[n][0]) < 1e30f && fabsf(add[n][1]) < 1e30f);
     odd = __any_sync(0xffffffffu, odd);
+    // 8 bits: the output is kept in units of v_unit, a page's scale, and the
+    // weights of a page with another scale take the ratio
+    [[maybe_unused]] float v_unit = 0.f, v_inv = 0.f;
     float off[NQ][2], l_run[NQ][2], o[NQ][KS][4];
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
@@ -525,8 +549,8 @@ __global__ void __launch_bounds__(kPdThreads, NQ * D <= 64 ? 4 : NQ * D <= 128 ?
       for (int j = 0; j < KS; ++j) o[n][j][0] = o[n][j][1] = o[n][j][2] = o[n][j][3] = 0.f;
     }
 
-    // this warp's tiles of the unit: x + k with (x - x0 + k) mod 4 = warp
-    for (int y = x + ((warp - (x - x0)) & (kPdWarps - 1)); y < xe; y += kPdWarps) {
+    // this warp's tiles of the unit: those with y mod 4 = warp
+    for (int y = x + ((warp - x) & (kPdWarps - 1)); y < xe; y += kPdWarps) {
       cp_async_wait<STAGES - 2>();
       __syncwarp();
       produce(stage == 0 ? STAGES - 1 : stage - 1);
@@ -562,10 +586,27 @@ __global__ void __launch_bounds__(kPdThreads, NQ * D <= 64 ? 4 : NQ * D <= 128 ?
           }
         }
       }
-      float k_scale = 1.f, v_scale = 1.f;
+      float k_scale = 1.f;
+      [[maybe_unused]] float ratio = 1.f;
       if constexpr (FP8) {
         k_scale = lds32f(vs + S::kTileBytes);
-        v_scale = lds32f(vs + S::kTileBytes + 4);
+        const float v_scale = lds32f(vs + S::kTileBytes + 4);
+        ratio = v_scale * v_inv;
+        // another unit where the ratio would cost the weights bits, or where
+        // there is none yet (zero, infinity and NaN go through the ratio)
+        const float size = fabsf(v_scale);
+        if (!(fabsf(ratio) >= 0.015625f && fabsf(ratio) <= 4.f) && size >= FLT_MIN && size <= 1.f / FLT_MIN) {
+          const float down = v_unit / size;
+#pragma unroll
+          for (int n = 0; n < NQ; ++n)
+#pragma unroll
+            for (int j = 0; j < KS; ++j)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[n][j][e] *= down;
+          v_unit = size;
+          v_inv = 1.f / size;
+          ratio = v_scale * v_inv;
+        }
       }
       const bool edge = key0 + KT - 1 > vis_first;  // some row does not see every key
       const bool near = p.mode == RELPOS_T5 && vis_first - (key0 + KT - 1) < p.t5_R;
@@ -745,7 +786,7 @@ __global__ void __launch_bounds__(kPdThreads, NQ * D <= 64 ? 4 : NQ * D <= 128 ?
               if constexpr (FP8) {
                 // 11 bits of a weight: its rounding (2^-12) is far below the
                 // output's (2^-9)
-                ph[n][i][e] = transpose8(pack_half2(a, c));
+                ph[n][i][e] = transpose8(pack_half2(a * ratio, c * ratio));
               } else {
                 // bf16 alone would round the weights as coarsely as the
                 // output: a second part carries the next 8 bits
@@ -770,39 +811,32 @@ __global__ void __launch_bounds__(kPdThreads, NQ * D <= 64 ? 4 : NQ * D <= 128 ?
           if (ONE && key0 + 16 * i + 8 * e + 2 * t + oo > last) w[0] = w[1] = w[2] = w[3] = 0;
         };
         if constexpr (FP8) {
-          uint32_t r[MT][2][2][4];
 #pragma unroll
-          for (int i = 0; i < MT; ++i)
+          for (int i = 0; i < MT; ++i) {
+            uint32_t r[2][2][4];
 #pragma unroll
             for (int e = 0; e < 2; ++e)
 #pragma unroll
-              for (int oo = 0; oo < 2; ++oo) row_words(i, e, oo, 0, r[i][e][oo]);
+              for (int oo = 0; oo < 2; ++oo) row_words(i, e, oo, 0, r[e][oo]);
 #pragma unroll
-          for (int w = 0; w < D / 32; ++w) {  // words of 4 dims that a lane holds of a row
-            float acc[NQ][2][4];
-#pragma unroll
-            for (int n = 0; n < NQ; ++n)
-#pragma unroll
-              for (int j = 0; j < 2; ++j) acc[n][j][0] = acc[n][j][1] = acc[n][j][2] = acc[n][j][3] = 0.f;
-#pragma unroll
-            for (int i = 0; i < MT; ++i) {
+            for (int w = 0; w < D / 32; ++w) {  // words of 4 dims that a lane holds of a row
 #pragma unroll
               for (int j = 0; j < 2; ++j) {
-                const uint32_t a = __byte_perm(r[i][0][0][w], r[i][0][1][w], j ? 0x7362 : 0x5140);
-                const uint32_t b = __byte_perm(r[i][1][0][w], r[i][1][1][w], j ? 0x7362 : 0x5140);
+                const uint32_t a = __byte_perm(r[0][0][w], r[0][1][w], j ? 0x7362 : 0x5140);
+                const uint32_t b = __byte_perm(r[1][0][w], r[1][1][w], j ? 0x7362 : 0x5140);
                 const uint32_t f[4] = {half2_lo(a), half2_hi(a), half2_lo(b), half2_hi(b)};
 #pragma unroll
-                for (int n = 0; n < NQ; ++n) mma16816<true>(acc[n][j], f, ph[n][i][0], ph[n][i][1]);
+                for (int n = 0; n < NQ; ++n) {
+                  float(&d)[4] = o[n][2 * w + j];
+                  const float was[4] = {d[0], d[1], d[2], d[3]};
+                  mma16816<true>(d, f, ph[n][i][0], ph[n][i][1]);
+                  if (ONE) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) d[e] = vis[n][e & 1] == last ? d[e] : was[e];
+                  }
+                }
               }
             }
-#pragma unroll
-            for (int n = 0; n < NQ; ++n)
-#pragma unroll
-              for (int j = 0; j < 2; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  if (!ONE || vis[n][e & 1] == last)
-                    o[n][2 * w + j][e] = fmaf(acc[n][j][e], v_scale, o[n][2 * w + j][e]);
           }
         } else {
 #pragma unroll
@@ -863,12 +897,12 @@ __global__ void __launch_bounds__(kPdThreads, NQ * D <= 64 ? 4 : NQ * D <= 128 ?
 
     // ---- the four warps' parts of the unit, joined in a fixed order: 2 into 0
     // and 3 into 1, then 1 into 0
-    const int tiles = xe - x, skew = (x - x0) & (kPdWarps - 1);
+    const int had = xe - x;  // tiles of the unit in this block
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        if (((warp - skew) & (kPdWarps - 1)) >= tiles) off[n][c] = -FLT_MAX;  // a warp without tiles
+        if (((warp - x) & (kPdWarps - 1)) >= had) off[n][c] = -FLT_MAX;  // a warp without tiles
         l_run[n][c] += __shfl_xor_sync(0xffffffffu, l_run[n][c], 4);
         l_run[n][c] += __shfl_xor_sync(0xffffffffu, l_run[n][c], 8);
         l_run[n][c] += __shfl_xor_sync(0xffffffffu, l_run[n][c], 16);
@@ -888,7 +922,7 @@ __global__ void __launch_bounds__(kPdThreads, NQ * D <= 64 ? 4 : NQ * D <= 128 ?
         float top = -FLT_MAX;
 #pragma unroll
         for (int w = 0; w < kPdWarps; ++w) top = fmaxf(top, ml[w * S::kRows].x);
-        const float down = ex2_approx(off[n][c] - top);
+        const float down = ex2_approx(off[n][c] - top) * (FP8 ? v_unit : 1.f);
 #pragma unroll
         for (int j = 0; j < KS; ++j) o[n][j][c] *= down, o[n][j][2 + c] *= down;
       }
@@ -939,11 +973,11 @@ __global__ void __launch_bounds__(kPdThreads, NQ * D <= 64 ? 4 : NQ * D <= 128 ?
       }
     }
     __syncthreads();
-    const bool whole = cc.t == 0 && tiles == cc.nt;
+    const bool whole = cc.t == 0 && had == cc.nt;
     const int slot = 2 * blockIdx.x + (cc.t == 0 ? 1 : 0);
     if (!whole && threadIdx.x == 0) {  // the same thread wrote the zeros before
-      const int xs = x - cc.t, c0 = xs / share;
-      p.ends[slot] = make_int4(c0, (xs + cc.nt - 1) / share - c0 + 1, cc.b, cc.u);
+      const int c0 = (at + kPdUnitCost) / size;
+      p.ends[slot] = make_int4(c0, (at + kPdUnitCost + cc.nt - 1) / size - c0 + 1, cc.b, cc.u);
     }
 #pragma unroll 1
     for (int i = threadIdx.x; i < rows * (D / 8); i += kPdThreads) {
@@ -981,7 +1015,8 @@ __global__ void __launch_bounds__(kPdThreads, NQ * D <= 64 ? 4 : NQ * D <= 128 ?
       }
     }
     __syncthreads();  // ml_s and the buffers are free again
-    cc.forward<KT>(p, xe - x);
+    at += kPdUnitCost + cc.nt;
+    cc.forward<KT>(p, had);
     x = xe;
   }
   cp_async_wait<0>();
