@@ -524,7 +524,8 @@ int relpos_rotary(const RelposRotaryPlan* plan, int dtype, int inverse, const Re
  * of the current step included. The kernels check lengths and page numbers
  * against the cache, skip what lies outside it and report it through
  * relpos_check_status() as RELPOS_ERR_PAGE; table entries beyond a sequence's
- * last page are never read.
+ * last page are never read. Make the first call on a device before any stream
+ * capture (it looks up the device status word and sizes launches).
  */
 typedef struct RelposPagedCache {
   void* k;
@@ -571,7 +572,8 @@ typedef struct RelposRowStrides {
  *
  * Slots outside the new tokens keep their bytes unless their page's scale
  * grows. Pages written by one call must not be shared by two of its
- * sequences, nor written or read by another stream meanwhile. Appending the
+ * sequences, appear twice in one, nor be written or read by another stream
+ * meanwhile. Appending the
  * same tokens again writes the same bytes. Asynchronous on `stream`, no
  * scratch.
  */
@@ -600,9 +602,9 @@ int relpos_paged_append(const RelposPagedCache* cache, const RelposRotaryPlan* p
  * Keys and values in masked or unused slots have no effect, whatever they
  * hold. The cache is read once for up to 8 or 16 rows (query heads of a group
  * times Lq) and again, mostly from L2, for each further 8 or 16. Scratch: up to
- * about 8 MB for partial results of sequences that several blocks share, from
- * cudaMallocAsync on `stream`, freed with cudaFreeAsync before the call
- * returns; none where the block table holds at most 16 tiles (256 tokens for
+ * about 8 MB for partial results of sequences that several blocks share, drawn
+ * on `stream` from a memory pool of the library (which keeps up to 64 MB for the
+ * calls to come) and given back before the call returns; none where the block table holds at most 16 tiles (256 tokens for
  * bf16 with d = 128, 512 otherwise). Results do not depend on what
  * else runs. Asynchronous on `stream`.
  */

@@ -1,6 +1,7 @@
 // paged_decode.cu -- relpos_paged_decode: argument checks, the choice of the
 // kernel variant, scratch and launches (the kernels are in paged_decode.cuh).
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -8,7 +9,6 @@
 #include <cstdint>
 #include <cstring>
 #include <mutex>
-#include <vector>
 
 #include "../../include/relpos_attn.h"
 #include "paged_decode.cuh"
@@ -22,29 +22,76 @@ PagedDecodeVariant variant_of(int d, int dtype, int rows8) {
   return d == 64 ? paged_decode_bf16_64(rows8) : paged_decode_bf16_128(rows8);
 }
 
+constexpr int kDevices = 64;
+std::mutex g_mu;  // guards what is kept between calls below
+
 // Blocks of a variant's decode kernel that an SM of the current device holds,
-// asked once for each variant and device (with the shared memory allowed for
-// its launches); 0 on failure.
-int resident_blocks(const PagedDecodeVariant& v) {
-  struct Known {
-    void (*kernel)(PagedDecodeParams);
-    int dev, blocks;
-  };
-  static std::mutex mu;
-  static std::vector<Known> known;
+// asked once for each device (with the shared memory allowed for the kernel's
+// launches); 0 on failure.
+int resident_blocks(int d, int dtype, int rows8, const PagedDecodeVariant& v) {
+  static int known[kDevices][8];
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-  std::lock_guard<std::mutex> lk(mu);
-  for (const Known& k : known)
-    if (k.kernel == v.decode && k.dev == dev) return k.blocks;
-  int n = 0;
-  if (cudaFuncSetAttribute(v.decode, cudaFuncAttributeMaxDynamicSharedMemorySize, v.smem) != cudaSuccess ||
-      cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, v.decode, kPdThreads, v.smem) != cudaSuccess) {
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) return 0;
+  int& n = known[dev][(d == 128) * 4 + (dtype == RELPOS_E4M3) * 2 + rows8 - 1];
+  std::lock_guard<std::mutex> lk(g_mu);
+  if (n == 0 &&
+      (cudaFuncSetAttribute(v.decode, cudaFuncAttributeMaxDynamicSharedMemorySize, v.smem) != cudaSuccess ||
+       cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, v.decode, kPdThreads, v.smem) != cudaSuccess)) {
     cudaGetLastError();
-    return 0;
+    n = 0;
   }
-  known.push_back({v.decode, dev, n});
   return n;
+}
+
+// The pool that scratch comes from, one of the library's own for each device:
+// the default pool gives its memory back whenever the host waits for the GPU,
+// and a call after that took 200 us for its scratch (every step of a decode loop
+// that looks at its token). This one keeps up to 64 MB.
+cudaMemPool_t scratch_pool() {
+  static cudaMemPool_t pools[kDevices];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) return nullptr;
+  std::lock_guard<std::mutex> lk(g_mu);
+  if (!pools[dev]) {
+    cudaMemPoolProps props = {};
+    props.allocType = cudaMemAllocationTypePinned;
+    props.location.type = cudaMemLocationTypeDevice;
+    props.location.id = dev;
+    cudaMemPool_t pool = nullptr;
+    cuuint64_t keep = 64ull << 20;
+    if (cudaMemPoolCreate(&pool, &props) != cudaSuccess ||
+        cudaMemPoolSetAttribute(pool, cudaMemPoolAttrReleaseThreshold, &keep) != cudaSuccess) {
+      cudaGetLastError();
+      return nullptr;
+    }
+    pools[dev] = pool;
+  }
+  return pools[dev];
+}
+
+// t5_setup, which walks the distances up to max_distance in logarithms, for
+// parameters that the last calls did not have; it depends on nothing else.
+int t5_thresholds(int num_buckets, int max_distance, int longest, T5Index* ix, int* R) {
+  struct Known {
+    int num_buckets, max_distance, longest, R;
+    T5Index ix;
+  };
+  static Known known[8];
+  static int next = 0;
+  std::lock_guard<std::mutex> lk(g_mu);
+  for (const Known& k : known) {
+    if (k.num_buckets == num_buckets && k.max_distance == max_distance && k.longest == longest) {
+      *ix = k.ix;
+      *R = k.R;
+      return RELPOS_OK;
+    }
+  }
+  const int rc = t5_setup(num_buckets, max_distance, 1, longest, ix, R);
+  if (rc == RELPOS_OK) {
+    known[next] = {num_buckets, max_distance, longest, *R, *ix};
+    next = (next + 1) % 8;
+  }
+  return rc;
 }
 
 }  // namespace
@@ -93,14 +140,14 @@ extern "C" int relpos_paged_decode(const RelposPagedCache* cache, const void* Q,
   // third fewer warps on an SM and take longer a tile: 4 heads x 16 sequences x
   // 16 rows in bf16, d = 64, 26 against 32 us at 4096 tokens (9 tiles a warp
   // with 8 rows), 92 against 83 at 16384 (36 tiles); 24 and 32 rows lose to both.
-  int occ = resident_blocks(v);
+  int occ = resident_blocks(cache->d, cache->dtype, 1, v);
   if (occ < 1) return RELPOS_ERR_CUDA;
   const bool wide = rt > 1 && units * tiles > 16ll * kPdWarps * occ * sms;
   if (wide) {
     v = variant_of(cache->d, cache->dtype, 2);
     rt = (rt + 1) / 2;
     units = static_cast<long long>(B) * cache->H * rt;
-    occ = resident_blocks(v);
+    occ = resident_blocks(cache->d, cache->dtype, 2, v);
     if (occ < 1) return RELPOS_ERR_CUDA;
   }
   const long long most = units * tiles;
@@ -128,7 +175,7 @@ extern "C" int relpos_paged_decode(const RelposPagedCache* cache, const void* Q,
   p.bias = static_cast<const float*>(bias);
   p.mode = bias_mode;
   if (bias_mode == RELPOS_T5) {
-    rc = t5_setup(num_buckets, max_distance, 1, capacity, &p.t5, &p.t5_R);
+    rc = t5_thresholds(num_buckets, max_distance, static_cast<int>(capacity), &p.t5, &p.t5_R);
     if (rc != RELPOS_OK) return rc;
   }
   p.scale_log2 = (scale != 0.f ? scale : 1.0f / std::sqrt(static_cast<float>(cache->d))) * kLog2e;
@@ -143,8 +190,9 @@ extern "C" int relpos_paged_decode(const RelposPagedCache* cache, const void* Q,
   float* scratch = nullptr;
   if (!p.direct) {
     const size_t slots = static_cast<size_t>(p.blocks) * 2 * p.rows;  // a multiple of 16
-    if (cudaMallocAsync(&scratch, slots * (cache->d + 2) * sizeof(float) + p.blocks * 2 * sizeof(int4), s) !=
-        cudaSuccess) {
+    const size_t bytes = slots * (cache->d + 2) * sizeof(float) + p.blocks * 2 * sizeof(int4);
+    cudaMemPool_t pool = scratch_pool();
+    if (!pool || cudaMallocFromPoolAsync(reinterpret_cast<void**>(&scratch), bytes, pool, s) != cudaSuccess) {
       cudaGetLastError();
       return RELPOS_ERR_CUDA;
     }

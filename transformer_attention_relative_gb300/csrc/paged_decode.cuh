@@ -1039,10 +1039,9 @@ __global__ void __launch_bounds__(kPdThreads) relpos_paged_combine_kernel(const 
   const int c0 = what.x, k = what.y, b = what.z, u = what.w;
   for (int i = blockIdx.x; i < p.B; i += gridDim.x) {
     if (__ldg(p.lens + i) > 0) continue;
-    for (int j = threadIdx.x; j < p.Hq * p.Lq * D; j += kPdThreads) {
-      const int r = j / D;
-      p.out[i * p.o_batch + r / p.Lq * p.o_head + r % p.Lq * p.o_row + j % D] = __float2bfloat16_rn(0.f);
-    }
+    for (int r = threadIdx.x / 32; r < p.Hq * p.Lq; r += kPdWarps)
+      for (int j = threadIdx.x % 32; j < D; j += 32)
+        p.out[i * p.o_batch + r / p.Lq * p.o_head + r % p.Lq * p.o_row + j] = __float2bfloat16_rn(0.f);
   }
   if (k == 0) return;
   const int h = u / p.rt, row0 = (u - h * p.rt) * p.rows, rows = min(p.G * p.Lq - row0, p.rows);

@@ -23,6 +23,7 @@ _device = torch._C._cuda_getDevice
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _empty_like = torch.empty_like
 _int32, _bf16 = torch.int32, torch.bfloat16
+_MOST = 2 ** 31 - 1  # the C entry points take sizes as 32-bit integers, ctypes cuts larger ones silently
 _Pair = _RotaryTensor * 2
 _entries = None
 
@@ -95,6 +96,8 @@ def _rotate(Q, plan, K, positions, offset, out, stream, inverse, what):
     if K is not None and K.dtype != Q.dtype:
         raise TypeError("Q, K and out must have one dtype")
     B, _, L, d = Q.shape
+    if B * L > _MOST or not -_MOST - 1 <= offset <= _MOST:
+        raise ValueError("more rows, or positions, than 32-bit integers hold")
     index = Q.get_device()
     _check_device(index, K, positions)
     if out is None:
@@ -213,6 +216,8 @@ def paged_append(cache, K, V, block_table, lens, *, cu_new=None, plan=None, stre
         raise ValueError("K and V must be [B,H,n,d], or [T,H,d] with cu_new")
     if shape[1] != cache.heads or shape[-1] != cache.head_dim:
         raise ValueError("K and V must have the cache's heads and head dimension")
+    if shape[0] * shape[-2] > _MOST:
+        raise ValueError("more rows than 32-bit integers hold")
     sk, sv = K.stride(), V.stride()
     if sk[-1] != 1 or sv[-1] != 1:
         raise ValueError("the last dimension must be contiguous")
@@ -267,6 +272,8 @@ def paged_decode(Q, cache, block_table, lens, *, bias=None, mode=None, num_bucke
     else:
         if mode != MODE_T5 and mode != MODE_ALIBI:
             raise ValueError("mode must be None, MODE_T5 or MODE_ALIBI")
+        if not 0 < max_distance <= _MOST:
+            raise ValueError("max_distance must be positive and fit 32 bits")
         if bias is None or bias.dtype != torch.float32 or not bias.is_contiguous():
             raise TypeError("bias must be a contiguous fp32 tensor")
         if bias.shape != ((num_buckets, Hq) if mode == MODE_T5 else (Hq,)):
