@@ -106,7 +106,7 @@ def load_library(path: str = LIB_PATH):
     ll, dbl, f, p = ctypes.c_longlong, ctypes.c_double, ctypes.c_float, ctypes.POINTER
     lib.relpos_rotary_plan_init.argtypes = [p(_RotaryPlan), i, i, dbl, i, dbl, dbl, dbl, dbl]
     lib.relpos_rotary_plan_init.restype = i
-    lib.relpos_rotary.argtypes = [p(_RotaryPlan), i, i, p(_RotaryTensor), i, i, i, i, vp, ll, i, vp]
+    lib.relpos_rotary.argtypes = [p(_RotaryPlan), i, i, vp, i, i, i, i, vp, ll, i, vp]
     lib.relpos_rotary.restype = i
     lib.relpos_paged_append.argtypes = [p(_PagedCache), p(_RotaryPlan), vp, vp, p(_RowStrides), p(_RowStrides), vp,
                                         i, i, i, vp, ll, i, vp, vp]

@@ -10,11 +10,12 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import struct
 
 import torch
 
 from . import (MODE_ALIBI, MODE_T5, RELPOS_BF16, RELPOS_E4M3, RELPOS_FP32, RELPOS_NO_BIAS, RELPOS_OK,
-               ROTARY_LAYOUTS, ROTARY_SCALINGS, RelposError, _PagedCache, _RotaryPlan, _RotaryTensor, _RowStrides,
+               ROTARY_LAYOUTS, ROTARY_SCALINGS, RelposError, _PagedCache, _RotaryPlan, _RowStrides,
                load_library, relpos_rotary_plan_init)
 
 _DTYPES = {torch.bfloat16: RELPOS_BF16, torch.float32: RELPOS_FP32}
@@ -24,7 +25,7 @@ _raw_stream = torch._C._cuda_getCurrentRawStream
 _empty_like = torch.empty_like
 _int32, _bf16 = torch.int32, torch.bfloat16
 _MOST = 2 ** 31 - 1  # the C entry points take sizes as 32-bit integers, ctypes cuts larger ones silently
-_Pair = _RotaryTensor * 2
+_tensor = struct.Struct("@PP6qi4x").pack  # a RelposRotaryTensor's bytes: quicker than its ctypes structure
 _entries = None
 
 
@@ -125,9 +126,9 @@ def _rotate(Q, plan, K, positions, offset, out, stream, inverse, what):
         if len(shape) == 2:
             step = positions.stride(0)
     if K is None:
-        n, desc = 1, _Pair(_row_of(Q, outs[0], B, L, d))
+        n, desc = 1, _tensor(*_row_of(Q, outs[0], B, L, d))
     else:
-        n, desc = 2, _Pair(_row_of(Q, outs[0], B, L, d), _row_of(K, outs[1], B, L, d))
+        n, desc = 2, _tensor(*_row_of(Q, outs[0], B, L, d)) + _tensor(*_row_of(K, outs[1], B, L, d))
     rc = _lib()[0](plan._ref, dtype, inverse, desc, n, B, L, d, ptr, step, offset,
                    _raw_stream(index) if stream is None else stream.cuda_stream)
     if rc != RELPOS_OK:
