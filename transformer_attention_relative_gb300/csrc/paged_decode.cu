@@ -69,29 +69,34 @@ cudaMemPool_t scratch_pool() {
   return pools[dev];
 }
 
-// t5_setup, which walks the distances up to max_distance in logarithms, for
-// parameters that the last calls did not have; it depends on nothing else.
-int t5_thresholds(int num_buckets, int max_distance, int longest, T5Index* ix, int* R) {
+// The T5 thresholds (t5_setup, which walks the distances up to max_distance in
+// logarithms) and the buckets of the first distances, for parameters that the
+// last calls did not have; they depend on nothing else.
+int set_t5(int num_buckets, int max_distance, int longest, PagedDecodeParams* p) {
   struct Known {
     int num_buckets, max_distance, longest, R;
     T5Index ix;
+    uint8_t bucket[kPdBuckets];
   };
   static Known known[8];
   static int next = 0;
   std::lock_guard<std::mutex> lk(g_mu);
-  for (const Known& k : known) {
-    if (k.num_buckets == num_buckets && k.max_distance == max_distance && k.longest == longest) {
-      *ix = k.ix;
-      *R = k.R;
-      return RELPOS_OK;
-    }
-  }
-  const int rc = t5_setup(num_buckets, max_distance, 1, longest, ix, R);
-  if (rc == RELPOS_OK) {
-    known[next] = {num_buckets, max_distance, longest, *R, *ix};
+  const Known* k = nullptr;
+  for (const Known& e : known)
+    if (e.num_buckets == num_buckets && e.max_distance == max_distance && e.longest == longest) k = &e;
+  if (!k) {
+    Known e = {num_buckets, max_distance, longest};
+    const int rc = t5_setup(num_buckets, max_distance, 1, longest, &e.ix, &e.R);
+    if (rc != RELPOS_OK) return rc;
+    for (int i = 0; i < kPdBuckets; ++i) e.bucket[i] = static_cast<uint8_t>(t5_bucket_dev(-i, e.ix));
+    known[next] = e;
+    k = &known[next];
     next = (next + 1) % 8;
   }
-  return rc;
+  p->t5 = k->ix;
+  p->t5_R = k->R;
+  std::memcpy(p->bucket, k->bucket, sizeof(k->bucket));
+  return RELPOS_OK;
 }
 
 }  // namespace
@@ -175,7 +180,7 @@ extern "C" int relpos_paged_decode(const RelposPagedCache* cache, const void* Q,
   p.bias = static_cast<const float*>(bias);
   p.mode = bias_mode;
   if (bias_mode == RELPOS_T5) {
-    rc = t5_thresholds(num_buckets, max_distance, static_cast<int>(capacity), &p.t5, &p.t5_R);
+    rc = set_t5(num_buckets, max_distance, static_cast<int>(capacity), &p);
     if (rc != RELPOS_OK) return rc;
   }
   p.scale_log2 = (scale != 0.f ? scale : 1.0f / std::sqrt(static_cast<float>(cache->d))) * kLog2e;

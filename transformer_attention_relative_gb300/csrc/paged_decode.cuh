@@ -32,7 +32,9 @@ namespace relpos {
 constexpr int kPdWarps = 4;
 constexpr int kPdThreads = 32 * kPdWarps;
 constexpr int kPdMinTiles = 4;  // fewest tiles of a block's share: one for each warp
-constexpr int kPdUnitCost = 8;  // what a unit costs a block beside its tiles, in tiles
+constexpr int kPdUnitCost = 12;  // what a unit costs a block beside its tiles, in tiles
+constexpr int kPdBuckets = 256;
+
 // The weights p are kept as 2^(logit - off) for a row offset `off` that starts
 // below every logit and moves up only when a logit comes more than kPdMost above
 // it, to kPdShift below the largest: most tiles then need no maximum across the
@@ -63,6 +65,7 @@ struct PagedDecodeParams {
   int mode;          // RELPOS_NO_BIAS, RELPOS_T5 or RELPOS_ALIBI
   int t5_R;
   T5Index t5;
+  uint8_t bucket[kPdBuckets];  // T5 buckets of the first distances
   float scale_log2;
   float* part_o;   // [blocks][2][rows][d] partial outputs
   float* part_ml;  // [blocks][2][rows][2] their offsets and sums
@@ -452,8 +455,9 @@ __global__ void __launch_bounds__(kPdThreads, NQ * D <= 64 ? 4 : NQ * D <= 128 ?
                      len - p.Lq - (cc.t + xe - x) * KT + 1 < p.t5_R;
     if (lut) {
       for (int i = threadIdx.x; i < p.G * lut_len; i += kPdThreads) {
-        const int hl = i / lut_len;
-        out_s[i] = to_log2(__ldg(p.bias + t5_bucket_dev(hl * lut_len - i, p.t5) * p.Hq + h * p.G + hl));
+        const int hl = i / lut_len, back = i - hl * lut_len;
+        const int bucket = back < kPdBuckets ? p.bucket[back] : t5_bucket_dev(-back, p.t5);
+        out_s[i] = to_log2(__ldg(p.bias + bucket * p.Hq + h * p.G + hl));
       }
       __syncthreads();
     }
