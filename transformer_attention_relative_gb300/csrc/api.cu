@@ -18,6 +18,7 @@
 #include "relpos_bwd.cuh"
 #include "relpos_common.cuh"
 #include "relpos_internal.h"
+#include "serving_internal.h"
 
 namespace relpos {
 namespace {

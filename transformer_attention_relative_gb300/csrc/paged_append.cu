@@ -26,6 +26,7 @@
 #include "paged.cuh"
 #include "ptx.cuh"
 #include "relpos_internal.h"
+#include "serving_internal.h"
 #include "rotary.cuh"
 
 namespace relpos {

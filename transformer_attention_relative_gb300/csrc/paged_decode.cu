@@ -13,6 +13,7 @@
 #include "../../include/relpos_attn.h"
 #include "paged_decode.cuh"
 #include "relpos_internal.h"
+#include "serving_internal.h"
 
 namespace relpos {
 namespace {

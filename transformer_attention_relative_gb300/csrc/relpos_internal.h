@@ -7,7 +7,6 @@
 #include <cstddef>
 #include <cstdint>
 
-#include "../../include/relpos_attn.h"
 #include "relpos_common.cuh"
 
 namespace relpos {
@@ -50,14 +49,6 @@ DecodeParams make_decode_params(const void* Q, const void* K, const void* V, con
                                 const int* key_pos, int B, int H, int Lq, int Lk, int causal,
                                 int q_offset, float scale_log2, const T5Index& t5, int R,
                                 float* part, void* out, bool out_f32);
-
-// the device status word that kernels record errors in, and the number of SMs,
-// of the current device (null and -1 on failure)
-int* device_status();
-int device_sms();
-
-// checks of a paged cache's sizes, types and pointers; a RELPOS_* code
-int check_paged_cache(const RelposPagedCache* cache);
 
 // true when p is 16-byte aligned (the kernels' vector loads and stores)
 bool aligned16(const void* p);

@@ -14,8 +14,8 @@
 
 #include "../../include/relpos_attn.h"
 #include "ptx.cuh"
-#include "relpos_internal.h"
 #include "rotary.cuh"
+#include "serving_internal.h"
 
 namespace relpos {
 namespace {
