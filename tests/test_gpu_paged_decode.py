@@ -187,6 +187,19 @@ def test_lowest_values_in_the_bias():
     np.testing.assert_array_equal(got, again)
 
 
+@pytest.mark.parametrize("dtype", [E4, BF])
+@pytest.mark.parametrize("mask", [-1e9, torch.finfo(torch.float32).min])
+def test_masks_over_many_tiles(dtype, mask):
+    """Every key masked by a bias that fp32 cannot add a product to without
+    losing it: an even softmax over all tiles, near ones and far ones. (|q.k| /
+    sqrt(d) stays below 32, half a step of fp32 at 1e9, so each logit is the mask
+    itself.)"""
+    cache, q, table, lens, _ = _case([1500, 40], 4, 2, 1, 64, 64, dtype, "t5", 25)
+    got = _gpu(cache, q, table, lens, torch.full((32, 4), mask), "t5").double().cpu().numpy()
+    ref, size = _ref(cache, 0 * q, table, lens, torch.zeros(32, 4), "t5")  # equal logits
+    _check(torch.from_numpy(got), ref, size, dtype == E4)
+
+
 @pytest.mark.parametrize("scale_exp", [-100, 60])
 def test_far_scales(scale_exp):
     """Page scales far from 1 on the values (and back on q for the keys)."""

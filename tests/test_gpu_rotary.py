@@ -168,6 +168,14 @@ def test_empty_sizes():
         assert rp.rotary(torch.zeros(shape, dtype=BF, device="cuda"), plan).shape == shape
 
 
+def test_more_heads_than_a_launch_dimension():
+    """One token of 80000 heads: more groups of heads than a grid is high."""
+    q, k = _x((1, 40000, 1, 2), BF, 16), _x((1, 40000, 1, 2), BF, 17)
+    plan = rp.RotaryPlan(2)
+    for y, x in zip(rp.rotary(q, plan, k, offset=3), (q, k)):
+        _check(y, x, [3], 2)
+
+
 def test_side_stream_and_graph():
     q = _x((2, 4, 100, 64), BF, 14)
     plan, pos = rp.RotaryPlan(64), torch.arange(100, dtype=torch.int32, device="cuda")

@@ -137,7 +137,7 @@ extern "C" int relpos_paged_decode(const RelposPagedCache* cache, const void* Q,
   int rt = (G * Lq + 7) / 8;
   long long units = static_cast<long long>(B) * cache->H * rt;
   const long long tiles = (capacity + v.tile - 1) / v.tile;  // of a unit, with every page in use
-  if (units > 0x7fffffffll || units * (tiles + kPdUnitCost) > 0x7fffffffll) return RELPOS_ERR_UNSUPPORTED;
+  if (units > (1 << 30) || units * (tiles + kPdUnitCost) > (1 << 30)) return RELPOS_ERR_UNSUPPORTED;
   if (static_cast<long long>(cache->num_pages) * cache->H > 0x7fffffffll) return RELPOS_ERR_UNSUPPORTED;
   const int sms = device_sms();
   if (sms <= 0) return RELPOS_ERR_CUDA;

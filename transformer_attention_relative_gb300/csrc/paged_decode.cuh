@@ -544,9 +544,11 @@ __global__ void __launch_bounds__(kPdThreads, NQ * D <= 64 ? 4 : NQ * D <= 128 ?
       }
     }
     const int vis_first = len - p.Lq + row0 / p.G;  // last key that every row sees
-    bool odd = false;  // a constant bias beside which a product has no bits
+    // a constant bias beside which products lose bits (a mask of -1e9, the
+    // type's lowest value): every tile then has to lose them alike
+    bool odd = false;
 #pragma unroll
-    for (int n = 0; n < NQ; ++n) odd |= !(fabsf(add[n][0]) < 1e30f && fabsf(add[n][1]) < 1e30f);
+    for (int n = 0; n < NQ; ++n) odd |= !(fabsf(add[n][0]) <= 4096.f && fabsf(add[n][1]) <= 4096.f);
     odd = __any_sync(0xffffffffu, odd);
     // 8 bits: the output is kept in units of v_unit, a page's scale, and the
     // weights of a page with another scale take the ratio
@@ -679,13 +681,11 @@ __global__ void __launch_bounds__(kPdThreads, NQ * D <= 64 ? 4 : NQ * D <= 128 ?
                 for (int e = 0; e < 2; ++e)
                   z[n][i][2 * e + c] = fmaf(sc[n][i][2 * e + c], cs, slow[((n * 2 + c) * MT + i) * 2 + e]) - off[n][c];
             } else if (p.mode != RELPOS_ALIBI) {
-              // bias and offset in one constant; a bias of the type's lowest
-              // values, beside which a product has no bits, takes it away
-              const float base = add[n][c] - off[n][c], cf = fabsf(add[n][c]) < 1e30f ? cs : 0.f;
 #pragma unroll
               for (int i = 0; i < MT; ++i)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) z[n][i][2 * e + c] = fmaf(sc[n][i][2 * e + c], cf, base);
+                for (int e = 0; e < 2; ++e)
+                  z[n][i][2 * e + c] = fmaf(sc[n][i][2 * e + c], cs, add[n][c]) - off[n][c];
             } else {
               const float back_f = static_cast<float>(back0);
 #pragma unroll

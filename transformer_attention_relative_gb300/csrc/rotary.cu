@@ -210,7 +210,7 @@ extern "C" int relpos_rotary(const RelposRotaryPlan* plan, int dtype, int invers
   // (1024 threads an SM, 52 registers each; 4 x 2048 tokens of 32 heads: 11.8 us
   // against 12.7 with twice and 14.6 with four times as many)
   const long long want = (static_cast<long long>(sms) * 1024 + n - 1) / n;
-  const int groups = static_cast<int>(std::min<long long>(want, heads));
+  const int groups = static_cast<int>(std::min<long long>({want, heads, 65535}));
   p.group = (heads + groups - 1) / groups;
   const int threads = static_cast<int>(std::min<long long>(kRotThreads, (n + 31) / 32 * 32));
   const dim3 grid(static_cast<unsigned>((n + threads - 1) / threads), (heads + p.group - 1) / p.group);
