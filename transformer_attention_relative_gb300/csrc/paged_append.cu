@@ -106,7 +106,8 @@ __device__ __noinline__ uint32_t rotated_codes_exact(float x1, float x2, unsigne
 // (6 us). At 80 registers three blocks of 256 threads share an SM; two (128
 // registers, all heads' loads at once) took 50 us.
 template <bool FP8, bool INTERLEAVED, int THREADS, int UNITS>
-__global__ void __launch_bounds__(THREADS, UNITS == 1 ? 768 / THREADS : 1) relpos_paged_append_kernel(const __grid_constant__ AppendParams p) {
+__global__ void __launch_bounds__(THREADS, UNITS == 1 ? 768 / THREADS : 1)
+    relpos_paged_append_kernel(const __grid_constant__ AppendParams p) {
   extern __shared__ float4 turn_s[];
   __shared__ int amax_s[2][kAppMaxGroup];
   __shared__ float had_s[2][kAppMaxGroup];      // scales so far (0 for a page taken anew)
@@ -501,8 +502,10 @@ extern "C" int relpos_paged_append(const RelposPagedCache* cache, const RelposRo
   p.group = static_cast<int>((cache->H + groups - 1) / groups);
   const bool inter = p.plan.layout == RELPOS_ROTARY_INTERLEAVED;
   const auto kernel = cache->dtype == RELPOS_E4M3
-                          ? (inter ? append_kernel<true, true>(threads, units) : append_kernel<true, false>(threads, units))
-                          : (inter ? append_kernel<false, true>(threads, units) : append_kernel<false, false>(threads, units));
+                          ? (inter ? append_kernel<true, true>(threads, units)
+                                   : append_kernel<true, false>(threads, units))
+                          : (inter ? append_kernel<false, true>(threads, units)
+                                   : append_kernel<false, false>(threads, units));
   const int smem = p.plan.rot_dim ? 64 * items : 0;
   if (smem > 48 * 1024 &&
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {

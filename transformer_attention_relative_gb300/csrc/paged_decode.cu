@@ -190,8 +190,9 @@ extern "C" int relpos_paged_decode(const RelposPagedCache* cache, const void* Q,
   // Sequences of up to 16 tiles at most (four of a warp) have a block for each
   // unit and no second launch: 4.9 against 6.7 us for 113 tokens of 16 heads.
   p.direct = tiles <= 4 * kPdMinTiles;
-  p.blocks = static_cast<int>(
-      p.direct ? units : std::min<long long>(static_cast<long long>(occ) * sms, (most + kPdMinTiles - 1) / kPdMinTiles));
+  p.blocks = static_cast<int>(p.direct ? units
+                                       : std::min<long long>(static_cast<long long>(occ) * sms,
+                                                             (most + kPdMinTiles - 1) / kPdMinTiles));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   float* scratch = nullptr;
   if (!p.direct) {

@@ -32,7 +32,6 @@
 #include "../../include/relpos_attn.h"
 #include "ptx.cuh"
 #include "relpos_common.cuh"
-#include "relpos_internal.h"
 
 namespace relpos {
 
@@ -76,7 +75,9 @@ struct PagedDecodeParams {
   float scale_log2;
   float* part_o;   // [blocks][2][rows][d] partial outputs
   float* part_ml;  // [blocks][2][rows][2] their offsets and sums
-  int4* ends;      // [blocks][2] what a slot holds: first block and number of blocks of its unit (0: nothing), sequence, unit
+  // [blocks][2] what a slot holds: first block and number of blocks of its unit
+  // (0: nothing), sequence, unit
+  int4* ends;
   int blocks;
   int direct;      // a block for each unit: nothing to combine
   int* status;
@@ -201,7 +202,8 @@ RP_DEVI Cursor locate(const PagedDecodeParams& p, int lane, int len0, int x, int
 
 template <int DST, int SRC>
 RP_DEVI void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0 + %2], [%1 + %3], 16;" ::"r"(dst), "l"(src), "n"(DST), "n"(SRC) : "memory");
+  asm volatile("cp.async.cg.shared.global [%0 + %2], [%1 + %3], 16;" ::"r"(dst), "l"(src), "n"(DST), "n"(SRC)
+               : "memory");
 }
 // `bytes` (16 or 0) are copied, the rest is zero
 template <int DST, int SRC>
@@ -220,7 +222,10 @@ RP_DEVI void cp_async_wait() {
 }
 RP_DEVI uint4 lds128(uint32_t a) {
   uint4 u;
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "r"(a) : "memory");
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
+               : "r"(a)
+               : "memory");
   return u;
 }
 RP_DEVI uint2 lds64(uint32_t a) {
@@ -649,124 +654,125 @@ __global__ void __launch_bounds__(kPdThreads, NQ * D <= 64 ? 4 : NQ * D <= 128 ?
         above = __any_sync(0xffffffffu, above);
       }
       if (above) {
-      float slow[NQ * MT * 4];  // biases, where a table of them does not fit
-      if (near && !lut) {
+        float slow[NQ * MT * 4];  // biases, where a table of them does not fit
+        if (near && !lut) {
 #pragma unroll 1
-        for (int i = 0; i < NQ * MT * 4; ++i) {
-          const int r = row0 + 8 * (i / (4 * MT)) + 2 * t + i / (2 * MT) % 2, qi = r / p.G;
-          const int back = len - p.Lq + qi - (key0 + 16 * (i / 2 % MT) + 8 * (i % 2) + g);
-          slow[i] = to_log2(__ldg(p.bias + t5_bucket_dev(-min(max(back, 0), p.t5_R), p.t5) * p.Hq + h * p.G + r - qi * p.G));
+          for (int i = 0; i < NQ * MT * 4; ++i) {
+            const int r = row0 + 8 * (i / (4 * MT)) + 2 * t + i / (2 * MT) % 2, qi = r / p.G;
+            const int back = len - p.Lq + qi - (key0 + 16 * (i / 2 % MT) + 8 * (i % 2) + g);
+            const int bucket = t5_bucket_dev(-min(max(back, 0), p.t5_R), p.t5);
+            slow[i] = to_log2(__ldg(p.bias + bucket * p.Hq + h * p.G + r - qi * p.G));
+          }
         }
-      }
-      // logit of row 8 n + 2 t + c and key 16 i + 8 e + g, less its row's offset
-      auto logits = [&](float (&z)[NQ][MT][4]) {
+        // logit of row 8 n + 2 t + c and key 16 i + 8 e + g, less its row's offset
+        auto logits = [&](float (&z)[NQ][MT][4]) {
+#pragma unroll
+          for (int n = 0; n < NQ; ++n) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const float cs = qs[n][c] * k_scale;
+              const int back0 = vis[n][c] - key0 - g;  // to key 16 i + 8 e: less 16 i + 8 e
+              if (near && lut) {
+                const float* biases = out_s + (row0 + 8 * n + 2 * t + c) % p.G * lut_len;
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                  for (int e = 0; e < 2; ++e)
+                    z[n][i][2 * e + c] = fmaf(sc[n][i][2 * e + c], cs,
+                                              biases[min(max(back0 - 16 * i - 8 * e, 0), p.t5_R)]) - off[n][c];
+              } else if (near) {
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                  for (int e = 0; e < 2; ++e)
+                    z[n][i][2 * e + c] = fmaf(sc[n][i][2 * e + c], cs, slow[((n * 2 + c) * MT + i) * 2 + e]) - off[n][c];
+              } else if (p.mode != RELPOS_ALIBI) {
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                  for (int e = 0; e < 2; ++e)
+                    z[n][i][2 * e + c] = fmaf(sc[n][i][2 * e + c], cs, add[n][c]) - off[n][c];
+              } else {
+                const float back_f = static_cast<float>(back0);
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                  for (int e = 0; e < 2; ++e)
+                    z[n][i][2 * e + c] =
+                        fmaf(sc[n][i][2 * e + c], cs, fmaf(-slope[n][c], back_f - (16 * i + 8 * e), -off[n][c]));
+              }
+              if (edge) {
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                  for (int e = 0; e < 2; ++e)
+                    if (back0 < 16 * i + 8 * e) z[n][i][2 * e + c] = -INFINITY;
+              }
+            }
+          }
+        };
+        // Offsets move by the logits themselves (less an offset far below them
+        // these have no bits left): the rows concerned take offset 0 and the
+        // logits are formed anew. At the warp's first tile of the unit that is
+        // where they stand.
+        float was[NQ][2];
+        bool moves[NQ][2], settle = y < x + kPdWarps;
 #pragma unroll
         for (int n = 0; n < NQ; ++n) {
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            const float cs = qs[n][c] * k_scale;
-            const int back0 = vis[n][c] - key0 - g;  // to key 16 i + 8 e: less 16 i + 8 e
-            if (near && lut) {
-              const float* biases = out_s + (row0 + 8 * n + 2 * t + c) % p.G * lut_len;
-#pragma unroll
-              for (int i = 0; i < MT; ++i)
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-                  z[n][i][2 * e + c] = fmaf(sc[n][i][2 * e + c], cs,
-                                            biases[min(max(back0 - 16 * i - 8 * e, 0), p.t5_R)]) - off[n][c];
-            } else if (near) {
-#pragma unroll
-              for (int i = 0; i < MT; ++i)
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-                  z[n][i][2 * e + c] = fmaf(sc[n][i][2 * e + c], cs, slow[((n * 2 + c) * MT + i) * 2 + e]) - off[n][c];
-            } else if (p.mode != RELPOS_ALIBI) {
-#pragma unroll
-              for (int i = 0; i < MT; ++i)
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-                  z[n][i][2 * e + c] = fmaf(sc[n][i][2 * e + c], cs, add[n][c]) - off[n][c];
-            } else {
-              const float back_f = static_cast<float>(back0);
-#pragma unroll
-              for (int i = 0; i < MT; ++i)
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-                  z[n][i][2 * e + c] =
-                      fmaf(sc[n][i][2 * e + c], cs, fmaf(-slope[n][c], back_f - (16 * i + 8 * e), -off[n][c]));
-            }
-            if (edge) {
-#pragma unroll
-              for (int i = 0; i < MT; ++i)
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-                  if (back0 < 16 * i + 8 * e) z[n][i][2 * e + c] = -INFINITY;
-            }
+            was[n][c] = -FLT_MAX;
+            moves[n][c] = true;
           }
         }
-      };
-      // Offsets move by the logits themselves (less an offset far below them
-      // these have no bits left): the rows concerned take offset 0 and the
-      // logits are formed anew. At the warp's first tile of the unit that is
-      // where they stand.
-      float was[NQ][2];
-      bool moves[NQ][2], settle = y < x + kPdWarps;
+        auto largest = [&](int n, int c) {
+          float top = -INFINITY;
 #pragma unroll
-      for (int n = 0; n < NQ; ++n) {
+          for (int i = 0; i < MT; ++i) top = fmaxf(top, fmaxf(z[n][i][c], z[n][i][2 + c]));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+          return fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+        };
+        while (true) {
+          logits(z);
+          if (settle) break;
+          above = false;
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          was[n][c] = -FLT_MAX;
-          moves[n][c] = true;
-        }
-      }
-      auto largest = [&](int n, int c) {
-        float top = -INFINITY;
+          for (int n = 0; n < NQ; ++n)
 #pragma unroll
-        for (int i = 0; i < MT; ++i) top = fmaxf(top, fmaxf(z[n][i][c], z[n][i][2 + c]));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-        return fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-      };
-      while (true) {
-        logits(z);
-        if (settle) break;
-        above = false;
+            for (int i = 0; i < MT; ++i)
 #pragma unroll
-        for (int n = 0; n < NQ; ++n)
+              for (int e = 0; e < 4; ++e) above |= z[n][i][e] > kPdMost;
+          if (!__any_sync(0xffffffffu, above)) break;
 #pragma unroll
-          for (int i = 0; i < MT; ++i)
+          for (int n = 0; n < NQ; ++n) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) above |= z[n][i][e] > kPdMost;
-        if (!__any_sync(0xffffffffu, above)) break;
-#pragma unroll
-        for (int n = 0; n < NQ; ++n) {
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            was[n][c] = off[n][c];
-            moves[n][c] = largest(n, c) > kPdMost;
-            if (moves[n][c]) off[n][c] = 0.f;
+            for (int c = 0; c < 2; ++c) {
+              was[n][c] = off[n][c];
+              moves[n][c] = largest(n, c) > kPdMost;
+              if (moves[n][c]) off[n][c] = 0.f;
+            }
           }
+          settle = true;
         }
-        settle = true;
-      }
-      if (settle) {
+        if (settle) {
 #pragma unroll
-        for (int n = 0; n < NQ; ++n) {
+          for (int n = 0; n < NQ; ++n) {
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const float top = fmaxf(largest(n, c) - kPdShift, -FLT_MAX);  // a row may see no key
-            if (moves[n][c]) {
-              off[n][c] = top;
-              const float down = ex2_approx(was[n][c] - top);
-              l_run[n][c] *= down;
+            for (int c = 0; c < 2; ++c) {
+              const float top = fmaxf(largest(n, c) - kPdShift, -FLT_MAX);  // a row may see no key
+              if (moves[n][c]) {
+                off[n][c] = top;
+                const float down = ex2_approx(was[n][c] - top);
+                l_run[n][c] *= down;
 #pragma unroll
-              for (int i = 0; i < MT; ++i) z[n][i][c] -= top, z[n][i][2 + c] -= top;
+                for (int i = 0; i < MT; ++i) z[n][i][c] -= top, z[n][i][2 + c] -= top;
 #pragma unroll
-              for (int j = 0; j < KS; ++j) o[n][j][c] *= down, o[n][j][2 + c] *= down;
+                for (int j = 0; j < KS; ++j) o[n][j][c] *= down, o[n][j][2 + c] *= down;
+              }
             }
           }
         }
-      }
       }
 #pragma unroll
       for (int n = 0; n < NQ; ++n) {
