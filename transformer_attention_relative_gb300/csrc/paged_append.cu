@@ -103,10 +103,12 @@ __device__ __noinline__ uint32_t rotated_codes_exact(float x1, float x2, unsigne
 // heads, d = 64, e4m3: 22 us for 52 MB, 660 instructions for a warp's 32 x 16 keys
 // and values; the test for borders is 2.4 us of it, the decisions next to one 3),
 // by its chain of loads (lengths, table, rows, scales) for a token a sequence
-// (6 us). At 80 registers three blocks of 256 threads share an SM; two (128
-// registers, all heads' loads at once) took 50 us.
+// (6 us). Three blocks of 256 threads share an SM for e4m3 (80 registers): 22.2 us
+// for the prompts above, 22.6 with two (128) and 32 with four (64, which spills 152
+// bytes). 16-bit caches, with no codes to decide, go with two: 4.7 us for 4 x 1001
+// tokens of 8 heads, d = 128, against 5.8 with three and 6.1 with four.
 template <bool FP8, bool INTERLEAVED, int THREADS, int UNITS>
-__global__ void __launch_bounds__(THREADS, UNITS == 1 ? 768 / THREADS : 1)
+__global__ void __launch_bounds__(THREADS, UNITS == 1 ? (FP8 ? 768 : 512) / THREADS : 1)
     relpos_paged_append_kernel(const __grid_constant__ AppendParams p) {
   extern __shared__ float4 turn_s[];
   __shared__ int amax_s[2][kAppMaxGroup];
