@@ -488,7 +488,9 @@ int relpos_rotary_plan_init(RelposRotaryPlan* plan, int rot_dim, int layout, dou
  *               the gradient of the call with inverse = 0 (x the gradient of
  *               its output).
  *   tensors     host array of `ntensors` (1 or 2) descriptions. out may be x
- *               itself (with x's strides); otherwise nothing may overlap.
+ *               itself (with x's strides); otherwise nothing may overlap:
+ *               strides of out below d where there is more than one row are
+ *               refused (an x of broadcast rows needs an out of its own).
  *   B, L, d     batch, rows and head dimension (even, >= the plan's rot_dim);
  *               an empty size makes the call a no-op.
  *   positions   device, int32: row l of batch element b is at
@@ -596,7 +598,8 @@ int relpos_paged_append(const RelposPagedCache* cache, const RelposRotaryPlan* p
  *               relpos_attn_fwd); RELPOS_ALIBI: bias device fp32 [Hq], the
  *               slopes, -slope |offset| is added.
  *   Q, out      device, bf16 [B, Hq, Lq, d] with the given strides in elements
- *               (rows of d contiguous values; out rows 2-byte aligned).
+ *               (rows of d contiguous values, 2-byte aligned). Rows of out may
+ *               not overlap: strides below d are refused; those of Q may.
  *   Lq          0 .. 8 rows (RELPOS_ERR_UNSUPPORTED beyond).
  *   scale       softmax scale, finite; 0 takes 1 / sqrt(d).
  * Keys and values in masked or unused slots have no effect, whatever they

@@ -386,3 +386,65 @@ def test_refusals():
     assert e.value.code == rp.RELPOS_ERR_UNSUPPORTED
     with pytest.raises(rp.RelposError):
         rp.paged_decode(q[:, :3], cache, table, lens)
+
+
+def test_broadcast_queries():
+    cache, q, table, lens, _ = _case([300, 70], 4, 2, 3, 64, 64, E4, "none", 31)
+    one = q[:, :1, :1].cuda().expand(2, 4, 3, 64)
+    args = cache, table.cuda(), lens.cuda()
+    assert torch.equal(rp.paged_decode(one, *args), rp.paged_decode(one.contiguous(), *args))
+    with pytest.raises(rp.RelposError) as e:
+        rp.paged_decode(one.contiguous(), *args, out=one)
+    assert e.value.code == rp.RELPOS_ERR_INVALID_ARG
+    assert rp.check_status() == 0
+
+
+def test_calls_from_several_threads():
+    """Threads with streams and T5 parameters of their own: what calls share on the host does not mix."""
+    import threading
+
+    cache, q, table, lens, bias = _case([2000, 130, 5], 8, 2, 1, 64, 64, E4, "t5", 32)
+    qd, td, ld, bd = q.cuda(), table.cuda(), lens.cuda(), bias.cuda()
+    shapes = [(32, 128), (32, 500), (16, 64), (8, 20), (24, 1000), (30, 77), (4, 9), (32, 33), (12, 300), (28, 128)]
+    run = lambda nb, md: rp.paged_decode(qd, cache, td, ld, bias=bd[:nb], mode=rp.MODE_T5, num_buckets=nb,  # noqa: E731
+                                         max_distance=md)
+    want = [run(*s) for s in shapes]
+    torch.cuda.synchronize()
+    same = []
+
+    def work(k):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            got = [(i, run(*shapes[i])) for i in ((k + 3 * j) % len(shapes) for j in range(60))]
+            torch.cuda.current_stream().synchronize()
+            same.extend(torch.equal(o, want[i]) for i, o in got)
+
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert len(same) == 4 * 60 and all(same) and rp.check_status() == 0
+
+
+def test_graphs_replayed_at_once():
+    """Two graphs, each with calls that need scratch, on two streams at the same time."""
+    cases = [_case([3000, 700, 1], 8, 2, 1, 64, 64, E4, "none", 33), _case([2600, 900], 8, 2, 2, 128, 64, BF, "none", 34)]
+    graphs, outs, want, inputs = [], [], [], []
+    for cache, q, table, lens, _ in cases:
+        args = q.cuda(), cache, table.cuda(), lens.cuda()
+        inputs.append(args)
+        want.append(rp.paged_decode(*args))
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append([rp.paged_decode(*args) for _ in range(4)])
+        graphs.append(g)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(15):
+        for s, g in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for w, os in zip(want, outs):
+        assert all(torch.equal(w, o) for o in os)
+    assert rp.check_status() == 0

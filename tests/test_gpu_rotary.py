@@ -212,3 +212,13 @@ def test_refusals():
             call()
     with pytest.raises(rp.RelposError):
         rp.rotary(q, rp.RotaryPlan(128))
+
+
+def test_broadcast_rows():
+    """One row for every head and position: read as it lies, never written over."""
+    plan = rp.RotaryPlan(64)
+    x = torch.randn(2, 1, 1, 64, device="cuda").to(torch.bfloat16).expand(2, 3, 9, 64)
+    assert torch.equal(rp.rotary(x, plan), rp.rotary(x.contiguous(), plan))
+    with pytest.raises(rp.RelposError) as e:
+        rp.rotary(x, plan, out=x)
+    assert e.value.code == rp.RELPOS_ERR_INVALID_ARG

@@ -178,3 +178,19 @@ def test_python_refuses_host_tensors_and_wrong_types():
         rp.PagedCache(q, q)
     with pytest.raises(TypeError):
         rp.PagedCache(q, q, torch.ones(2, 2).double(), torch.ones(2, 2))
+
+
+@pytest.mark.parametrize("B,H,L,strides", [
+    (2, 1, 1, (0, 64, 64)), (1, 2, 1, (64, 0, 64)), (1, 1, 2, (64, 64, 0)), (1, 1, 2, (64, 64, 63)), (1, 2, 1, (64, -63, 64)),
+])
+def test_outputs_whose_rows_overlap(B, H, L, strides):
+    """An expanded tensor as the output: blocks would write one row at a time of several."""
+    t = (rp._RotaryTensor * 1)()
+    t[0].x, t[0].out, t[0].H = 16, 32, H
+    t[0].x_batch = t[0].x_head = t[0].x_row = 64
+    t[0].out_batch, t[0].out_head, t[0].out_row = strides
+    assert rp.relpos_rotary(rp.RotaryPlan(64)._ref, 0, 0, t, 1, B, L, 64, None, 0, 0, None) == BAD
+    c = _cache(H=1)
+    q, o = rp._RowStrides(0, 0, 0), rp._RowStrides(*strides)
+    assert rp.relpos_paged_decode(ctypes.byref(c), v(16), ctypes.byref(q), B, H, L, v(16), 4, 4, v(16), -1, None, 32,
+                                  128, 0.0, v(64), ctypes.byref(o), None) == BAD

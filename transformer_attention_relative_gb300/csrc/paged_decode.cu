@@ -126,6 +126,8 @@ extern "C" int relpos_paged_decode(const RelposPagedCache* cache, const void* Q,
                          reinterpret_cast<uintptr_t>(bias);
   if (!Q || !out || !lens || !block_table || (ints & 3u)) return RELPOS_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(Q) | reinterpret_cast<uintptr_t>(out)) & 1u) return RELPOS_ERR_INVALID_ARG;
+  if (rows_overlap(B, os->batch, cache->d) || rows_overlap(Hq, os->head, cache->d) || rows_overlap(Lq, os->row, cache->d))
+    return RELPOS_ERR_INVALID_ARG;
   if (bias_mode != RELPOS_NO_BIAS && !bias) return RELPOS_ERR_INVALID_ARG;
   if (max_pages == 0 || cache->num_pages == 0) return RELPOS_ERR_INVALID_ARG;
   if (B > 1 && table_stride < max_pages) return RELPOS_ERR_INVALID_ARG;

@@ -202,6 +202,10 @@ extern "C" int relpos_rotary(const RelposRotaryPlan* plan, int dtype, int invers
   p.sign = inverse ? -1.f : 1.f;
   const long long n = static_cast<long long>(B) * L * p.units;
   if (n > 0x7fffffffll) return RELPOS_ERR_UNSUPPORTED;
+  for (int i = 0; i < ntensors; ++i)
+    if (tensors[i].H > 0 && (rows_overlap(B, tensors[i].out_batch, d) || rows_overlap(L, tensors[i].out_row, d) ||
+                             rows_overlap(tensors[i].H, tensors[i].out_head, d)))
+      return RELPOS_ERR_INVALID_ARG;
   p.n = static_cast<unsigned>(n);
   const int sms = device_sms();
   if (sms <= 0) return RELPOS_ERR_CUDA;

@@ -11,6 +11,9 @@ namespace relpos {
 int* device_status();
 int device_sms();
 
+// whether two of n rows of d values, `stride` apart, share values
+inline bool rows_overlap(int n, long long stride, int d) { return n > 1 && stride < d && stride > -d; }
+
 // checks of a paged cache's sizes, types and pointers; a RELPOS_* code
 int check_paged_cache(const RelposPagedCache* cache);
 
