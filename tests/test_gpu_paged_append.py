@@ -179,6 +179,35 @@ def test_odd_values():
         _same(cache, want)
 
 
+@pytest.mark.parametrize("old", [0, 40])
+def test_infinities_that_are_turned(old):
+    """From position 0 on, where a rotation changes nothing, and further out: they saturate, beside their partners'
+    NaN where the formula has one."""
+    H, d, page = 2, 64, 32
+    cache, kv, table, cu, lens = _case([5], [old], H, d, page, E4, 41)
+    kv[0, 0, 3], kv[0, 0, 40], kv[2, 0, 9] = float("inf"), float("-inf"), float("-inf")
+    want = _expect(_snapshot(cache), kv, table, cu, lens, page, H, 64)
+    rp.paged_append(cache, kv.cuda()[:, :H], kv.cuda()[:, H:], table.cuda(), lens.cuda(), cu_new=cu.cuda(),
+                    plan=rp.RotaryPlan(64))
+    assert rp.check_status() == 0
+    _same(cache, want)
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+def test_many_open_codes(layout):
+    """Infinities leave the codes of their pairs open, thousands of them here; the heads beside theirs keep their own."""
+    H, d, page, n = 16, 64, 64, 500
+    cache, kv, table, cu, lens = _case([n] * 8, [33 * b for b in range(8)], H, d, page, E4, 42)
+    kv[600:700, 5] = float("inf")
+    kv[640, 5, ::3] = float("-inf")
+    kv[650:660, 6, 4:20] = float("-inf")
+    want = _expect(_snapshot(cache), kv, table, cu, lens, page, H, 64, layout)
+    rp.paged_append(cache, kv.cuda()[:, :H], kv.cuda()[:, H:], table.cuda(), lens.cuda(), cu_new=cu.cuda(),
+                    plan=rp.RotaryPlan(64, layout=layout))
+    assert rp.check_status() == 0
+    _same(cache, want)
+
+
 def test_bad_pages_and_lengths_are_skipped_and_reported():
     """The kernel's own checks of page numbers, lengths and row ranges: nothing
     is written, the status says so once, good sequences are served."""

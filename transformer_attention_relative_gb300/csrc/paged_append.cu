@@ -18,6 +18,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -340,9 +341,11 @@ __global__ void __launch_bounds__(THREADS, UNITS == 1 ? (FP8 ? 768 : 512) / THRE
         // The fp32 rotation is off by less than 2^-22 (|a| + |q|): sine and
         // cosine by 2^-23, two products and a sum by 2^-24 each; by twice that
         // times the amplitude where there is one; by nothing at position 0,
-        // where many values do lie on a border.
-        const float slack =
-            ik * (amplitude != 1.f ? 4.76837158e-07f * amplitude : page0 + slot ? 2.38418579e-07f : 0.f);
+        // where many values do lie on a border (but 0 times an infinity would
+        // be NaN: a head that has one leaves all but its zeros open there).
+        const float slack = amplitude != 1.f ? ik * 4.76837158e-07f * amplitude
+                            : page0 + slot   ? ik * 2.38418579e-07f
+                                             : amax_s[0][h] < 0x7f80 ? 0.f : FLT_MAX;
         uint32_t doubt = 0;  // pairs whose codes the fp32 rotation leaves open
         if (turns) {
           uint32_t code[8];  // of pair m: first member's code, second's in the next byte
