@@ -163,6 +163,47 @@ def test_codes_next_to_borders():
     _same(cache, want)
 
 
+def _pairs_next_to_borders(second):
+    """(position, frequency, first member) of pairs with this second member whose y1 lies within the fp32 rotation's
+    error 2^-22 (|x1| + |x2|) of a border between codes, but not within 2^-36 of it: the oracle's angles, of up to
+    4096 in 64 bits, are off by 2^-40."""
+    w, _ = so.rotary_frequencies(64)
+    pos = np.arange(1, 4096, dtype=np.float64)
+    found = []
+    for m in range(32):
+        c, s = np.cos(pos * w[m]), np.sin(pos * w[m])
+        for x1 in 1.0 + np.arange(128) / 128.0:
+            y = np.abs(x1 * c - second * s) / so.e4m3_scale(max(x1, second) * 2.0 ** 0.5)
+            step = np.ldexp(1.0, np.maximum(np.frexp(y)[1] - 1, -6) - 3)
+            gap = np.abs(y / step - np.floor(y / step) - 0.5) * step * so.e4m3_scale(max(x1, second) * 2.0 ** 0.5)
+            size = x1 + second
+            found += [(int(pos[i]), m, x1) for i in np.nonzero((gap < 2.0 ** -22 * size) & (gap > 2.0 ** -36 * size))[0]]
+    return found
+
+
+@pytest.mark.parametrize("second", [0.0, 1.0])
+def test_pairs_next_to_borders(second):
+    """Keys made of the pairs that the fp32 rotation cannot decide."""
+    found = _pairs_next_to_borders(second)
+    assert len(found) > 40
+    B, page = len(found), 32
+    cache = rp.PagedCache.empty(B, 1, 64, page_size=page, dtype=E4)
+    cache.k_scale.fill_(2.0 ** -40)
+    cache.v_scale.fill_(2.0 ** -40)
+    table = torch.full((B, 4096 // page), -1, dtype=torch.int32)
+    kv = torch.zeros(B, 2, 64)
+    for b, (pos, m, x1) in enumerate(found):
+        table[b, pos // page] = b
+        kv[b, 0, m], kv[b, 0, 32 + m] = x1, second
+    kv = kv.to(BF)
+    cu, lens = torch.arange(B + 1, dtype=torch.int32), torch.tensor([f[0] + 1 for f in found], dtype=torch.int32)
+    want = _expect(_snapshot(cache), kv, table, cu, lens, page, 1, 64)
+    rp.paged_append(cache, kv.cuda()[:, :1], kv.cuda()[:, 1:], table.cuda(), lens.cuda(), cu_new=cu.cuda(),
+                    plan=rp.RotaryPlan(64))
+    assert rp.check_status() == 0
+    _same(cache, want)
+
+
 def test_odd_values():
     """Zeros, the smallest and largest magnitudes, infinities and NaN."""
     H, d, page = 1, 64, 32

@@ -68,27 +68,98 @@ RP_DEVI uint32_t e4m3x2(float lo, float hi) {
   return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
 }
 
-// A value in 64 bits to its e4m3 code: rounded to fp32 with the last bit made
-// odd where that dropped anything, so that the second rounding sees on which
-// side of a border the value lies.
-RP_DEVI uint32_t e4m3_of(double v) {
-  float f = __double2float_rz(v);
-  if (static_cast<double>(f) != v) f = __int_as_float(__float_as_int(f) | 1);
-  return e4m3x2(f, 0.f) & 0xffu;
+// Sine and cosine of `turn` 2^-64ths of a turn in units of 2^-62, off by at most 4
+// of them: the Taylor series of the distance to the nearest quarter turn (at most
+// pi / 4; the first terms left out are below 2^-63), in units of 2^-64.
+RP_DEVI void sincos_fixed(unsigned long long turn, long long& s, long long& c) {
+  const unsigned quarter = static_cast<unsigned>((turn + (1ull << 61)) >> 62);
+  const long long rest = static_cast<long long>(turn - (static_cast<unsigned long long>(quarter) << 62));
+  const unsigned long long far = rest < 0 ? -static_cast<unsigned long long>(rest) : rest;
+  const unsigned long long x = __umul64hi(far << 2, 0xc90fdaa22168c234ull) << 1;  // times pi / 4 in 2^-64
+  const unsigned long long z = __umul64hi(x, x);
+  // 1 / 3! - z / 5! + ... - z^7 / 17! and 1 / 4! - z / 6! + ... - z^7 / 18!
+  constexpr unsigned long long kSin[8] = {0x2aaaaaaaaaaaaaabull, 0x222222222222222ull, 0xd00d00d00d00dull, 0x2e3bc74aad8eull,
+                                          0x6b99159fd5ull, 0xb092309dull, 0xd73f9full, 0xca96ull};
+  constexpr unsigned long long kCos[8] = {0xaaaaaaaaaaaaaabull, 0x5b05b05b05b05bull, 0x1a01a01a01a02ull, 0x49f93edde28ull,
+                                          0x8f76c77fcull, 0xc9cba54ull, 0xd73faull, 0xb41ull};
+  unsigned long long p = kSin[7], q = kCos[7];
+#pragma unroll
+  for (int i = 6; i >= 0; --i) {
+    p = kSin[i] - __umul64hi(z, p);
+    q = kCos[i] - __umul64hi(z, q);
+  }
+  s = static_cast<long long>((x - __umul64hi(__umul64hi(z, x), p)) >> 2);
+  c = static_cast<long long>((1ull << 62) - (z >> 3) + (__umul64hi(__umul64hi(z, z), q) >> 2));
+  if (rest < 0) s = -s;
+  if (quarter & 1) {
+    const long long was = s;
+    s = c;
+    c = -was;
+  }
+  if (quarter & 2) s = -s, c = -c;
 }
 
-// The pair's codes from the rotation in 64 bits (y1's in the low byte). Taken
-// where the fp32 rotation cannot tell on which side of a border of the e4m3
-// grid its result lies, about once in 10^5 values.
+// m 2^e, as u with the top bit set times 2^e
+struct Scaled {
+  unsigned long long u;
+  int e;
+  RP_DEVI void normalize() {
+    const int n = __clzll(u) & 63;
+    u <<= n, e -= n;
+  }
+  RP_DEVI void times(unsigned long long by, int by_e) {  // `by` with its top bit set too
+    u = __umul64hi(u, by), e += by_e + 64;
+    normalize();
+  }
+};
+
+// The pair's codes from the rotation in 64-bit integers (y1's in the low byte).
+// Taken where the fp32 rotation cannot tell on which side of a border of the e4m3
+// grid its result lies, about once in 10^5 values. Each product of an 8-bit
+// mantissa and a sine or cosine of 2^-54 is exact; their sum is scaled and cut to
+// 24 bits, the last made odd where that dropped anything, so that the rounding to
+// a code sees on which side of a border the value lies. Fixed point since 64-bit
+// floating point is slow here: a token's step took 6.2 us with it against 5.5,
+// prompts 21.6 against 20.3.
 __device__ __noinline__ uint32_t rotated_codes_exact(float x1, float x2, unsigned long long turns, int pos,
                                                      double amplitude, float inv) {
-  const long long t =
-      static_cast<long long>(turns * static_cast<unsigned long long>(static_cast<long long>(pos)));
-  double s, c;
-  sincospi(static_cast<double>(t) * 1.0842021724855044e-19, &s, &c);  // t / 2^63 half turns
-  const double a = amplitude * inv;
-  const double u = x1, v = x2;
-  return e4m3_of((u * c - v * s) * a) | (e4m3_of((u * s + v * c) * a) << 8);
+  long long s, c;
+  sincos_fixed(turns * static_cast<unsigned long long>(static_cast<long long>(pos)), s, c);
+  const uint32_t b1 = __float_as_uint(x1), b2 = __float_as_uint(x2);
+  const int f1 = b1 >> 23 & 255, f2 = b2 >> 23 & 255;
+  const int e1 = max(f1, 1), e2 = max(f2, 1), top = max(e1, e2);
+  long long m1 = (b1 >> 16 & 127) | (f1 ? 128 : 0), m2 = (b2 >> 16 & 127) | (f2 ? 128 : 0);
+  if (b1 >> 31) m1 = -m1;
+  if (b2 >> 31) m2 = -m2;
+  const int d1 = min(top - e1, 63), d2 = min(top - e2, 63);
+  s >>= 8, c >>= 8;
+  const long long y[2] = {(m1 * c >> d1) - (m2 * s >> d2), (m1 * s >> d1) + (m2 * c >> d2)};
+  const unsigned long long amp = __double_as_longlong(amplitude);
+  const uint32_t inv_bits = __float_as_uint(inv);
+  Scaled by = {inv_bits & 0x7fffffu, max(static_cast<int>(inv_bits >> 23), 1) - 150};
+  if (inv_bits >> 23) by.u |= 1u << 23;
+  const bool plain = f1 < 255 && f2 < 255 && by.u != 0;
+  by.normalize();
+  const float sf = static_cast<float>(s) * 0x1p-54f, cf = static_cast<float>(c) * 0x1p-54f;
+  uint32_t code = 0;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    float f;
+    if (plain && y[i] != 0) {
+      Scaled v = {static_cast<unsigned long long>(y[i] < 0 ? -y[i] : y[i]), top - 134 - 54};
+      v.normalize();
+      v.times(amp << 11 | 1ull << 63, static_cast<int>(amp >> 52) - 1023 - 63);
+      v.times(by.u, by.e);
+      const uint32_t cut = static_cast<uint32_t>(v.u >> 40) | ((v.u & ((1ull << 40) - 1)) != 0);
+      // what is below half of the smallest code may be so by more or less
+      f = static_cast<float>(cut) * __int_as_float((min(max(v.e + 40, -120), 100) + 127) << 23);
+      if (y[i] < 0) f = -f;
+    } else {  // zeros, infinities and NaN
+      f = (i ? fmaf(x1, sf, x2 * cf) : fmaf(x1, cf, x2 * -sf)) * inv;
+    }
+    code |= (e4m3x2(f, 0.f) & 0xffu) << 8 * i;
+  }
+  return code;
 }
 
 // A block takes one page that gets new tokens and `group` heads of it. Its
@@ -101,12 +172,12 @@ __device__ __noinline__ uint32_t rotated_codes_exact(float x1, float x2, unsigne
 // two sines, then the two cosines, of pairs 2 j and 2 j + 1 of a unit in plane j.
 //
 // Bounded by instruction issue where there is much to write (8531 tokens of 16
-// heads, d = 64, e4m3: 22 us for 52 MB, 660 instructions for a warp's 32 x 16 keys
-// and values; the test for borders is 2.4 us of it, the decisions next to one 3),
+// heads, d = 64, e4m3: 20.3 us for 52 MB; the test for borders is 1 us of it, the
+// decisions next to one 2.4),
 // by its chain of loads (lengths, table, rows, scales) for a token a sequence
-// (6 us). Three blocks of 256 threads share an SM for e4m3 (80 registers): 22.2 us
-// for the prompts above, 22.6 with two (128) and 32 with four (64, which spills 152
-// bytes). 16-bit caches, with no codes to decide, go with two: 4.7 us for 4 x 1001
+// (5.5 us). Three blocks of 256 threads share an SM for e4m3 (80 registers); with
+// the 64-bit decisions still in floating point the prompts above took 22.2 us so,
+// 22.6 with two (128) and 32 with four (64, which spills 152 bytes). 16-bit caches, with no codes to decide, go with two: 4.7 us for 4 x 1001
 // tokens of 8 heads, d = 128, against 5.8 with three and 6.1 with four.
 template <bool FP8, bool INTERLEAVED, int THREADS, int UNITS>
 __global__ void __launch_bounds__(THREADS, UNITS == 1 ? (FP8 ? 768 : 512) / THREADS : 1)
