@@ -172,13 +172,15 @@ __device__ __noinline__ uint32_t rotated_codes_exact(float x1, float x2, unsigne
 // two sines, then the two cosines, of pairs 2 j and 2 j + 1 of a unit in plane j.
 //
 // Bounded by instruction issue where there is much to write (8531 tokens of 16
-// heads, d = 64, e4m3: 20.3 us for 52 MB; the test for borders is 1 us of it, the
-// decisions next to one 2.4),
+// heads, d = 64, e4m3: 20.3 us for 52 MB, 650 instructions for a warp's 32 x 16 keys
+// and values; the test for borders is 1 us of it, the decisions next to one 2.4),
 // by its chain of loads (lengths, table, rows, scales) for a token a sequence
-// (5.5 us). Three blocks of 256 threads share an SM for e4m3 (80 registers); with
-// the 64-bit decisions still in floating point the prompts above took 22.2 us so,
-// 22.6 with two (128) and 32 with four (64, which spills 152 bytes). 16-bit caches, with no codes to decide, go with two: 4.7 us for 4 x 1001
-// tokens of 8 heads, d = 128, against 5.8 with three and 6.1 with four.
+// (5.4 us). Decisions noted down and taken together at the block's end: 0.2 us
+// less for the prompts, 0.4 more for a token. Three blocks of 256 threads share an
+// SM for e4m3 (80 registers); with the decisions still in floating point the
+// prompts took 22.2 us so, 22.6 with two (128) and 32 with four (64, which spills
+// 152 bytes). 16-bit caches, with no codes to decide, go with two: 4.7 us for
+// 4 x 1001 tokens of 8 heads, d = 128, against 5.8 with three and 6.1 with four.
 template <bool FP8, bool INTERLEAVED, int THREADS, int UNITS>
 __global__ void __launch_bounds__(THREADS, UNITS == 1 ? (FP8 ? 768 : 512) / THREADS : 1)
     relpos_paged_append_kernel(const __grid_constant__ AppendParams p) {
