@@ -49,6 +49,18 @@ constexpr int kPdBuckets = 256;
 // of the offset's logit and vanish below 2^-29.
 constexpr float kPdShift = 5.f, kPdMost = 13.f;
 
+// 8-bit values: the output is kept in units of v_unit, a power of two near the
+// scales of the pages, and the weights of a page take its scale's ratio to it.
+// Where a page's ratio is outside [kPdRatioLow, kPdRatioHigh] the unit moves to
+// its scale, but only between these bounds: a page may have any scale (zero
+// values 2^-120, an infinite one 2^120), and sums of weights (2^13), codes (448)
+// and ratios over 2^28 keys, 2^53, stay finite when they move from the upper
+// bound's unit to the lower one's. Pages of smaller scale add their products
+// with the ratio in fp32, and so do all tiles from a page of larger scale on, in
+// units of twice the upper bound.
+constexpr float kPdRatioLow = 0.015625f, kPdRatioHigh = 4.f;
+constexpr float kPdUnitLow = 0x1p-32f, kPdUnitHigh = 0x1p32f;
+
 struct PagedDecodeParams {
   const uint8_t* k;
   const uint8_t* v;
@@ -314,6 +326,9 @@ RP_DEVI void for_each(std::integer_sequence<int, I...>, F&& f) {
   (f(std::integral_constant<int, I>{}), ...);
 }
 
+// 1 / x for a normal power of two
+RP_DEVI float inverse_pow2(float x) { return __uint_as_float(0x7f000000u - __float_as_uint(x)); }
+
 // log2 units, a finite value staying finite (a table may hold the type's lowest)
 RP_DEVI float to_log2(float x) {
   return fabsf(x) <= FLT_MAX ? fminf(fmaxf(x * kLog2e, -FLT_MAX), FLT_MAX) : x;
@@ -555,9 +570,7 @@ __global__ void __launch_bounds__(kPdThreads, NQ * D <= 64 ? 4 : NQ * D <= 128 ?
 #pragma unroll
     for (int n = 0; n < NQ; ++n) odd |= !(fabsf(add[n][0]) <= 4096.f && fabsf(add[n][1]) <= 4096.f);
     odd = __any_sync(0xffffffffu, odd);
-    // 8 bits: the output is kept in units of v_unit, a page's scale, and the
-    // weights of a page with another scale take the ratio
-    [[maybe_unused]] float v_unit = 0.f, v_inv = 0.f;
+    [[maybe_unused]] float v_inv = 0.f;  // 1 / v_unit, 0 before the first tile
     float off[NQ][2], l_run[NQ][2], o[NQ][KS][4];
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
@@ -606,24 +619,27 @@ __global__ void __launch_bounds__(kPdThreads, NQ * D <= 64 ? 4 : NQ * D <= 128 ?
       }
       float k_scale = 1.f;
       [[maybe_unused]] float ratio = 1.f;
+      [[maybe_unused]] auto outside = [&] { return !(fabsf(ratio) >= kPdRatioLow && fabsf(ratio) <= kPdRatioHigh); };
       if constexpr (FP8) {
         k_scale = lds32f(vs + S::kTileBytes);
         const float v_scale = lds32f(vs + S::kTileBytes + 4);
         ratio = v_scale * v_inv;
-        // another unit where the ratio would cost the weights bits, or where
-        // there is none yet (zero, infinity and NaN go through the ratio)
-        const float size = fabsf(v_scale);
-        if (!(fabsf(ratio) >= 0.015625f && fabsf(ratio) <= 4.f) && size >= FLT_MIN && size <= 1.f / FLT_MIN) {
-          const float down = v_unit / size;
+        if (outside()) {  // NaN too
+          const float size = fabsf(v_scale), v_unit = v_inv == 0.f ? 0.f : inverse_pow2(v_inv);
+          const float unit = size > kPdUnitHigh   ? 2.f * kPdUnitHigh
+                             : size >= kPdUnitLow ? __uint_as_float(__float_as_uint(size) & 0x7f800000u)
+                                                  : fmaxf(v_unit, kPdUnitLow);
+          if (v_unit <= kPdUnitHigh && unit != v_unit) {
+            v_inv = inverse_pow2(unit);
+            const float down = v_unit * v_inv;
 #pragma unroll
-          for (int n = 0; n < NQ; ++n)
+            for (int n = 0; n < NQ; ++n)
 #pragma unroll
-            for (int j = 0; j < KS; ++j)
+              for (int j = 0; j < KS; ++j)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) o[n][j][e] *= down;
-          v_unit = size;
-          v_inv = 1.f / size;
-          ratio = v_scale * v_inv;
+                for (int e = 0; e < 4; ++e) o[n][j][e] *= down;
+            ratio = v_scale * v_inv;
+          }
         }
       }
       const bool edge = key0 + KT - 1 > vis_first;  // some row does not see every key
@@ -786,15 +802,16 @@ __global__ void __launch_bounds__(kPdThreads, NQ * D <= 64 ? 4 : NQ * D <= 128 ?
         }
       }
 
-      // o^T += v^T p^T, for the rows and the keys of one query position (ONE)
-      // or all
-      auto add_values = [&](auto one, int last) {
-        constexpr bool ONE = decltype(one)::value;
+      // o^T += v^T p^T. SLOW: each product by itself, times the page's ratio,
+      // for the rows and the keys of one query position or (`all`) of every one.
+      auto add_values = [&](auto slow_path, int last, bool all) {
+        constexpr bool SLOW = decltype(slow_path)::value;
+        [[maybe_unused]] const float factor = SLOW ? 1.f : ratio;
         uint32_t ph[NQ][MT][2];
         [[maybe_unused]] uint32_t pl[FP8 ? 1 : NQ][MT][2];
 #pragma unroll
         for (int n = 0; n < NQ; ++n) {
-          const bool mine[2] = {!ONE || vis[n][0] == last, !ONE || vis[n][1] == last};
+          const bool mine[2] = {!SLOW || all || vis[n][0] == last, !SLOW || all || vis[n][1] == last};
 #pragma unroll
           for (int i = 0; i < MT; ++i) {
 #pragma unroll
@@ -803,7 +820,7 @@ __global__ void __launch_bounds__(kPdThreads, NQ * D <= 64 ? 4 : NQ * D <= 128 ?
               if constexpr (FP8) {
                 // 11 bits of a weight: its rounding (2^-12) is far below the
                 // output's (2^-9)
-                ph[n][i][e] = transpose8(pack_half2(a * ratio, c * ratio));
+                ph[n][i][e] = transpose8(pack_half2(a * factor, c * factor));
               } else {
                 // bf16 alone would round the weights as coarsely as the
                 // output: a second part carries the next 8 bits
@@ -825,7 +842,7 @@ __global__ void __launch_bounds__(kPdThreads, NQ * D <= 64 ? 4 : NQ * D <= 128 ?
             const uint4 u = lds128(a);
             w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
           }
-          if (ONE && key0 + 16 * i + 8 * e + 2 * t + oo > last) w[0] = w[1] = w[2] = w[3] = 0;
+          if (SLOW && !all && key0 + 16 * i + 8 * e + 2 * t + oo > last) w[0] = w[1] = w[2] = w[3] = 0;
         };
         if constexpr (FP8) {
 #pragma unroll
@@ -845,11 +862,17 @@ __global__ void __launch_bounds__(kPdThreads, NQ * D <= 64 ? 4 : NQ * D <= 128 ?
 #pragma unroll
                 for (int n = 0; n < NQ; ++n) {
                   float(&d)[4] = o[n][2 * w + j];
-                  const float was[4] = {d[0], d[1], d[2], d[3]};
-                  mma16816<true>(d, f, ph[n][i][0], ph[n][i][1]);
-                  if (ONE) {
+                  if constexpr (SLOW) {
+                    float y[4] = {0.f, 0.f, 0.f, 0.f};
+                    mma16816<true>(y, f, ph[n][i][0], ph[n][i][1]);
+                    // d = 128: the ratio anew, since held through the loop it
+                    // makes 8 rows' variant spill (3 % longer)
+                    auto times = [&] { return D == 128 && NQ == 1 ? lds32f(vs + S::kTileBytes + 4) * v_inv : ratio; };
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) d[e] = vis[n][e & 1] == last ? d[e] : was[e];
+                    for (int e = 0; e < 4; ++e)
+                      if (all || vis[n][e & 1] == last) d[e] = fmaf(y[e], times(), d[e]);
+                  } else {
+                    mma16816<true>(d, f, ph[n][i][0], ph[n][i][1]);
                   }
                 }
               }
@@ -876,7 +899,7 @@ __global__ void __launch_bounds__(kPdThreads, NQ * D <= 64 ? 4 : NQ * D <= 128 ?
                   const float was[4] = {d[0], d[1], d[2], d[3]};
                   mma16816<false>(d, f, ph[n][i][0], ph[n][i][1]);
                   mma16816<false>(d, f, pl[n][i][0], pl[n][i][1]);
-                  if (ONE) {
+                  if (SLOW) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) d[e] = vis[n][e & 1] == last ? d[e] : was[e];
                   }
@@ -905,10 +928,11 @@ __global__ void __launch_bounds__(kPdThreads, NQ * D <= 64 ? 4 : NQ * D <= 128 ?
         }
         foul = __any_sync(0xffffffffu, foul);
       }
-      if (foul) {
-        for (int i = 0; i < p.Lq; ++i) add_values(std::true_type{}, len - p.Lq + i);
+      if (foul || (FP8 && outside())) {
+#pragma unroll 1
+        for (int i = foul ? 0 : p.Lq - 1; i < p.Lq; ++i) add_values(std::true_type{}, len - p.Lq + i, !foul);
       } else {
-        add_values(std::false_type{}, 0);
+        add_values(std::false_type{}, 0, true);
       }
     }
 
@@ -939,7 +963,7 @@ __global__ void __launch_bounds__(kPdThreads, NQ * D <= 64 ? 4 : NQ * D <= 128 ?
         float top = -FLT_MAX;
 #pragma unroll
         for (int w = 0; w < kPdWarps; ++w) top = fmaxf(top, ml[w * S::kRows].x);
-        const float down = ex2_approx(off[n][c] - top) * (FP8 ? v_unit : 1.f);
+        const float down = ex2_approx(off[n][c] - top) * (FP8 && v_inv != 0.f ? inverse_pow2(v_inv) : 1.f);
 #pragma unroll
         for (int j = 0; j < KS; ++j) o[n][j][c] *= down, o[n][j][2 + c] *= down;
       }
