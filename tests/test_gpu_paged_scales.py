@@ -123,9 +123,38 @@ def test_scales_over_their_whole_range(d, order):
 def test_scales_at_the_ends_of_fp32(exponent):
     """A cache from elsewhere: very large scales, and subnormal ones, on every page."""
     g = torch.Generator().manual_seed(8)
-    codes = (torch.randn(2, 3, 1, 32, 64, generator=g) * torch.tensor([1.0, 64.0])[:, None, None, None, None]).clamp(-448, 448).to(E4)
+    codes = torch.randn(2, 3, 1, 32, 64, generator=g)
+    codes[1] *= 64.0
+    codes = codes.clamp(-448, 448).to(E4)
     scale = torch.full((3, 1), 2.0 ** exponent, dtype=torch.float64).float()
     cache = rp.PagedCache(codes[0].cuda(), codes[1].cuda(), torch.ones(3, 1).cuda(), scale.cuda())
     q = torch.randn(1, 1, 1, 64, generator=g).to(BF)
     table = torch.tensor([[2, 0, 1]], dtype=torch.int32)
     _check(cache, q, table, [90], _decode(cache, table, [90], q))
+
+
+@pytest.mark.parametrize("factor", [64.0, 32.0, 4.0])
+@pytest.mark.parametrize("d", [64, 128])
+def test_weak_keys_behind_a_page_of_larger_scale(d, factor):
+    """The first page has a larger value scale and holds, in each of its four tiles, a key that dominates the softmax
+    and has zero values; the output is the sum over the equal weak keys of the other pages, 2^-17.9 of the largest
+    weight each (8.25 x 12 / 8 nats). Each warp meets the first page before them."""
+    g = torch.Generator().manual_seed(9)
+    pages, page = 4, 128
+    k = torch.zeros(pages, 1, page, d)
+    k[0, 0, ::32, 0] = 12.0
+    v = torch.randn(pages, 1, page, d, generator=g).abs() * 64.0
+    v[0] = 0.0
+    scale = torch.full((pages, 1), 2.0 ** -6)
+    scale[0] *= factor
+    cache = rp.PagedCache(k.to(E4).cuda(), v.clamp(0, 448).to(E4).cuda(), torch.ones(pages, 1).cuda(), scale.cuda())
+    q = torch.zeros(1, 1, 1, d)
+    q[..., 0] = 8.25
+    table = torch.arange(pages, dtype=torch.int32)[None]
+    lens = torch.tensor([pages * page], dtype=torch.int32)
+    got = rp.paged_decode(q.to(BF).cuda(), cache, table.cuda(), lens.cuda(), scale=0.125)
+    assert rp.check_status() == 0
+    c = {n: getattr(cache, n).double().cpu().numpy() for n in ("k", "v", "k_scale", "v_scale")}
+    ref, size = so.paged_decode(q.double().numpy(), c, table.numpy(), [pages * page], page, scale=0.125)
+    bad = np.abs(got.double().cpu().numpy() - ref) / (2.0 ** -8 * ref + size * (2.0 ** -11 + 2.0 ** -12))
+    assert bad.max() <= 1.0, float(bad.max())

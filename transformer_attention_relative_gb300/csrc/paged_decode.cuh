@@ -44,9 +44,10 @@ constexpr int kPdBuckets = 256;
 // The weights p are kept as 2^(logit - off) for a row offset `off` that starts
 // below every logit and moves up only when a logit comes more than kPdMost above
 // it, to kPdShift below the largest: most tiles then need no maximum across the
-// warp and no rescaling. Weights stay below 2^13, so that fp16 ones (8-bit
-// caches, up to 4 times larger by their page's scale) keep 11 bits down to 2^-19
-// of the offset's logit and vanish below 2^-29.
+// warp and no rescaling. Weights stay below 2^13, and fp16 ones (8-bit caches)
+// take a factor between 1/2 and 4 with their page's scale: they keep 11 bits
+// down to 2^-18 of a row's largest weight, 2^5 or more, and below that are off by
+// 2^-29 of it at most: n keys together by n 2^-29 (2^-12 of it for 131072).
 constexpr float kPdShift = 5.f, kPdMost = 13.f;
 
 // 8-bit values: the output is kept in units of v_unit, a power of two near the
@@ -58,7 +59,7 @@ constexpr float kPdShift = 5.f, kPdMost = 13.f;
 // bound's unit to the lower one's. Pages of smaller scale add their products
 // with the ratio in fp32, and so do all tiles from a page of larger scale on, in
 // units of twice the upper bound.
-constexpr float kPdRatioLow = 0.015625f, kPdRatioHigh = 4.f;
+constexpr float kPdRatioLow = 0.5f, kPdRatioHigh = 4.f;
 constexpr float kPdUnitLow = 0x1p-32f, kPdUnitHigh = 0x1p32f;
 
 struct PagedDecodeParams {
