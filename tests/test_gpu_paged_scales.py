@@ -158,3 +158,27 @@ def test_weak_keys_behind_a_page_of_larger_scale(d, factor):
     ref, size = so.paged_decode(q.double().numpy(), c, table.numpy(), [pages * page], page, scale=0.125)
     bad = np.abs(got.double().cpu().numpy() - ref) / (2.0 ** -8 * ref + size * (2.0 ** -11 + 2.0 ** -12))
     assert bad.max() <= 1.0, float(bad.max())
+
+
+@pytest.mark.parametrize("rows", [1, 3])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+def test_a_scale_that_is_not_finite_stays_with_its_page(rows, bad):
+    """The newest token starts a page whose value scale is not finite: the rows before it do not see that page."""
+    g = torch.Generator().manual_seed(10)
+    codes = torch.randn(2, 3, 1, 32, 64, generator=g).to(E4)
+    scales = torch.ones(2, 3, 1)
+    n = 65  # the last token alone in the third page
+    table = torch.tensor([[1, 2, 0]], dtype=torch.int32)
+    q = torch.randn(1, 2, rows, 64, generator=g).to(BF)
+    good = rp.PagedCache(codes[0].cuda(), codes[1].cuda(), scales[0].cuda(), scales[1].cuda())
+    want = _decode(good, table, [n], q)
+    scales[1, 0] = bad
+    cache = rp.PagedCache(codes[0].cuda(), codes[1].cuda(), scales[0].cuda(), scales[1].cuda())
+    got = _decode(cache, table, [n], q)
+    assert not got[:, :, -1].isfinite().any()
+    if rows > 1:
+        c = {x: getattr(good, x).double().cpu().numpy() for x in ("k", "v", "k_scale", "v_scale")}
+        ref, size = so.paged_decode(q.double().numpy(), c, table.numpy(), [n], 32)
+        got, ref, size = got[:, :, :-1].double().cpu().numpy(), ref[:, :, :-1], size[:, :, :-1]
+        assert np.all(np.abs(got - ref) <= 2.0 ** -8 * np.abs(ref) + size * (2.0 ** -11 + 2.0 ** -12))
+    assert want.isfinite().all()

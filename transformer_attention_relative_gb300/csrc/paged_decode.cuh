@@ -911,11 +911,12 @@ __global__ void __launch_bounds__(kPdThreads, NQ * D <= 64 ? 4 : NQ * D <= 128 ?
         }
       };
       // Where rows of one tile see different keys and a value that some of
-      // them do not see is not finite (0 times it is NaN), the rows of each
-      // query position go alone, with the values that they do not see as
-      // zeros.
+      // them do not see, or the page's scale, is not finite (0 times it is
+      // NaN), the rows of each query position that see a key go alone, with
+      // the values that they do not see as zeros.
       bool foul = false;
       if (edge && p.Lq > 1) {
+        if constexpr (FP8) foul = !(fabsf(ratio) <= FLT_MAX);
 #pragma unroll
         for (int i = lane; i < KT * S::kChunks; i += 32) {
           const uint4 u = lds128(vs + 16 * i);
@@ -931,7 +932,8 @@ __global__ void __launch_bounds__(kPdThreads, NQ * D <= 64 ? 4 : NQ * D <= 128 ?
       }
       if (foul || (FP8 && outside())) {
 #pragma unroll 1
-        for (int i = foul ? 0 : p.Lq - 1; i < p.Lq; ++i) add_values(std::true_type{}, len - p.Lq + i, !foul);
+        for (int i = foul ? 0 : p.Lq - 1; i < p.Lq; ++i)
+          if (len - p.Lq + i >= key0) add_values(std::true_type{}, len - p.Lq + i, !foul);
       } else {
         add_values(std::false_type{}, 0, true);
       }
