@@ -525,8 +525,10 @@ int relpos_rotary(const RelposRotaryPlan* plan, int dtype, int inverse, const Re
  * between rows; lens is device int32 [B]: the tokens of each sequence, those
  * of the current step included. The kernels check lengths and page numbers
  * against the cache, skip what lies outside it and report it through
- * relpos_check_status() as RELPOS_ERR_PAGE; table entries beyond a sequence's
- * last page are never read. Make the first call on a device before any stream
+ * relpos_check_status() as RELPOS_ERR_PAGE: a sequence longer than its row of
+ * the block table (nothing is appended; its rows of a decode are zero), and a
+ * page number that is none (its tokens are not written; a decode leaves its
+ * keys out). Table entries beyond a sequence's last page are never read. Make the first call on a device before any stream
  * capture (it looks up the device status word and sizes launches).
  */
 typedef struct RelposPagedCache {

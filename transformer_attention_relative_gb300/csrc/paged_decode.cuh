@@ -115,6 +115,16 @@ namespace {
 // equal share of all units' work, whatever the lengths, and its warps every
 // fourth tile of it.
 
+// Tokens of a sequence; none where the block table cannot hold them (which the
+// kernel that writes the sequence's zero rows reports).
+RP_DEVI int seq_len(const PagedDecodeParams& p, int b) {
+  const int len = b < p.B ? __ldg(p.lens + b) : 0;
+  return len <= p.max_len ? max(len, 0) : 0;
+}
+RP_DEVI void report_length(const PagedDecodeParams& p, int b) {
+  if (__ldg(p.lens + b) > p.max_len) atomicCAS(p.status, 0, RELPOS_ERR_PAGE);
+}
+
 // Place in the sequence of tiles: sequence and its length, unit of it, tile of
 // the unit.
 struct Cursor {
@@ -125,7 +135,7 @@ struct Cursor {
   RP_DEVI void enter(const PagedDecodeParams& p) {  // the first sequence from b on that has tiles
     nt = len = 0;
     for (; b < p.B; ++b) {
-      len = min(max(__ldg(p.lens + b), 0), p.max_len);
+      len = seq_len(p, b);
       nt = (len + KT - 1) / KT;
       pages = p.table + b * p.table_stride;
       if (nt) return;
@@ -145,10 +155,6 @@ struct Cursor {
     }
   }
 };
-
-RP_DEVI int seq_len(const PagedDecodeParams& p, int b) {
-  return b < p.B ? min(max(__ldg(p.lens + b), 0), p.max_len) : 0;
-}
 
 // A block's share of the work. A unit counts its tiles and kPdUnitCost more, for
 // what a block spends on each unit that it touches (its query rows, its first
@@ -371,6 +377,7 @@ __global__ void __launch_bounds__(kPdThreads, NQ * D <= 64 ? 4 : NQ * D <= 128 ?
     pc.h = pc.u / p.rt;
     pc.pages = p.table + pc.b * p.table_stride;
     if (tiles == 0) {  // no key is seen: zero rows
+      if (threadIdx.x == 0) report_length(p, pc.b);
       const int row0 = (pc.u - pc.h * p.rt) * S::kRows;
       for (int i = threadIdx.x; i < min(p.G * p.Lq - row0, S::kRows) * D; i += kPdThreads) {
         const int r = row0 + i / D, qi = r / p.G;
@@ -398,6 +405,7 @@ __global__ void __launch_bounds__(kPdThreads, NQ * D <= 64 ? 4 : NQ * D <= 128 ?
   int px = warp;
   auto page_of = [&](const Cursor& c) { return __ldg(c.pages + ((c.t * KT) >> p.log_page)); };
   int next_page = px < tiles ? page_of(pc) : 0;  // a step ahead: its load does not delay the copies
+  unsigned missing = 0;  // bit s: stage s is of a page that does not exist
   const int r0 = lane / S::kChunks, ch = lane % S::kChunks;
   const uint32_t dst0 = r0 * S::kRowBytes + ((ch ^ swizzle<S::kChunks>(r0)) << 4);
   constexpr int kStep = 32 / S::kChunks;  // rows between a lane's copies
@@ -408,10 +416,12 @@ __global__ void __launch_bounds__(kPdThreads, NQ * D <= 64 ? 4 : NQ * D <= 128 ?
       const int key0 = pc.t * KT;
       int valid = pc.len - key0;
       uint32_t page = next_page;
+      missing &= ~(1u << stage);
       if (page >= static_cast<uint32_t>(p.num_pages)) {  // zeros in its place, and the error on record
         if (lane == 0) atomicCAS(p.status, 0, RELPOS_ERR_PAGE);
         page = 0;
         valid = 0;
+        missing |= 1u << stage;
       }
       const uint32_t ph = page * p.Hkv + pc.h;  // (page, head) pairs of a pool are fewer than 2^31
       const size_t at = static_cast<size_t>(ph) * page_bytes + (key0 & ((1 << p.log_page) - 1)) * S::kRowBytes;
@@ -472,7 +482,6 @@ __global__ void __launch_bounds__(kPdThreads, NQ * D <= 64 ? 4 : NQ * D <= 128 ?
   while (x < tiles) {
     const int xe = min(tiles, x + cc.nt - cc.t);  // the unit's tiles in this block
     const int len = cc.len;
-    if (threadIdx.x == 0 && __ldg(p.lens + cc.b) > p.max_len) atomicCAS(p.status, 0, RELPOS_ERR_PAGE);
     const int h = cc.h, row0 = (cc.u - h * p.rt) * S::kRows;
     const int rows = min(p.G * p.Lq - row0, S::kRows);
 
@@ -581,13 +590,16 @@ __global__ void __launch_bounds__(kPdThreads, NQ * D <= 64 ? 4 : NQ * D <= 128 ?
       for (int j = 0; j < KS; ++j) o[n][j][0] = o[n][j][1] = o[n][j][2] = o[n][j][3] = 0.f;
     }
 
+    bool first = true;  // no tile of the unit yet
     // this warp's tiles of the unit: those with y mod 4 = warp
     for (int y = x + ((warp - x) & (kPdWarps - 1)); y < xe; y += kPdWarps) {
       cp_async_wait<STAGES - 2>();
       __syncwarp();
       produce(stage == 0 ? STAGES - 1 : stage - 1);
       const uint32_t ks = ring + stage * S::kStageBytes, vs = ks + S::kTileBytes;
+      const bool skip = missing >> stage & 1;
       if (++stage == STAGES) stage = 0;
+      if (skip) continue;
       const int key0 = (cc.t + y - x) * KT;
 
       // scores: lane (g, t) holds keys 16 i + g (+ 8) and rows 8 n + 2 t, + 1
@@ -648,7 +660,7 @@ __global__ void __launch_bounds__(kPdThreads, NQ * D <= 64 ? 4 : NQ * D <= 128 ?
       // The common tile: every row sees it, its biases are linear in the key's
       // position, and no logit passes its row's offset by too much.
       float z[NQ][MT][4];
-      bool above = edge || near || odd || y < x + kPdWarps;
+      bool above = edge || near || odd || first;
       if (!above) {
 #pragma unroll
         for (int n = 0; n < NQ; ++n) {
@@ -733,7 +745,7 @@ __global__ void __launch_bounds__(kPdThreads, NQ * D <= 64 ? 4 : NQ * D <= 128 ?
         // logits are formed anew. At the warp's first tile of the unit that is
         // where they stand.
         float was[NQ][2];
-        bool moves[NQ][2], settle = y < x + kPdWarps;
+        bool moves[NQ][2], settle = first;
 #pragma unroll
         for (int n = 0; n < NQ; ++n) {
 #pragma unroll
@@ -802,6 +814,8 @@ __global__ void __launch_bounds__(kPdThreads, NQ * D <= 64 ? 4 : NQ * D <= 128 ?
           }
         }
       }
+
+      first = false;
 
       // o^T += v^T p^T. SLOW: each product by itself, times the page's ratio,
       // for the rows and the keys of one query position or (`all`) of every one.
@@ -946,7 +960,7 @@ __global__ void __launch_bounds__(kPdThreads, NQ * D <= 64 ? 4 : NQ * D <= 128 ?
     for (int n = 0; n < NQ; ++n) {
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        if (((warp - x) & (kPdWarps - 1)) >= had) off[n][c] = -FLT_MAX;  // a warp without tiles
+        if (first) off[n][c] = -FLT_MAX;  // a warp without tiles
         l_run[n][c] += __shfl_xor_sync(0xffffffffu, l_run[n][c], 4);
         l_run[n][c] += __shfl_xor_sync(0xffffffffu, l_run[n][c], 8);
         l_run[n][c] += __shfl_xor_sync(0xffffffffu, l_run[n][c], 16);
@@ -1082,7 +1096,8 @@ __global__ void __launch_bounds__(kPdThreads) relpos_paged_combine_kernel(const 
   const int4 what = __ldcg(p.ends + 2 * blockIdx.x + end);
   const int c0 = what.x, k = what.y, b = what.z, u = what.w;
   for (int i = blockIdx.x; i < p.B; i += gridDim.x) {
-    if (__ldg(p.lens + i) > 0) continue;
+    if (seq_len(p, i) > 0) continue;
+    if (threadIdx.x == 0) report_length(p, i);
     for (int r = threadIdx.x / 32; r < p.Hq * p.Lq; r += kPdWarps)
       for (int j = threadIdx.x % 32; j < D; j += 32)
         p.out[i * p.o_batch + r / p.Lq * p.o_head + r % p.Lq * p.o_row + j] = __float2bfloat16_rn(0.f);
