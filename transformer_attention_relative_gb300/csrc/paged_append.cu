@@ -414,11 +414,13 @@ __global__ void __launch_bounds__(THREADS, UNITS == 1 ? (FP8 ? 768 : 512) / THRE
         // The fp32 rotation is off by less than 2^-22 (|a| + |q|): sine and
         // cosine by 2^-23, two products and a sum by 2^-24 each; by twice that
         // times the amplitude where there is one; by nothing at position 0,
-        // where many values do lie on a border (but 0 times an infinity would
-        // be NaN: a head that has one leaves all but its zeros open there).
-        const float slack = amplitude != 1.f ? ik * 4.76837158e-07f * amplitude
-                            : page0 + slot   ? ik * 2.38418579e-07f
-                                             : amax_s[0][h] < 0x7f80 ? 0.f : FLT_MAX;
+        // where many values do lie on a border. A head with magnitudes of the
+        // largest scale leaves all but its zeros open: an amplitude may take
+        // them past fp32, and 0 times an infinity would be NaN.
+        const float slack = want_k == 0x1p120f ? FLT_MAX
+                            : amplitude != 1.f ? ik * 4.76837158e-07f * amplitude
+                            : page0 + slot     ? ik * 2.38418579e-07f
+                                               : 0.f;
         uint32_t doubt = 0;  // pairs whose codes the fp32 rotation leaves open
         if (turns) {
           uint32_t code[8];  // of pair m: first member's code, second's in the next byte
