@@ -64,6 +64,24 @@ RP_DEVI uint2 codes8(const float (&f)[8], float inv) {
   return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
 }
 
+RP_DEVI bool is_pow2(float x) { return (__float_as_uint(x) & 0x7fffffu) == 0; }
+
+// A result y of an operation that rounded towards zero, its last bit made odd
+// where the operation dropped something: rounded to a code it then falls on the
+// side of a border that the exact result lies on.
+RP_DEVI float sticky(float y, bool dropped) { return __uint_as_float(__float_as_uint(y) | (dropped ? 1u : 0u)); }
+
+// The code of x / scale for a scale (2^-120 or more) that is no power of two
+RP_DEVI uint8_t code_over(float x, float scale) {
+  const float up = scale < 0x1p-60f ? 0x1p60f : 1.f;  // the division's remainder has to be representable
+  x *= up;
+  scale *= up;
+  const float q = __fdiv_rz(x, scale);
+  // beyond 1024 it saturates (infinity and NaN stay as they are)
+  return __nv_cvt_float_to_fp8(sticky(q, fabsf(q) < 1024.f && fmaf(-q, scale, x) != 0.f), __NV_SATFINITE, __NV_E4M3);
+}
+
+// 8 codes times ratio = old scale / new scale, the new one a power of two
 RP_DEVI uint2 moved8(const uint2& u, float ratio) {
   uint32_t w[2] = {u.x, u.y};
 #pragma unroll
@@ -74,8 +92,11 @@ RP_DEVI uint2 moved8(const uint2& u, float ratio) {
       const __half2_raw r =
           __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>((w[e] >> (16 * h)) & 0xffffu), __NV_E4M3);
       const float2 f = __half22float2(__half2(r));
-      const uint32_t c =
-          __nv_cvt_float2_to_fp8x2(make_float2(f.x * ratio, f.y * ratio), __NV_SATFINITE, __NV_E4M3);
+      // towards zero and sticky: the product may have more than fp32's 24 bits
+      float2 y = make_float2(__fmul_rz(f.x, ratio), __fmul_rz(f.y, ratio));
+      y.x = sticky(y.x, fmaf(f.x, ratio, -y.x) != 0.f);
+      y.y = sticky(y.y, fmaf(f.y, ratio, -y.y) != 0.f);
+      const uint32_t c = __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
       out |= c << (16 * h);
     }
     w[e] = out;

@@ -116,13 +116,15 @@ struct Scaled {
 // The pair's codes from the rotation in 64-bit integers (y1's in the low byte).
 // Taken where the fp32 rotation cannot tell on which side of a border of the e4m3
 // grid its result lies, about once in 10^5 values. Each product of an 8-bit
-// mantissa and a sine or cosine of 2^-54 is exact; their sum is scaled and cut to
+// mantissa and a sine or cosine of 2^-54 is exact; their sum is multiplied by inv,
+// a power of two, (DIVIDED) divided by a 24-bit mantissa, divisor / 2^23, and cut to
 // 24 bits, the last made odd where that dropped anything, so that the rounding to
 // a code sees on which side of a border the value lies. Fixed point since 64-bit
 // floating point is slow here: a token's step took 6.2 us with it against 5.5,
 // prompts 21.6 against 20.3.
+template <bool DIVIDED>
 __device__ __noinline__ uint32_t rotated_codes_exact(float x1, float x2, unsigned long long turns, int pos,
-                                                     double amplitude, float inv) {
+                                                     double amplitude, float inv, uint32_t divisor = 0) {
   long long s, c;
   sincos_fixed(turns * static_cast<unsigned long long>(static_cast<long long>(pos)), s, c);
   const uint32_t b1 = __float_as_uint(x1), b2 = __float_as_uint(x2);
@@ -150,6 +152,11 @@ __device__ __noinline__ uint32_t rotated_codes_exact(float x1, float x2, unsigne
       v.normalize();
       v.times(amp << 11 | 1ull << 63, static_cast<int>(amp >> 52) - 1023 - 63);
       v.times(by.u, by.e);
+      if constexpr (DIVIDED) {
+        const unsigned long long whole = v.u / divisor;  // 40 bits or more
+        v.u = whole | (whole * divisor != v.u), v.e += 23;
+        v.normalize();
+      }
       const uint32_t cut = static_cast<uint32_t>(v.u >> 40) | ((v.u & ((1ull << 40) - 1)) != 0);
       // what is below half of the smallest code may be so by more or less
       f = static_cast<float>(cut) * __int_as_float((min(max(v.e + 40, -120), 100) + 127) << 23);
@@ -160,6 +167,43 @@ __device__ __noinline__ uint32_t rotated_codes_exact(float x1, float x2, unsigne
     code |= (e4m3x2(f, 0.f) & 0xffu) << 8 * i;
   }
   return code;
+}
+
+// The codes of a page that was quantised elsewhere, with a scale that is no power
+// of two, and keeps it: the block's tokens t_lo .. t_hi - 1 of the heads that are
+// so, divided by it, over the codes by its rounded inverse. After a block's other
+// work, and out of line, so that it costs the others no registers.
+template <bool INTERLEAVED>
+__device__ __noinline__ void divided_codes(const AppendParams& p, const float (&had)[2][kAppMaxGroup],
+                                           const int (&amax)[2][kAppMaxGroup], int nheads, size_t page_rows, int page0,
+                                           int t_lo, int t_hi, const __nv_bfloat16* K, const __nv_bfloat16* V) {
+  const int d = p.cache.d, pairs = p.plan.rot_dim >> 1;
+  for (int i = 0; i < 2 * nheads; ++i) {
+    const int w = i >= nheads, h = i - w * nheads;
+    const float scale = had[w][h];
+    if (is_pow2(scale) || !(scale_for(amax[w][h], w ? p.exp_v : p.exp_k) <= scale)) continue;
+    const uint32_t bits = __float_as_uint(scale);
+    const float inv = 1.f / __uint_as_float(bits & 0x7f800000u);  // a power of two
+    const __nv_bfloat16* x = w ? V + h * p.v_head : K + h * p.k_head;
+    const long long step = w ? p.v_row : p.k_row;
+    uint8_t* codes = static_cast<uint8_t*>(w ? p.cache.v : p.cache.k) + ((page_rows + h) << p.log_page) * d;
+    const int turned = w ? 0 : pairs, units = d - turned;  // of a token: pairs, then single values
+    for (int j = threadIdx.x; j < (t_hi - t_lo) * units; j += blockDim.x) {
+      const int slot = t_lo + j / units, m = j % units;
+      const __nv_bfloat16* row = x + slot * step;
+      uint8_t* to = codes + slot * d;
+      if (m < turned) {
+        const int e1 = INTERLEAVED ? 2 * m : m, e2 = INTERLEAVED ? e1 + 1 : e1 + pairs;
+        const uint32_t both =
+            rotated_codes_exact<true>(__bfloat162float(row[e1]), __bfloat162float(row[e2]), p.plan.turns[m],
+                                      page0 + slot, p.plan.amplitude, inv, (bits & 0x7fffffu) | 0x800000u);
+        to[e1] = static_cast<uint8_t>(both);
+        to[e2] = static_cast<uint8_t>(both >> 8);
+      } else {
+        to[m + turned] = code_over(__bfloat162float(row[m + turned]), scale);
+      }
+    }
+  }
 }
 
 // A block takes one page that gets new tokens and `group` heads of it. Its
@@ -290,6 +334,7 @@ __global__ void __launch_bounds__(THREADS, UNITS == 1 ? (FP8 ? 768 : 512) / THRE
   };
   load(0);
 
+  bool odd = false;  // a scale so far that is no power of two
   if constexpr (FP8) {
     for (int i = tid; i < 2 * nheads; i += THREADS) {
       const int w = i >= nheads, h = i - w * nheads;
@@ -297,6 +342,7 @@ __global__ void __launch_bounds__(THREADS, UNITS == 1 ? (FP8 ? 768 : 512) / THRE
       const float had = t_lo > 0 ? (w ? p.cache.v_scale : p.cache.k_scale)[page_rows + h] : 0.f;
       had_s[w][h] = had;
       had_inv_s[w][h] = 1.f / had;
+      odd |= !is_pow2(had);
     }
   }
   const float amplitude = static_cast<float>(p.plan.amplitude);
@@ -316,7 +362,10 @@ __global__ void __launch_bounds__(THREADS, UNITS == 1 ? (FP8 ? 768 : 512) / THRE
       }
     }
   }
-  __syncthreads();
+  if constexpr (FP8)
+    odd = __syncthreads_or(odd);
+  else
+    __syncthreads();
 
   for (int head = 0; head < nheads; head += step_heads) {
     if constexpr (FP8) {
@@ -406,7 +455,7 @@ __global__ void __launch_bounds__(THREADS, UNITS == 1 ? (FP8 ? 768 : 512) / THRE
         uint8_t* vo = static_cast<uint8_t*>(p.cache.v) + at;
         const float want_k = scale_for(amax_s[0][h], p.exp_k), want_v = scale_for(amax_s[1][h], p.exp_v);
         // 1 over the scale: exact from a power of two's bits, but the page's
-        // scale so far may be any number
+        // scale so far may be any number (whose codes are divided below)
         const bool same_k = want_k <= had_s[0][h], same_v = want_v <= had_s[1][h];
         const float ik = same_k ? had_inv_s[0][h] : __int_as_float((254 << 23) - __float_as_int(want_k));
         const float iv = same_v ? had_inv_s[1][h] : __int_as_float((254 << 23) - __float_as_int(want_v));
@@ -474,13 +523,18 @@ __global__ void __launch_bounds__(THREADS, UNITS == 1 ? (FP8 ? 768 : 512) / THRE
           const int m = __ffs(doubt) - 1;
           doubt &= doubt - 1;
           const int e1 = INTERLEAVED ? d1 + 2 * m : d1 + m, e2 = INTERLEAVED ? e1 + 1 : d2 + m;
-          const uint32_t both = rotated_codes_exact(__bfloat162float(row[e1]), __bfloat162float(row[e2]),
-                                                    p.plan.turns[8 * unit + m], page0 + slot, p.plan.amplitude, ik);
+          const uint32_t both = rotated_codes_exact<false>(__bfloat162float(row[e1]), __bfloat162float(row[e2]),
+                                                           p.plan.turns[8 * unit + m], page0 + slot,
+                                                           p.plan.amplitude, ik);
           ko[e1] = static_cast<uint8_t>(both);
           ko[e2] = static_cast<uint8_t>(both >> 8);
         }
       }
     }
+  }
+  if (FP8 && odd) {
+    __syncthreads();
+    divided_codes<INTERLEAVED>(p, had_s, amax_s, nheads, page_rows, page0, t_lo, t_hi, p.K + k_base, p.V + v_base);
   }
 }
 
