@@ -26,6 +26,15 @@ PagedDecodeVariant variant_of(int d, int dtype, int rows8) {
 constexpr int kDevices = 64;
 std::mutex g_mu;  // guards what is kept between calls below
 
+// What is set up once may come up first in a call under stream capture, where
+// calls that touch no stream are refused too unless the thread says that they are
+// meant.
+struct OutsideCapture {
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+  OutsideCapture() { cudaThreadExchangeStreamCaptureMode(&mode); }
+  ~OutsideCapture() { cudaThreadExchangeStreamCaptureMode(&mode); }
+};
+
 // Blocks of a variant's decode kernel that an SM of the current device holds,
 // asked once for each device (with the shared memory allowed for the kernel's
 // launches); 0 on failure.
@@ -35,11 +44,13 @@ int resident_blocks(int d, int dtype, int rows8, const PagedDecodeVariant& v) {
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) return 0;
   int& n = known[dev][(d == 128) * 4 + (dtype == RELPOS_E4M3) * 2 + rows8 - 1];
   std::lock_guard<std::mutex> lk(g_mu);
-  if (n == 0 &&
-      (cudaFuncSetAttribute(v.decode, cudaFuncAttributeMaxDynamicSharedMemorySize, v.smem) != cudaSuccess ||
-       cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, v.decode, kPdThreads, v.smem) != cudaSuccess)) {
-    cudaGetLastError();
-    n = 0;
+  if (n == 0) {
+    OutsideCapture mode;
+    if (cudaFuncSetAttribute(v.decode, cudaFuncAttributeMaxDynamicSharedMemorySize, v.smem) != cudaSuccess ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, v.decode, kPdThreads, v.smem) != cudaSuccess) {
+      cudaGetLastError();
+      n = 0;
+    }
   }
   return n;
 }
@@ -54,6 +65,7 @@ cudaMemPool_t scratch_pool() {
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) return nullptr;
   std::lock_guard<std::mutex> lk(g_mu);
   if (!pools[dev]) {
+    OutsideCapture mode;
     cudaMemPoolProps props = {};
     props.allocType = cudaMemAllocationTypePinned;
     props.location.type = cudaMemLocationTypeDevice;
