@@ -247,6 +247,27 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _output_of(stream, make):
+    """The tensor that ``make()`` allocates, for a call on ``stream``.
+
+    Memory of the current stream may still be in use there by kernels that ``stream`` does not wait for, so it comes from
+    ``stream``'s; and it is not given out again before what the current stream has read of it by then.
+    """
+    import torch
+    if stream is None:
+        return make()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream)
+    here = torch.cuda.current_stream()
+    if stream == here:
+        return make()
+    with torch.cuda.stream(stream):
+        out = make()
+    if out.is_cuda:
+        out.record_stream(here)
+    return out
+
+
 def attention(Q, K, V, table0, table1=None, *, mode: int = MODE_T5, num_buckets: int = 32,
               rel_param: int = 128, causal: bool = False, q_offset: int = 0, out=None,
               stream=None, lengths=None):
@@ -270,7 +291,7 @@ def attention(Q, K, V, table0, table1=None, *, mode: int = MODE_T5, num_buckets:
         if t is not None and (not t.is_cuda or not t.is_contiguous()):
             raise ValueError("tensors must be contiguous CUDA tensors")
     if out is None:
-        out = torch.empty_like(Q)
+        out = _output_of(stream, lambda: torch.empty_like(Q))
     if lengths is not None:
         if lengths.dtype != torch.int32 or not lengths.is_cuda or not lengths.is_contiguous():
             raise TypeError("lengths must be a contiguous int32 CUDA tensor")
@@ -292,7 +313,7 @@ def index_ids(mode: int, rel_first: int, n: int, *, num_buckets: int = 32, rel_p
               causal: bool = False, device="cuda", stream=None):
     """Device index ids for offsets rel_first .. rel_first + n - 1 (int32 tensor)."""
     import torch
-    out = torch.empty(n, dtype=torch.int32, device=device)
+    out = _output_of(stream, lambda: torch.empty(n, dtype=torch.int32, device=device))
     rc = relpos_index_ids(mode, n, rel_first, num_buckets, rel_param, int(causal), _ptr(out),
                           _stream(stream))
     if rc != RELPOS_OK:
@@ -322,7 +343,7 @@ def t5_decode_positions(Q, K, V, bias, key_pos, *, num_buckets: int = 32, max_di
     if key_pos.dtype != torch.int32:
         raise TypeError("key_pos must be int32")
     if out is None:
-        out = torch.empty_like(Q)
+        out = _output_of(stream, lambda: torch.empty_like(Q))
     rc = relpos_t5_decode_positions(_ptr(Q), _ptr(K), _ptr(V), _ptr(bias), _ptr(key_pos), B, H, Lq,
                                     Lk, num_buckets, max_distance, int(causal), q_offset, _ptr(out),
                                     _stream(stream))
@@ -347,7 +368,7 @@ def alibi_decode_positions(Q, K, V, slopes, key_pos, *, causal: bool = True, q_o
     if key_pos.dtype != torch.int32:
         raise TypeError("key_pos must be int32")
     if out is None:
-        out = torch.empty_like(Q)
+        out = _output_of(stream, lambda: torch.empty_like(Q))
     rc = relpos_alibi_decode_positions(_ptr(Q), _ptr(K), _ptr(V), _ptr(slopes), _ptr(key_pos), B, H, Lq, Lk,
                                        int(causal), q_offset, _ptr(out), _stream(stream))
     if rc != RELPOS_OK:
@@ -370,8 +391,8 @@ def t5_attention_backward(Q, K, V, dO, bias, *, num_buckets: int = 32, max_dista
             raise ValueError("tensors must be contiguous CUDA tensors")
     if any(t.dtype != torch.bfloat16 for t in (Q, K, V, dO)) or bias.dtype != torch.float32:
         raise TypeError("Q, K, V, dO must be bf16 and bias fp32")
-    dQ, dK, dV = torch.empty_like(Q), torch.empty_like(K), torch.empty_like(V)
-    dbias = torch.empty_like(bias)
+    dQ, dK, dV = (_output_of(stream, lambda: torch.empty_like(t)) for t in (Q, K, V))
+    dbias = _output_of(stream, lambda: torch.empty_like(bias))
     rc = relpos_t5_attn_bwd(_ptr(Q), _ptr(K), _ptr(V), _ptr(dO), _ptr(bias), B, H, Lq, Lk, d,
                             num_buckets, max_distance, int(causal), q_offset, _ptr(dQ), _ptr(dK),
                             _ptr(dV), _ptr(dbias), _stream(stream))
@@ -395,8 +416,8 @@ def alibi_attention_backward(Q, K, V, dO, slopes, *, causal: bool = False, q_off
             raise ValueError("tensors must be contiguous CUDA tensors")
     if any(t.dtype != torch.bfloat16 for t in (Q, K, V, dO)) or slopes.dtype != torch.float32:
         raise TypeError("Q, K, V, dO must be bf16 and slopes fp32")
-    dQ, dK, dV = torch.empty_like(Q), torch.empty_like(K), torch.empty_like(V)
-    dslopes = torch.empty_like(slopes)
+    dQ, dK, dV = (_output_of(stream, lambda: torch.empty_like(t)) for t in (Q, K, V))
+    dslopes = _output_of(stream, lambda: torch.empty_like(slopes))
     rc = relpos_alibi_attn_bwd(_ptr(Q), _ptr(K), _ptr(V), _ptr(dO), _ptr(slopes), B, H, Lq, Lk, d,
                                int(causal), q_offset, _ptr(dQ), _ptr(dK), _ptr(dV), _ptr(dslopes),
                                _stream(stream))
@@ -420,9 +441,9 @@ def shaw_attention_backward(Q, K, V, dO, aK, aV, *, clip_k: int = 16, causal: bo
             raise ValueError("tensors must be contiguous CUDA tensors")
     if any(t.dtype != torch.bfloat16 for t in (Q, K, V, dO, aK, aV)):
         raise TypeError("Q, K, V, dO, aK, aV must be bf16")
-    dQ, dK, dV = torch.empty_like(Q), torch.empty_like(K), torch.empty_like(V)
-    daK = torch.empty(aK.shape, dtype=torch.float32, device=aK.device)
-    daV = torch.empty(aV.shape, dtype=torch.float32, device=aV.device)
+    dQ, dK, dV = (_output_of(stream, lambda: torch.empty_like(t)) for t in (Q, K, V))
+    daK = _output_of(stream, lambda: torch.empty_like(aK, dtype=torch.float32))
+    daV = _output_of(stream, lambda: torch.empty_like(aV, dtype=torch.float32))
     rc = relpos_shaw_attn_bwd(_ptr(Q), _ptr(K), _ptr(V), _ptr(dO), _ptr(aK), _ptr(aV), B, H, Lq, Lk, d,
                               clip_k, int(causal), q_offset, _ptr(dQ), _ptr(dK), _ptr(dV), _ptr(daK),
                               _ptr(daV), _stream(stream))
@@ -446,9 +467,9 @@ def deberta_attention_backward(Q, K, V, dO, Pk, Pq, *, k: int = 256, causal: boo
             raise ValueError("tensors must be contiguous CUDA tensors")
     if any(t.dtype != torch.bfloat16 for t in (Q, K, V, dO, Pk, Pq)):
         raise TypeError("Q, K, V, dO, Pk, Pq must be bf16")
-    dQ, dK, dV = torch.empty_like(Q), torch.empty_like(K), torch.empty_like(V)
-    dPk = torch.empty(Pk.shape, dtype=torch.float32, device=Pk.device)
-    dPq = torch.empty(Pq.shape, dtype=torch.float32, device=Pq.device)
+    dQ, dK, dV = (_output_of(stream, lambda: torch.empty_like(t)) for t in (Q, K, V))
+    dPk = _output_of(stream, lambda: torch.empty_like(Pk, dtype=torch.float32))
+    dPq = _output_of(stream, lambda: torch.empty_like(Pq, dtype=torch.float32))
     rc = relpos_deberta_attn_bwd(_ptr(Q), _ptr(K), _ptr(V), _ptr(dO), _ptr(Pk), _ptr(Pq), B, H, Lq, Lk, d,
                                  k, int(causal), q_offset, _ptr(dQ), _ptr(dK), _ptr(dV), _ptr(dPk),
                                  _ptr(dPq), _stream(stream))

@@ -15,7 +15,7 @@ import struct
 import torch
 
 from . import (MODE_ALIBI, MODE_T5, RELPOS_BF16, RELPOS_E4M3, RELPOS_FP32, RELPOS_NO_BIAS, RELPOS_OK,
-               ROTARY_LAYOUTS, ROTARY_SCALINGS, RelposError, _PagedCache, _RotaryPlan, _RowStrides,
+               ROTARY_LAYOUTS, ROTARY_SCALINGS, RelposError, _output_of, _PagedCache, _RotaryPlan, _RowStrides,
                load_library, relpos_rotary_plan_init)
 
 _DTYPES = {torch.bfloat16: RELPOS_BF16, torch.float32: RELPOS_FP32}
@@ -102,7 +102,10 @@ def _rotate(Q, plan, K, positions, offset, out, stream, inverse, what):
     index = Q.get_device()
     _check_device(index, K, positions)
     if out is None:
-        outs = (_empty_like(Q),) if K is None else (_empty_like(Q), _empty_like(K))
+        if stream is None:
+            outs = (_empty_like(Q),) if K is None else (_empty_like(Q), _empty_like(K))
+        else:
+            outs = tuple(_output_of(stream, lambda: _empty_like(x)) for x in ((Q,) if K is None else (Q, K)))
     else:
         ins, outs = ((Q,), (out,)) if K is None else ((Q, K), tuple(out))
         if len(outs) != len(ins):
@@ -256,7 +259,7 @@ def paged_decode(Q, cache, block_table, lens, *, bias=None, mode=None, num_bucke
     if d != cache.head_dim:
         raise ValueError("Q must have the cache's head dimension")
     if out is None:
-        out = _empty_like(Q)
+        out = _empty_like(Q) if stream is None else _output_of(stream, lambda: _empty_like(Q))
     elif out.shape != Q.shape:
         raise ValueError("out must have Q's shape")
     q0, q1, q2, q3 = Q.stride()
