@@ -20,8 +20,9 @@ from . import (MODE_ALIBI, MODE_T5, RELPOS_BF16, RELPOS_E4M3, RELPOS_FP32, RELPO
 
 _DTYPES = {torch.bfloat16: RELPOS_BF16, torch.float32: RELPOS_FP32}
 _byref = ctypes.byref
-_device = getattr(torch._C, "_cuda_getDevice", None)  # a torch without CUDA has neither
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+# what torch's own wrappers call, which saves a microsecond each; those where a torch has them no longer
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda index: torch.cuda.current_stream(index).cuda_stream)
 _empty_like = torch.empty_like
 _int32, _bf16 = torch.int32, torch.bfloat16
 _MOST = 2 ** 31 - 1  # the C entry points take sizes as 32-bit integers, ctypes cuts larger ones silently
