@@ -619,6 +619,14 @@ int relpos_paged_decode(const RelposPagedCache* cache, const void* Q, const Relp
                         const int* lens, int bias_mode, const void* bias, int num_buckets, int max_distance,
                         float scale, void* out, const RelposRowStrides* out_strides, void* stream);
 
+/*
+ * relpos_selftest_paged_decode_split -- how a relpos_paged_decode of these sizes
+ * is cut up on the current device: rows of a unit of work (8 or 16) and kernel
+ * launches (1 or 2). Launches nothing. Lets a test make sure which kernels it runs.
+ */
+int relpos_selftest_paged_decode_split(const RelposPagedCache* cache, int B, int Hq, int Lq, int max_pages, int* rows,
+                                       int* launches);
+
 #ifdef __cplusplus
 }
 #endif

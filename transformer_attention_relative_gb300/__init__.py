@@ -36,7 +36,7 @@ EXPORTED = ("relpos_attn_fwd", "relpos_attn_fwd_padded", "relpos_index_ids", "re
             "relpos_selftest_wait_timeout", "relpos_t5_decode_noalloc", "relpos_t5_decode_positions",
             "relpos_t5_attn_bwd", "relpos_alibi_attn_bwd", "relpos_shaw_attn_bwd", "relpos_deberta_attn_bwd",
             "relpos_alibi_decode_positions", "relpos_rotary_plan_init", "relpos_rotary", "relpos_paged_append",
-            "relpos_paged_decode")
+            "relpos_paged_decode", "relpos_selftest_paged_decode_split")
 
 _lib = None
 
@@ -114,6 +114,8 @@ def load_library(path: str = LIB_PATH):
     lib.relpos_paged_decode.argtypes = [p(_PagedCache), vp, p(_RowStrides), i, i, i, vp, ll, i, vp, i, vp, i, i, f, vp,
                                         p(_RowStrides), vp]
     lib.relpos_paged_decode.restype = i
+    lib.relpos_selftest_paged_decode_split.argtypes = [p(_PagedCache), i, i, i, i, p(i), p(i)]
+    lib.relpos_selftest_paged_decode_split.restype = i
     _lib = lib
     return lib
 
@@ -229,6 +231,11 @@ def relpos_paged_decode(cache, Q, q_strides, B, Hq, Lq, block_table, table_strid
     return load_library().relpos_paged_decode(cache, Q, q_strides, B, Hq, Lq, block_table, table_stride, max_pages,
                                               lens, bias_mode, bias, num_buckets, max_distance, scale, out,
                                               out_strides, stream)
+
+
+def relpos_selftest_paged_decode_split(cache, B, Hq, Lq, max_pages, rows, launches) -> int:
+    """Rows of a unit and launches of a paged decode of these sizes, on the current device."""
+    return load_library().relpos_selftest_paged_decode_split(cache, B, Hq, Lq, max_pages, rows, launches)
 
 
 strerror = relpos_strerror

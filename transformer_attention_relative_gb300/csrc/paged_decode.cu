@@ -112,10 +112,72 @@ int set_t5(int num_buckets, int max_distance, int longest, PagedDecodeParams* p)
   return RELPOS_OK;
 }
 
+// How a call is cut up: the variant, rows of a unit and units that a key/value
+// head takes, blocks, and whether each unit has its block and there is no second
+// launch.
+struct Split {
+  PagedDecodeVariant v;
+  int rows, rt, blocks, direct;
+};
+
+int split_of(const RelposPagedCache* cache, int B, int Hq, int Lq, int max_pages, Split* out) {
+  const int G = Hq / cache->H;
+  if (G > 65535) return RELPOS_ERR_UNSUPPORTED;
+  const long long capacity = static_cast<long long>(max_pages) * cache->page;
+  if (capacity > (1 << 28)) return RELPOS_ERR_UNSUPPORTED;
+  out->v = variant_of(cache->d, cache->dtype, 1);
+  out->rt = (G * Lq + 7) / 8;
+  long long units = static_cast<long long>(B) * cache->H * out->rt;
+  const long long tiles = (capacity + out->v.tile - 1) / out->v.tile;  // of a unit, with every page in use
+  if (units > (1 << 30) || units * (tiles + kPdUnitCost) > (1 << 30)) return RELPOS_ERR_UNSUPPORTED;
+  if (static_cast<long long>(cache->num_pages) * cache->H > 0x7fffffffll) return RELPOS_ERR_UNSUPPORTED;
+  const int sms = device_sms();
+  if (sms <= 0) return RELPOS_ERR_CUDA;
+  // Rows of a unit: 8, or 16 where a key/value head has more than 8 and the
+  // batch is large. 16 rows read each tile once instead of twice but keep a
+  // third fewer warps on an SM and take longer a tile: 4 heads x 16 sequences x
+  // 16 rows in bf16, d = 64, 26 against 32 us at 4096 tokens (9 tiles a warp
+  // with 8 rows), 92 against 83 at 16384 (36 tiles); 24 and 32 rows lose to both.
+  int occ = resident_blocks(cache->d, cache->dtype, 1, out->v);
+  if (occ < 1) return RELPOS_ERR_CUDA;
+  const bool wide = out->rt > 1 && units * tiles > 16ll * kPdWarps * occ * sms;
+  if (wide) {
+    out->v = variant_of(cache->d, cache->dtype, 2);
+    out->rt = (out->rt + 1) / 2;
+    units = static_cast<long long>(B) * cache->H * out->rt;
+    occ = resident_blocks(cache->d, cache->dtype, 2, out->v);
+    if (occ < 1) return RELPOS_ERR_CUDA;
+  }
+  out->rows = wide ? 16 : 8;
+  // Sequences of up to 16 tiles at most (four of a warp) have a block for each
+  // unit and no second launch: 4.9 against 6.7 us for 113 tokens of 16 heads.
+  out->direct = tiles <= 4 * kPdMinTiles;
+  out->blocks = static_cast<int>(out->direct ? units
+                                             : std::min<long long>(static_cast<long long>(occ) * sms,
+                                                                   (units * tiles + kPdMinTiles - 1) / kPdMinTiles));
+  return RELPOS_OK;
+}
+
 }  // namespace
 }  // namespace relpos
 
 using namespace relpos;
+
+extern "C" int relpos_selftest_paged_decode_split(const RelposPagedCache* cache, int B, int Hq, int Lq, int max_pages,
+                                                  int* rows, int* launches) {
+  const int rc = check_paged_cache(cache);
+  if (rc != RELPOS_OK) return rc;
+  if (!rows || !launches || cache->H < 1 || cache->num_pages < 1 || B < 1 || Hq < 1 || Hq % cache->H || Lq < 1 ||
+      max_pages < 1)
+    return RELPOS_ERR_INVALID_ARG;
+  if (Lq > 8) return RELPOS_ERR_UNSUPPORTED;
+  Split split;
+  const int err = split_of(cache, B, Hq, Lq, max_pages, &split);
+  if (err != RELPOS_OK) return err;
+  *rows = split.rows;
+  *launches = split.direct ? 1 : 2;
+  return RELPOS_OK;
+}
 
 extern "C" int relpos_paged_decode(const RelposPagedCache* cache, const void* Q, const RelposRowStrides* qs, int B,
                                    int Hq, int Lq, const int* block_table, long long table_stride, int max_pages,
@@ -143,34 +205,11 @@ extern "C" int relpos_paged_decode(const RelposPagedCache* cache, const void* Q,
   if (bias_mode != RELPOS_NO_BIAS && !bias) return RELPOS_ERR_INVALID_ARG;
   if (max_pages == 0 || cache->num_pages == 0) return RELPOS_ERR_INVALID_ARG;
   if (B > 1 && table_stride < max_pages) return RELPOS_ERR_INVALID_ARG;
-  const int G = Hq / cache->H;
-  if (G > 65535) return RELPOS_ERR_UNSUPPORTED;
+  Split split;
+  rc = split_of(cache, B, Hq, Lq, max_pages, &split);
+  if (rc != RELPOS_OK) return rc;
+  const PagedDecodeVariant& v = split.v;
   const long long capacity = static_cast<long long>(max_pages) * cache->page;
-  if (capacity > (1 << 28)) return RELPOS_ERR_UNSUPPORTED;
-  PagedDecodeVariant v = variant_of(cache->d, cache->dtype, 1);
-  int rt = (G * Lq + 7) / 8;
-  long long units = static_cast<long long>(B) * cache->H * rt;
-  const long long tiles = (capacity + v.tile - 1) / v.tile;  // of a unit, with every page in use
-  if (units > (1 << 30) || units * (tiles + kPdUnitCost) > (1 << 30)) return RELPOS_ERR_UNSUPPORTED;
-  if (static_cast<long long>(cache->num_pages) * cache->H > 0x7fffffffll) return RELPOS_ERR_UNSUPPORTED;
-  const int sms = device_sms();
-  if (sms <= 0) return RELPOS_ERR_CUDA;
-  // Rows of a unit: 8, or 16 where a key/value head has more than 8 and the
-  // batch is large. 16 rows read each tile once instead of twice but keep a
-  // third fewer warps on an SM and take longer a tile: 4 heads x 16 sequences x
-  // 16 rows in bf16, d = 64, 26 against 32 us at 4096 tokens (9 tiles a warp
-  // with 8 rows), 92 against 83 at 16384 (36 tiles); 24 and 32 rows lose to both.
-  int occ = resident_blocks(cache->d, cache->dtype, 1, v);
-  if (occ < 1) return RELPOS_ERR_CUDA;
-  const bool wide = rt > 1 && units * tiles > 16ll * kPdWarps * occ * sms;
-  if (wide) {
-    v = variant_of(cache->d, cache->dtype, 2);
-    rt = (rt + 1) / 2;
-    units = static_cast<long long>(B) * cache->H * rt;
-    occ = resident_blocks(cache->d, cache->dtype, 2, v);
-    if (occ < 1) return RELPOS_ERR_CUDA;
-  }
-  const long long most = units * tiles;
 
   PagedDecodeParams p;
   std::memset(&p, 0, sizeof(p));
@@ -191,7 +230,7 @@ extern "C" int relpos_paged_decode(const RelposPagedCache* cache, const void* Q,
   p.table_stride = table_stride;
   p.max_len = static_cast<int>(capacity);
   p.lens = lens;
-  p.B = B, p.Hq = Hq, p.Lq = Lq, p.G = G, p.rows = wide ? 16 : 8, p.rt = rt;
+  p.B = B, p.Hq = Hq, p.Lq = Lq, p.G = Hq / cache->H, p.rows = split.rows, p.rt = split.rt;
   p.bias = static_cast<const float*>(bias);
   p.mode = bias_mode;
   if (bias_mode == RELPOS_T5) {
@@ -201,12 +240,8 @@ extern "C" int relpos_paged_decode(const RelposPagedCache* cache, const void* Q,
   p.scale_log2 = (scale != 0.f ? scale : 1.0f / std::sqrt(static_cast<float>(cache->d))) * kLog2e;
   p.status = device_status();
   if (!p.status) return RELPOS_ERR_CUDA;
-  // Sequences of up to 16 tiles at most (four of a warp) have a block for each
-  // unit and no second launch: 4.9 against 6.7 us for 113 tokens of 16 heads.
-  p.direct = tiles <= 4 * kPdMinTiles;
-  p.blocks = static_cast<int>(p.direct ? units
-                                       : std::min<long long>(static_cast<long long>(occ) * sms,
-                                                             (most + kPdMinTiles - 1) / kPdMinTiles));
+  p.direct = split.direct;
+  p.blocks = split.blocks;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   float* scratch = nullptr;
   if (!p.direct) {
