@@ -561,7 +561,12 @@ __global__ void __launch_bounds__(kPdThreads, NQ * D <= 64 ? 4 : NQ * D <= 128 ?
       float far = 0.f, sl = 0.f;
       if (real) {
         last = len - p.Lq + i;
-        if (p.mode == RELPOS_ALIBI) sl = __ldg(p.bias + hq) * kLog2e;
+        if (p.mode == RELPOS_ALIBI) {
+          // from 2^90 on a row has its own key alone; times a distance it
+          // stays finite
+          sl = __ldg(p.bias + hq) * kLog2e;
+          if (fabsf(sl) > 0x1p90f) sl = copysignf(0x1p90f, sl);
+        }
         if (p.mode == RELPOS_T5) far = to_log2(__ldg(p.bias + (p.t5.slots - 1) * p.Hq + hq));
       }
 #pragma unroll
