@@ -517,7 +517,9 @@ int relpos_rotary(const RelposRotaryPlan* plan, int dtype, int inverse, const Re
  *   k, v             device, [num_pages, H, page, d], 16-byte aligned: bf16, or
  *                    e4m3 codes (1 byte).
  *   k_scale, v_scale device, fp32 [num_pages, H] (E4M3 only): a stored value is
- *                    its code times its page's and head's scale.
+ *                    its code times its page's and head's scale. The append
+ *                    writes powers of two; pages quantised elsewhere may have
+ *                    others.
  *   d                64 or 128; page 32, 64 or 128 (RELPOS_ERR_UNSUPPORTED
  *                    otherwise). Host struct, copied into each launch.
  *
@@ -570,15 +572,14 @@ typedef struct RelposRowStrides {
  * never becomes smaller than it was while the page is being filled (a page
  * whose first token is written starts afresh), and when it grows the codes
  * already in the page are rounded to it. Codes are the correctly rounded ones
- * (nearest, ties to even; a value next to a border is decided in 64 bits). An
- * infinity takes the largest scale and saturates, NaN stays NaN and has no
+ * (nearest, ties to even; a value next to a border is decided in 64 bits), also
+ * in a page whose scale so far is no power of two and is kept. An infinity takes the largest scale and saturates, NaN stays NaN and has no
  * share in the scale.
  *
  * Slots outside the new tokens keep their bytes unless their page's scale
  * grows. Pages written by one call must not be shared by two of its
  * sequences, appear twice in one, nor be written or read by another stream
- * meanwhile. Appending the
- * same tokens again writes the same bytes. Asynchronous on `stream`, no
+ * meanwhile. Appending the same tokens again writes the same bytes. Asynchronous on `stream`, no
  * scratch.
  */
 int relpos_paged_append(const RelposPagedCache* cache, const RelposRotaryPlan* plan, const void* K, const void* V,
@@ -605,13 +606,21 @@ int relpos_paged_append(const RelposPagedCache* cache, const RelposRotaryPlan* p
  *   Lq          0 .. 8 rows (RELPOS_ERR_UNSUPPORTED beyond).
  *   scale       softmax scale, finite; 0 takes 1 / sqrt(d).
  * Keys and values in masked or unused slots have no effect, whatever they
- * hold. The cache is read once for up to 8 or 16 rows (query heads of a group
+ * hold, nor has a page's scale on rows that see no key of the page. Sums are
+ * fp32, of weights up to 2^13 and values, before the division by the weights'
+ * sum: values from about 2^100 on may overflow to infinity. A weight is rounded
+ * for its product with the value: to 16 bits in BF16 caches, in E4M3 caches to
+ * 11 bits down to 2^-18 of the row's largest weight and to 2^-29 of that below.
+ * The cache is read once for up to 8 or 16 rows (query heads of a group
  * times Lq) and again, mostly from L2, for each further 8 or 16. Scratch: up to
  * about 8 MB for partial results of sequences that several blocks share, drawn
  * on `stream` from a memory pool of the library (which keeps up to 64 MB for the
- * calls to come) and given back before the call returns; none where the block table holds at most 16 tiles (256 tokens for
- * bf16 with d = 128, 512 otherwise). Results do not depend on what
- * else runs. Asynchronous on `stream`.
+ * calls to come) and given back before the call returns; none where the block
+ * table holds at most 16 tiles (256 tokens for bf16 with d = 128, 512
+ * otherwise). What a call costs beside its tokens follows the width of the block
+ * table (launches, rows read together), so it should be no wider than the
+ * longest sequence needs. Results do not depend on what else runs. Asynchronous
+ * on `stream`.
  */
 #define RELPOS_NO_BIAS (-1)
 int relpos_paged_decode(const RelposPagedCache* cache, const void* Q, const RelposRowStrides* q_strides, int B,

@@ -104,15 +104,4 @@ RP_DEVI uint2 moved8(const uint2& u, float ratio) {
   return make_uint2(w[0], w[1]);
 }
 
-// The codes of one unit of a token (dims d1 .. d1 + 7 and d2 .. d2 + 7) to
-// another scale; ratio = old scale / new scale.
-RP_DEVI void move_codes(uint8_t* row, int d1, int d2, float ratio) {
-  if (ratio == 1.f) return;
-  uint2* a = reinterpret_cast<uint2*>(row + d1);
-  uint2* b = reinterpret_cast<uint2*>(row + d2);
-  const uint2 u = *a, v = *b;
-  *a = moved8(u, ratio);
-  *b = moved8(v, ratio);
-}
-
 }  // namespace relpos

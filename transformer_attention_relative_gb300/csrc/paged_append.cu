@@ -115,7 +115,7 @@ struct Scaled {
 
 // The pair's codes from the rotation in 64-bit integers (y1's in the low byte).
 // Taken where the fp32 rotation cannot tell on which side of a border of the e4m3
-// grid its result lies, about once in 10^5 values. Each product of an 8-bit
+// grid its result lies, about once in 3 x 10^4 values. Each product of an 8-bit
 // mantissa and a sine or cosine of 2^-54 is exact; their sum is multiplied by inv,
 // a power of two, (DIVIDED) divided by a 24-bit mantissa, divisor / 2^23, and cut to
 // 24 bits, the last made odd where that dropped anything, so that the rounding to
@@ -215,11 +215,12 @@ __device__ __noinline__ void divided_codes(const AppendParams& p, const float (&
 // formed once for the block, in shared memory: [4][slots * units] float4, the
 // two sines, then the two cosines, of pairs 2 j and 2 j + 1 of a unit in plane j.
 //
-// Bounded by instruction issue where there is much to write (8531 tokens of 16
-// heads, d = 64, e4m3: 20.3 us for 52 MB, 650 instructions for a warp's 32 x 16 keys
-// and values; the test for borders is 1 us of it, the decisions next to one 2.4),
-// by its chain of loads (lengths, table, rows, scales) for a token a sequence
-// (5.4 us). Decisions noted down and taken together at the block's end: 0.2 us
+// 8531 tokens of 16 heads, d = 64, e4m3: 20.8 us for 52 MB. The launch is one wave
+// of 408 blocks with work, of 6, 6 and 4 heads, three to an SM at most, whose
+// loads are uneven; in it issue is 59 % busy (640 instructions for a warp's 32 x 16
+// keys and values) with a third of the warps resident. The test for borders is 1 us
+// of it, the decisions next to one, long chains in single lanes, 2.4. A token a
+// sequence: 5.4 us, its chain of loads (lengths, table, rows, scales). Decisions noted down and taken together at the block's end: 0.2 us
 // less for the prompts, 0.4 more for a token. Three blocks of 256 threads share an
 // SM for e4m3 (80 registers); with the decisions still in floating point the
 // prompts took 22.2 us so, 22.6 with two (128) and 32 with four (64, which spills

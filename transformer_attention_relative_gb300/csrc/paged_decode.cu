@@ -133,11 +133,15 @@ int split_of(const RelposPagedCache* cache, int B, int Hq, int Lq, int max_pages
   if (static_cast<long long>(cache->num_pages) * cache->H > 0x7fffffffll) return RELPOS_ERR_UNSUPPORTED;
   const int sms = device_sms();
   if (sms <= 0) return RELPOS_ERR_CUDA;
-  // Rows of a unit: 8, or 16 where a key/value head has more than 8 and the
-  // batch is large. 16 rows read each tile once instead of twice but keep a
-  // third fewer warps on an SM and take longer a tile: 4 heads x 16 sequences x
-  // 16 rows in bf16, d = 64, 26 against 32 us at 4096 tokens (9 tiles a warp
-  // with 8 rows), 92 against 83 at 16384 (36 tiles); 24 and 32 rows lose to both.
+  // Rows of a unit: 8, or 16 where a key/value head has more than 8 and a warp
+  // more than 16 tiles. 16 rows read each tile once instead of twice but keep a
+  // third fewer warps on an SM and take longer a tile. us with 8 / 16 rows for 16
+  // sequences x 4 heads x 16 rows at 2048, 4096, 8192 and 16384 tokens:
+  //   bf16  d =  64   16 / 20   25 / 30   51 / 47   94 / 75   16 rows from 9728 on
+  //   bf16  d = 128   27 / 25   54 / 36   97 / 58  181 / 97   from 3648
+  //   e4m3  d =  64   15 / 17   19 / 21   29 / 30   48 / 43   from 9728
+  //   e4m3  d = 128   20 / 21   28 / 28   53 / 40   97 / 62   from 7296
+  // 24 and 32 rows lose to both.
   int occ = resident_blocks(cache->d, cache->dtype, 1, out->v);
   if (occ < 1) return RELPOS_ERR_CUDA;
   const bool wide = out->rt > 1 && units * tiles > 16ll * kPdWarps * occ * sms;
@@ -150,7 +154,7 @@ int split_of(const RelposPagedCache* cache, int B, int Hq, int Lq, int max_pages
   }
   out->rows = wide ? 16 : 8;
   // Sequences of up to 16 tiles at most (four of a warp) have a block for each
-  // unit and no second launch: 4.9 against 6.7 us for 113 tokens of 16 heads.
+  // unit and no second launch: 5.0 against 7.3 us for 113 tokens of 16 heads.
   out->direct = tiles <= 4 * kPdMinTiles;
   out->blocks = static_cast<int>(out->direct ? units
                                              : std::min<long long>(static_cast<long long>(occ) * sms,

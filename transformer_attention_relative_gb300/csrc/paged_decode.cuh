@@ -13,7 +13,7 @@
 // the streamed tile.
 //
 // Bounded by HBM for large batches: 32 x 4096 tokens of 16 heads in 8 bits (269
-// MB) 52 us, 5.2 TB/s, 93 % of a copy's rate while it streams (slope over the
+// MB) 51 us, 5.3 TB/s, 93 % of a copy's rate while it streams (slope over the
 // length) and 9 us for its start, the spread of the blocks' ends and the joining
 // kernel; 2 x 131075 tokens, d = 128, 16 query and 4 key heads 56 us. Small
 // batches are bounded by the chain lengths, table, tile, products, joining: 113
