@@ -5,8 +5,10 @@
  * backward passes (relpos_t5_attn_bwd, relpos_shaw_attn_bwd,
  * relpos_deberta_attn_bwd, relpos_alibi_attn_bwd), and what serving from a
  * paged key/value cache takes: rotary positions (relpos_rotary), appending to
- * the cache (relpos_paged_append) and decoding over it (relpos_paged_decode),
- * at the end of this header.
+ * the cache (relpos_paged_append), decoding over it (relpos_paged_decode, and
+ * relpos_paged_tree_decode for trees of drafted tokens), keeping accepted drafts
+ * (relpos_paged_compact) and giving out and copying its pages
+ * (relpos_paged_assign, relpos_paged_copy), at the end of this header.
  *
  * One forward call computes multi-head attention whose logits carry a relative-
  * position term that is formed inside the kernel and never written to
@@ -85,6 +87,8 @@ extern "C" {
                                           relpos_t5_decode_noalloc */
 #define RELPOS_ERR_PAGE (-6)           /* a kernel met a length, a row range or a page number
                                           outside the paged cache and skipped it */
+#define RELPOS_ERR_TREE (-7)           /* a kernel met a number of nodes, a parent or a kept node
+                                        outside a tree of drafted tokens and skipped it */
 
 /*
  * relpos_attn_fwd -- attention forward with an in-kernel relative term.
@@ -192,9 +196,9 @@ int relpos_index_ids(int mode, int n, int rel_first, int num_buckets, int rel_pa
 /*
  * relpos_check_status -- synchronize `stream` and report whether any kernel
  * of this library hit a bounded-wait limit since the last check
- * (RELPOS_ERR_DEVICE_TIMEOUT) or met a page number or length outside its paged
- * cache (RELPOS_ERR_PAGE), whichever came first, or a CUDA error
- * (RELPOS_ERR_CUDA). Clears the recorded device status. Blocking.
+ * (RELPOS_ERR_DEVICE_TIMEOUT), met a page number or length outside its paged
+ * cache (RELPOS_ERR_PAGE) or something outside a tree of drafted tokens
+ * (RELPOS_ERR_TREE), whichever came first, or a CUDA error (RELPOS_ERR_CUDA). Clears the recorded device status. Blocking.
  */
 int relpos_check_status(void* stream);
 
@@ -635,6 +639,127 @@ int relpos_paged_decode(const RelposPagedCache* cache, const void* Q, const Relp
  */
 int relpos_selftest_paged_decode_split(const RelposPagedCache* cache, int B, int Hq, int Lq, int max_pages, int* rows,
                                        int* launches);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Drafted tokens. A step of speculative decoding appends a tree of drafted tokens
+ * to each sequence, runs the model over all of them at once, keeps the branch that
+ * the model agrees with and forgets the others: relpos_paged_append, then for each
+ * layer relpos_paged_tree_decode, then relpos_paged_compact.
+ *
+ * The nodes of sequence b lie in its last n_b slots, node i in slot base + i with
+ * base = lens[b] - n_b. parents[i] is an earlier node, or -1 where the node follows
+ * the slots before the drafted ones; its depth is then 0, else one more than its
+ * parent's. It stands at position base + depth: keys that are turned by position
+ * (relpos_rotary with these positions) are appended with a null plan.
+ */
+
+/*
+ * relpos_paged_tree_decode -- attention of the nodes of each sequence's tree: row i
+ * sees the slots before the drafted ones, itself and its ancestors, at the offsets
+ * between their positions. Otherwise as relpos_paged_decode.
+ *
+ *   Q, out      device, bf16 [B, Hq, n, d], row i of a sequence its node i. Rows
+ *               from n_b on are zero.
+ *   n           0 .. 64 nodes (RELPOS_ERR_UNSUPPORTED beyond).
+ *   nodes       device, int32 [B]: n_b, 0 .. n; null: n each.
+ *   parents     device, int32, node i of sequence b at parents[b * parent_stride +
+ *               i] (parent_stride 0: one tree for the whole batch).
+ * All other arguments, scratch and the way in which pages that do not exist are
+ * left out as for relpos_paged_decode. A parent that is neither -1 nor an earlier
+ * node counts as -1, and a sequence with n_b outside 0 .. n or above its length
+ * has zero rows; relpos_check_status() reports both as RELPOS_ERR_TREE.
+ */
+int relpos_paged_tree_decode(const RelposPagedCache* cache, const void* Q, const RelposRowStrides* q_strides, int B,
+                             int Hq, int n, const int* block_table, long long table_stride, int max_pages,
+                             const int* lens, const int* nodes, const int* parents, long long parent_stride,
+                             int bias_mode, const void* bias, int num_buckets, int max_distance, float scale,
+                             void* out, const RelposRowStrides* out_strides, void* stream);
+
+/*
+ * relpos_paged_compact -- keep some of each sequence's drafted tokens: slot base + i
+ * takes the key and the value of slot base + kept[i], for i < counts[b]. All are
+ * read before the first is written, so kept may name nodes in any order. The
+ * sequence's length is base + counts[b] from then on (lens is not written).
+ *
+ *   lens        device, int32 [B]: the tokens of each sequence, the drafted ones
+ *               included; an entry <= 0 is skipped.
+ *   nodes       device, int32 [B]: drafted tokens of each sequence; null: n each.
+ *   kept        device, int32, entry i of sequence b at kept[b * kept_stride + i].
+ *   m           entries of a row of kept, 0 .. 64 (RELPOS_ERR_UNSUPPORTED beyond).
+ *   counts      device, int32 [B], 0 .. min(m, n_b); null: min(m, n_b).
+ * E4M3 caches: where a token changes its page, that page's scale for a head becomes
+ * the larger of its own and the pages' that its new tokens come from, and the codes
+ * in it are rounded to it; a token that stays in its page, or comes from one of
+ * the same scale, keeps its code. Rows of Kept with an entry outside the tree keep
+ * that slot as it was, a sequence with a count outside its range all of them
+ * (RELPOS_ERR_TREE); pages that do not exist as in relpos_paged_append. Slots behind
+ * the kept tokens hold what they held, at their page's new scale. Pages written must
+ * not be shared by two sequences of the call. Asynchronous on `stream`, no scratch.
+ */
+int relpos_paged_compact(const RelposPagedCache* cache, int B, const int* block_table, long long table_stride,
+                         int max_pages, const int* lens, const int* nodes, int n, const int* kept,
+                         long long kept_stride, int m, const int* counts, void* stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Pages of a cache. One count for each page says how many rows of block tables (or
+ * holders outside of them, a store of prefixes for instance) refer to it; 0 is free.
+ */
+
+/*
+ * relpos_paged_assign -- a new block table from an old one: sequences that grow,
+ * shrink, end or go on from another's tokens (beams, shared prefixes).
+ * The old rows' references are given up; new row i continues old row source[i] for
+ * the first keep = min(lens[source[i]], new_lens[i]) tokens and has pages for
+ * new_lens[i]:
+ *   - the pages that those tokens fill are shared;
+ *   - a last page that they fill in part, and that the row may therefore write to,
+ *     stays with it where nobody else holds the page: no reference from elsewhere, no
+ *     new row that has it as a filled one, no lower new row that continues it too.
+ *     Else the row gets a fresh page in its place and the entry (page, fresh page,
+ *     tokens) in copies, for relpos_paged_copy;
+ *   - the pages behind are fresh.
+ * Fresh pages are those that nobody refers to any more, the lowest numbers first, to
+ * the rows in order and to a row's entries in order. With the sequences' own rows
+ * as their sources, growing never copies; new_lens 0 frees a sequence.
+ *
+ *   refs        device, int32 [num_pages], the old rows' references included.
+ *   page        tokens of a page: 32, 64 or 128 (RELPOS_ERR_UNSUPPORTED otherwise).
+ *   block_table, table_stride, max_pages, lens, B: the old rows. lens is what their
+ *               pages hold: row b has ceil(lens[b] / page) of them.
+ *   source      device, int32 [B2]: -1 .. B - 1, -1 a new sequence; null: row i
+ *               continues row i (a new sequence from B on).
+ *   new_lens    device, int32 [B2]; negative counts as 0.
+ *   B2          0 .. 8192 (RELPOS_ERR_UNSUPPORTED beyond).
+ *   new_table   device, int32 [B2, new_max_pages], rows new_stride elements apart;
+ *               every entry is written, -1 behind a row's last page. Not the old
+ *               table, nor overlapping it.
+ *   new_refs    device, int32 [num_pages]; may be refs.
+ *   copies      device, int32 [B2, 3]: row i's copy, or -1, -1, -1.
+ * What does not fit is reported as RELPOS_ERR_PAGE: an old row longer than its block
+ * table (it counts as empty), a new row longer than its own (likewise), a source or
+ * a page number that is none, a count below the references that are given up, and
+ * too few free pages (the entries left over are -1, without a copy). One launch,
+ * asynchronous on `stream`, no scratch; the result does not depend on its timing.
+ */
+int relpos_paged_assign(const int* refs, int num_pages, int page, const int* block_table, long long table_stride,
+                        int max_pages, const int* lens, int B, const int* source, const int* new_lens, int B2,
+                        int* new_table, long long new_stride, int new_max_pages, int* new_refs, int* copies,
+                        void* stream);
+
+/*
+ * relpos_paged_copy -- copy pages within a cache: for each of the N entries (from,
+ * to, tokens) the keys and values of the first `tokens` slots of page `from`, every
+ * head, and in E4M3 caches its scales, go to page `to`.
+ *
+ *   copies      device, int32 [N, 3]; from = -1: none. Numbers that are no pages, or
+ *               tokens outside 0 .. page, are reported (RELPOS_ERR_PAGE) and the
+ *               entry is skipped. tokens = 0 copies nothing.
+ * A page that one entry writes must not be read or written by another. Asynchronous
+ * on `stream`, no scratch.
+ */
+int relpos_paged_copy(const RelposPagedCache* cache, const int* copies, int N, void* stream);
 
 #ifdef __cplusplus
 }

@@ -27,6 +27,7 @@ RELPOS_ERR_CUDA = -3
 RELPOS_ERR_DEVICE_TIMEOUT = -4
 RELPOS_ERR_SCRATCH_LIMIT = -5
 RELPOS_ERR_PAGE = -6
+RELPOS_ERR_TREE = -7
 RELPOS_NO_BIAS = -1
 
 ROTARY_LAYOUTS = {"half": 0, "interleaved": 1}
@@ -36,7 +37,8 @@ EXPORTED = ("relpos_attn_fwd", "relpos_attn_fwd_padded", "relpos_index_ids", "re
             "relpos_selftest_wait_timeout", "relpos_t5_decode_noalloc", "relpos_t5_decode_positions",
             "relpos_t5_attn_bwd", "relpos_alibi_attn_bwd", "relpos_shaw_attn_bwd", "relpos_deberta_attn_bwd",
             "relpos_alibi_decode_positions", "relpos_rotary_plan_init", "relpos_rotary", "relpos_paged_append",
-            "relpos_paged_decode", "relpos_selftest_paged_decode_split")
+            "relpos_paged_decode", "relpos_selftest_paged_decode_split", "relpos_paged_tree_decode",
+            "relpos_paged_compact", "relpos_paged_assign", "relpos_paged_copy")
 
 _lib = None
 
@@ -116,6 +118,15 @@ def load_library(path: str = LIB_PATH):
     lib.relpos_paged_decode.restype = i
     lib.relpos_selftest_paged_decode_split.argtypes = [p(_PagedCache), i, i, i, i, p(i), p(i)]
     lib.relpos_selftest_paged_decode_split.restype = i
+    lib.relpos_paged_tree_decode.argtypes = [p(_PagedCache), vp, p(_RowStrides), i, i, i, vp, ll, i, vp, vp, vp, ll, i, vp,
+                                             i, i, f, vp, p(_RowStrides), vp]
+    lib.relpos_paged_tree_decode.restype = i
+    lib.relpos_paged_compact.argtypes = [p(_PagedCache), i, vp, ll, i, vp, vp, i, vp, ll, i, vp, vp]
+    lib.relpos_paged_compact.restype = i
+    lib.relpos_paged_assign.argtypes = [vp, i, i, vp, ll, i, vp, i, vp, vp, i, vp, ll, i, vp, vp, vp]
+    lib.relpos_paged_assign.restype = i
+    lib.relpos_paged_copy.argtypes = [p(_PagedCache), vp, i, vp]
+    lib.relpos_paged_copy.restype = i
     _lib = lib
     return lib
 
@@ -236,6 +247,34 @@ def relpos_paged_decode(cache, Q, q_strides, B, Hq, Lq, block_table, table_strid
 def relpos_selftest_paged_decode_split(cache, B, Hq, Lq, max_pages, rows, launches) -> int:
     """Rows of a unit and launches of a paged decode of these sizes, on the current device."""
     return load_library().relpos_selftest_paged_decode_split(cache, B, Hq, Lq, max_pages, rows, launches)
+
+
+def relpos_paged_tree_decode(cache, Q, q_strides, B, Hq, n, block_table, table_stride, max_pages, lens, nodes, parents,
+                             parent_stride, bias_mode, bias, num_buckets, max_distance, scale, out, out_strides,
+                             stream) -> int:
+    """Attention of the nodes of each sequence's tree of drafted tokens."""
+    return load_library().relpos_paged_tree_decode(cache, Q, q_strides, B, Hq, n, block_table, table_stride, max_pages,
+                                                   lens, nodes, parents, parent_stride, bias_mode, bias, num_buckets,
+                                                   max_distance, scale, out, out_strides, stream)
+
+
+def relpos_paged_compact(cache, B, block_table, table_stride, max_pages, lens, nodes, n, kept, kept_stride, m, counts,
+                         stream) -> int:
+    """Keep some of each sequence's drafted tokens."""
+    return load_library().relpos_paged_compact(cache, B, block_table, table_stride, max_pages, lens, nodes, n, kept,
+                                               kept_stride, m, counts, stream)
+
+
+def relpos_paged_assign(refs, num_pages, page, block_table, table_stride, max_pages, lens, B, source, new_lens, B2,
+                        new_table, new_stride, new_max_pages, new_refs, copies, stream) -> int:
+    """A new block table from an old one: sequences that grow, shrink, end or go on from others."""
+    return load_library().relpos_paged_assign(refs, num_pages, page, block_table, table_stride, max_pages, lens, B, source,
+                                              new_lens, B2, new_table, new_stride, new_max_pages, new_refs, copies, stream)
+
+
+def relpos_paged_copy(cache, copies, N, stream) -> int:
+    """Copy pages within a cache."""
+    return load_library().relpos_paged_copy(cache, copies, N, stream)
 
 
 strerror = relpos_strerror
@@ -486,5 +525,5 @@ def deberta_attention_backward(Q, K, V, dO, Pk, Pq, *, k: int = 256, causal: boo
 
 
 # rotary positions and the paged key/value cache
-from .serving import (PagedCache, RotaryPlan, paged_append, paged_decode, rotary,  # noqa: E402,F401
-                      rotary_backward)
+from .serving import (PagedCache, RotaryPlan, paged_append, paged_assign, paged_compact,  # noqa: E402,F401
+                      paged_copy, paged_decode, paged_tree_decode, rotary, rotary_backward)

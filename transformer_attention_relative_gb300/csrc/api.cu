@@ -242,6 +242,7 @@ extern "C" const char* relpos_strerror(int code) {
     case RELPOS_ERR_DEVICE_TIMEOUT: return "device-side bounded wait timed out";
     case RELPOS_ERR_SCRATCH_LIMIT: return "request exceeds the fixed scratch of the no-allocation decode";
     case RELPOS_ERR_PAGE: return "length, row range or page number outside the paged cache";
+    case RELPOS_ERR_TREE: return "node count, parent or kept node outside a tree of drafted tokens";
     default: return "unknown error";
   }
 }
@@ -281,7 +282,7 @@ extern "C" int relpos_check_status(void* stream) {
     const int zero = 0;
     if (cudaMemcpy(sp, &zero, sizeof(int), cudaMemcpyHostToDevice) != cudaSuccess)
       return RELPOS_ERR_CUDA;
-    return v == RELPOS_ERR_PAGE ? RELPOS_ERR_PAGE : RELPOS_ERR_DEVICE_TIMEOUT;
+    return v == RELPOS_ERR_PAGE || v == RELPOS_ERR_TREE ? v : RELPOS_ERR_DEVICE_TIMEOUT;
   }
   return RELPOS_OK;
 }

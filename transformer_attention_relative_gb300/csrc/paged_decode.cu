@@ -18,9 +18,18 @@
 namespace relpos {
 namespace {
 
-PagedDecodeVariant variant_of(int d, int dtype, int rows8) {
+// P: PagedDecodeParams, or PagedTreeParams for the nodes of drafted trees
+template <class P>
+PagedVariant<P> variant_of(int d, int dtype, int rows8);
+template <>
+PagedDecodeVariant variant_of<PagedDecodeParams>(int d, int dtype, int rows8) {
   if (dtype == RELPOS_E4M3) return d == 64 ? paged_decode_e4m3_64(rows8) : paged_decode_e4m3_128(rows8);
   return d == 64 ? paged_decode_bf16_64(rows8) : paged_decode_bf16_128(rows8);
+}
+template <>
+PagedTreeVariant variant_of<PagedTreeParams>(int d, int dtype, int rows8) {
+  if (dtype == RELPOS_E4M3) return d == 64 ? paged_tree_e4m3_64(rows8) : paged_tree_e4m3_128(rows8);
+  return d == 64 ? paged_tree_bf16_64(rows8) : paged_tree_bf16_128(rows8);
 }
 
 constexpr int kDevices = 64;
@@ -38,7 +47,8 @@ struct OutsideCapture {
 // Blocks of a variant's decode kernel that an SM of the current device holds,
 // asked once for each device (with the shared memory allowed for the kernel's
 // launches); 0 on failure.
-int resident_blocks(int d, int dtype, int rows8, const PagedDecodeVariant& v) {
+template <class P>
+int resident_blocks(int d, int dtype, int rows8, const PagedVariant<P>& v) {
   static int known[kDevices][8];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) return 0;
@@ -115,17 +125,19 @@ int set_t5(int num_buckets, int max_distance, int longest, PagedDecodeParams* p)
 // How a call is cut up: the variant, rows of a unit and units that a key/value
 // head takes, blocks, and whether each unit has its block and there is no second
 // launch.
+template <class P>
 struct Split {
-  PagedDecodeVariant v;
+  PagedVariant<P> v;
   int rows, rt, blocks, direct;
 };
 
-int split_of(const RelposPagedCache* cache, int B, int Hq, int Lq, int max_pages, Split* out) {
+template <class P>
+int split_of(const RelposPagedCache* cache, int B, int Hq, int Lq, int max_pages, Split<P>* out) {
   const int G = Hq / cache->H;
   if (G > 65535) return RELPOS_ERR_UNSUPPORTED;
   const long long capacity = static_cast<long long>(max_pages) * cache->page;
   if (capacity > (1 << 28)) return RELPOS_ERR_UNSUPPORTED;
-  out->v = variant_of(cache->d, cache->dtype, 1);
+  out->v = variant_of<P>(cache->d, cache->dtype, 1);
   out->rt = (G * Lq + 7) / 8;
   long long units = static_cast<long long>(B) * cache->H * out->rt;
   const long long tiles = (capacity + out->v.tile - 1) / out->v.tile;  // of a unit, with every page in use
@@ -146,7 +158,7 @@ int split_of(const RelposPagedCache* cache, int B, int Hq, int Lq, int max_pages
   if (occ < 1) return RELPOS_ERR_CUDA;
   const bool wide = out->rt > 1 && units * tiles > 16ll * kPdWarps * occ * sms;
   if (wide) {
-    out->v = variant_of(cache->d, cache->dtype, 2);
+    out->v = variant_of<P>(cache->d, cache->dtype, 2);
     out->rt = (out->rt + 1) / 2;
     units = static_cast<long long>(B) * cache->H * out->rt;
     occ = resident_blocks(cache->d, cache->dtype, 2, out->v);
@@ -162,32 +174,12 @@ int split_of(const RelposPagedCache* cache, int B, int Hq, int Lq, int max_pages
   return RELPOS_OK;
 }
 
-}  // namespace
-}  // namespace relpos
-
-using namespace relpos;
-
-extern "C" int relpos_selftest_paged_decode_split(const RelposPagedCache* cache, int B, int Hq, int Lq, int max_pages,
-                                                  int* rows, int* launches) {
-  const int rc = check_paged_cache(cache);
-  if (rc != RELPOS_OK) return rc;
-  if (!rows || !launches || cache->H < 1 || cache->num_pages < 1 || B < 1 || Hq < 1 || Hq % cache->H || Lq < 1 ||
-      max_pages < 1)
-    return RELPOS_ERR_INVALID_ARG;
-  if (Lq > 8) return RELPOS_ERR_UNSUPPORTED;
-  Split split;
-  const int err = split_of(cache, B, Hq, Lq, max_pages, &split);
-  if (err != RELPOS_OK) return err;
-  *rows = split.rows;
-  *launches = split.direct ? 1 : 2;
-  return RELPOS_OK;
-}
-
-extern "C" int relpos_paged_decode(const RelposPagedCache* cache, const void* Q, const RelposRowStrides* qs, int B,
-                                   int Hq, int Lq, const int* block_table, long long table_stride, int max_pages,
-                                   const int* lens, int bias_mode, const void* bias, int num_buckets,
-                                   int max_distance, float scale, void* out, const RelposRowStrides* os,
-                                   void* stream) {
+// What both calls check and do; what the tree's has beside is in *p already.
+template <class P>
+int decode_call(const RelposPagedCache* cache, const void* Q, const RelposRowStrides* qs, int B, int Hq, int Lq,
+                int most_rows, const int* block_table, long long table_stride, int max_pages, const int* lens,
+                int bias_mode, const void* bias, int num_buckets, int max_distance, float scale, void* out,
+                const RelposRowStrides* os, void* stream, P p) {
   int rc = check_paged_cache(cache);
   if (rc != RELPOS_OK) return rc;
   if (bias_mode != RELPOS_NO_BIAS && bias_mode != RELPOS_T5 && bias_mode != RELPOS_ALIBI)
@@ -197,7 +189,7 @@ extern "C" int relpos_paged_decode(const RelposPagedCache* cache, const void* Q,
     if (rc != RELPOS_OK) return rc;
   }
   if (!qs || !os || B < 0 || Hq < 0 || Lq < 0 || max_pages < 0 || !std::isfinite(scale)) return RELPOS_ERR_INVALID_ARG;
-  if (Lq > 8) return RELPOS_ERR_UNSUPPORTED;
+  if (Lq > most_rows) return RELPOS_ERR_UNSUPPORTED;
   if (B == 0 || Hq == 0 || Lq == 0) return RELPOS_OK;
   if (cache->H == 0 || Hq % cache->H) return RELPOS_ERR_INVALID_ARG;
   const uintptr_t ints = reinterpret_cast<uintptr_t>(block_table) | reinterpret_cast<uintptr_t>(lens) |
@@ -209,14 +201,12 @@ extern "C" int relpos_paged_decode(const RelposPagedCache* cache, const void* Q,
   if (bias_mode != RELPOS_NO_BIAS && !bias) return RELPOS_ERR_INVALID_ARG;
   if (max_pages == 0 || cache->num_pages == 0) return RELPOS_ERR_INVALID_ARG;
   if (B > 1 && table_stride < max_pages) return RELPOS_ERR_INVALID_ARG;
-  Split split;
+  Split<P> split;
   rc = split_of(cache, B, Hq, Lq, max_pages, &split);
   if (rc != RELPOS_OK) return rc;
-  const PagedDecodeVariant& v = split.v;
+  const PagedVariant<P>& v = split.v;
   const long long capacity = static_cast<long long>(max_pages) * cache->page;
 
-  PagedDecodeParams p;
-  std::memset(&p, 0, sizeof(p));
   p.k = static_cast<const uint8_t*>(cache->k);
   p.v = static_cast<const uint8_t*>(cache->v);
   p.k_scale = cache->k_scale;
@@ -281,4 +271,55 @@ extern "C" int relpos_paged_decode(const RelposPagedCache* cache, const void* Q,
     return RELPOS_ERR_CUDA;
   }
   return RELPOS_OK;
+}
+
+}  // namespace
+}  // namespace relpos
+
+using namespace relpos;
+
+extern "C" int relpos_selftest_paged_decode_split(const RelposPagedCache* cache, int B, int Hq, int Lq, int max_pages,
+                                                  int* rows, int* launches) {
+  const int rc = check_paged_cache(cache);
+  if (rc != RELPOS_OK) return rc;
+  if (!rows || !launches || cache->H < 1 || cache->num_pages < 1 || B < 1 || Hq < 1 || Hq % cache->H || Lq < 1 ||
+      max_pages < 1)
+    return RELPOS_ERR_INVALID_ARG;
+  if (Lq > 8) return RELPOS_ERR_UNSUPPORTED;
+  Split<PagedDecodeParams> split;
+  const int err = split_of(cache, B, Hq, Lq, max_pages, &split);
+  if (err != RELPOS_OK) return err;
+  *rows = split.rows;
+  *launches = split.direct ? 1 : 2;
+  return RELPOS_OK;
+}
+
+extern "C" int relpos_paged_decode(const RelposPagedCache* cache, const void* Q, const RelposRowStrides* qs, int B,
+                                   int Hq, int Lq, const int* block_table, long long table_stride, int max_pages,
+                                   const int* lens, int bias_mode, const void* bias, int num_buckets,
+                                   int max_distance, float scale, void* out, const RelposRowStrides* os,
+                                   void* stream) {
+  PagedDecodeParams p;
+  std::memset(&p, 0, sizeof(p));
+  return decode_call(cache, Q, qs, B, Hq, Lq, 8, block_table, table_stride, max_pages, lens, bias_mode, bias,
+                     num_buckets, max_distance, scale, out, os, stream, p);
+}
+
+extern "C" int relpos_paged_tree_decode(const RelposPagedCache* cache, const void* Q, const RelposRowStrides* qs, int B,
+                                        int Hq, int n, const int* block_table, long long table_stride, int max_pages,
+                                        const int* lens, const int* nodes, const int* parents,
+                                        long long parent_stride, int bias_mode, const void* bias, int num_buckets,
+                                        int max_distance, float scale, void* out, const RelposRowStrides* os,
+                                        void* stream) {
+  if (B > 0 && Hq > 0 && n > 0) {
+    const uintptr_t ints = reinterpret_cast<uintptr_t>(nodes) | reinterpret_cast<uintptr_t>(parents);
+    if (!parents || (ints & 3u) || parent_stride < 0) return RELPOS_ERR_INVALID_ARG;
+  }
+  PagedTreeParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.nodes = nodes;
+  p.parents = parents;
+  p.parent_stride = parent_stride;
+  return decode_call(cache, Q, qs, B, Hq, n, kMaxNodes, block_table, table_stride, max_pages, lens, bias_mode, bias,
+                     num_buckets, max_distance, scale, out, os, stream, p);
 }

@@ -96,17 +96,33 @@ struct PagedDecodeParams {
   int* status;
 };
 
+// The new rows as the nodes of a tree: row i of Lq is node i of a sequence's
+// nodes[b] (null: Lq) last tokens.
+struct PagedTreeParams : PagedDecodeParams {
+  const int* nodes;
+  const int* parents;
+  long long parent_stride;
+};
+constexpr int kMaxNodes = 64;  // a row's ancestors are a word's bits
+
 // A variant's kernels, tile size and shared memory; one translation unit each
 // for the head dimensions and types. `rows8`: 8-row groups of a unit.
-struct PagedDecodeVariant {
-  void (*decode)(PagedDecodeParams);
-  void (*combine)(PagedDecodeParams);
+template <class P>
+struct PagedVariant {
+  void (*decode)(P);
+  void (*combine)(P);
   int tile, smem;
 };
+using PagedDecodeVariant = PagedVariant<PagedDecodeParams>;
 PagedDecodeVariant paged_decode_e4m3_64(int rows8);
 PagedDecodeVariant paged_decode_e4m3_128(int rows8);
 PagedDecodeVariant paged_decode_bf16_64(int rows8);
 PagedDecodeVariant paged_decode_bf16_128(int rows8);
+using PagedTreeVariant = PagedVariant<PagedTreeParams>;
+PagedTreeVariant paged_tree_e4m3_64(int rows8);
+PagedTreeVariant paged_tree_e4m3_128(int rows8);
+PagedTreeVariant paged_tree_bf16_64(int rows8);
+PagedTreeVariant paged_tree_bf16_128(int rows8);
 
 namespace {
 
@@ -124,6 +140,61 @@ RP_DEVI int seq_len(const PagedDecodeParams& p, int b) {
 RP_DEVI void report_length(const PagedDecodeParams& p, int b) {
   if (__ldg(p.lens + b) > p.max_len) atomicCAS(p.status, 0, RELPOS_ERR_PAGE);
 }
+// Nodes of a sequence's tree, and its tokens: none where it has no nodes, more
+// than Lq or more than tokens.
+RP_DEVI int node_count(const PagedTreeParams& p, int b) { return p.nodes ? __ldg(p.nodes + b) : p.Lq; }
+RP_DEVI int seq_len(const PagedTreeParams& p, int b) {
+  const int len = seq_len(static_cast<const PagedDecodeParams&>(p), b);
+  if (len == 0) return 0;
+  const int n = node_count(p, b);
+  return n > 0 && n <= min(p.Lq, len) ? len : 0;
+}
+RP_DEVI void report_length(const PagedTreeParams& p, int b) {
+  report_length(static_cast<const PagedDecodeParams&>(p), b);
+  const int len = __ldg(p.lens + b), n = node_count(p, b);
+  if (len > 0 && (n < 0 || n > p.Lq || n > len)) atomicCAS(p.status, 0, RELPOS_ERR_TREE);
+}
+// Rows of a query that a sequence has: all, or one for each node
+RP_DEVI int row_count(const PagedDecodeParams& p, int) { return p.Lq; }
+RP_DEVI int row_count(const PagedTreeParams& p, int b) { return node_count(p, b); }
+
+// The lines of a tree: bit i of a node i and those of its ancestors, by taking
+// the line of an ancestor twice as far up each time. A parent that is not an
+// earlier node is none (and -1 the one that is not reported). A warp's call.
+RP_DEVI void tree_lines(const PagedTreeParams& p, int b, int n, int lane, unsigned long long* line) {
+  const int* parents = p.parents + b * p.parent_stride;
+  int up[2];
+#pragma unroll
+  for (int m = 0; m < 2; ++m) {
+    const int i = lane + 32 * m;
+    up[m] = -1;
+    if (i < n) {
+      const int a = __ldg(parents + i);
+      if (a >= 0 && a < i)
+        up[m] = a;
+      else if (a != -1)
+        atomicCAS(p.status, 0, RELPOS_ERR_TREE);
+    }
+  }
+  unsigned long long bits[2] = {1ull << lane, 1ull << (lane + 32)};
+#pragma unroll 1
+  for (int step = 1; step < n; step *= 2) {
+    unsigned long long more[2];
+    int next[2];
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      const int a = max(up[m], 0), from = a & 31;
+      const unsigned long long lo = __shfl_sync(0xffffffffu, bits[0], from), hi = __shfl_sync(0xffffffffu, bits[1], from);
+      const int up_lo = __shfl_sync(0xffffffffu, up[0], from), up_hi = __shfl_sync(0xffffffffu, up[1], from);
+      more[m] = up[m] < 0 ? 0 : a < 32 ? lo : hi;
+      next[m] = up[m] < 0 ? -1 : a < 32 ? up_lo : up_hi;
+    }
+#pragma unroll
+    for (int m = 0; m < 2; ++m) bits[m] |= more[m], up[m] = next[m];
+  }
+  line[lane] = bits[0];
+  line[lane + 32] = bits[1];
+}
 
 // Place in the sequence of tiles: sequence and its length, unit of it, tile of
 // the unit.
@@ -131,8 +202,8 @@ struct Cursor {
   int b, u, t, nt, len;
   int h;             // key/value head of the unit
   const int* pages;  // the sequence's row of the block table
-  template <int KT>
-  RP_DEVI void enter(const PagedDecodeParams& p) {  // the first sequence from b on that has tiles
+  template <int KT, class P>
+  RP_DEVI void enter(const P& p) {  // the first sequence from b on that has tiles
     nt = len = 0;
     for (; b < p.B; ++b) {
       len = seq_len(p, b);
@@ -141,8 +212,8 @@ struct Cursor {
       if (nt) return;
     }
   }
-  template <int KT>
-  RP_DEVI void forward(const PagedDecodeParams& p, int by) {
+  template <int KT, class P>
+  RP_DEVI void forward(const P& p, int by) {
     t += by;
     while (t >= nt && b < p.B) {
       t -= nt;
@@ -168,8 +239,8 @@ RP_DEVI int unit_cost(int len) {
   return len > 0 ? (len + KT - 1) / KT + kPdUnitCost : 0;
 }
 
-template <int KT>
-RP_DEVI int total_cost(const PagedDecodeParams& p, int lane, int len0) {
+template <int KT, class P>
+RP_DEVI int total_cost(const P& p, int lane, int len0) {
   int sum = unit_cost<KT>(len0);
   for (int b = lane + 32; b < p.B; b += 32) sum += unit_cost<KT>(seq_len(p, b));
   return __reduce_add_sync(0xffffffffu, sum) * p.Hkv * p.rt;
@@ -178,8 +249,8 @@ RP_DEVI int total_cost(const PagedDecodeParams& p, int lane, int len0) {
 // The cursor at the first tile at or behind cost x of all units (behind the last
 // one: sequence p.B), the cost at which its unit starts and the number of tiles
 // before it.
-template <int KT>
-RP_DEVI Cursor locate(const PagedDecodeParams& p, int lane, int len0, int x, int& unit_at, int& before) {
+template <int KT, class P>
+RP_DEVI Cursor locate(const P& p, int lane, int len0, int x, int& unit_at, int& before) {
   const int per = p.Hkv * p.rt;
   Cursor c{p.B, 0, 0, 0, 0, 0, p.table};
   int cost = 0, seqs = 0;  // of the sequences looked at, a unit each
@@ -350,9 +421,14 @@ RP_DEVI float to_log2(float x) {
 // scores' tile transposed across the warp (movmatrix). 8-bit keys and values
 // become fp16, exactly (the e4m3 form of the instruction takes more
 // instructions here: 510 a tile against 453).
-template <int D, bool FP8, int NQ, int KT, int STAGES>
+//
+// A tree's rows (P = PagedTreeParams) see the slots before the drafted ones and,
+// of these, the bits of their ancestors' word; distances go by depth. Tiles that
+// hold a drafted slot take these per element, the others are a chain's.
+template <int D, bool FP8, int NQ, int KT, int STAGES, class P>
 __global__ void __launch_bounds__(kPdThreads, NQ * D <= 64 ? 4 : NQ * D <= 128 ? 3 : 2)
-    relpos_paged_decode_kernel(const __grid_constant__ PagedDecodeParams p) {
+    relpos_paged_decode_kernel(const __grid_constant__ P p) {
+  constexpr bool TREE = std::is_same_v<P, PagedTreeParams>;
   using S = Shape<D, FP8, NQ, KT, STAGES>;
   constexpr int MT = KT / 16;   // 16-key tiles of the scores, 16-key steps of v^T p^T
   constexpr int KS = D / 16;    // 16-dim steps of k . q, 16-dim tiles of the output
@@ -477,6 +553,9 @@ __global__ void __launch_bounds__(kPdThreads, NQ * D <= 64 ? 4 : NQ * D <= 128 ?
   // the first of the 4 dims that a lane holds of q and of a key for step s
   auto dim_of = [&](int s) { return FP8 ? 16 * (t + 4 * (s / 4)) + 4 * (s % 4) : 8 * (t + 4 * (s / 2)) + 4 * (s % 2); };
 
+  [[maybe_unused]] __shared__ unsigned long long line[TREE ? kMaxNodes : 1];  // a node's bit and its ancestors'
+  [[maybe_unused]] int tree_of = -1;  // the sequence whose tree that is
+
   int stage = 0;
   int x = 0;
   while (x < tiles) {
@@ -484,12 +563,35 @@ __global__ void __launch_bounds__(kPdThreads, NQ * D <= 64 ? 4 : NQ * D <= 128 ?
     const int len = cc.len;
     const int h = cc.h, row0 = (cc.u - h * p.rt) * S::kRows;
     const int rows = min(p.G * p.Lq - row0, S::kRows);
+    const int live = row_count(p, cc.b);  // of the Lq rows
+    const int base = len - live;          // position of row 0; tree: the first drafted slot
+    if constexpr (TREE) {
+      if (tree_of != cc.b) {
+        if (warp == 0) tree_lines(p, cc.b, live, lane, line);
+        __syncthreads();
+        tree_of = cc.b;
+      }
+    }
+    // of node i and slot base + j (j < 0: a slot that all see)
+    [[maybe_unused]] auto sees = [&](int i, int j) {
+      return i < live && (j < 0 || (j < live && (line[i] >> j & 1)));
+    };
+    [[maybe_unused]] auto depth = [&](int i) { return i < live ? __popcll(line[i]) - 1 : 0; };
+    // from row i's position to that of the key in slot `key`
+    auto distance = [&](int i, int key) {
+      if constexpr (TREE) {
+        const int j = key - base;
+        return depth(i) - (j < 0 ? j : depth(j));
+      } else {
+        return base + i - key;
+      }
+    };
 
     // T5: the biases of the distances below the last bucket's, for each head
     // of the group, in the joining buffers (free while tiles are read)
     const int lut_len = p.t5_R + 1;
     const bool lut = p.mode == RELPOS_T5 && p.G * static_cast<long long>(lut_len) <= 2 * S::kRows * D &&
-                     len - p.Lq - (cc.t + xe - x) * KT + 1 < p.t5_R;
+                     base - (cc.t + xe - x) * KT + 1 < p.t5_R;
     if (lut) {
       for (int i = threadIdx.x; i < p.G * lut_len; i += kPdThreads) {
         const int hl = i / lut_len, back = i - hl * lut_len;
@@ -560,7 +662,10 @@ __global__ void __launch_bounds__(kPdThreads, NQ * D <= 64 ? 4 : NQ * D <= 128 ?
       int last = -1;
       float far = 0.f, sl = 0.f;
       if (real) {
-        last = len - p.Lq + i;
+        if constexpr (TREE)
+          last = base + depth(i);  // its position; what it sees is asked where it matters
+        else
+          last = base + i;
         if (p.mode == RELPOS_ALIBI) {
           // from 2^90 on a row has its own key alone; times a distance it
           // stays finite
@@ -578,7 +683,7 @@ __global__ void __launch_bounds__(kPdThreads, NQ * D <= 64 ? 4 : NQ * D <= 128 ?
         slope[n][c] = __shfl_sync(0xffffffffu, sl, from);
       }
     }
-    const int vis_first = len - p.Lq + row0 / p.G;  // last key that every row sees
+    const int vis_first = TREE ? base - 1 : base + row0 / p.G;  // last key that every row sees
     // a constant bias beside which products lose bits (a mask of -1e9, the
     // type's lowest value): every tile then has to lose them alike
     bool odd = false;
@@ -693,7 +798,7 @@ __global__ void __launch_bounds__(kPdThreads, NQ * D <= 64 ? 4 : NQ * D <= 128 ?
 #pragma unroll 1
           for (int i = 0; i < NQ * MT * 4; ++i) {
             const int r = row0 + 8 * (i / (4 * MT)) + 2 * t + i / (2 * MT) % 2, qi = r / p.G;
-            const int back = len - p.Lq + qi - (key0 + 16 * (i / 2 % MT) + 8 * (i % 2) + g);
+            const int back = distance(qi, key0 + 16 * (i / 2 % MT) + 8 * (i % 2) + g);
             const int bucket = t5_bucket_dev(-min(max(back, 0), p.t5_R), p.t5);
             slow[i] = to_log2(__ldg(p.bias + bucket * p.Hq + h * p.G + r - qi * p.G));
           }
@@ -706,6 +811,26 @@ __global__ void __launch_bounds__(kPdThreads, NQ * D <= 64 ? 4 : NQ * D <= 128 ?
             for (int c = 0; c < 2; ++c) {
               const float cs = qs[n][c] * k_scale;
               const int back0 = vis[n][c] - key0 - g;  // to key 16 i + 8 e: less 16 i + 8 e
+              if (TREE && edge) {
+                const int r = row0 + 8 * n + 2 * t + c, node = r / p.G;
+#pragma unroll
+                for (int i = 0; i < MT; ++i) {
+#pragma unroll
+                  for (int e = 0; e < 2; ++e) {
+                    const int key = key0 + 16 * i + 8 * e + g, back = distance(node, key);
+                    float bias = add[n][c];
+                    if (near && lut)
+                      bias = out_s[(r - node * p.G) * lut_len + min(max(back, 0), p.t5_R)];
+                    else if (near)
+                      bias = slow[((n * 2 + c) * MT + i) * 2 + e];
+                    else if (p.mode == RELPOS_ALIBI)
+                      bias = -slope[n][c] * fabsf(static_cast<float>(back));
+                    z[n][i][2 * e + c] =
+                        sees(node, key - base) ? fmaf(sc[n][i][2 * e + c], cs, bias) - off[n][c] : -INFINITY;
+                  }
+                }
+                continue;
+              }
               if (near && lut) {
                 const float* biases = out_s + (row0 + 8 * n + 2 * t + c) % p.G * lut_len;
 #pragma unroll
@@ -823,15 +948,22 @@ __global__ void __launch_bounds__(kPdThreads, NQ * D <= 64 ? 4 : NQ * D <= 128 ?
       first = false;
 
       // o^T += v^T p^T. SLOW: each product by itself, times the page's ratio,
-      // for the rows and the keys of one query position or (`all`) of every one.
+      // for the rows and the keys of one query position (tree: node) or (`all`) of
+      // every one.
       auto add_values = [&](auto slow_path, int last, bool all) {
         constexpr bool SLOW = decltype(slow_path)::value;
+        auto is_last = [&](int n, int c) {
+          if constexpr (TREE)
+            return (row0 + 8 * n + 2 * t + c) / p.G == last;
+          else
+            return vis[n][c] == last;
+        };
         [[maybe_unused]] const float factor = SLOW ? 1.f : ratio;
         uint32_t ph[NQ][MT][2];
         [[maybe_unused]] uint32_t pl[FP8 ? 1 : NQ][MT][2];
 #pragma unroll
         for (int n = 0; n < NQ; ++n) {
-          const bool mine[2] = {!SLOW || all || vis[n][0] == last, !SLOW || all || vis[n][1] == last};
+          const bool mine[2] = {!SLOW || all || is_last(n, 0), !SLOW || all || is_last(n, 1)};
 #pragma unroll
           for (int i = 0; i < MT; ++i) {
 #pragma unroll
@@ -862,7 +994,10 @@ __global__ void __launch_bounds__(kPdThreads, NQ * D <= 64 ? 4 : NQ * D <= 128 ?
             const uint4 u = lds128(a);
             w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
           }
-          if (SLOW && !all && key0 + 16 * i + 8 * e + 2 * t + oo > last) w[0] = w[1] = w[2] = w[3] = 0;
+          if (SLOW && !all) {
+            const int key = key0 + 16 * i + 8 * e + 2 * t + oo;
+            if (TREE ? !sees(last, key - base) : key > last) w[0] = w[1] = w[2] = w[3] = 0;
+          }
         };
         if constexpr (FP8) {
 #pragma unroll
@@ -890,7 +1025,7 @@ __global__ void __launch_bounds__(kPdThreads, NQ * D <= 64 ? 4 : NQ * D <= 128 ?
                     auto times = [&] { return D == 128 && NQ == 1 ? lds32f(vs + S::kTileBytes + 4) * v_inv : ratio; };
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                      if (all || vis[n][e & 1] == last) d[e] = fmaf(y[e], times(), d[e]);
+                      if (all || is_last(n, e & 1)) d[e] = fmaf(y[e], times(), d[e]);
                   } else {
                     mma16816<true>(d, f, ph[n][i][0], ph[n][i][1]);
                   }
@@ -918,10 +1053,19 @@ __global__ void __launch_bounds__(kPdThreads, NQ * D <= 64 ? 4 : NQ * D <= 128 ?
                   float(&d)[4] = o[n][4 * half + w];
                   const float was[4] = {d[0], d[1], d[2], d[3]};
                   mma16816<false>(d, f, ph[n][i][0], ph[n][i][1]);
-                  mma16816<false>(d, f, pl[n][i][0], pl[n][i][1]);
+                  if constexpr (TREE && SLOW) {
+                    // an infinite value goes with the weight's first part alone: the
+                    // second may be 0 or below
+                    uint32_t fin[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) fin[e] = f[e] & ~__vcmpeq2(f[e] & 0x7f807f80u, 0x7f807f80u);
+                    mma16816<false>(d, fin, pl[n][i][0], pl[n][i][1]);
+                  } else {
+                    mma16816<false>(d, f, pl[n][i][0], pl[n][i][1]);
+                  }
                   if (SLOW) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) d[e] = vis[n][e & 1] == last ? d[e] : was[e];
+                    for (int e = 0; e < 4; ++e) d[e] = is_last(n, e & 1) ? d[e] : was[e];
                   }
                 }
               }
@@ -934,7 +1078,7 @@ __global__ void __launch_bounds__(kPdThreads, NQ * D <= 64 ? 4 : NQ * D <= 128 ?
       // NaN), the rows of each query position that see a key go alone, with
       // the values that they do not see as zeros.
       bool foul = false;
-      if (edge && p.Lq > 1) {
+      if (edge && (TREE || live > 1)) {
         if constexpr (FP8) foul = !(fabsf(ratio) <= FLT_MAX);
 #pragma unroll
         for (int i = lane; i < KT * S::kChunks; i += 32) {
@@ -951,8 +1095,16 @@ __global__ void __launch_bounds__(kPdThreads, NQ * D <= 64 ? 4 : NQ * D <= 128 ?
       }
       if (foul || (FP8 && outside())) {
 #pragma unroll 1
-        for (int i = foul ? 0 : p.Lq - 1; i < p.Lq; ++i)
-          if (len - p.Lq + i >= key0) add_values(std::true_type{}, len - p.Lq + i, !foul);
+        for (int i = foul ? 0 : live - 1; i < live; ++i) {
+          if constexpr (TREE) {
+            // the tile's slots among the drafted ones
+            const int j = max(key0 - base, 0);
+            const bool some = key0 < base || (j < kMaxNodes && line[i] >> j & ((1ull << KT) - 1));
+            if (!foul || some) add_values(std::true_type{}, i, !foul);
+          } else if (base + i >= key0) {
+            add_values(std::true_type{}, base + i, !foul);
+          }
+        }
       } else {
         add_values(std::false_type{}, 0, true);
       }
@@ -1054,6 +1206,7 @@ __global__ void __launch_bounds__(kPdThreads, NQ * D <= 64 ? 4 : NQ * D <= 128 ?
       const float4* v = reinterpret_cast<const float4*>(out_s + r * D + dim);
       float4 a = v[0], b = v[1];
       if (whole) {
+        if (TREE && (row0 + r) / p.G >= live) a = b = make_float4(0.f, 0.f, 0.f, 0.f), sum = 0.f;  // no node
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
         const uint32_t w[4] = {pack_bf2(a.x * inv, a.y * inv), pack_bf2(a.z * inv, a.w * inv),
                                pack_bf2(b.x * inv, b.y * inv), pack_bf2(b.z * inv, b.w * inv)};
@@ -1092,8 +1245,8 @@ __global__ void __launch_bounds__(kPdThreads, NQ * D <= 64 ? 4 : NQ * D <= 128 ?
 // its threads for each end. What a slot holds the decode kernel has noted, so
 // that nothing is searched for here: these blocks mostly start when that
 // kernel's leave their SM.
-template <int D>
-__global__ void __launch_bounds__(kPdThreads) relpos_paged_combine_kernel(const __grid_constant__ PagedDecodeParams p) {
+template <int D, class P>
+__global__ void __launch_bounds__(kPdThreads) relpos_paged_combine_kernel(const __grid_constant__ P p) {
   griddep_launch_dependents();
   griddep_wait();
   constexpr int kHalf = kPdThreads / 2;
@@ -1143,8 +1296,9 @@ __global__ void __launch_bounds__(kPdThreads) relpos_paged_combine_kernel(const 
       join(m2, l2, v);
     }
     if (i < count && part == 0) {
-      const float inv = l == 0.f ? 0.f : 1.f / l;
       const int qi = (row0 + r) / p.G, hq = h * p.G + (row0 + r) - qi * p.G;
+      if (qi >= row_count(p, b)) acc = make_float4(0.f, 0.f, 0.f, 0.f), l = 0.f;  // no node
+      const float inv = l == 0.f ? 0.f : 1.f / l;
       __nv_bfloat16* op = p.out + b * p.o_batch + hq * p.o_head + qi * p.o_row + 4 * d4;
       const uint32_t w[2] = {pack_bf2(acc.x * inv, acc.y * inv), pack_bf2(acc.z * inv, acc.w * inv)};
       if (p.o_vec) {
@@ -1160,9 +1314,9 @@ __global__ void __launch_bounds__(kPdThreads) relpos_paged_combine_kernel(const 
   }
 }
 
-template <int D, bool FP8, int NQ, int KT, int STAGES>
-PagedDecodeVariant paged_decode_variant() {
-  return {relpos_paged_decode_kernel<D, FP8, NQ, KT, STAGES>, relpos_paged_combine_kernel<D>, KT,
+template <int D, bool FP8, int NQ, int KT, int STAGES, class P = PagedDecodeParams>
+PagedVariant<P> paged_decode_variant() {
+  return {relpos_paged_decode_kernel<D, FP8, NQ, KT, STAGES, P>, relpos_paged_combine_kernel<D, P>, KT,
           Shape<D, FP8, NQ, KT, STAGES>::kSmem};
 }
 

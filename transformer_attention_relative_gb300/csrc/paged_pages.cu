@@ -1,0 +1,572 @@
+// paged_pages.cu -- the pages of a paged key/value cache ("Relative Position
+// Embeddings, in depth", section "Kernels and the KV cache"): which sequence has
+// which (relpos_paged_assign), copying them (relpos_paged_copy) and keeping some
+// of a sequence's drafted tokens (relpos_paged_compact).
+
+#include <cooperative_groups.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <climits>
+#include <cstdint>
+#include <cstring>
+
+#include "../../include/relpos_attn.h"
+#include "paged.cuh"
+#include "ptx.cuh"
+#include "relpos_internal.h"
+#include "serving_internal.h"
+
+namespace relpos {
+namespace {
+
+namespace cg = cooperative_groups;
+
+RP_DEVI void report(int* status, int code) { atomicCAS(status, 0, code); }
+
+// ------------------------------------------------------------------ copy
+
+struct CopyParams {
+  RelposPagedCache cache;
+  const int* copies;  // [N, 3]
+  int N, row_bytes;
+  int* status;
+};
+
+constexpr int kCopyThreads = 256;
+
+// A block copies one head's keys or values of one entry: `tokens` rows that lie
+// one after another.
+__global__ void __launch_bounds__(kCopyThreads) relpos_paged_copy_kernel(const __grid_constant__ CopyParams p) {
+  griddep_wait();
+  const int parts = 2 * p.cache.H;
+  const int i = blockIdx.x / parts, part = blockIdx.x - i * parts, h = part >> 1;
+  const int from = __ldg(p.copies + 3 * i), to = __ldg(p.copies + 3 * i + 1), tokens = __ldg(p.copies + 3 * i + 2);
+  if (from == -1) return;
+  if (from < 0 || from >= p.cache.num_pages || to < 0 || to >= p.cache.num_pages || tokens < 0 ||
+      tokens > p.cache.page) {
+    if (threadIdx.x == 0) report(p.status, RELPOS_ERR_PAGE);
+    return;
+  }
+  if (from == to || tokens == 0) return;
+  const long long src = static_cast<long long>(from) * p.cache.H + h, dst = static_cast<long long>(to) * p.cache.H + h;
+  const long long page_bytes = static_cast<long long>(p.cache.page) * p.row_bytes;
+  uint8_t* const base = static_cast<uint8_t*>(part & 1 ? p.cache.v : p.cache.k);
+  const uint4* s = reinterpret_cast<const uint4*>(base + src * page_bytes);
+  uint4* d = reinterpret_cast<uint4*>(base + dst * page_bytes);
+  const int n = tokens * p.row_bytes / 16;
+  for (int x = threadIdx.x; x < n; x += kCopyThreads) d[x] = s[x];
+  if (p.cache.dtype == RELPOS_E4M3 && threadIdx.x == 0) {
+    float* scale = part & 1 ? p.cache.v_scale : p.cache.k_scale;
+    scale[dst] = scale[src];
+  }
+}
+
+// ------------------------------------------------------------------ compact
+
+constexpr int kCompactThreads = 128;
+constexpr int kMaxKept = 64;
+constexpr int kSpan = kMaxKept / 32 + 1;  // pages that as many slots touch
+
+struct CompactParams {
+  RelposPagedCache cache;
+  int row_bytes, log_page;
+  const int* table;
+  long long table_stride;
+  int max_pages;
+  const int* lens;
+  const int* nodes;
+  int n;
+  const int* kept;
+  long long kept_stride;
+  int m;
+  const int* counts;
+  int* status;
+};
+
+// x (a code's value) times `had` over a scale that is no power of two, to the
+// nearest code: the quotient in 64 bits towards zero, its last bit made odd where
+// something was dropped, so that the rounding to a code is the only one.
+RP_DEVI uint32_t code_rescaled(float x, float had, float want) {
+  const double y = static_cast<double>(x) * had;  // 4 and 24 bits: exact
+  double q = __ddiv_rz(y, static_cast<double>(want));
+  if (isfinite(q) && fma(-q, static_cast<double>(want), y) != 0.0)
+    q = __longlong_as_double(__double_as_longlong(q) | 1);
+  return __nv_cvt_double_to_fp8(q, __NV_SATFINITE, __NV_E4M3);
+}
+
+// 16 codes of a page with scale `had` as codes with scale `want`
+RP_DEVI uint4 rescaled16(uint4 u, float had, float want) {
+  if (had == want) return u;
+  if (is_pow2(want)) {
+    const float ratio = had / want;
+    const uint2 a = moved8(make_uint2(u.x, u.y), ratio), b = moved8(make_uint2(u.z, u.w), ratio);
+    return make_uint4(a.x, a.y, b.x, b.y);
+  }
+  uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll 1
+  for (int e = 0; e < 4; ++e) {
+    uint32_t out = 0;
+#pragma unroll 1
+    for (int s = 0; s < 32; s += 8) {
+      const __half_raw r = __nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(w[e] >> s & 0xffu), __NV_E4M3);
+      out |= code_rescaled(__half2float(__half(r)), had, want) << s;
+    }
+    w[e] = out;
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// of two scales the one of the larger magnitude (NaN: the other)
+RP_DEVI float larger(float a, float b) { return !(fabsf(b) <= fabsf(a)) && b == b ? b : a; }
+
+// A block takes one head's keys or values of one sequence: it holds every kept
+// token's row in registers before it writes the first, so that rows may be taken
+// in any order.
+__global__ void __launch_bounds__(kCompactThreads) relpos_paged_compact_kernel(const __grid_constant__ CompactParams p) {
+  __shared__ int from[kMaxKept], to[kMaxKept];  // row of the pool (page * slots + slot), -1: none
+  __shared__ float had[kMaxKept];
+  __shared__ float was[kSpan], want[kSpan];     // scales of the pages that take tokens
+  __shared__ int page_no[kSpan];
+  griddep_wait();
+  const int b = blockIdx.y, h = blockIdx.x >> 1, val = blockIdx.x & 1, tid = threadIdx.x;
+  const bool first = blockIdx.x == 0;  // the one that reports
+  const int len = __ldg(p.lens + b);
+  if (len <= 0) return;
+  const int n = p.nodes ? __ldg(p.nodes + b) : p.n;
+  const int count = p.counts ? __ldg(p.counts + b) : min(p.m, n);
+  if (len > static_cast<long long>(p.max_pages) << p.log_page || n < 0 || n > len || count < 0 || count > min(p.m, n)) {
+    if (first && tid == 0)
+      report(p.status, len > static_cast<long long>(p.max_pages) << p.log_page ? RELPOS_ERR_PAGE : RELPOS_ERR_TREE);
+    return;
+  }
+  if (count == 0) return;
+  const bool eight = p.cache.dtype == RELPOS_E4M3;
+  const int base = len - n, page0 = base >> p.log_page, slots = 1 << p.log_page;
+  const int* row = p.table + b * p.table_stride;
+  float* const scale = val ? p.cache.v_scale : p.cache.k_scale;
+  if (tid < kSpan) {
+    const int last = (base + count - 1) >> p.log_page;
+    int page = page0 + tid <= last ? __ldg(row + page0 + tid) : -1;
+    if (page0 + tid <= last && (page < 0 || page >= p.cache.num_pages)) {
+      if (first) report(p.status, RELPOS_ERR_PAGE);
+      page = -1;
+    }
+    page_no[tid] = page;
+    was[tid] = want[tid] = eight && page >= 0 ? scale[static_cast<long long>(page) * p.cache.H + h] : 1.f;
+  }
+  __syncthreads();
+  if (tid < count) {
+    const int j = __ldg(p.kept + b * p.kept_stride + tid);
+    int src = -1;
+    if (j < 0 || j >= n) {
+      if (first) report(p.status, RELPOS_ERR_TREE);
+    } else {
+      const int page = __ldg(row + ((base + j) >> p.log_page));
+      if (page < 0 || page >= p.cache.num_pages) {
+        if (first) report(p.status, RELPOS_ERR_PAGE);
+      } else {
+        src = page;
+      }
+    }
+    const int own = page_no[((base + tid) >> p.log_page) - page0];
+    const bool moves = src >= 0 && own >= 0 && j != tid;
+    from[tid] = moves ? (base + j) & (slots - 1) | src << p.log_page : -1;
+    to[tid] = moves ? (base + tid) & (slots - 1) | own << p.log_page : -1;
+    had[tid] = moves && eight ? scale[static_cast<long long>(src) * p.cache.H + h] : 1.f;
+  }
+  __syncthreads();
+  if (eight && tid < kSpan && page_no[tid] >= 0) {
+    float w = was[tid];
+    const int lo = max(((page0 + tid) << p.log_page) - base, 0), hi = min(((page0 + tid + 1) << p.log_page) - base, count);
+    for (int i = lo; i < hi; ++i)
+      if (from[i] >= 0) w = larger(w, had[i]);
+    want[tid] = w;
+  }
+  uint8_t* const pool = static_cast<uint8_t*>(val ? p.cache.v : p.cache.k);
+  const int chunks = p.row_bytes / 16;
+  // 16 bytes of a pool row of this head
+  auto at = [&](int r, int chunk) {
+    const long long page = r >> p.log_page;
+    return reinterpret_cast<uint4*>(pool + (((page * p.cache.H + h) << p.log_page) + (r & (slots - 1))) * p.row_bytes) + chunk;
+  };
+  constexpr int kHeld = kMaxKept * 16 / kCompactThreads;  // chunks of a thread at most
+  uint4 held[kHeld];
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) {
+    const int x = tid + i * kCompactThreads, t = x / chunks;
+    if (t < count && from[t] >= 0) held[i] = *at(from[t], x - t * chunks);
+  }
+  __syncthreads();
+  if (eight) {
+    // codes in a page whose scale grows move to it (those of the slots that are
+    // written below with them)
+    for (int s = 0; s < kSpan; ++s) {
+      if (page_no[s] < 0 || !(want[s] != was[s])) continue;
+      for (int x = tid; x < slots * chunks; x += kCompactThreads) {
+        uint4* q = at(page_no[s] << p.log_page, x);
+        *q = rescaled16(*q, was[s], want[s]);
+      }
+      if (tid == 0) scale[static_cast<long long>(page_no[s]) * p.cache.H + h] = want[s];
+    }
+    __syncthreads();
+  }
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) {
+    const int x = tid + i * kCompactThreads, t = x / chunks;
+    if (t < count && from[t] >= 0) {
+      const uint4 u = eight ? rescaled16(held[i], had[t], want[((base + t) >> p.log_page) - page0]) : held[i];
+      *at(to[t], x - t * chunks) = u;
+    }
+  }
+}
+
+// ------------------------------------------------------------------ assign
+
+struct AssignParams {
+  const int* refs;
+  int num_pages, log_page;
+  const int* table;
+  long long table_stride;
+  int max_pages;
+  const int* lens;
+  int B;
+  const int* source;
+  const int* new_lens;
+  int B2;
+  int* new_table;
+  long long new_stride;
+  int new_max;
+  int* new_refs;
+  int* copies;
+  int* status;
+};
+
+constexpr int kAssignThreads = 1024, kAssignBlocks = 8, kMaxRows = 8192;
+constexpr int kAssignWarps = kAssignThreads / 32;
+constexpr int kIsCopy = 1 << 30;
+
+// What a new row is made of
+struct NewRow {
+  int full;   // pages that it shares
+  int part;   // tokens in the page after them, which it continues
+  int tail;   // that page, -1: none
+  int pages;  // that it has in the end
+  const int* from;
+};
+
+RP_DEVI int pages_of(int len, int log_page) { return static_cast<int>((static_cast<unsigned>(len) + (1u << log_page) - 1) >> log_page); }
+RP_DEVI bool is_page(const AssignParams& p, int page) { return page >= 0 && page < p.num_pages; }
+
+// tokens of an old row; none where the block table cannot hold them
+RP_DEVI int old_len(const AssignParams& p, int b, bool tell) {
+  const int len = __ldg(p.lens + b);
+  if (len <= static_cast<long long>(p.max_pages) << p.log_page) return max(len, 0);
+  if (tell) report(p.status, RELPOS_ERR_PAGE);
+  return 0;
+}
+
+RP_DEVI NewRow new_row(const AssignParams& p, int i, bool tell) {
+  int want = __ldg(p.new_lens + i);
+  if (want > static_cast<long long>(p.new_max) << p.log_page) {
+    if (tell) report(p.status, RELPOS_ERR_PAGE);
+    want = 0;
+  }
+  want = max(want, 0);
+  int s = p.source ? __ldg(p.source + i) : i < p.B ? i : -1;
+  if (s < -1 || s >= p.B) {
+    if (tell) report(p.status, RELPOS_ERR_PAGE);
+    s = -1;
+  }
+  const int keep = s < 0 ? 0 : min(old_len(p, s, false), want);
+  NewRow r;
+  r.from = p.table + (s < 0 ? 0 : s * p.table_stride);
+  r.full = keep >> p.log_page;
+  r.part = keep & ((1 << p.log_page) - 1);
+  r.tail = r.part ? __ldg(r.from + r.full) : -1;
+  if (!is_page(p, r.tail)) r.tail = -1;
+  r.pages = pages_of(want, p.log_page);
+  return r;
+}
+
+// One cluster does it all: its barriers (under a microsecond) stand between the
+// passes over the rows and the pages, which take little time themselves.
+__global__ void __cluster_dims__(kAssignBlocks, 1, 1) __launch_bounds__(kAssignThreads)
+    relpos_paged_assign_kernel(const __grid_constant__ AssignParams p) {
+  extern __shared__ int rows_s[];
+  int* const first = rows_s;           // [B2 + 1] fresh pages of the rows before
+  int* const at = rows_s + p.B2 + 1;   // [B2] entry of a row's first fresh page (and kIsCopy)
+  __shared__ int sums[kAssignWarps + 1];
+  __shared__ int free_of[kAssignBlocks];  // free pages of each block's share
+  cg::cluster_group cluster = cg::this_cluster();
+  const int rank = cluster.block_rank();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int all = rank * kAssignThreads + tid, warps = kAssignBlocks * kAssignWarps;
+  griddep_wait();
+
+  for (int i = all; i < p.num_pages; i += kAssignBlocks * kAssignThreads) {
+    const int r = __ldg(p.refs + i);
+    if (r < 0) report(p.status, RELPOS_ERR_PAGE);
+    p.new_refs[i] = max(r, 0);
+  }
+  cluster.sync();
+
+  // the old rows' references go; more of them than a page has are an error
+  for (int b = rank * kAssignWarps + warp; b < p.B; b += warps) {
+    const int* row = p.table + b * p.table_stride;
+    const int n = pages_of(old_len(p, b, lane == 0), p.log_page);
+    for (int j = lane; j < n; j += 32) {
+      const int page = __ldg(row + j);
+      if (!is_page(p, page)) {
+        report(p.status, RELPOS_ERR_PAGE);
+      } else if (atomicSub(p.new_refs + page, 1) <= 0) {
+        atomicAdd(p.new_refs + page, 1);
+        report(p.status, RELPOS_ERR_PAGE);
+      }
+    }
+  }
+  cluster.sync();
+
+  // the pages that new rows share
+  for (int i = rank * kAssignWarps + warp; i < p.B2; i += warps) {
+    const NewRow r = new_row(p, i, lane == 0);
+    int* out = p.new_table + i * p.new_stride;
+    for (int j = lane; j < p.new_max; j += 32) {
+      int page = -1;
+      if (j < r.full) {
+        page = __ldg(r.from + j);
+        if (is_page(p, page))
+          atomicAdd(p.new_refs + page, 1);
+        else
+          page = -1;
+      }
+      out[j] = page;
+    }
+    if (lane < 3) p.copies[3 * i + lane] = -1;
+  }
+  cluster.sync();
+
+  // A last page that is filled in part and that nobody else holds goes to the
+  // lowest row that continues it: the count, which is 0, takes that row.
+  for (int i = all; i < p.B2; i += kAssignBlocks * kAssignThreads) {
+    const NewRow r = new_row(p, i, false);
+    if (r.tail >= 0 && __ldcg(p.new_refs + r.tail) <= 0) atomicMin(p.new_refs + r.tail, INT_MIN + i);
+  }
+  cluster.sync();
+
+  // Fresh pages that each row needs, and their sums, in every block; the free
+  // pages of this block's share.
+  int before = 0;
+  for (int i0 = 0; i0 < p.B2; i0 += kAssignThreads) {
+    const int i = i0 + tid;
+    int need = 0;
+    if (i < p.B2) {
+      const NewRow r = new_row(p, i, false);
+      const bool stays = r.tail >= 0 && __ldcg(p.new_refs + r.tail) == INT_MIN + i;
+      need = r.pages - r.full - stays;
+      at[i] = (r.full + stays) | (r.tail >= 0 && !stays ? kIsCopy : 0);
+      if (stays && rank == 0) p.new_table[i * p.new_stride + r.full] = r.tail;
+    }
+    int upto = need;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += y;
+    }
+    __syncthreads();
+    if (lane == 31) sums[warp] = upto;
+    __syncthreads();
+    int base = before;
+    for (int w = 0; w < kAssignWarps; ++w) {
+      if (w < warp) base += sums[w];
+      before += sums[w];
+    }
+    if (i < p.B2) first[i] = base + upto - need;
+  }
+  const int total = before;
+  // a warp's pages: a run of whole 32s
+  const int run = (p.num_pages + 32 * warps - 1) / (32 * warps) * 32;
+  const int page0 = min((rank * kAssignWarps + warp) * run, p.num_pages), page1 = min(page0 + run, p.num_pages);
+  int mine = 0;
+  for (int i = page0 + lane; i - lane < page1; i += 32)
+    mine += __popc(__ballot_sync(0xffffffffu, i < page1 && __ldcg(p.new_refs + i) == 0));
+  __syncthreads();
+  if (lane == 0) sums[warp] = mine;
+  __syncthreads();
+  int rest = 0, of_block = 0;
+  for (int w = 0; w < kAssignWarps; ++w) {
+    if (w < warp) rest += sums[w];
+    of_block += sums[w];
+  }
+  if (tid < kAssignBlocks) *cluster.map_shared_rank(free_of + rank, tid) = of_block;
+  if (tid == 0) first[p.B2] = total;
+  cluster.sync();
+
+  // the rows that keep a last page, and the k-th free page to the k-th request
+  for (int i = all; i < p.B2; i += kAssignBlocks * kAssignThreads) {
+    const NewRow r = new_row(p, i, false);
+    if (r.tail >= 0 && !(at[i] & kIsCopy)) p.new_refs[r.tail] = 1;
+  }
+  int free_all = 0;
+  for (int w = 0; w < kAssignBlocks; ++w) {
+    if (w < rank) rest += free_of[w];
+    free_all += free_of[w];
+  }
+  if (all == 0 && total > free_all) report(p.status, RELPOS_ERR_PAGE);
+  for (int i = page0 + lane; i - lane < page1 && rest < total; i += 32) {
+    const bool is_free = i < page1 && __ldcg(p.new_refs + i) == 0;
+    const unsigned some = __ballot_sync(0xffffffffu, is_free);
+    const int k = rest + __popc(some & ((1u << lane) - 1));
+    rest += __popc(some);
+    if (!is_free || k >= total) continue;
+    int lo = 0, hi = p.B2;  // the last row with first[row] <= k has a request there
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (first[mid] <= k) lo = mid; else hi = mid;
+    }
+    const int j = (at[lo] & ~kIsCopy) + k - first[lo];
+    p.new_table[lo * p.new_stride + j] = i;
+    p.new_refs[i] = 1;
+    if (k == first[lo] && (at[lo] & kIsCopy)) {
+      const NewRow r = new_row(p, lo, false);
+      p.copies[3 * lo] = r.tail;
+      p.copies[3 * lo + 1] = i;
+      p.copies[3 * lo + 2] = r.part;
+    }
+  }
+}
+
+int log_of(int page) { return page == 32 ? 5 : page == 64 ? 6 : page == 128 ? 7 : -1; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+template <class P>
+cudaError_t launch(void (*kernel)(P), dim3 grid, int threads, size_t smem, void* stream, const P& p) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p);
+  if (e != cudaSuccess) cudaGetLastError();
+  return e;
+}
+
+}  // namespace
+}  // namespace relpos
+
+using namespace relpos;
+
+extern "C" int relpos_paged_copy(const RelposPagedCache* cache, const int* copies, int N, void* stream) {
+  const int rc = check_paged_cache(cache);
+  if (rc != RELPOS_OK) return rc;
+  if (N < 0) return RELPOS_ERR_INVALID_ARG;
+  if (N == 0 || cache->H == 0 || cache->num_pages == 0) return RELPOS_OK;
+  if (!copies || !aligned4(copies)) return RELPOS_ERR_INVALID_ARG;
+  const long long blocks = 2ll * N * cache->H;
+  if (blocks > INT_MAX) return RELPOS_ERR_UNSUPPORTED;
+  CopyParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.cache = *cache;
+  p.copies = copies;
+  p.N = N;
+  p.row_bytes = cache->d * (cache->dtype == RELPOS_E4M3 ? 1 : 2);
+  p.status = device_status();
+  if (!p.status) return RELPOS_ERR_CUDA;
+  return launch(relpos_paged_copy_kernel, dim3(static_cast<unsigned>(blocks)), kCopyThreads, 0, stream, p) == cudaSuccess
+             ? RELPOS_OK
+             : RELPOS_ERR_CUDA;
+}
+
+extern "C" int relpos_paged_compact(const RelposPagedCache* cache, int B, const int* block_table,
+                                    long long table_stride, int max_pages, const int* lens, const int* nodes, int n,
+                                    const int* kept, long long kept_stride, int m, const int* counts, void* stream) {
+  const int rc = check_paged_cache(cache);
+  if (rc != RELPOS_OK) return rc;
+  if (B < 0 || max_pages < 0 || n < 0 || m < 0) return RELPOS_ERR_INVALID_ARG;
+  if (m > kMaxKept || B > 65535) return RELPOS_ERR_UNSUPPORTED;
+  if (B == 0 || m == 0 || cache->H == 0) return RELPOS_OK;
+  if (!block_table || !lens || !kept || !aligned4(block_table) || !aligned4(lens) || !aligned4(kept) ||
+      !aligned4(nodes) || !aligned4(counts))
+    return RELPOS_ERR_INVALID_ARG;
+  if (max_pages == 0 || cache->num_pages == 0) return RELPOS_ERR_INVALID_ARG;
+  if (B > 1 && (table_stride < max_pages || kept_stride < m)) return RELPOS_ERR_INVALID_ARG;
+  // a slot of the pool as a 32-bit number
+  if (static_cast<long long>(cache->num_pages) * cache->page > INT_MAX ||
+      static_cast<long long>(max_pages) * cache->page > (1 << 28))
+    return RELPOS_ERR_UNSUPPORTED;
+  CompactParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.cache = *cache;
+  p.row_bytes = cache->d * (cache->dtype == RELPOS_E4M3 ? 1 : 2);
+  p.log_page = log_of(cache->page);
+  p.table = block_table;
+  p.table_stride = table_stride;
+  p.max_pages = max_pages;
+  p.lens = lens;
+  p.nodes = nodes;
+  p.n = n;
+  p.kept = kept;
+  p.kept_stride = kept_stride;
+  p.m = m;
+  p.counts = counts;
+  p.status = device_status();
+  if (!p.status) return RELPOS_ERR_CUDA;
+  return launch(relpos_paged_compact_kernel, dim3(2 * cache->H, B), kCompactThreads, 0, stream, p) == cudaSuccess
+             ? RELPOS_OK
+             : RELPOS_ERR_CUDA;
+}
+
+extern "C" int relpos_paged_assign(const int* refs, int num_pages, int page, const int* block_table,
+                                   long long table_stride, int max_pages, const int* lens, int B, const int* source,
+                                   const int* new_lens, int B2, int* new_table, long long new_stride, int new_max_pages,
+                                   int* new_refs, int* copies, void* stream) {
+  if (num_pages < 0 || B < 0 || B2 < 0 || max_pages < 0 || new_max_pages < 0 || page <= 0) return RELPOS_ERR_INVALID_ARG;
+  const int log_page = log_of(page);
+  if (log_page < 0 || B2 > kMaxRows || static_cast<long long>(std::max(max_pages, new_max_pages)) * page > (1 << 28) ||
+      static_cast<long long>(B2) * new_max_pages > INT_MAX || static_cast<long long>(B) * max_pages > INT_MAX)
+    return RELPOS_ERR_UNSUPPORTED;
+  if (!aligned4(refs) || !aligned4(block_table) || !aligned4(lens) || !aligned4(source) || !aligned4(new_lens) ||
+      !aligned4(new_table) || !aligned4(new_refs) || !aligned4(copies))
+    return RELPOS_ERR_INVALID_ARG;
+  if (num_pages > 0 && (!refs || !new_refs)) return RELPOS_ERR_INVALID_ARG;
+  if (B > 0 && (!lens || (max_pages > 0 && !block_table))) return RELPOS_ERR_INVALID_ARG;
+  if (B2 > 0 && (!new_lens || !copies || (new_max_pages > 0 && !new_table))) return RELPOS_ERR_INVALID_ARG;
+  if ((B > 1 && table_stride < max_pages) || (B2 > 1 && new_stride < new_max_pages)) return RELPOS_ERR_INVALID_ARG;
+  if (new_table && new_table == block_table) return RELPOS_ERR_INVALID_ARG;
+  if (num_pages == 0 && B2 == 0) return RELPOS_OK;
+  AssignParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.refs = refs;
+  p.num_pages = num_pages;
+  p.log_page = log_page;
+  p.table = block_table;
+  p.table_stride = table_stride;
+  p.max_pages = max_pages;
+  p.lens = lens;
+  p.B = B;
+  p.source = source;
+  p.new_lens = new_lens;
+  p.B2 = B2;
+  p.new_table = new_table;
+  p.new_stride = new_stride;
+  p.new_max = new_max_pages;
+  p.new_refs = new_refs;
+  p.copies = copies;
+  p.status = device_status();
+  if (!p.status) return RELPOS_ERR_CUDA;
+  const size_t smem = (2 * static_cast<size_t>(B2) + 1) * sizeof(int);
+  if (smem > 40 * 1024 &&
+      cudaFuncSetAttribute(relpos_paged_assign_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           (2 * kMaxRows + 1) * sizeof(int)) != cudaSuccess) {
+    cudaGetLastError();
+    return RELPOS_ERR_CUDA;
+  }
+  return launch(relpos_paged_assign_kernel, dim3(kAssignBlocks), kAssignThreads, smem, stream, p) == cudaSuccess
+             ? RELPOS_OK
+             : RELPOS_ERR_CUDA;
+}

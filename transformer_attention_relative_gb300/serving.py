@@ -1,4 +1,5 @@
-"""Rotary positions and the paged key/value cache over CUDA tensors.
+"""Rotary positions and the paged key/value cache over CUDA tensors: appending, decoding (also trees of drafted
+tokens), keeping accepted drafts, giving out and copying pages.
 
 Marshalling only, as in the package's other functions: checks of types, shapes
 and strides, allocation of the outputs, and one call of the C entry point on the
@@ -41,7 +42,8 @@ def _lib():
     global _entries
     if _entries is None:
         lib = load_library()
-        _entries = (lib.relpos_rotary, lib.relpos_paged_append, lib.relpos_paged_decode)
+        _entries = (lib.relpos_rotary, lib.relpos_paged_append, lib.relpos_paged_decode, lib.relpos_paged_tree_decode,
+                    lib.relpos_paged_compact, lib.relpos_paged_assign, lib.relpos_paged_copy)
     return _entries
 
 
@@ -246,6 +248,34 @@ def paged_append(cache, K, V, block_table, lens, *, cu_new=None, plan=None, stre
         raise RelposError(rc, "relpos_paged_append")
 
 
+def _check_counts(x, B, name):
+    """Pointer to an int32 [B] tensor, None for None."""
+    if x is None:
+        return None
+    if x.dtype != _int32:
+        raise TypeError(f"{name} must be int32")
+    if x.shape != (B,) or (B > 1 and x.stride(0) != 1):
+        raise ValueError(f"{name} must be a contiguous [B]")
+    return x.data_ptr()
+
+
+def _check_bias(bias, mode, num_buckets, max_distance, Hq):
+    """(mode, pointer) of a decode's bias as the C entry points take them."""
+    if mode is None:
+        if bias is not None:
+            raise ValueError("a bias needs its mode")
+        return RELPOS_NO_BIAS, None
+    if mode != MODE_T5 and mode != MODE_ALIBI:
+        raise ValueError("mode must be None, MODE_T5 or MODE_ALIBI")
+    if not 0 < max_distance <= _MOST:
+        raise ValueError("max_distance must be positive and fit 32 bits")
+    if bias is None or bias.dtype != torch.float32 or not bias.is_contiguous():
+        raise TypeError("bias must be a contiguous fp32 tensor")
+    if bias.shape != ((num_buckets, Hq) if mode == MODE_T5 else (Hq,)):
+        raise ValueError("bias must be [num_buckets, Hq] for MODE_T5, [Hq] for MODE_ALIBI")
+    return mode, bias.data_ptr()
+
+
 def paged_decode(Q, cache, block_table, lens, *, bias=None, mode=None, num_buckets: int = 32,
                  max_distance: int = 128, scale: float = 0.0, out=None, stream=None):
     """Run ``relpos_paged_decode``: attention of each sequence's newest rows over its cached tokens; returns ``out``.
@@ -270,23 +300,133 @@ def paged_decode(Q, cache, block_table, lens, *, bias=None, mode=None, num_bucke
     step, pages = _check_table(block_table, lens, B)
     index = cache._index
     _check_device(index, Q, out, block_table, lens, bias)
-    if mode is None:
-        if bias is not None:
-            raise ValueError("a bias needs its mode")
-        mode, ptr = RELPOS_NO_BIAS, None
-    else:
-        if mode != MODE_T5 and mode != MODE_ALIBI:
-            raise ValueError("mode must be None, MODE_T5 or MODE_ALIBI")
-        if not 0 < max_distance <= _MOST:
-            raise ValueError("max_distance must be positive and fit 32 bits")
-        if bias is None or bias.dtype != torch.float32 or not bias.is_contiguous():
-            raise TypeError("bias must be a contiguous fp32 tensor")
-        if bias.shape != ((num_buckets, Hq) if mode == MODE_T5 else (Hq,)):
-            raise ValueError("bias must be [num_buckets, Hq] for MODE_T5, [Hq] for MODE_ALIBI")
-        ptr = bias.data_ptr()
+    mode, ptr = _check_bias(bias, mode, num_buckets, max_distance, Hq)
     rc = _lib()[2](cache._ref, Q.data_ptr(), _strides(q0, q1, q2), B, Hq, Lq, block_table.data_ptr(), step,
                    pages, lens.data_ptr(), mode, ptr, num_buckets, max_distance, scale, out.data_ptr(),
                    _strides(o0, o1, o2), _raw_stream(index) if stream is None else stream.cuda_stream)
     if rc != RELPOS_OK:
         raise RelposError(rc, "relpos_paged_decode")
     return out
+
+
+def paged_tree_decode(Q, cache, block_table, lens, parents, *, nodes=None, bias=None, mode=None, num_buckets: int = 32,
+                      max_distance: int = 128, scale: float = 0.0, out=None, stream=None):
+    """Run ``relpos_paged_tree_decode``: attention of the nodes of each sequence's tree of drafted tokens; returns ``out``.
+
+    Q bf16 [B,Hq,n,d] (n <= 64) holds the nodes, the last ``nodes[b]`` (int32 [B]; all n without it) of the lens[b] cached
+    tokens. parents int32 [B,n], or [n] for one tree of all: an earlier node, or -1 for one that follows the context. A row
+    sees the context, itself and its ancestors; node i is at position lens[b] - nodes[b] + its depth. Rows without a node
+    are zero. The other arguments as ``paged_decode``.
+    """
+    if Q.dtype != _bf16 or (out is not None and out.dtype != _bf16):
+        raise TypeError("Q and out must be bf16")
+    B, Hq, n, d = Q.shape
+    if d != cache.head_dim:
+        raise ValueError("Q must have the cache's head dimension")
+    if parents.dtype != _int32:
+        raise TypeError("parents must be int32")
+    if parents.shape != (B, n) and parents.shape != (n,):
+        raise ValueError("parents must be [B, n] or [n]")
+    if n > 1 and parents.stride(-1) != 1:
+        raise ValueError("parents must be contiguous along a tree")
+    up = parents.stride(0) if parents.dim() == 2 else 0
+    if out is None:
+        out = _empty_like(Q) if stream is None else _output_of(stream, lambda: _empty_like(Q))
+    elif out.shape != Q.shape:
+        raise ValueError("out must have Q's shape")
+    q0, q1, q2, q3 = Q.stride()
+    o0, o1, o2, o3 = out.stride()
+    if q3 != 1 or o3 != 1:
+        raise ValueError("the last dimension must be contiguous")
+    step, pages = _check_table(block_table, lens, B)
+    index = cache._index
+    _check_device(index, Q, out, block_table, lens, parents, nodes, bias)
+    mode, ptr = _check_bias(bias, mode, num_buckets, max_distance, Hq)
+    rc = _lib()[3](cache._ref, Q.data_ptr(), _strides(q0, q1, q2), B, Hq, n, block_table.data_ptr(), step, pages,
+                   lens.data_ptr(), _check_counts(nodes, B, "nodes"), parents.data_ptr(), up, mode, ptr, num_buckets,
+                   max_distance, scale, out.data_ptr(), _strides(o0, o1, o2),
+                   _raw_stream(index) if stream is None else stream.cuda_stream)
+    if rc != RELPOS_OK:
+        raise RelposError(rc, "relpos_paged_tree_decode")
+    return out
+
+
+def paged_compact(cache, block_table, lens, kept, n, *, counts=None, stream=None):
+    """Run ``relpos_paged_compact``: of each sequence's drafted tokens keep the nodes ``kept[b, :counts[b]]``, in that order.
+
+    ``lens`` (int32 [B]) counts the drafted tokens, ``n`` of every sequence or an int32 [B] of their numbers; kept int32
+    [B, m] (m <= 64); counts int32 [B], all m (or n) without it. Afterwards sequence b has lens[b] - n[b] + counts[b] tokens.
+    """
+    if kept.dtype != _int32:
+        raise TypeError("kept must be int32")
+    B, m = kept.shape
+    if m > 1 and kept.stride(1) != 1:
+        raise ValueError("rows of kept must be contiguous")
+    if isinstance(n, torch.Tensor):
+        nodes, drafted = n, 0
+    else:
+        nodes, drafted = None, n
+        if not 0 <= n <= _MOST:
+            raise ValueError("n must be a number of tokens")
+    step, pages = _check_table(block_table, lens, B)
+    index = cache._index
+    _check_device(index, block_table, lens, kept, nodes, counts)
+    rc = _lib()[4](cache._ref, B, block_table.data_ptr(), step, pages, lens.data_ptr(), _check_counts(nodes, B, "n"), drafted,
+                   kept.data_ptr(), kept.stride(0), m, _check_counts(counts, B, "counts"),
+                   _raw_stream(index) if stream is None else stream.cuda_stream)
+    if rc != RELPOS_OK:
+        raise RelposError(rc, "relpos_paged_compact")
+
+
+def paged_assign(refs, block_table, lens, new_lens, page_size: int, *, source=None, max_pages=None, stream=None):
+    """Run ``relpos_paged_assign``: pages for sequences that grow, shrink, end or go on from others.
+
+    refs int32 [num_pages] counts the references to each page; block_table int32 [B, max_pages] and lens int32 [B] are the
+    rows so far. New row i continues row ``source[i]`` (int32 [B2]; -1 a new sequence; without it row i) and gets pages for
+    new_lens[i] (int32 [B2]) tokens. Returns (new block table [B2, max_pages], new refs, copies int32 [B2, 3]); ``copies`` go
+    to ``paged_copy``, once for every layer's cache, before the new rows are written.
+    """
+    if refs.dtype != _int32 or new_lens.dtype != _int32:
+        raise TypeError("refs and new_lens must be int32")
+    if refs.dim() != 1 or not refs.is_contiguous() or new_lens.dim() != 1:
+        raise ValueError("refs must be a contiguous [num_pages] and new_lens [B2]")
+    B, B2, P = lens.shape[0], new_lens.shape[0], refs.shape[0]
+    step, pages = _check_table(block_table, lens, B)
+    if max_pages is None:
+        max_pages = pages
+    if not 0 <= max_pages <= _MOST:
+        raise ValueError("max_pages must be a number of pages")
+    if P > _MOST:
+        raise ValueError("more pages than 32-bit integers hold")
+    index = refs.get_device()
+    _check_device(index, block_table, lens, new_lens, source)
+    if source is None and B2 != B:
+        raise ValueError("without sources there are as many new rows as old ones")
+    src, want = _check_counts(source, B2, "source"), _check_counts(new_lens, B2, "new_lens")
+    if stream is None:
+        table, counts, copies = block_table.new_empty((B2, max_pages)), _empty_like(refs), refs.new_empty((B2, 3))
+    else:
+        table, counts, copies = (_output_of(stream, lambda: refs.new_empty(s)) for s in ((B2, max_pages), (P,), (B2, 3)))
+    rc = _lib()[5](refs.data_ptr(), P, page_size, block_table.data_ptr(), step, pages, lens.data_ptr(), B, src, want, B2,
+                   table.data_ptr(), max_pages, max_pages, counts.data_ptr(), copies.data_ptr(),
+                   _raw_stream(index) if stream is None else stream.cuda_stream)
+    if rc != RELPOS_OK:
+        raise RelposError(rc, "relpos_paged_assign")
+    return table, counts, copies
+
+
+def paged_copy(cache, copies, *, stream=None):
+    """Run ``relpos_paged_copy``: for each row (from, to, tokens) of ``copies`` (int32 [N, 3]; from -1: none) the first
+    ``tokens`` slots of page ``from``, keys, values and scales, go to page ``to``."""
+    if copies.dtype != _int32:
+        raise TypeError("copies must be int32")
+    if copies.dim() != 2 or copies.shape[1] != 3 or not copies.is_contiguous():
+        raise ValueError("copies must be a contiguous [N, 3]")
+    if copies.shape[0] > _MOST:
+        raise ValueError("more copies than 32-bit integers hold")
+    index = cache._index
+    _check_device(index, copies)
+    rc = _lib()[6](cache._ref, copies.data_ptr(), copies.shape[0],
+                   _raw_stream(index) if stream is None else stream.cuda_stream)
+    if rc != RELPOS_OK:
+        raise RelposError(rc, "relpos_paged_copy")
