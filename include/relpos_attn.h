@@ -639,6 +639,9 @@ int relpos_paged_decode(const RelposPagedCache* cache, const void* Q, const Relp
  */
 int relpos_selftest_paged_decode_split(const RelposPagedCache* cache, int B, int Hq, int Lq, int max_pages, int* rows,
                                        int* launches);
+/* the same for a relpos_paged_tree_decode of n nodes (rows 8, 16, or up to 128 on the tensor cores' wide products) */
+int relpos_selftest_paged_tree_split(const RelposPagedCache* cache, int B, int Hq, int n, int max_pages, int* rows,
+                                     int* launches);
 
 /*
  * ---------------------------------------------------------------------------

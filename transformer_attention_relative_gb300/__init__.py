@@ -38,7 +38,7 @@ EXPORTED = ("relpos_attn_fwd", "relpos_attn_fwd_padded", "relpos_index_ids", "re
             "relpos_t5_attn_bwd", "relpos_alibi_attn_bwd", "relpos_shaw_attn_bwd", "relpos_deberta_attn_bwd",
             "relpos_alibi_decode_positions", "relpos_rotary_plan_init", "relpos_rotary", "relpos_paged_append",
             "relpos_paged_decode", "relpos_selftest_paged_decode_split", "relpos_paged_tree_decode",
-            "relpos_paged_compact", "relpos_paged_assign", "relpos_paged_copy")
+            "relpos_paged_compact", "relpos_paged_assign", "relpos_paged_copy", "relpos_selftest_paged_tree_split")
 
 _lib = None
 
@@ -118,6 +118,8 @@ def load_library(path: str = LIB_PATH):
     lib.relpos_paged_decode.restype = i
     lib.relpos_selftest_paged_decode_split.argtypes = [p(_PagedCache), i, i, i, i, p(i), p(i)]
     lib.relpos_selftest_paged_decode_split.restype = i
+    lib.relpos_selftest_paged_tree_split.argtypes = [p(_PagedCache), i, i, i, i, p(i), p(i)]
+    lib.relpos_selftest_paged_tree_split.restype = i
     lib.relpos_paged_tree_decode.argtypes = [p(_PagedCache), vp, p(_RowStrides), i, i, i, vp, ll, i, vp, vp, vp, ll, i, vp,
                                              i, i, f, vp, p(_RowStrides), vp]
     lib.relpos_paged_tree_decode.restype = i
@@ -247,6 +249,11 @@ def relpos_paged_decode(cache, Q, q_strides, B, Hq, Lq, block_table, table_strid
 def relpos_selftest_paged_decode_split(cache, B, Hq, Lq, max_pages, rows, launches) -> int:
     """Rows of a unit and launches of a paged decode of these sizes, on the current device."""
     return load_library().relpos_selftest_paged_decode_split(cache, B, Hq, Lq, max_pages, rows, launches)
+
+
+def relpos_selftest_paged_tree_split(cache, B, Hq, n, max_pages, rows, launches) -> int:
+    """Rows of a unit and launches of a tree decode of these sizes, on the current device."""
+    return load_library().relpos_selftest_paged_tree_split(cache, B, Hq, n, max_pages, rows, launches)
 
 
 def relpos_paged_tree_decode(cache, Q, q_strides, B, Hq, n, block_table, table_stride, max_pages, lens, nodes, parents,

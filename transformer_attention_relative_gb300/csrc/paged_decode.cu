@@ -9,6 +9,7 @@
 #include <cstdint>
 #include <cstring>
 #include <mutex>
+#include <type_traits>
 
 #include "../../include/relpos_attn.h"
 #include "paged_decode.cuh"
@@ -129,7 +130,10 @@ template <class P>
 struct Split {
   PagedVariant<P> v;
   int rows, rt, blocks, direct;
+  bool wide;  // the kernel of paged_wide.cu in place of v.decode
 };
+
+constexpr int kWideFrom = 17;  // rows of a key/value head
 
 template <class P>
 int split_of(const RelposPagedCache* cache, int B, int Hq, int Lq, int max_pages, Split<P>* out) {
@@ -137,6 +141,20 @@ int split_of(const RelposPagedCache* cache, int B, int Hq, int Lq, int max_pages
   if (G > 65535) return RELPOS_ERR_UNSUPPORTED;
   const long long capacity = static_cast<long long>(max_pages) * cache->page;
   if (capacity > (1 << 28)) return RELPOS_ERR_UNSUPPORTED;
+  out->wide = std::is_same_v<P, PagedTreeParams> && G * Lq >= kWideFrom;
+  if (out->wide) {
+    out->rt = (G * Lq + kWideRows - 1) / kWideRows;
+    out->rows = (G * Lq + out->rt - 1) / out->rt;
+    const long long units = static_cast<long long>(B) * cache->H * out->rt;
+    const long long tiles = (capacity + kWideTile - 1) / kWideTile;
+    if (units > (1 << 30) || units * (tiles + kWideUnitCost) > (1 << 30)) return RELPOS_ERR_UNSUPPORTED;
+    if (static_cast<long long>(cache->num_pages) * cache->H > 0x7fffffffll) return RELPOS_ERR_UNSUPPORTED;
+    const int sms = device_sms();
+    if (sms <= 0) return RELPOS_ERR_CUDA;
+    out->direct = tiles <= 2;
+    out->blocks = static_cast<int>(out->direct ? units : std::min<long long>(sms, units * tiles));
+    return RELPOS_OK;
+  }
   out->v = variant_of<P>(cache->d, cache->dtype, 1);
   out->rt = (G * Lq + 7) / 8;
   long long units = static_cast<long long>(B) * cache->H * out->rt;
@@ -204,7 +222,7 @@ int decode_call(const RelposPagedCache* cache, const void* Q, const RelposRowStr
   Split<P> split;
   rc = split_of(cache, B, Hq, Lq, max_pages, &split);
   if (rc != RELPOS_OK) return rc;
-  const PagedVariant<P>& v = split.v;
+  PagedVariant<P> v = split.v;
   const long long capacity = static_cast<long long>(max_pages) * cache->page;
 
   p.k = static_cast<const uint8_t*>(cache->k);
@@ -250,6 +268,11 @@ int decode_call(const RelposPagedCache* cache, const void* Q, const RelposRowStr
     p.part_ml = scratch + slots * cache->d;
     p.ends = reinterpret_cast<int4*>(p.part_ml + slots * 2);
   }
+  bool ok = true;
+  if constexpr (std::is_same_v<P, PagedTreeParams>) {
+    if (split.wide)
+      ok = paged_wide_launch(cache->d, cache->dtype, *cache, p, p.blocks, &v.combine, s) == RELPOS_OK;
+  }
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -260,7 +283,7 @@ int decode_call(const RelposPagedCache* cache, const void* Q, const RelposRowStr
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  bool ok = cudaLaunchKernelEx(&cfg, v.decode, p) == cudaSuccess;
+  if (!split.wide) ok = cudaLaunchKernelEx(&cfg, v.decode, p) == cudaSuccess;
   if (!p.direct) {
     cfg.dynamicSmemBytes = 0;
     ok = ok && cudaLaunchKernelEx(&cfg, v.combine, p) == cudaSuccess;
@@ -278,20 +301,31 @@ int decode_call(const RelposPagedCache* cache, const void* Q, const RelposRowStr
 
 using namespace relpos;
 
-extern "C" int relpos_selftest_paged_decode_split(const RelposPagedCache* cache, int B, int Hq, int Lq, int max_pages,
-                                                  int* rows, int* launches) {
+template <class P>
+static int selftest_split(const RelposPagedCache* cache, int B, int Hq, int Lq, int most_rows, int max_pages, int* rows,
+                          int* launches) {
   const int rc = check_paged_cache(cache);
   if (rc != RELPOS_OK) return rc;
   if (!rows || !launches || cache->H < 1 || cache->num_pages < 1 || B < 1 || Hq < 1 || Hq % cache->H || Lq < 1 ||
       max_pages < 1)
     return RELPOS_ERR_INVALID_ARG;
-  if (Lq > 8) return RELPOS_ERR_UNSUPPORTED;
-  Split<PagedDecodeParams> split;
+  if (Lq > most_rows) return RELPOS_ERR_UNSUPPORTED;
+  Split<P> split;
   const int err = split_of(cache, B, Hq, Lq, max_pages, &split);
   if (err != RELPOS_OK) return err;
   *rows = split.rows;
   *launches = split.direct ? 1 : 2;
   return RELPOS_OK;
+}
+
+extern "C" int relpos_selftest_paged_decode_split(const RelposPagedCache* cache, int B, int Hq, int Lq, int max_pages,
+                                                  int* rows, int* launches) {
+  return selftest_split<PagedDecodeParams>(cache, B, Hq, Lq, 8, max_pages, rows, launches);
+}
+
+extern "C" int relpos_selftest_paged_tree_split(const RelposPagedCache* cache, int B, int Hq, int n, int max_pages,
+                                                int* rows, int* launches) {
+  return selftest_split<PagedTreeParams>(cache, B, Hq, n, kMaxNodes, max_pages, rows, launches);
 }
 
 extern "C" int relpos_paged_decode(const RelposPagedCache* cache, const void* Q, const RelposRowStrides* qs, int B,

@@ -39,6 +39,9 @@ constexpr int kPdWarps = 4;
 constexpr int kPdThreads = 32 * kPdWarps;
 constexpr int kPdMinTiles = 4;  // fewest tiles of a block's share: one for each warp
 constexpr int kPdUnitCost = 12;  // what a unit costs a block beside its tiles, in tiles
+constexpr int kWideUnitCost = 3;  // the same in tiles of 128 keys (paged_wide.cu)
+template <int KT>
+inline constexpr int unit_extra = KT == 128 ? kWideUnitCost : kPdUnitCost;
 constexpr int kPdBuckets = 256;
 
 // The weights p are kept as 2^(logit - off) for a row offset `off` that starts
@@ -123,6 +126,11 @@ PagedTreeVariant paged_tree_e4m3_64(int rows8);
 PagedTreeVariant paged_tree_e4m3_128(int rows8);
 PagedTreeVariant paged_tree_bf16_64(int rows8);
 PagedTreeVariant paged_tree_bf16_128(int rows8);
+
+// Units of up to 128 rows on the tensor cores' 128-row products (paged_wide.cu)
+constexpr int kWideRows = 128, kWideTile = 128;
+int paged_wide_launch(int d, int dtype, const RelposPagedCache& cache, const PagedTreeParams& p, int blocks,
+                      void (**combine)(PagedTreeParams), cudaStream_t stream);
 
 namespace {
 
@@ -236,7 +244,7 @@ struct Cursor {
 // Cost of a sequence's unit
 template <int KT>
 RP_DEVI int unit_cost(int len) {
-  return len > 0 ? (len + KT - 1) / KT + kPdUnitCost : 0;
+  return len > 0 ? (len + KT - 1) / KT + unit_extra<KT> : 0;
 }
 
 template <int KT, class P>
@@ -273,20 +281,20 @@ RP_DEVI Cursor locate(const P& p, int lane, int len0, int x, int& unit_at, int& 
       seqs += __popc(some & ((1u << l) - 1));
       c.b = b0 + l;
       c.len = __shfl_sync(0xffffffffu, len, l);
-      c.nt = unit - kPdUnitCost;
+      c.nt = unit - unit_extra<KT>;
       c.pages = p.table + c.b * p.table_stride;
       c.u = (x - cost * per) / unit;
       unit_at = cost * per + c.u * unit;
-      c.t = max(x - unit_at - kPdUnitCost, 0);
+      c.t = max(x - unit_at - unit_extra<KT>, 0);
       c.h = c.u / p.rt;
-      before = (cost - seqs * kPdUnitCost) * per + c.u * c.nt + c.t;
+      before = (cost - seqs * unit_extra<KT>) * per + c.u * c.nt + c.t;
       return c;
     }
     cost += __shfl_sync(0xffffffffu, upto, 31);
     seqs += __popc(some);
   }
   unit_at = cost * per;
-  before = (cost - seqs * kPdUnitCost) * per;
+  before = (cost - seqs * unit_extra<KT>) * per;
   return c;
 }
 
