@@ -33,6 +33,11 @@ PagedTreeVariant variant_of<PagedTreeParams>(int d, int dtype, int rows8) {
   return d == 64 ? paged_tree_bf16_64(rows8) : paged_tree_bf16_128(rows8);
 }
 
+PagedWideLaunch* wide_of(int d, int dtype) {
+  if (dtype == RELPOS_E4M3) return d == 64 ? paged_wide_e4m3_64 : paged_wide_e4m3_128;
+  return d == 64 ? paged_wide_bf16_64 : paged_wide_bf16_128;
+}
+
 constexpr int kDevices = 64;
 std::mutex g_mu;  // guards what is kept between calls below
 
@@ -130,18 +135,18 @@ template <class P>
 struct Split {
   PagedVariant<P> v;
   int rows, rt, blocks, direct;
-  bool wide;  // the kernel of paged_wide.cu in place of v.decode
+  bool wide;  // the kernel of paged_wide.cuh in place of v.decode
 };
 
 constexpr int kWideFrom = 17;  // rows of a key/value head
 
 template <class P>
-int split_of(const RelposPagedCache* cache, int B, int Hq, int Lq, int max_pages, Split<P>* out) {
+int split_of(const RelposPagedCache* cache, int B, int Hq, int Lq, int max_pages, int near, Split<P>* out) {
   const int G = Hq / cache->H;
   if (G > 65535) return RELPOS_ERR_UNSUPPORTED;
   const long long capacity = static_cast<long long>(max_pages) * cache->page;
   if (capacity > (1 << 28)) return RELPOS_ERR_UNSUPPORTED;
-  out->wide = std::is_same_v<P, PagedTreeParams> && G * Lq >= kWideFrom;
+  out->wide = std::is_same_v<P, PagedTreeParams> && G * Lq >= kWideFrom && static_cast<long long>(G) * near <= kWideLut;
   if (out->wide) {
     out->rt = (G * Lq + kWideRows - 1) / kWideRows;
     out->rows = (G * Lq + out->rt - 1) / out->rt;
@@ -219,11 +224,15 @@ int decode_call(const RelposPagedCache* cache, const void* Q, const RelposRowStr
   if (bias_mode != RELPOS_NO_BIAS && !bias) return RELPOS_ERR_INVALID_ARG;
   if (max_pages == 0 || cache->num_pages == 0) return RELPOS_ERR_INVALID_ARG;
   if (B > 1 && table_stride < max_pages) return RELPOS_ERR_INVALID_ARG;
+  const long long capacity = static_cast<long long>(max_pages) * cache->page;
+  if (bias_mode == RELPOS_T5 && capacity <= (1 << 28)) {
+    rc = set_t5(num_buckets, max_distance, static_cast<int>(capacity), &p);
+    if (rc != RELPOS_OK) return rc;
+  }
   Split<P> split;
-  rc = split_of(cache, B, Hq, Lq, max_pages, &split);
+  rc = split_of(cache, B, Hq, Lq, max_pages, bias_mode == RELPOS_T5 ? p.t5_R + 1 : 0, &split);
   if (rc != RELPOS_OK) return rc;
   PagedVariant<P> v = split.v;
-  const long long capacity = static_cast<long long>(max_pages) * cache->page;
 
   p.k = static_cast<const uint8_t*>(cache->k);
   p.v = static_cast<const uint8_t*>(cache->v);
@@ -245,10 +254,6 @@ int decode_call(const RelposPagedCache* cache, const void* Q, const RelposRowStr
   p.B = B, p.Hq = Hq, p.Lq = Lq, p.G = Hq / cache->H, p.rows = split.rows, p.rt = split.rt;
   p.bias = static_cast<const float*>(bias);
   p.mode = bias_mode;
-  if (bias_mode == RELPOS_T5) {
-    rc = set_t5(num_buckets, max_distance, static_cast<int>(capacity), &p);
-    if (rc != RELPOS_OK) return rc;
-  }
   p.scale_log2 = (scale != 0.f ? scale : 1.0f / std::sqrt(static_cast<float>(cache->d))) * kLog2e;
   p.status = device_status();
   if (!p.status) return RELPOS_ERR_CUDA;
@@ -271,7 +276,7 @@ int decode_call(const RelposPagedCache* cache, const void* Q, const RelposRowStr
   bool ok = true;
   if constexpr (std::is_same_v<P, PagedTreeParams>) {
     if (split.wide)
-      ok = paged_wide_launch(cache->d, cache->dtype, *cache, p, p.blocks, &v.combine, s) == RELPOS_OK;
+      ok = wide_of(cache->d, cache->dtype)(*cache, p, p.blocks, &v.combine, s) == RELPOS_OK;
   }
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -311,7 +316,7 @@ static int selftest_split(const RelposPagedCache* cache, int B, int Hq, int Lq, 
     return RELPOS_ERR_INVALID_ARG;
   if (Lq > most_rows) return RELPOS_ERR_UNSUPPORTED;
   Split<P> split;
-  const int err = split_of(cache, B, Hq, Lq, max_pages, &split);
+  const int err = split_of(cache, B, Hq, Lq, max_pages, 0, &split);
   if (err != RELPOS_OK) return err;
   *rows = split.rows;
   *launches = split.direct ? 1 : 2;

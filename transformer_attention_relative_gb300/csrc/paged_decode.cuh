@@ -39,7 +39,7 @@ constexpr int kPdWarps = 4;
 constexpr int kPdThreads = 32 * kPdWarps;
 constexpr int kPdMinTiles = 4;  // fewest tiles of a block's share: one for each warp
 constexpr int kPdUnitCost = 12;  // what a unit costs a block beside its tiles, in tiles
-constexpr int kWideUnitCost = 3;  // the same in tiles of 128 keys (paged_wide.cu)
+constexpr int kWideUnitCost = 3;  // the same in tiles of 128 keys (paged_wide.cuh)
 template <int KT>
 inline constexpr int unit_extra = KT == 128 ? kWideUnitCost : kPdUnitCost;
 constexpr int kPdBuckets = 256;
@@ -127,10 +127,12 @@ PagedTreeVariant paged_tree_e4m3_128(int rows8);
 PagedTreeVariant paged_tree_bf16_64(int rows8);
 PagedTreeVariant paged_tree_bf16_128(int rows8);
 
-// Units of up to 128 rows on the tensor cores' 128-row products (paged_wide.cu)
-constexpr int kWideRows = 128, kWideTile = 128;
-int paged_wide_launch(int d, int dtype, const RelposPagedCache& cache, const PagedTreeParams& p, int blocks,
-                      void (**combine)(PagedTreeParams), cudaStream_t stream);
+// Units of up to 256 rows on the tensor cores' 128-row products (paged_wide.cuh)
+constexpr int kWideRows = 256, kWideTile = 128;
+constexpr int kWideLut = 2048;  // T5 biases of near distances that it keeps, of all heads of a group
+using PagedWideLaunch = int(const RelposPagedCache& cache, const PagedTreeParams& p, int blocks,
+                            void (**combine)(PagedTreeParams), cudaStream_t stream);
+PagedWideLaunch paged_wide_bf16_64, paged_wide_bf16_128, paged_wide_e4m3_64, paged_wide_e4m3_128;
 
 namespace {
 

@@ -1,0 +1,1067 @@
+// paged_wide.cuh -- attention of trees of drafted tokens over a paged key/value
+// cache where many rows share a key/value head: the kernel of paged_decode.cuh
+// with the 128-row products of the tensor cores (tcgen05) in place of 8 or 16 rows
+// ("Relative Position Embeddings, in depth", section "Kernels and the KV cache").
+//
+//   S = Q K^T (128 rows x 128 keys, in tensor memory), P = 2^(S scale + bias - m),
+//   O += P V,  out = O / sum P
+//
+// A unit is a sequence, key/value head and some of its rows (query heads of the
+// group times nodes). Two softmax warpgroups share its key tiles in one of three ways:
+//   up to 256 rows (PAIR): each takes half the rows and every tile;
+//   up to 128 rows: each takes all rows and every other tile;
+//   up to 64 or 32 rows (REP = 2, 4): the same, and the rows stand 2 or 4 times in the
+//     128 of a product, each copy with a half or quarter of a tile's keys: as many
+//     products, but a thread has 64 or 32 exponentials a tile, and the chain from
+//     scores to weights, which few rows cannot hide, is as much shorter.
+// What the warpgroups and copies hold apart (maximum, sum, O) is joined at the unit's
+// end. Blocks take equal shares of all units' tiles, as in paged_decode.cuh, one block
+// an SM.
+//
+//   warp 0        producer: a tile's pages, K and V in turn, into a ring of shared
+//                 memory (bf16: tensor copies, swizzled; e4m3: bulk copies).
+//   warps 1, 3    issuers of the products, one for each softmax warpgroup.
+//   warps 4-11    the softmax warpgroups; thread t holds row t of a product.
+//   warps 12-15   a unit's query rows into shared memory; e4m3: codes to 16-bit tiles;
+//                 both: values that some row must not see.
+//
+// Number formats. bf16 caches: weights enter the product as two bf16 parts, 16 bits
+// together, since bf16 alone would round them as coarsely as the output. 8-bit caches:
+// where the page scales of a unit's tiles lie within 2^15 of each other, codes times
+// the scale's power of two over the largest one are exact in fp16, weights are fp16
+// (11 bits down to 2^-19 of a row's largest weight, 2^-30 of it below) and query rows
+// fp16 after a power of two that brings their largest value into [1, 2). Elsewhere
+// (zero pages, scales that are not finite) codes times that power of two are bf16,
+// exact at any scale, with weights in two parts. The rest of a scale that is no power
+// of two goes to the scores (keys) and weights (values) in fp32.
+//
+// Tiles that hold a drafted slot or the sequence's end, or with T5 distances below
+// the last bucket, go through tensor memory once more: their logits, masks included,
+// are formed 16 columns at a time in a loop and written back, and the common path
+// takes them as they are. Values of drafted slots that are not finite are zeros in
+// the products (0 times them would be NaN in rows that must not see them); rows that
+// do see one add it at the end.
+
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <cstdint>
+#include <cstring>
+
+#include "paged_decode.cuh"
+#include "relpos_internal.h"
+#include "serving_internal.h"
+
+namespace relpos {
+namespace {
+
+constexpr int kWideThreads = 512;
+constexpr uint32_t kTmemCols = 512, kColS = 0, kColO = 256;  // S (then P) of warpgroup x at 128 x, O at 256 + x D
+constexpr float kRescale = 8.f;  // the running maximum moves when a row's grows by this (log2)
+constexpr float kF16Shift = 5.f;  // fp16 weights are 2^5 times those of bf16: up to 2^13 (2^14 with a scale's rest)
+constexpr int kF16Window = 15;    // exponents of page scales below the largest
+
+// REP: copies of the rows in a product; 0: PAIR
+template <int D, bool FP8, int REP>
+struct Wide {
+  static constexpr bool kPair = REP == 0;
+  static constexpr int kCopies = kPair ? 1 : REP;
+  static constexpr int kLanes = 128 / kCopies;                        // rows of a copy, and keys of a row in it
+  static constexpr int kRows = kPair ? 256 : kLanes;                  // of a unit at most
+  static constexpr int kHalves = D / 64;
+  static constexpr uint32_t kQTile = 128 * D * 2;
+  static constexpr uint32_t kTile = 128 * D * 2;                      // a 16-bit tile of keys or values
+  static constexpr uint32_t kRaw = 128 * D;                           // and of codes
+  static constexpr int kSlots = FP8 ? (D == 64 ? 6 : 3) : (D == 64 ? 8 : 4);  // 16-bit tiles
+  // positions between two values in one slot: with an odd number of slots keys and
+  // values take turns there
+  static constexpr int kValueTurn = kSlots % 2 ? 2 * kSlots : kSlots;
+  static constexpr int kRawSlots = FP8 ? (D == 64 ? 6 : kPair ? 3 : 3) : 0;
+  static constexpr uint32_t kOffQ = 0;
+  static constexpr uint32_t kOffTile = kOffQ + (kPair ? 2 : 1) * kQTile;
+  static constexpr uint32_t kOffRaw = kOffTile + kSlots * kTile;
+  static constexpr uint32_t kOffJoin = kOffRaw + kRawSlots * kRaw;    // REP > 1: 32 columns of 256 rows to be joined
+  static constexpr uint32_t kOffLut = kOffJoin + (kCopies > 1 ? 256 * 33 * 4 : 0);
+  static constexpr uint32_t kOffLine = kOffLut + kWideLut * 4;        // ancestors' words
+  static constexpr uint32_t kOffDeep = kOffLine + kMaxNodes * 8;      // depths
+  static constexpr uint32_t kOffMl = kOffDeep + kMaxNodes * 4;        // [2][128] maximum and sum
+  static constexpr uint32_t kOffQx = kOffMl + 2 * 128 * 8;            // [2][256] exponents of query rows
+  static constexpr uint32_t kOffInfo = kOffQx + 2 * 256 * 4;          // [2] UnitInfo
+  static constexpr uint32_t kOffBar = kOffInfo + 64;
+  // barriers
+  static constexpr uint32_t kFull = 0;                                // tile slots: written
+  static constexpr uint32_t kEmpty = kFull + kSlots;                  // and read
+  static constexpr uint32_t kRawFull = kEmpty + kSlots;
+  static constexpr uint32_t kRawEmpty = kRawFull + kRawSlots;
+  static constexpr uint32_t kQFull = kRawEmpty + kRawSlots;
+  static constexpr uint32_t kQEmpty = kQFull + 1;
+  static constexpr uint32_t kSFull = kQEmpty + 1;                     // + warpgroup
+  static constexpr uint32_t kPFull = kSFull + 2;
+  static constexpr uint32_t kODone = kPFull + 2;
+  static constexpr uint32_t kOFree = kODone + 2;
+  static constexpr uint32_t kClean = kOFree + 2;                      // bf16: a slot's values looked through
+  static constexpr uint32_t kFinal = kClean + (FP8 ? 0 : kSlots);
+  static constexpr uint32_t kBars = kFinal + 2;
+  static constexpr uint32_t kOffMisc = kOffBar + kBars * 8;           // TMEM address, foul flag, 8 ints of the converters
+  static constexpr uint32_t kSmem = kOffMisc + 64 + 1024;             // and room to align
+};
+
+// What the converters find out about a unit's tiles in this block, for the others
+struct UnitInfo {
+  int f16;     // fp16 products, else bf16
+  int ek, ev;  // fp16: exponents that keys and values are in units of
+};
+
+// A block's units, as each role walks them
+struct Walk {
+  Cursor c;
+  int tiles, x, xe;  // tiles of the block; those of the present unit [x, xe)
+  int base, live;    // first drafted slot, nodes
+  RP_DEVI void load(const PagedTreeParams& p) {
+    xe = min(tiles, x + c.nt - c.t);
+    live = row_count(p, c.b);
+    base = c.len - live;
+  }
+  RP_DEVI bool next(const PagedTreeParams& p) {
+    c.template forward<kWideTile>(p, xe - x);
+    x = xe;
+    if (x >= tiles) return false;
+    load(p);
+    return true;
+  }
+  // tile j of the unit's in this block; whether it needs masks
+  RP_DEVI int key0(int j) const { return (c.t + j) * kWideTile; }
+  RP_DEVI bool special(int j) const { return key0(j) + kWideTile > base; }
+};
+
+// 2^e and the rest (1 <= |m| < 2) of a page's scale; what has no such parts stays whole
+RP_DEVI void split_scale(float s, float& pow2, float& m) {
+  const uint32_t e = __float_as_uint(s) & 0x7f800000u;
+  const bool whole = e == 0u || e == 0x7f800000u;
+  pow2 = whole ? s : __uint_as_float(e);
+  m = whole ? 1.f : __uint_as_float((__float_as_uint(s) & 0x807fffffu) | 0x3f800000u);
+}
+
+RP_DEVI void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+RP_DEVI void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+RP_DEVI float half_lo(uint32_t h) { return __half2float(__ushort_as_half(static_cast<unsigned short>(h))); }
+RP_DEVI float half_hi(uint32_t h) { return __half2float(__ushort_as_half(static_cast<unsigned short>(h >> 16))); }
+RP_DEVI bool foul_bf16(uint32_t w) { return __vcmpeq2(w & 0x7f807f80u, 0x7f807f80u) != 0; }
+
+RP_DEVI void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+RP_DEVI void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+RP_DEVI void tmem_ld8_wait(uint32_t (&r)[8]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7])::"memory");
+}
+RP_DEVI void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
+RP_DEVI void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+RP_DEVI void tmem_ld16_wait(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                 "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
+}
+RP_DEVI uint32_t mul_half2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+RP_DEVI int exponent_of(float s) { return static_cast<int>(__float_as_uint(s) >> 23 & 255u) - 127; }
+// x 2^e for any e (one rounding where the result is below the normal numbers)
+RP_DEVI float times_pow2(float x, int e) {
+  const int a = min(max(e, -126), 127), b = min(max(e - a, -126), 127);
+  return x * __uint_as_float(static_cast<uint32_t>(a + 127) << 23) * __uint_as_float(static_cast<uint32_t>(b + 127) << 23);
+}
+
+// two codes times a scale as bf16
+RP_DEVI uint32_t bf16_of(uint32_t h2, float s) { return pack_bf16x2(half_lo(h2) * s, half_hi(h2) * s); }
+
+template <int D, bool FP8, int REP>
+__global__ void __launch_bounds__(kWideThreads, 1)
+    relpos_paged_wide_kernel(const __grid_constant__ PagedTreeParams p, const __grid_constant__ CUtensorMap tm_k,
+                             const __grid_constant__ CUtensorMap tm_v) {
+  using W = Wide<D, FP8, REP>;
+  constexpr int KT = kWideTile;
+  constexpr bool kPair = W::kPair;
+  constexpr int kStep = kPair ? 1 : 2;  // a warpgroup's tiles: x, x + 2, .. or all
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  uint8_t* const smem = smem_raw + (sbase - smem_u32(smem_raw));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  auto bar = [&](uint32_t i) { return sbase + W::kOffBar + 8 * i; };
+  volatile int* const foul = reinterpret_cast<volatile int*>(smem + W::kOffMisc + 4);
+  UnitInfo* const infos = reinterpret_cast<UnitInfo*>(smem + W::kOffInfo);
+  int* const q_exp = reinterpret_cast<int*>(smem + W::kOffQx);
+
+  if (threadIdx.x == 0) {
+    for (uint32_t i = 0; i < W::kBars; ++i) {
+      uint32_t n = 1;
+      if (FP8 && i < W::kEmpty) n = 128;                        // converted by a warpgroup
+      if (i >= W::kEmpty && i < W::kRawFull) n = kPair ? 2 : 1; // read by both issuers' products
+      if (i >= W::kRawEmpty && i < W::kQFull) n = 4;            // a warp each
+      if (i == W::kQFull) n = 128;
+      if (i == W::kQEmpty) n = 2;                               // both issuers
+      if (i >= W::kClean && i < W::kFinal) n = 4;
+      if (i == W::kPFull || i == W::kPFull + 1) n = 128;
+      if (i == W::kOFree || i == W::kOFree + 1) n = 256;
+      mbar_init(bar(i), n);
+    }
+    *foul = 0;
+    fence_mbar_init();
+  }
+  if (warp == 2) {
+    tmem_alloc(sbase + W::kOffMisc, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + W::kOffMisc);
+
+  griddep_wait();
+  Walk w;
+  int size = 0, at = 0;  // cost of a block's share, and that at which the present unit starts
+  {
+    const int per = p.Hkv * p.rt;
+    if (p.direct) {
+      w.c.b = blockIdx.x / per;
+      w.c.u = blockIdx.x - w.c.b * per;
+      w.c.t = 0;
+      w.c.len = seq_len(p, w.c.b);
+      w.c.nt = w.tiles = (w.c.len + KT - 1) / KT;
+      w.c.h = w.c.u / p.rt;
+      w.c.pages = p.table + w.c.b * p.table_stride;
+      if (w.tiles == 0) {  // no key is seen: zero rows
+        if (threadIdx.x == 0) report_length(p, w.c.b);
+        const int row0 = (w.c.u - w.c.h * p.rt) * p.rows;
+        for (int i = threadIdx.x; i < min(p.G * p.Lq - row0, p.rows) * D; i += kWideThreads) {
+          const int r = row0 + i / D, qi = r / p.G;
+          p.out[w.c.b * p.o_batch + (w.c.h * p.G + r - qi * p.G) * p.o_head + qi * p.o_row + i % D] =
+              __float2bfloat16_rn(0.f);
+        }
+      }
+    } else {
+      const int len0 = seq_len(p, lane);
+      const int total = total_cost<KT>(p, lane, len0);
+      size = max((total + p.blocks - 1) / p.blocks, 1 + unit_extra<KT>);
+      if (threadIdx.x == 128) p.ends[2 * blockIdx.x] = p.ends[2 * blockIdx.x + 1] = make_int4(0, 0, 0, 0);
+      const int begin = min(static_cast<int>(blockIdx.x) * size, total);
+      int first, last, unused;
+      locate<KT>(p, lane, len0, min(begin + size, total), unused, last);
+      w.c = locate<KT>(p, lane, len0, begin, at, first);
+      w.tiles = begin == total ? 0 : last - first;
+    }
+    w.x = 0;
+  }
+  const bool some = w.tiles > 0;
+  if (some) w.load(p);
+  bool ok = true;
+
+  if (warp < 4) {
+    setmaxnreg_dec<56>();
+    if (warp == 0 && some) {
+      // ------------------------------------------------------------ producer
+      uint32_t pos = 0;  // of the ring: K of tile i at 2 i, V behind it
+      const int per_tile = KT >> p.log_page;  // pages of a tile
+      constexpr int kRing = FP8 ? W::kRawSlots : W::kSlots;
+      constexpr uint32_t kSlotBytes = FP8 ? W::kRaw : W::kTile;
+      const uint32_t full0 = FP8 ? W::kRawFull : W::kFull, empty0 = FP8 ? W::kRawEmpty : W::kEmpty;
+      const uint32_t ring = sbase + (FP8 ? W::kOffRaw : W::kOffTile);
+      const uint32_t none = static_cast<uint32_t>(p.num_pages) * p.Hkv;  // beyond the pool: zeros
+      do {
+        for (int j = 0; ok && j < w.xe - w.x; ++j) {
+          const int key = w.key0(j) + (lane << p.log_page);
+          int page = -1;
+          bool there = false;
+          if (lane < per_tile && key < w.c.len) {
+            page = __ldg(w.c.pages + (key >> p.log_page));
+            there = page >= 0 && page < p.num_pages;
+            if (!there) atomicCAS(p.status, 0, RELPOS_ERR_PAGE);
+          }
+          const uint32_t ph = there ? static_cast<uint32_t>(page) * p.Hkv + w.c.h : none;
+          const uint32_t n = __popc(__ballot_sync(0xffffffffu, there));
+          for (int kv = 0; ok && kv < 2; ++kv, ++pos) {
+            const uint32_t slot = pos % kRing;
+            if (pos >= kRing) ok = mbar_wait_warp(bar(empty0 + slot), (pos / kRing - 1) & 1);
+            if (!ok) break;
+            const uint32_t dst = ring + slot * kSlotBytes;
+            if (lane == 0)
+              mbar_arrive_expect_tx(bar(full0 + slot), FP8 ? (n * W::kRaw) >> (7 - p.log_page) : W::kTile);
+            __syncwarp();
+            if (lane < per_tile) {
+              if constexpr (FP8) {
+                const uint32_t bytes = static_cast<uint32_t>(D) << p.log_page;
+                if (there) bulk_load(dst + lane * bytes, (kv ? p.v : p.k) + static_cast<size_t>(ph) * bytes, bytes, bar(full0 + slot));
+              } else {
+                for (int hf = 0; hf < W::kHalves; ++hf)
+                  tma_load_3d(dst + hf * 16384 + ((lane << p.log_page) * 128), kv ? &tm_v : &tm_k, bar(full0 + slot), 64 * hf,
+                              0, static_cast<int>(ph));
+              }
+            }
+            __syncwarp();
+          }
+        }
+      } while (ok && w.next(p));
+      // never leave with copies in flight
+      for (uint32_t k = pos > kRing ? pos - kRing : 0; k < pos; ++k)
+        mbar_wait_warp(bar(full0 + k % kRing), (k / kRing) & 1, 100000000ull);
+    } else if ((warp == 1 || warp == 3) && some) {
+      // ------------------------------------------------------------ issuers
+      const uint32_t x = warp == 1 ? 0u : 1u;
+      const uint32_t s_col = tmem + kColS + 128 * x, o_col = tmem + kColO + D * x;
+      const uint64_t dq = smem_desc_sw128(sbase + W::kOffQ + (kPair ? x * W::kQTile : 0u), 16, 1024);
+      uint32_t seq = 0, mine = 0, unit = 0;  // tiles before the unit, own products, units
+      do {
+        const int n = w.xe - w.x;
+        ok = mbar_wait_warp(bar(W::kQFull), unit & 1);
+        const bool f16 = FP8 && infos[unit & 1].f16;
+        // the operands' type: bf16 (1) or fp16 (0)
+        const uint32_t types = f16 ? 0u : (1u << 7) | (1u << 10);
+        constexpr uint32_t kTypes = (1u << 7) | (1u << 10);
+        const uint32_t idesc_s = (idesc_bf16_f32(128, KT, 0, 0) & ~kTypes) | types;
+        const uint32_t idesc_o = (idesc_bf16_f32(128, D, 0, 1) & ~kTypes) | types;
+        for (int j = kPair ? 0 : x; ok && j < n; j += kStep) {
+          const uint32_t kp = 2 * (seq + j), vp = kp + 1;
+          const uint32_t ks = kp % W::kSlots, vs = vp % W::kSlots;
+          ok = mbar_wait_warp(bar(W::kFull + ks), (kp / W::kSlots) & 1);
+          // P of the last tile lies in S's columns
+          if (ok && mine > 0) ok = mbar_wait_warp(bar(W::kODone + x), (mine - 1) & 1);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t dk = smem_desc_sw128(sbase + W::kOffTile + ks * W::kTile, 16, 1024);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint64_t off = (kk >> 2) * 1024 + 2 * (kk & 3);
+            umma_bf16_ss_elect(s_col, dq + off, dk + off, idesc_s, kk > 0);
+          }
+          tc_commit_elect(bar(W::kSFull + x));
+          tc_commit_elect(bar(W::kEmpty + ks));
+          if (j + kStep >= n) tc_commit_elect(bar(W::kQEmpty));  // own last scores of the unit
+          ok = mbar_wait_warp(bar(W::kPFull + x), mine & 1);
+          if (ok && j < kStep && unit > 0) ok = mbar_wait_warp(bar(W::kOFree + x), (unit - 1) & 1);
+          if (ok) ok = mbar_wait_warp(bar(W::kFull + vs), (vp / W::kSlots) & 1);
+          if (!FP8 && ok) ok = mbar_wait_warp(bar(W::kClean + vs), (vp / W::kValueTurn) & 1);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t dv = smem_desc_sw128(sbase + W::kOffTile + vs * W::kTile, 16384, 1024);
+#pragma unroll
+          for (int kk = 0; kk < KT / 16; ++kk)
+            umma_bf16_ts_elect(o_col, s_col + 8 * kk, dv + 128 * kk, idesc_o, j >= kStep || kk > 0);
+          if (!f16) {
+#pragma unroll
+            for (int kk = 0; kk < KT / 16; ++kk)
+              umma_bf16_ts_elect(o_col, s_col + 64 + 8 * kk, dv + 128 * kk, idesc_o, 1u);
+          }
+          tc_commit_elect(bar(W::kODone + x));
+          tc_commit_elect(bar(W::kEmpty + vs));
+          ++mine;
+        }
+        if (!kPair && n == 1 && x == 1) tc_commit_elect(bar(W::kQEmpty));  // no tile of the unit
+        seq += n;
+        ++unit;
+      } while (ok && w.next(p));
+      tc_commit_elect(bar(W::kFinal + x));
+      mbar_wait_warp(bar(W::kFinal + x), 0, 100000000ull);
+    }
+  } else if (warp < 12) {
+    setmaxnreg_inc<184>();
+    // -------------------------------------------------------------- softmax
+    const int x = (warp - 4) >> 2, t = threadIdx.x & 127;
+    constexpr int NC = W::kLanes;                    // columns of a thread
+    const int copy = t / NC, col0 = copy * NC;       // NC rows a copy, too
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + lanes + kColS + 128 * x, tO = tmem + lanes + kColO;
+    float* const lut = reinterpret_cast<float*>(smem + W::kOffLut);
+    unsigned long long* const line = reinterpret_cast<unsigned long long*>(smem + W::kOffLine);
+    int* const deep = reinterpret_cast<int*>(smem + W::kOffDeep);
+    float2* const ml = reinterpret_cast<float2*>(smem + W::kOffMl);
+    const int lut_len = p.t5_R + 1;
+    uint32_t mine = 0, unit = 0;
+    int tree_of = -1, lut_of = -1;
+    if (some) do {
+      const int n = w.xe - w.x, len = w.c.len, base = w.base, live = w.live, h = w.c.h;
+      const int row0 = (w.c.u - h * p.rt) * p.rows, rows = min(p.G * p.Lq - row0, p.rows);
+      // the tree, and the biases of the distances below the last bucket's
+      if (tree_of != w.c.b && warp == 4) {
+        tree_lines(p, w.c.b, live, lane, line);
+        __syncwarp();
+        for (int i = lane; i < kMaxNodes; i += 32) deep[i] = i < live ? __popcll(line[i]) - 1 : 0;
+      }
+      tree_of = w.c.b;
+      if (p.mode == RELPOS_T5 && lut_of != h) {
+        for (int i = threadIdx.x - 128; i < p.G * lut_len; i += 256) {
+          const int hl = i / lut_len, back = i - hl * lut_len;
+          const int bucket = back < kPdBuckets ? p.bucket[back] : t5_bucket_dev(-back, p.t5);
+          lut[i] = to_log2(__ldg(p.bias + bucket * p.Hq + h * p.G + hl));
+        }
+        lut_of = h;
+      }
+      named_bar_sync(1, 256);
+      // this thread's row of the unit
+      const int half = (rows + 1) >> 1;
+      const int ri = kPair ? x * half + t : t - col0;
+      const bool real = kPair ? t < half && ri < rows : ri < rows;
+      const int r = row0 + ri, node = r / p.G, hq = h * p.G + r - node * p.G;
+      const bool active = real && node < live;
+      const bool any = __any_sync(0xffffffffu, active);
+      const unsigned long long sees = active ? line[node] : 0ull;
+      const float* const my_lut = lut + (active ? (r - node * p.G) * lut_len : 0);
+      const int depth = active ? __popcll(sees) - 1 : 0;
+      float far = 0.f, slope = 0.f;
+      if (active && p.mode == RELPOS_T5) far = to_log2(__ldg(p.bias + (p.t5.slots - 1) * p.Hq + hq));
+      if (active && p.mode == RELPOS_ALIBI) {
+        slope = __ldg(p.bias + hq) * kLog2e;
+        if (fabsf(slope) > 0x1p90f) slope = copysignf(0x1p90f, slope);
+      }
+      // a constant beside which products lose bits: every tile loses them alike
+      const bool odd = __any_sync(0xffffffffu, !(fabsf(far) <= 4096.f));
+      float scale = p.scale_log2, slope_raw = 0.f;  // of this row's scores
+      bool f16 = false, plain = true;
+      int ev = 0;
+
+      float m_run = -INFINITY, l_run = 0.f;
+      // pages of a tile's 32-key groups and, of 8 bits, their scales' rests: lane
+      // g < 4 has the group's page and key scale, lane 4 + g its value scale
+      int page_ahead = -1;
+      auto look = [&](int j) {
+        const int key = w.key0(j) + 32 * (lane & 3);
+        page_ahead = lane < 8 && j < n && key < len ? __ldg(w.c.pages + (key >> p.log_page)) : -1;
+        if (page_ahead >= p.num_pages) page_ahead = -1;
+      };
+      const int j0 = kPair ? 0 : x;
+      look(j0);
+      for (int j = j0; ok && j < n; j += kStep, ++mine) {
+        const int key0 = w.key0(j);
+        const int page = page_ahead;
+        float rest = 1.f;  // of this lane's scale
+        if (FP8 && page >= 0) {
+          float pow2;
+          split_scale(__ldg((lane < 4 ? p.k_scale : p.v_scale) + static_cast<size_t>(page) * p.Hkv + h), pow2, rest);
+        }
+        look(j + kStep);
+        const unsigned there = __ballot_sync(0xffffffffu, page >= 0) & 0xfu;
+        const unsigned rests = FP8 ? __ballot_sync(0xffffffffu, rest != 1.f) : 0u;
+        ok = __all_sync(0xffffffffu, mbar_wait(bar(W::kSFull + x), mine & 1));
+        if (!ok) break;
+        tc_fence_after();
+        if (j == j0) {
+          if constexpr (FP8) {
+            const UnitInfo info = infos[unit & 1];
+            f16 = info.f16;
+            if (f16) {
+              ev = info.ev;
+              scale = times_pow2(p.scale_log2, info.ek + q_exp[(unit & 1) * 256 + (kPair ? 128 * x + t : ri)]);
+            }
+          }
+          if (p.mode == RELPOS_ALIBI) slope_raw = slope / scale;
+          // scores whose largest is the largest logit, distances that go into them
+          plain = __all_sync(0xffffffffu, !active || (scale > 0.f && fabsf(slope_raw) <= 0x1p60f));
+        }
+        if (any) {
+          const bool near = p.mode == RELPOS_T5 && base - (key0 + KT) < p.t5_R;
+          const bool masks = w.special(j) || there != 0xfu;
+          const bool whole = masks || near || odd || !plain || (rests & 0xfu);
+          if (whole) {  // the scores become logits
+#pragma unroll 1
+            for (int q = 0; q < NC / 16; ++q) {
+              uint32_t s[16];
+              tmem_ld16(tS + col0 + 16 * q, s);
+              const int group = (col0 + 16 * q) >> 5;
+              const float mul = FP8 ? scale * __shfl_sync(0xffffffffu, rest, group) : scale;
+              const int o0 = key0 + col0 + 16 * q - base;  // among the drafted slots
+              unsigned vis = 0xffffu;
+              if (o0 >= 0)
+                vis = o0 < kMaxNodes ? static_cast<unsigned>(sees >> o0) : 0u;
+              else if (o0 > -16)
+                vis = static_cast<unsigned>(sees << -o0) | ((1u << -o0) - 1u);
+              if (!(there >> group & 1)) vis = 0u;
+              float bias[16];
+              if (p.mode == RELPOS_NO_BIAS || (p.mode == RELPOS_T5 && !near)) {
+#pragma unroll
+                for (int c = 0; c < 16; ++c) bias[c] = far;
+              } else {
+                int back[16];
+#pragma unroll
+                for (int c = 0; c < 16; ++c) back[c] = depth - o0 - c;
+                if (o0 > -16) {
+#pragma unroll
+                  for (int c = 0; c < 16; ++c)
+                    if (o0 + c >= 0) back[c] = depth - deep[min(o0 + c, kMaxNodes - 1)];
+                }
+                if (p.mode == RELPOS_T5) {
+#pragma unroll
+                  for (int c = 0; c < 16; ++c) bias[c] = my_lut[min(max(back[c], 0), p.t5_R)];
+                } else {
+#pragma unroll
+                  for (int c = 0; c < 16; ++c) bias[c] = -slope * fabsf(static_cast<float>(back[c]));
+                }
+              }
+              tmem_ld16_wait(s);
+#pragma unroll
+              for (int c = 0; c < 16; ++c)
+                s[c] = vis >> c & 1 ? __float_as_uint(fmaf(__uint_as_float(s[c]), mul, bias[c])) : 0xff800000u;
+              tmem_st16(tS + col0 + 16 * q, s);
+            }
+            tmem_st_wait();
+          }
+          uint32_t sr[NC / 32][32];
+#pragma unroll
+          for (int q = 0; q < NC / 32; ++q) tmem_ld32(tS + col0 + 32 * q, sr[q]);
+#pragma unroll
+          for (int q = 0; q < NC / 32; ++q) tmem_ld_wait(sr[q]);
+          float* const xs = reinterpret_cast<float*>(&sr[0][0]);
+          float addc = 0.f, mul = 1.f;
+          if (!whole) {
+            mul = scale;
+            addc = far;
+            if (p.mode == RELPOS_ALIBI) {  // slope (key - position): a constant and the column's part
+              addc = slope * static_cast<float>(key0 + col0 - base - depth);
+#pragma unroll
+              for (int c = 0; c < NC; c += 2) {
+                const float2 a = __ffma2_rn(make_float2(static_cast<float>(c), static_cast<float>(c + 1)),
+                                            make_float2(slope_raw, slope_raw), make_float2(xs[c], xs[c + 1]));
+                xs[c] = a.x;
+                xs[c + 1] = a.y;
+              }
+            }
+          }
+          float m0 = -INFINITY, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < NC; c += 8) {
+            m0 = max3f(m0, xs[c], xs[c + 1]);
+            m1 = max3f(m1, xs[c + 2], xs[c + 3]);
+            m2 = max3f(m2, xs[c + 4], xs[c + 5]);
+            m3 = max3f(m3, xs[c + 6], xs[c + 7]);
+          }
+          const float top = fmaf(fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)), mul, addc);
+          const float m_new = fmaxf(m_run, top);
+          const bool moves = m_new > m_run + kRescale;
+          const float alpha = moves ? ex2_approx(m_run - m_new) : 1.f;
+          if (moves) m_run = m_new;
+          float off = addc - (m_run == -INFINITY ? 0.f : m_run);
+          if (FP8 && f16) off += kF16Shift;
+          // O's last product is done (S came behind it), and the next waits for P
+          if (j >= kStep && __any_sync(0xffffffffu, moves)) {
+            l_run *= alpha;
+#pragma unroll 1
+            for (int q = 0; q < D / 16; ++q) {
+              uint32_t o[16];
+              tmem_ld16(tO + D * x + 16 * q, o);
+              tmem_ld16_wait(o);
+#pragma unroll
+              for (int c = 0; c < 16; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
+              tmem_st16(tO + D * x + 16 * q, o);
+            }
+          }
+          // weights: P's columns are pairs of keys; other copies' keys are zeros
+          const float2 mul2 = make_float2(mul, mul), off2 = make_float2(off, off);
+          float2 sum0 = make_float2(0.f, 0.f), sum1 = make_float2(0.f, 0.f);
+          const uint32_t tP = tS + col0 / 2;
+          auto weights = [&](auto half_type) {
+            constexpr bool F16 = decltype(half_type)::value;
+#pragma unroll
+            for (int q = 0; q < NC / 32; ++q) {
+              uint32_t hi[16];
+              [[maybe_unused]] uint32_t lo[16];
+              [[maybe_unused]] const float v_rest = FP8 ? __shfl_sync(0xffffffffu, rest, 4 + (col0 >> 5) + q) : 1.f;
+#pragma unroll
+              for (int c = 0; c < 16; ++c) {
+                const float2 z = __ffma2_rn(make_float2(xs[32 * q + 2 * c], xs[32 * q + 2 * c + 1]), mul2, off2);
+                float a = ex2_approx(z.x), b = ex2_approx(z.y);
+                if (c & 1)
+                  sum1 = __fadd2_rn(sum1, make_float2(a, b));
+                else
+                  sum0 = __fadd2_rn(sum0, make_float2(a, b));
+                if constexpr (FP8) a *= v_rest, b *= v_rest;
+                if constexpr (F16) {
+                  hi[c] = pack_half2(a, b);
+                } else {
+                  hi[c] = pack_bf16x2(a, b);
+                  lo[c] = pack_bf16x2(a - __uint_as_float(hi[c] << 16), b - __uint_as_float(hi[c] & 0xffff0000u));
+                }
+              }
+              tmem_st16(tP + 16 * q, hi);
+              if constexpr (!F16) tmem_st16(tP + 64 + 16 * q, lo);
+            }
+            if constexpr (W::kCopies > 1) {
+              uint32_t zero[16];
+#pragma unroll
+              for (int c = 0; c < 16; ++c) zero[c] = 0u;
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                if (q * 32 / NC == copy) continue;
+                tmem_st16(tS + 16 * q, zero);
+                if constexpr (!F16) tmem_st16(tS + 64 + 16 * q, zero);
+              }
+            }
+          };
+          if (FP8 && f16)
+            weights(std::true_type{});
+          else
+            weights(std::false_type{});
+          l_run += (sum0.x + sum0.y) + (sum1.x + sum1.y);
+          tmem_st_wait();
+        }
+        tc_fence_before();
+        mbar_arrive(bar(W::kPFull + x));
+      }
+      // ---- the unit's parts joined. After a wait that ran out a warp goes on without
+      // waiting, so that all meet at the barriers.
+      if (ok && n > j0) ok = __all_sync(0xffffffffu, mbar_wait(bar(W::kODone + x), (mine - 1) & 1));
+      if (f16 && m_run != -INFINITY) m_run -= kF16Shift;  // what O and the sum are relative to
+      ml[128 * x + t] = make_float2(m_run, l_run);
+      // the exponent of O goes with the other warpgroup's too
+      int* const evs = reinterpret_cast<int*>(smem + W::kOffMisc + 48);
+      if (t == 0) evs[x] = ev;
+      named_bar_sync(1, 256);
+      tc_fence_after();
+      const bool whole = w.c.t == 0 && n == w.c.nt;
+      const int slot = 2 * blockIdx.x + (w.c.t == 0 ? 1 : 0);
+      if (!whole && threadIdx.x == 128) {  // the same thread wrote the zeros before
+        const int c0 = (at + unit_extra<KT>) / size;
+        p.ends[slot] = make_int4(c0, (at + unit_extra<KT> + w.c.nt - 1) / size - c0 + 1, w.c.b, w.c.u);
+      }
+      // a weight of 0 would make NaN of what is nothing
+      auto part_of = [](float2 part, float m) { return part.x == -INFINITY ? 0.f : ex2_approx(part.x - m); };
+      auto sum_of = [](float2 part, float by) { return part.y == 0.f ? 0.f : part.y * by; };
+      const float unit_v = times_pow2(1.f, evs[0]);  // (where one warpgroup has tiles, that is 0)
+      // a row's place in the output, or among the parts
+      float* const part = p.part_o + (static_cast<size_t>(slot) * p.rows + ri) * D;
+      __nv_bfloat16* const to = p.out + w.c.b * p.o_batch + hq * p.o_head + node * p.o_row;
+      float m = m_run, sum = l_run;
+      if constexpr (W::kCopies == 1) {
+        float by0 = 1.f, by1 = 0.f;
+        if constexpr (!kPair) {
+          const float2 p0 = ml[t], p1 = ml[128 + t];
+          m = fmaxf(p0.x, p1.x);
+          by0 = part_of(p0, m), by1 = part_of(p1, m);
+          sum = sum_of(p0, by0) + sum_of(p1, by1);
+        }
+        const float inv = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
+        const uint32_t tO0 = tO + (kPair ? D * x : 0);
+        const int from = kPair ? 0 : x * (D / 2), upto = kPair ? D : from + D / 2;
+#pragma unroll 1
+        for (int col = from; col < upto; col += 8) {
+          uint32_t o0[8], o1[8];
+          tmem_ld8(tO0 + col, o0);
+          if (!kPair) tmem_ld8(tO0 + D + col, o1);
+          tmem_ld8_wait(o0);
+          if (!kPair) tmem_ld8_wait(o1);
+          if (!real) continue;
+          float v[8];
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            v[c] = __uint_as_float(o0[c]) * by0;
+            if (!kPair && n > 1) v[c] += __uint_as_float(o1[c]) * by1;
+            v[c] = active ? v[c] * inv * unit_v : 0.f;
+          }
+          if (!whole) {
+            float4* const to4 = reinterpret_cast<float4*>(part + col);
+            to4[0] = make_float4(v[0], v[1], v[2], v[3]);
+            to4[1] = make_float4(v[4], v[5], v[6], v[7]);
+          } else if (p.o_vec) {
+            *reinterpret_cast<uint4*>(to + col) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                                             pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+          } else {
+#pragma unroll
+            for (int c = 0; c < 8; ++c) to[col + c] = __float2bfloat16_rn(v[c]);
+          }
+        }
+      } else {
+        // all copies of both warpgroups, in order, through shared memory
+        constexpr int kParts = 2 * W::kCopies;
+        float2 parts[kParts];
+        m = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < kParts; ++i) {
+          parts[i] = ml[i * NC + ri];
+          m = fmaxf(m, parts[i].x);
+        }
+        sum = 0.f;
+        float mine_by = 0.f;
+#pragma unroll
+        for (int i = 0; i < kParts; ++i) {
+          const float by = part_of(parts[i], m);
+          sum += sum_of(parts[i], by);
+          if (i == x * W::kCopies + copy) mine_by = by;
+        }
+        const float inv = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
+        float* const join = reinterpret_cast<float*>(smem + W::kOffJoin);
+#pragma unroll 1
+        for (int col = 0; col < D; col += 32) {
+          uint32_t o[32];
+          tmem_ld32(tO + D * x + col, o);
+          tmem_ld_wait(o);
+          float* const mine_at = join + (threadIdx.x - 128) * 33;
+#pragma unroll
+          for (int c = 0; c < 32; ++c)
+            mine_at[c] = active && n > x ? __uint_as_float(o[c]) * mine_by * inv * unit_v : 0.f;
+          named_bar_sync(1, 256);
+          // 4 columns of a row a thread
+          for (int i = threadIdx.x - 128; i < rows * 8; i += 256) {
+            const int row = i >> 3, c = 4 * (i & 7);
+            float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int k = 0; k < kParts; ++k)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) v[e] += join[(k * NC + row) * 33 + c + e];
+            const int rr = row0 + row, nd = rr / p.G;
+            if (!whole) {
+              *reinterpret_cast<float4*>(p.part_o + (static_cast<size_t>(slot) * p.rows + row) * D + col + c) =
+                  make_float4(v[0], v[1], v[2], v[3]);
+            } else {
+              __nv_bfloat16* const op =
+                  p.out + w.c.b * p.o_batch + (h * p.G + rr - nd * p.G) * p.o_head + nd * p.o_row + col + c;
+              if (p.o_vec) {
+                *reinterpret_cast<uint2*>(op) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+              } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) op[e] = __float2bfloat16_rn(v[e]);
+              }
+            }
+          }
+          named_bar_sync(1, 256);
+        }
+      }
+      if (*foul && active && copy == 0) {
+        // drafted values of this block's tiles that are not finite, for the rows that
+        // see them: infinities and NaN as their sum
+        const int lo = max(w.key0(0) - base, 0), hi = min(w.key0(n), len) - base;
+        const int from = kPair ? 0 : x * (D / 2), upto = kPair ? D : from + D / 2;
+#pragma unroll 1
+        for (int c = from; c < upto; ++c) {
+          float y = 0.f;
+#pragma unroll 1
+          for (int i = lo; i < hi; ++i) {
+            const int key = base + i, page = sees >> i & 1 ? __ldg(w.c.pages + (key >> p.log_page)) : -1;
+            if (page < 0 || page >= p.num_pages) continue;
+            const size_t ph = static_cast<size_t>(page) * p.Hkv + h;
+            const size_t el = ((ph << p.log_page) + (key & ((1 << p.log_page) - 1))) * D + c;
+            float a;
+            if constexpr (FP8)
+              a = half_lo(half2_lo(__ldg(p.v + el))) * __ldg(p.v_scale + ph);
+            else
+              a = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p.v)[el]);
+            if (!(fabsf(a) <= FLT_MAX)) y += a;
+          }
+          if (y == 0.f) continue;
+          if (whole)
+            to[c] = __float2bfloat16_rn(y);
+          else
+            part[c] = y;
+        }
+      }
+      if (!whole && (kPair || x == 0) && copy == 0 && real)
+        *reinterpret_cast<float2*>(p.part_ml + 2 * (static_cast<size_t>(slot) * p.rows + ri)) =
+            make_float2(m == -INFINITY ? -FLT_MAX : m, sum);
+      tc_fence_before();
+      mbar_arrive(bar(W::kOFree));
+      mbar_arrive(bar(W::kOFree + 1));
+      at += unit_extra<KT> + w.c.nt;
+      ++unit;
+    } while (w.next(p));
+  } else {
+    setmaxnreg_dec<88>();
+    // -------------------------------------------------------------- query rows, values
+    const int t = threadIdx.x & 127, wq = warp & 3;
+    uint32_t unit = 0, seq = 0;
+    int* const range = reinterpret_cast<int*>(smem + W::kOffMisc + 16);  // [4][2] of the warps
+    if (some) do {
+      const int n = w.xe - w.x, len = w.c.len, base = w.base, h = w.c.h;
+      const int row0 = (w.c.u - h * p.rt) * p.rows, rows = min(p.G * p.Lq - row0, p.rows);
+      if (ok && unit > 0) ok = __all_sync(0xffffffffu, mbar_wait(bar(W::kQEmpty), (unit - 1) & 1));
+      bool f16 = false;
+      int ek = 0, ev = 0;
+      if constexpr (FP8) {
+        // exponents of the pages' scales: the largest, and how far below it the
+        // smallest may be (one that has none is as far as can be)
+        int top_k = -200, low_k = 200, top_v = -200, low_v = 200;
+        const int first = w.key0(0) >> p.log_page, last = (min(w.key0(n), len) - 1) >> p.log_page;
+#pragma unroll 4
+        for (int i = first + t; i <= last; i += 128) {
+          const int page = __ldg(w.c.pages + i);
+          if (page < 0 || page >= p.num_pages) continue;
+          const size_t ph = static_cast<size_t>(page) * p.Hkv + h;
+          const float sk = fabsf(__ldg(p.k_scale + ph)), sv = fabsf(__ldg(p.v_scale + ph));
+          const int a = sk >= FLT_MIN && sk <= FLT_MAX ? exponent_of(sk) : -1000;
+          const int b = sv >= FLT_MIN && sv <= FLT_MAX ? exponent_of(sv) : -1000;
+          top_k = max(top_k, a), low_k = min(low_k, a), top_v = max(top_v, b), low_v = min(low_v, b);
+        }
+        top_k = __reduce_max_sync(0xffffffffu, top_k), low_k = __reduce_min_sync(0xffffffffu, low_k);
+        top_v = __reduce_max_sync(0xffffffffu, top_v), low_v = __reduce_min_sync(0xffffffffu, low_v);
+        // 9 bits each (of exponents + 256; clamped)
+        auto bits = [](int e) { return min(max(e + 256, 0), 511); };
+        named_bar_sync(2, 128);  // the last unit's are read
+        if (lane == 0) range[2 * wq] = bits(top_k) << 16 | bits(low_k), range[2 * wq + 1] = bits(top_v) << 16 | bits(low_v);
+        named_bar_sync(2, 128);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          top_k = max(top_k, (range[2 * i] >> 16) - 256), low_k = min(low_k, (range[2 * i] & 0xffff) - 256);
+          top_v = max(top_v, (range[2 * i + 1] >> 16) - 256), low_v = min(low_v, (range[2 * i + 1] & 0xffff) - 256);
+        }
+        f16 = top_k - low_k <= kF16Window && top_v - low_v <= kF16Window;
+        ek = max(top_k, -126), ev = max(top_v, -126);
+        if (t == 0) infos[unit & 1] = UnitInfo{f16, ek, ev};
+      }
+      // query rows: 8 values a lane, D / 8 lanes a row, 4 rows' loads at a time
+      constexpr int kQLanes = D / 8, kQStep = 128 / kQLanes;  // rows of a step
+      constexpr int kQRows = kPair ? 256 : 128;               // of the tiles
+      const int half = (rows + 1) >> 1;
+#pragma unroll 1
+      for (int i0 = 0; i0 < kQRows; i0 += 4 * kQStep) {
+        uint4 u[4];
+        const int c = t % kQLanes;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int line_of = i0 + e * kQStep + t / kQLanes;  // row of the tiles
+          const int ri = kPair ? (line_of >> 7) * half + (line_of & 127) : line_of % W::kLanes;
+          const int r = row0 + ri, node = r / p.G, hq = h * p.G + r - node * p.G;
+          u[e] = make_uint4(0u, 0u, 0u, 0u);
+          if (ri < rows && (!kPair || (line_of & 127) < half) && node < w.live) {
+            const __nv_bfloat16* q = p.Q + w.c.b * p.q_batch + hq * p.q_head + node * p.q_row + 8 * c;
+            if (p.q_vec) {
+              u[e] = __ldg(reinterpret_cast<const uint4*>(q));
+            } else {
+              const unsigned short* y = reinterpret_cast<const unsigned short*>(q);
+              u[e] = make_uint4(y[0] | y[1] << 16, y[2] | y[3] << 16, y[4] | y[5] << 16, y[6] | y[7] << 16);
+            }
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int line_of = i0 + e * kQStep + t / kQLanes;
+          uint32_t y[4] = {u[e].x, u[e].y, u[e].z, u[e].w};
+          if (FP8 && f16) {
+            // to fp16 by way of a power of two that brings the row's largest value into
+            // [1, 2): exact but for values below 2^-14 of it
+            uint32_t big = 0;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) big = __vmaxu2(big, y[k] & 0x7fff7fffu);
+            big = max(big & 0xffffu, big >> 16);
+#pragma unroll
+            for (int o = 1; o < kQLanes; o *= 2) big = max(big, __shfl_xor_sync(0xffffffffu, big, o));
+            const int ex = min(126, max(-126, static_cast<int>(big >> 7) - 127));
+            const float down = __int_as_float((127 - ex) << 23);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              y[k] = pack_half2(__uint_as_float(y[k] << 16) * down, __uint_as_float(y[k] & 0xffff0000u) * down);
+            if (c == 0) q_exp[(unit & 1) * 256 + line_of] = ex;
+          }
+          sts128(sbase + W::kOffQ + (line_of >> 7) * W::kQTile + (c >> 3) * 16384 + (line_of & 127) * 128 +
+                     (((c & 7) ^ (line_of & 7)) << 4),
+                 y[0], y[1], y[2], y[3]);
+        }
+      }
+      fence_async_smem();
+      mbar_arrive(bar(W::kQFull));
+      for (int j = 0; ok && j < n; ++j) {
+        const int key0 = w.key0(j);
+        const bool special = w.special(j);
+        if constexpr (FP8) {
+          // this warp's 32 keys: one page
+          const int key = key0 + 32 * wq;
+          int page = key < len ? __ldg(w.c.pages + (key >> p.log_page)) : -1;
+          if (page >= p.num_pages) page = -1;
+          float s2[2] = {0.f, 0.f}, unused;
+          if (page >= 0) {
+            const size_t ph = static_cast<size_t>(page) * p.Hkv + h;
+            split_scale(__ldg(p.k_scale + ph), s2[0], unused);
+            split_scale(__ldg(p.v_scale + ph), s2[1], unused);
+          }
+          for (int kv = 0; kv < 2; ++kv) {
+            const uint32_t pos = 2 * (seq + j) + kv, rs = pos % W::kRawSlots, cs = pos % W::kSlots;
+            ok = mbar_wait(bar(W::kRawFull + rs), (pos / W::kRawSlots) & 1);
+            if (pos >= W::kSlots) ok = ok && mbar_wait(bar(W::kEmpty + cs), (pos / W::kSlots - 1) & 1);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            const uint32_t raw = sbase + W::kOffRaw + rs * W::kRaw, to = sbase + W::kOffTile + cs * W::kTile;
+            // fp16: in units of the largest scale's power of two
+            const float s = kv ? s2[1] : s2[0];
+            const float s16 = times_pow2(s, -(kv ? ev : ek));
+            const uint32_t by = pack_half2(s16, s16);
+            const bool clean = kv && special && key0 + 32 * wq + 31 >= base;
+            // 8 rows a step, 4 lanes a row (of half a row at d = 128, odd rows the other
+            // half, so that reads and writes meet all banks); 4 steps' loads at a time
+            auto row_of = [&](int it) { return 32 * wq + 8 * (D == 64 ? it : it >> 1) + (lane >> 2); };
+            auto half_of = [&](int it) { return D == 64 ? 0 : (it ^ row_of(it)) & 1; };
+            const int g = lane & 3;
+#pragma unroll
+            for (int it0 = 0; it0 < 4 * W::kHalves; it0 += 4) {
+              uint4 u[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int r = row_of(it0 + e);
+                u[e] = lds128(raw + r * D + half_of(it0 + e) * 64 + g * 16);
+                if (page < 0 || key0 + r >= len) u[e] = make_uint4(0u, 0u, 0u, 0u);
+              }
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int r = row_of(it0 + e);
+                const uint32_t c4[4] = {u[e].x, u[e].y, u[e].z, u[e].w};
+                uint32_t o[8];
+                if (f16) {
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) {
+                    o[2 * k] = mul_half2(half2_lo(c4[k]), by);
+                    o[2 * k + 1] = mul_half2(half2_hi(c4[k]), by);
+                  }
+                } else {
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) {
+                    o[2 * k] = bf16_of(half2_lo(c4[k]), s);
+                    o[2 * k + 1] = bf16_of(half2_hi(c4[k]), s);
+                  }
+                }
+                if (clean && key0 + r >= base) {
+                  const uint32_t ones = f16 ? 0x7c007c00u : 0x7f807f80u;  // exponents of what is not finite
+                  uint32_t bad = key0 + r >= len ? ~0u : 0u;
+#pragma unroll
+                  for (int k = 0; k < 8; ++k) {
+                    const uint32_t no = __vcmpeq2(o[k] & ones, ones);
+                    if (no && key0 + r < len) *foul = 1;
+                    o[k] &= ~(no | bad);
+                  }
+                }
+                const uint32_t to_row = to + half_of(it0 + e) * 16384 + r * 128;
+                sts128(to_row + (((2 * g) ^ (r & 7)) << 4), o[0], o[1], o[2], o[3]);
+                sts128(to_row + (((2 * g + 1) ^ (r & 7)) << 4), o[4], o[5], o[6], o[7]);
+              }
+            }
+            fence_async_smem();
+            mbar_arrive(bar(W::kFull + cs));
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(W::kRawEmpty + rs));
+          }
+        } else {
+          const uint32_t pos = 2 * (seq + j) + 1, vs = pos % W::kSlots;
+          ok = __all_sync(0xffffffffu, mbar_wait(bar(W::kFull + vs), (pos / W::kSlots) & 1));
+          if (!ok) break;
+          const uint32_t to = sbase + W::kOffTile + vs * W::kTile;
+          // rows from the first drafted slot on
+          for (int i = special ? t : 128 * W::kHalves * 8; i < 128 * W::kHalves * 8; i += 128) {
+            const int r = (i >> 3) & 127, key = key0 + r;
+            if (key < base) continue;
+            const uint32_t a = to + (i >> 10) * 16384 + r * 128 + (i & 7) * 16;
+            if (key >= len) {
+              sts128(a, 0u, 0u, 0u, 0u);
+              continue;
+            }
+            const uint4 u = lds128(a);
+            if (foul_bf16(u.x) || foul_bf16(u.y) || foul_bf16(u.z) || foul_bf16(u.w)) {
+              *foul = 1;
+              auto finite = [](uint32_t y) { return y & ~__vcmpeq2(y & 0x7f807f80u, 0x7f807f80u); };
+              sts128(a, finite(u.x), finite(u.y), finite(u.z), finite(u.w));
+            }
+          }
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(W::kClean + vs));
+        }
+      }
+      seq += n;
+      ++unit;
+    } while (w.next(p));  // (after a wait that ran out too, for the barriers' sake)
+  }
+  if (!ok && lane == 0) atomicCAS(p.status, 0, RELPOS_ERR_DEVICE_TIMEOUT);
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 2) tmem_dealloc(tmem, kTmemCols);
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encoder() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      return static_cast<PFN_cuTensorMapEncodeTiled_v12000>(nullptr);
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  }();
+  return fn;
+}
+
+// A pool's pages as [page and head, slot, dim], in boxes of one page's 64 columns
+bool page_map(CUtensorMap* m, const void* pool, const RelposPagedCache& c) {
+  auto fn = encoder();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(c.d), static_cast<cuuint64_t>(c.page),
+                              static_cast<cuuint64_t>(c.num_pages) * c.H};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(c.d) * 2, static_cast<cuuint64_t>(c.d) * 2 * c.page};
+  const cuuint32_t box[3] = {64u, static_cast<cuuint32_t>(c.page), 1u};
+  const cuuint32_t step[3] = {1u, 1u, 1u};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(pool), dims, strides, box, step,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, bool FP8, int REP>
+int launch_wide(const RelposPagedCache& cache, const PagedTreeParams& p, int blocks, void (**combine)(PagedTreeParams),
+                cudaStream_t stream) {
+  using W = Wide<D, FP8, REP>;
+  static_assert(W::kSmem <= 232448, "shared memory of a block");
+  if (cudaFuncSetAttribute(relpos_paged_wide_kernel<D, FP8, REP>, cudaFuncAttributeMaxDynamicSharedMemorySize, W::kSmem) !=
+      cudaSuccess)
+    return RELPOS_ERR_CUDA;
+  CUtensorMap k, v;
+  std::memset(&k, 0, sizeof(k));
+  std::memset(&v, 0, sizeof(v));
+  if (!FP8 && (!page_map(&k, cache.k, cache) || !page_map(&v, cache.v, cache))) return RELPOS_ERR_CUDA;
+  *combine = relpos_paged_combine_kernel<D, PagedTreeParams>;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(kWideThreads);
+  cfg.dynamicSmemBytes = W::kSmem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, relpos_paged_wide_kernel<D, FP8, REP>, p, k, v) == cudaSuccess ? RELPOS_OK : RELPOS_ERR_CUDA;
+}
+
+template <int D, bool FP8>
+int launch_wide(const RelposPagedCache& cache, const PagedTreeParams& p, int blocks, void (**combine)(PagedTreeParams),
+                cudaStream_t stream) {
+  if (p.rows > 128) return launch_wide<D, FP8, 0>(cache, p, blocks, combine, stream);
+  if (p.rows > 64) return launch_wide<D, FP8, 1>(cache, p, blocks, combine, stream);
+  if (p.rows > 32) return launch_wide<D, FP8, 2>(cache, p, blocks, combine, stream);
+  return launch_wide<D, FP8, 4>(cache, p, blocks, combine, stream);
+}
+
+}  // namespace
+}  // namespace relpos
