@@ -11,9 +11,11 @@
 //   up to 256 rows (PAIR): each takes half the rows and every tile;
 //   up to 128 rows: each takes all rows and every other tile;
 //   up to 64 or 32 rows (REP = 2, 4): the same, and the rows stand 2 or 4 times in the
-//     128 of a product, each copy with a half or quarter of a tile's keys: as many
-//     products, but a thread has 64 or 32 exponentials a tile, and the chain from
-//     scores to weights, which few rows cannot hide, is as much shorter.
+//     128 of a product, each copy with a half or quarter of the keys: as many products,
+//     but a thread has a half or quarter of the exponentials, and the chain from scores
+//     to weights, which few rows cannot hide, is as much shorter.
+// A warpgroup goes through its tiles by halves of 64 keys, with a buffer of scores for
+// either half: the scores of the next half are there when a half's weights are done.
 // What the warpgroups and copies hold apart (maximum, sum, O) is joined at the unit's
 // end. Blocks take equal shares of all units' tiles, as in paged_decode.cuh, one block
 // an SM.
@@ -61,38 +63,53 @@ namespace relpos {
 namespace {
 
 constexpr int kWideThreads = 512;
-constexpr uint32_t kTmemCols = 512, kColS = 0, kColO = 256;  // S (then P) of warpgroup x at 128 x, O at 256 + x D
+// S (then P) of warpgroup x and half y of a tile at 128 x + 64 y, O at 256 + x D
+constexpr uint32_t kTmemCols = 512, kColS = 0, kColO = 256;
+constexpr int kHalf = 64;  // keys of a half
 constexpr float kRescale = 8.f;  // the running maximum moves when a row's grows by this (log2)
 constexpr float kF16Shift = 5.f;  // fp16 weights are 2^5 times those of bf16: up to 2^13 (2^14 with a scale's rest)
 constexpr int kF16Window = 15;    // exponents of page scales below the largest
+
+// What the converters know of a tile's 32-key groups, for the softmax; as many as
+// they can be ahead and more
+struct TileInfo {
+  float rest[8];    // of the keys' and the values' scales
+  uint8_t flags[4]; // 1: the page is there; 2, 4: the rest of the keys' (values') scale is not 1
+};
+constexpr int kTileInfos = 8;
 
 // REP: copies of the rows in a product; 0: PAIR
 template <int D, bool FP8, int REP>
 struct Wide {
   static constexpr bool kPair = REP == 0;
   static constexpr int kCopies = kPair ? 1 : REP;
-  static constexpr int kLanes = 128 / kCopies;                        // rows of a copy, and keys of a row in it
+  static constexpr int kLanes = 128 / kCopies;                        // rows of a copy
+  static constexpr int kCols = kHalf / kCopies;                       // and keys of a half in it
   static constexpr int kRows = kPair ? 256 : kLanes;                  // of a unit at most
   static constexpr int kHalves = D / 64;
   static constexpr uint32_t kQTile = 128 * D * 2;
   static constexpr uint32_t kTile = 128 * D * 2;                      // a 16-bit tile of keys or values
   static constexpr uint32_t kRaw = 128 * D;                           // and of codes
-  static constexpr int kSlots = FP8 ? (D == 64 ? 6 : 3) : (D == 64 ? 8 : 4);  // 16-bit tiles
+  // 16-bit tiles: an issuer holds a tile's values while it waits for the keys of its
+  // next tile, which lie 3 positions on (PAIR: 1)
+  static constexpr int kSlots = FP8 ? (D == 64 ? 6 : kPair ? 3 : 4) : (D == 64 ? 8 : 4);
+  static_assert(kSlots >= (kPair ? 3 : 4), "ring of tiles");
   // positions between two values in one slot: with an odd number of slots keys and
   // values take turns there
   static constexpr int kValueTurn = kSlots % 2 ? 2 * kSlots : kSlots;
-  static constexpr int kRawSlots = FP8 ? (D == 64 ? 6 : kPair ? 3 : 3) : 0;
+  static constexpr int kRawSlots = FP8 ? (D == 64 ? 6 : kCopies > 1 ? 2 : 3) : 0;
   static constexpr uint32_t kOffQ = 0;
   static constexpr uint32_t kOffTile = kOffQ + (kPair ? 2 : 1) * kQTile;
   static constexpr uint32_t kOffRaw = kOffTile + kSlots * kTile;
-  static constexpr uint32_t kOffJoin = kOffRaw + kRawSlots * kRaw;    // REP > 1: 32 columns of 256 rows to be joined
-  static constexpr uint32_t kOffLut = kOffJoin + (kCopies > 1 ? 256 * 33 * 4 : 0);
+  static constexpr uint32_t kOffJoin = kOffRaw + kRawSlots * kRaw;    // REP > 1: 16 columns of 256 rows to be joined
+  static constexpr uint32_t kOffLut = kOffJoin + (kCopies > 1 ? 256 * 17 * 4 : 0);
   static constexpr uint32_t kOffLine = kOffLut + kWideLut * 4;        // ancestors' words
   static constexpr uint32_t kOffDeep = kOffLine + kMaxNodes * 8;      // depths
   static constexpr uint32_t kOffMl = kOffDeep + kMaxNodes * 4;        // [2][128] maximum and sum
   static constexpr uint32_t kOffQx = kOffMl + 2 * 128 * 8;            // [2][256] exponents of query rows
   static constexpr uint32_t kOffInfo = kOffQx + 2 * 256 * 4;          // [2] UnitInfo
-  static constexpr uint32_t kOffBar = kOffInfo + 64;
+  static constexpr uint32_t kOffTiles = kOffInfo + 64;                // [kTileInfos] TileInfo
+  static constexpr uint32_t kOffBar = kOffTiles + kTileInfos * 48;
   // barriers
   static constexpr uint32_t kFull = 0;                                // tile slots: written
   static constexpr uint32_t kEmpty = kFull + kSlots;                  // and read
@@ -100,10 +117,10 @@ struct Wide {
   static constexpr uint32_t kRawEmpty = kRawFull + kRawSlots;
   static constexpr uint32_t kQFull = kRawEmpty + kRawSlots;
   static constexpr uint32_t kQEmpty = kQFull + 1;
-  static constexpr uint32_t kSFull = kQEmpty + 1;                     // + warpgroup
-  static constexpr uint32_t kPFull = kSFull + 2;
-  static constexpr uint32_t kODone = kPFull + 2;
-  static constexpr uint32_t kOFree = kODone + 2;
+  static constexpr uint32_t kSFull = kQEmpty + 1;                     // + 2 warpgroup + half
+  static constexpr uint32_t kPFull = kSFull + 4;
+  static constexpr uint32_t kODone = kPFull + 4;
+  static constexpr uint32_t kOFree = kODone + 4;                      // + warpgroup
   static constexpr uint32_t kClean = kOFree + 2;                      // bf16: a slot's values looked through
   static constexpr uint32_t kFinal = kClean + (FP8 ? 0 : kSlots);
   static constexpr uint32_t kBars = kFinal + 2;
@@ -137,6 +154,37 @@ struct Walk {
   // tile j of the unit's in this block; whether it needs masks
   RP_DEVI int key0(int j) const { return (c.t + j) * kWideTile; }
   RP_DEVI bool special(int j) const { return key0(j) + kWideTile > base; }
+};
+
+// A block's share. Each role calls this for itself, behind its register limit: what is
+// live across the roles' branch is kept to the lowest of them (and was spilled).
+struct Share {
+  Walk w;
+  int size, at;  // cost of a block's share, and that at which the present unit starts
+  RP_DEVI Share(const PagedTreeParams& p, int lane) : size(0), at(0) {
+    constexpr int KT = kWideTile;
+    const int per = p.Hkv * p.rt;
+    if (p.direct) {
+      w.c.b = blockIdx.x / per;
+      w.c.u = blockIdx.x - w.c.b * per;
+      w.c.t = 0;
+      w.c.len = seq_len(p, w.c.b);
+      w.c.nt = w.tiles = (w.c.len + KT - 1) / KT;
+      w.c.h = w.c.u / p.rt;
+      w.c.pages = p.table + w.c.b * p.table_stride;
+    } else {
+      const int len0 = seq_len(p, lane);
+      const int total = total_cost<KT>(p, lane, len0);
+      size = max((total + p.blocks - 1) / p.blocks, 1 + unit_extra<KT>);
+      const int begin = min(static_cast<int>(blockIdx.x) * size, total);
+      int first, last, unused;
+      locate<KT>(p, lane, len0, min(begin + size, total), unused, last);
+      w.c = locate<KT>(p, lane, len0, begin, at, first);
+      w.tiles = begin == total ? 0 : last - first;
+    }
+    w.x = 0;
+    if (w.tiles > 0) w.load(p);
+  }
 };
 
 // 2^e and the rest (1 <= |m| < 2) of a page's scale; what has no such parts stays whole
@@ -224,19 +272,20 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   auto bar = [&](uint32_t i) { return sbase + W::kOffBar + 8 * i; };
   volatile int* const foul = reinterpret_cast<volatile int*>(smem + W::kOffMisc + 4);
+  TileInfo* const tile_infos = reinterpret_cast<TileInfo*>(smem + W::kOffTiles);
   UnitInfo* const infos = reinterpret_cast<UnitInfo*>(smem + W::kOffInfo);
   int* const q_exp = reinterpret_cast<int*>(smem + W::kOffQx);
 
   if (threadIdx.x == 0) {
     for (uint32_t i = 0; i < W::kBars; ++i) {
       uint32_t n = 1;
-      if (FP8 && i < W::kEmpty) n = 128;                        // converted by a warpgroup
+      if (FP8 && i < W::kEmpty) n = 4;                          // converted by four warps
       if (i >= W::kEmpty && i < W::kRawFull) n = kPair ? 2 : 1; // read by both issuers' products
       if (i >= W::kRawEmpty && i < W::kQFull) n = 4;            // a warp each
       if (i == W::kQFull) n = 128;
       if (i == W::kQEmpty) n = 2;                               // both issuers
       if (i >= W::kClean && i < W::kFinal) n = 4;
-      if (i == W::kPFull || i == W::kPFull + 1) n = 128;
+      if (i >= W::kPFull && i < W::kODone) n = 128;
       if (i == W::kOFree || i == W::kOFree + 1) n = 256;
       mbar_init(bar(i), n);
     }
@@ -253,46 +302,12 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + W::kOffMisc);
 
   griddep_wait();
-  Walk w;
-  int size = 0, at = 0;  // cost of a block's share, and that at which the present unit starts
-  {
-    const int per = p.Hkv * p.rt;
-    if (p.direct) {
-      w.c.b = blockIdx.x / per;
-      w.c.u = blockIdx.x - w.c.b * per;
-      w.c.t = 0;
-      w.c.len = seq_len(p, w.c.b);
-      w.c.nt = w.tiles = (w.c.len + KT - 1) / KT;
-      w.c.h = w.c.u / p.rt;
-      w.c.pages = p.table + w.c.b * p.table_stride;
-      if (w.tiles == 0) {  // no key is seen: zero rows
-        if (threadIdx.x == 0) report_length(p, w.c.b);
-        const int row0 = (w.c.u - w.c.h * p.rt) * p.rows;
-        for (int i = threadIdx.x; i < min(p.G * p.Lq - row0, p.rows) * D; i += kWideThreads) {
-          const int r = row0 + i / D, qi = r / p.G;
-          p.out[w.c.b * p.o_batch + (w.c.h * p.G + r - qi * p.G) * p.o_head + qi * p.o_row + i % D] =
-              __float2bfloat16_rn(0.f);
-        }
-      }
-    } else {
-      const int len0 = seq_len(p, lane);
-      const int total = total_cost<KT>(p, lane, len0);
-      size = max((total + p.blocks - 1) / p.blocks, 1 + unit_extra<KT>);
-      if (threadIdx.x == 128) p.ends[2 * blockIdx.x] = p.ends[2 * blockIdx.x + 1] = make_int4(0, 0, 0, 0);
-      const int begin = min(static_cast<int>(blockIdx.x) * size, total);
-      int first, last, unused;
-      locate<KT>(p, lane, len0, min(begin + size, total), unused, last);
-      w.c = locate<KT>(p, lane, len0, begin, at, first);
-      w.tiles = begin == total ? 0 : last - first;
-    }
-    w.x = 0;
-  }
-  const bool some = w.tiles > 0;
-  if (some) w.load(p);
   bool ok = true;
-
   if (warp < 4) {
-    setmaxnreg_dec<56>();
+    setmaxnreg_dec<72>();
+    Share share(p, lane);
+    Walk& w = share.w;
+    const bool some = w.tiles > 0;
     if (warp == 0 && some) {
       // ------------------------------------------------------------ producer
       uint32_t pos = 0;  // of the ring: K of tile i at 2 i, V behind it
@@ -344,7 +359,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       const uint32_t x = warp == 1 ? 0u : 1u;
       const uint32_t s_col = tmem + kColS + 128 * x, o_col = tmem + kColO + D * x;
       const uint64_t dq = smem_desc_sw128(sbase + W::kOffQ + (kPair ? x * W::kQTile : 0u), 16, 1024);
-      uint32_t seq = 0, mine = 0, unit = 0;  // tiles before the unit, own products, units
+      uint32_t seq = 0, mine = 0, unit = 0;  // tiles before the unit, own halves, units
       do {
         const int n = w.xe - w.x;
         ok = mbar_wait_warp(bar(W::kQFull), unit & 1);
@@ -352,45 +367,55 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         // the operands' type: bf16 (1) or fp16 (0)
         const uint32_t types = f16 ? 0u : (1u << 7) | (1u << 10);
         constexpr uint32_t kTypes = (1u << 7) | (1u << 10);
-        const uint32_t idesc_s = (idesc_bf16_f32(128, KT, 0, 0) & ~kTypes) | types;
+        const uint32_t idesc_s = (idesc_bf16_f32(128, kHalf, 0, 0) & ~kTypes) | types;
         const uint32_t idesc_o = (idesc_bf16_f32(128, D, 0, 1) & ~kTypes) | types;
-        for (int j = kPair ? 0 : x; ok && j < n; j += kStep) {
-          const uint32_t kp = 2 * (seq + j), vp = kp + 1;
-          const uint32_t ks = kp % W::kSlots, vs = vp % W::kSlots;
-          ok = mbar_wait_warp(bar(W::kFull + ks), (kp / W::kSlots) & 1);
-          // P of the last tile lies in S's columns
-          if (ok && mine > 0) ok = mbar_wait_warp(bar(W::kODone + x), (mine - 1) & 1);
-          if (!ok) break;
+        const int j0 = kPair ? 0 : x;
+        const int halves = j0 < n ? 2 * ((n - j0 + kStep - 1) / kStep) : 0;  // of the own tiles
+        auto tile_of = [&](int i) { return seq + j0 + (i >> 1) * kStep; };
+        // scores of half i
+        auto scores = [&](int i) {
+          const uint32_t kp = 2 * tile_of(i), ks = kp % W::kSlots, c = mine + i, y = i & 1;
+          if (y == 0) ok = ok && mbar_wait_warp(bar(W::kFull + ks), (kp / W::kSlots) & 1);
+          // the weights of the last half but one lie in its columns
+          if (ok && c >= 2) ok = mbar_wait_warp(bar(W::kODone + 2 * x + y), ((c - 2) >> 1) & 1);
+          if (!ok) return;
           tc_fence_after();
-          const uint64_t dk = smem_desc_sw128(sbase + W::kOffTile + ks * W::kTile, 16, 1024);
+          const uint64_t dk = smem_desc_sw128(sbase + W::kOffTile + ks * W::kTile + y * 8192, 16, 1024);
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint64_t off = (kk >> 2) * 1024 + 2 * (kk & 3);
-            umma_bf16_ss_elect(s_col, dq + off, dk + off, idesc_s, kk > 0);
+            umma_bf16_ss_elect(s_col + kHalf * y, dq + off, dk + off, idesc_s, kk > 0);
           }
-          tc_commit_elect(bar(W::kSFull + x));
-          tc_commit_elect(bar(W::kEmpty + ks));
-          if (j + kStep >= n) tc_commit_elect(bar(W::kQEmpty));  // own last scores of the unit
-          ok = mbar_wait_warp(bar(W::kPFull + x), mine & 1);
-          if (ok && j < kStep && unit > 0) ok = mbar_wait_warp(bar(W::kOFree + x), (unit - 1) & 1);
-          if (ok) ok = mbar_wait_warp(bar(W::kFull + vs), (vp / W::kSlots) & 1);
-          if (!FP8 && ok) ok = mbar_wait_warp(bar(W::kClean + vs), (vp / W::kValueTurn) & 1);
+          tc_commit_elect(bar(W::kSFull + 2 * x + y));
+          if (y) tc_commit_elect(bar(W::kEmpty + ks));
+          if (i == halves - 1) tc_commit_elect(bar(W::kQEmpty));
+        };
+        if (halves) scores(0);
+        if (halves && ok) scores(1);
+        for (int i = 0; ok && i < halves; ++i) {
+          const uint32_t vp = 2 * tile_of(i) + 1, vs = vp % W::kSlots, c = mine + i, y = i & 1;
+          ok = mbar_wait_warp(bar(W::kPFull + 2 * x + y), (c >> 1) & 1);
+          if (ok && i == 0 && unit > 0) ok = mbar_wait_warp(bar(W::kOFree + x), (unit - 1) & 1);
+          if (ok && y == 0) ok = mbar_wait_warp(bar(W::kFull + vs), (vp / W::kSlots) & 1);
+          if (!FP8 && ok && y == 0) ok = mbar_wait_warp(bar(W::kClean + vs), (vp / W::kValueTurn) & 1);
           if (!ok) break;
           tc_fence_after();
-          const uint64_t dv = smem_desc_sw128(sbase + W::kOffTile + vs * W::kTile, 16384, 1024);
+          const uint64_t dv = smem_desc_sw128(sbase + W::kOffTile + vs * W::kTile + y * 8192, 16384, 1024);
+          const uint32_t p_col = s_col + kHalf * y;
 #pragma unroll
-          for (int kk = 0; kk < KT / 16; ++kk)
-            umma_bf16_ts_elect(o_col, s_col + 8 * kk, dv + 128 * kk, idesc_o, j >= kStep || kk > 0);
+          for (int kk = 0; kk < kHalf / 16; ++kk)
+            umma_bf16_ts_elect(o_col, p_col + 8 * kk, dv + 128 * kk, idesc_o, i > 0 || kk > 0);
           if (!f16) {
 #pragma unroll
-            for (int kk = 0; kk < KT / 16; ++kk)
-              umma_bf16_ts_elect(o_col, s_col + 64 + 8 * kk, dv + 128 * kk, idesc_o, 1u);
+            for (int kk = 0; kk < kHalf / 16; ++kk)
+              umma_bf16_ts_elect(o_col, p_col + 32 + 8 * kk, dv + 128 * kk, idesc_o, 1u);
           }
-          tc_commit_elect(bar(W::kODone + x));
-          tc_commit_elect(bar(W::kEmpty + vs));
-          ++mine;
+          tc_commit_elect(bar(W::kODone + 2 * x + y));
+          if (y) tc_commit_elect(bar(W::kEmpty + vs));
+          if (i + 2 < halves) scores(i + 2);
         }
-        if (!kPair && n == 1 && x == 1) tc_commit_elect(bar(W::kQEmpty));  // no tile of the unit
+        if (halves == 0) tc_commit_elect(bar(W::kQEmpty));  // no tile of the unit
+        mine += halves;
         seq += n;
         ++unit;
       } while (ok && w.next(p));
@@ -398,19 +423,25 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       mbar_wait_warp(bar(W::kFinal + x), 0, 100000000ull);
     }
   } else if (warp < 12) {
-    setmaxnreg_inc<184>();
+    setmaxnreg_inc<168>();
+    Share share(p, lane);
+    Walk& w = share.w;
+    int& at = share.at;
+    const int size = share.size;
+    if (!p.direct && threadIdx.x == 128) p.ends[2 * blockIdx.x] = p.ends[2 * blockIdx.x + 1] = make_int4(0, 0, 0, 0);
+    const bool some = w.tiles > 0;
     // -------------------------------------------------------------- softmax
     const int x = (warp - 4) >> 2, t = threadIdx.x & 127;
-    constexpr int NC = W::kLanes;                    // columns of a thread
-    const int copy = t / NC, col0 = copy * NC;       // NC rows a copy, too
+    constexpr int NC = W::kCols;                     // columns of a thread, of a half's
+    const int copy = t / W::kLanes, col0 = copy * NC;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t tS = tmem + lanes + kColS + 128 * x, tO = tmem + lanes + kColO;
+    const uint32_t tS0 = tmem + lanes + kColS + 128 * x, tO = tmem + lanes + kColO;
     float* const lut = reinterpret_cast<float*>(smem + W::kOffLut);
     unsigned long long* const line = reinterpret_cast<unsigned long long*>(smem + W::kOffLine);
     int* const deep = reinterpret_cast<int*>(smem + W::kOffDeep);
     float2* const ml = reinterpret_cast<float2*>(smem + W::kOffMl);
     const int lut_len = p.t5_R + 1;
-    uint32_t mine = 0, unit = 0;
+    uint32_t mine = 0, unit = 0, seq = 0;  // halves, units, tiles before
     int tree_of = -1, lut_of = -1;
     if (some) do {
       const int n = w.xe - w.x, len = w.c.len, base = w.base, live = w.live, h = w.c.h;
@@ -433,7 +464,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       named_bar_sync(1, 256);
       // this thread's row of the unit
       const int half = (rows + 1) >> 1;
-      const int ri = kPair ? x * half + t : t - col0;
+      const int ri = kPair ? x * half + t : t % W::kLanes;
       const bool real = kPair ? t < half && ri < rows : ri < rows;
       const int r = row0 + ri, node = r / p.G, hq = h * p.G + r - node * p.G;
       const bool active = real && node < live;
@@ -454,194 +485,206 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       int ev = 0;
 
       float m_run = -INFINITY, l_run = 0.f;
-      // pages of a tile's 32-key groups and, of 8 bits, their scales' rests: lane
-      // g < 4 has the group's page and key scale, lane 4 + g its value scale
+      // bf16: pages of a tile's 32-key groups in lanes 0 .. 3, a tile ahead
       int page_ahead = -1;
       auto look = [&](int j) {
-        const int key = w.key0(j) + 32 * (lane & 3);
-        page_ahead = lane < 8 && j < n && key < len ? __ldg(w.c.pages + (key >> p.log_page)) : -1;
-        if (page_ahead >= p.num_pages) page_ahead = -1;
+        const int key = w.key0(j) + 32 * lane;
+        page_ahead = !FP8 && lane < 4 && j < n && key < len ? __ldg(w.c.pages + (key >> p.log_page)) : -1;
       };
       const int j0 = kPair ? 0 : x;
       look(j0);
-      for (int j = j0; ok && j < n; j += kStep, ++mine) {
-        const int key0 = w.key0(j);
-        const int page = page_ahead;
-        float rest = 1.f;  // of this lane's scale
-        if (FP8 && page >= 0) {
-          float pow2;
-          split_scale(__ldg((lane < 4 ? p.k_scale : p.v_scale) + static_cast<size_t>(page) * p.Hkv + h), pow2, rest);
+      for (int j = j0; ok && j < n; j += kStep) {
+        unsigned there = 0xfu, k_rests = 0u, v_rests = 0u;
+        if constexpr (!FP8) {
+          there = __ballot_sync(0xffffffffu, page_ahead >= 0 && page_ahead < p.num_pages) & 0xfu;
+          look(j + kStep);
         }
-        look(j + kStep);
-        const unsigned there = __ballot_sync(0xffffffffu, page >= 0) & 0xfu;
-        const unsigned rests = FP8 ? __ballot_sync(0xffffffffu, rest != 1.f) : 0u;
-        ok = __all_sync(0xffffffffu, mbar_wait(bar(W::kSFull + x), mine & 1));
-        if (!ok) break;
-        tc_fence_after();
-        if (j == j0) {
-          if constexpr (FP8) {
-            const UnitInfo info = infos[unit & 1];
-            f16 = info.f16;
-            if (f16) {
-              ev = info.ev;
-              scale = times_pow2(p.scale_log2, info.ek + q_exp[(unit & 1) * 256 + (kPair ? 128 * x + t : ri)]);
-            }
-          }
-          if (p.mode == RELPOS_ALIBI) slope_raw = slope / scale;
-          // scores whose largest is the largest logit, distances that go into them
-          plain = __all_sync(0xffffffffu, !active || (scale > 0.f && fabsf(slope_raw) <= 0x1p60f));
-        }
-        if (any) {
-          const bool near = p.mode == RELPOS_T5 && base - (key0 + KT) < p.t5_R;
-          const bool masks = w.special(j) || there != 0xfu;
-          const bool whole = masks || near || odd || !plain || (rests & 0xfu);
-          if (whole) {  // the scores become logits
+        const TileInfo& info = tile_infos[(seq + j) % kTileInfos];
 #pragma unroll 1
-            for (int q = 0; q < NC / 16; ++q) {
-              uint32_t s[16];
-              tmem_ld16(tS + col0 + 16 * q, s);
-              const int group = (col0 + 16 * q) >> 5;
-              const float mul = FP8 ? scale * __shfl_sync(0xffffffffu, rest, group) : scale;
-              const int o0 = key0 + col0 + 16 * q - base;  // among the drafted slots
-              unsigned vis = 0xffffu;
-              if (o0 >= 0)
-                vis = o0 < kMaxNodes ? static_cast<unsigned>(sees >> o0) : 0u;
-              else if (o0 > -16)
-                vis = static_cast<unsigned>(sees << -o0) | ((1u << -o0) - 1u);
-              if (!(there >> group & 1)) vis = 0u;
-              float bias[16];
-              if (p.mode == RELPOS_NO_BIAS || (p.mode == RELPOS_T5 && !near)) {
+        for (int y = 0; y < 2; ++y, ++mine) {
+          const int key0 = w.key0(j) + kHalf * y;
+          ok = ok && __all_sync(0xffffffffu, mbar_wait(bar(W::kSFull + 2 * x + y), (mine >> 1) & 1));
+          if (!ok) break;
+          tc_fence_after();
+          if (FP8 && y == 0) {
+            const uint32_t flags = *reinterpret_cast<const uint32_t*>(info.flags);
+            auto bits = [&](int of) {
+              const uint32_t f = flags >> of & 0x01010101u;
+              return (f | f >> 7 | f >> 14 | f >> 21) & 0xfu;
+            };
+            there = bits(0), k_rests = bits(1), v_rests = bits(2);
+          }
+          if (j == j0 && y == 0) {
+            if constexpr (FP8) {
+              const UnitInfo u = infos[unit & 1];
+              f16 = u.f16;
+              if (f16) {
+                ev = u.ev;
+                scale = times_pow2(p.scale_log2, u.ek + q_exp[(unit & 1) * 256 + (kPair ? 128 * x + t : ri)]);
+              }
+            }
+            if (p.mode == RELPOS_ALIBI) slope_raw = slope / scale;
+            // scores whose largest is the largest logit, distances that go into them
+            plain = __all_sync(0xffffffffu, !active || (scale > 0.f && fabsf(slope_raw) <= 0x1p60f));
+          }
+          if (any) {
+            const uint32_t tS = tS0 + kHalf * y;
+            const bool near = p.mode == RELPOS_T5 && base - (key0 + kHalf) < p.t5_R;
+            const unsigned both = 3u << 2 * y;  // this half's groups
+            const bool whole = key0 + kHalf > base || (there & both) != both || near || odd || !plain || (k_rests & both);
+            if (whole) {  // the scores become logits
+#pragma unroll 1
+              for (int q = 0; q < NC / 16; ++q) {
+                uint32_t s[16];
+                tmem_ld16(tS + col0 + 16 * q, s);
+                const int group = 2 * y + ((col0 + 16 * q) >> 5);
+                const float mul = FP8 ? scale * info.rest[group] : scale;
+                const int o0 = key0 + col0 + 16 * q - base;  // among the drafted slots
+                unsigned vis = 0xffffu;
+                if (o0 >= 0)
+                  vis = o0 < kMaxNodes ? static_cast<unsigned>(sees >> o0) : 0u;
+                else if (o0 > -16)
+                  vis = static_cast<unsigned>(sees << -o0) | ((1u << -o0) - 1u);
+                if (!(there >> group & 1)) vis = 0u;
+                float bias[16];
+                if (p.mode == RELPOS_NO_BIAS || (p.mode == RELPOS_T5 && !near)) {
 #pragma unroll
-                for (int c = 0; c < 16; ++c) bias[c] = far;
-              } else {
-                int back[16];
-#pragma unroll
-                for (int c = 0; c < 16; ++c) back[c] = depth - o0 - c;
-                if (o0 > -16) {
-#pragma unroll
-                  for (int c = 0; c < 16; ++c)
-                    if (o0 + c >= 0) back[c] = depth - deep[min(o0 + c, kMaxNodes - 1)];
-                }
-                if (p.mode == RELPOS_T5) {
-#pragma unroll
-                  for (int c = 0; c < 16; ++c) bias[c] = my_lut[min(max(back[c], 0), p.t5_R)];
+                  for (int c = 0; c < 16; ++c) bias[c] = far;
                 } else {
+                  int back[16];
 #pragma unroll
-                  for (int c = 0; c < 16; ++c) bias[c] = -slope * fabsf(static_cast<float>(back[c]));
+                  for (int c = 0; c < 16; ++c) back[c] = depth - o0 - c;
+                  if (o0 > -16) {
+#pragma unroll
+                    for (int c = 0; c < 16; ++c)
+                      if (o0 + c >= 0) back[c] = depth - deep[min(o0 + c, kMaxNodes - 1)];
+                  }
+                  if (p.mode == RELPOS_T5) {
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) bias[c] = my_lut[min(max(back[c], 0), p.t5_R)];
+                  } else {
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) bias[c] = -slope * fabsf(static_cast<float>(back[c]));
+                  }
+                }
+                tmem_ld16_wait(s);
+#pragma unroll
+                for (int c = 0; c < 16; ++c)
+                  s[c] = vis >> c & 1 ? __float_as_uint(fmaf(__uint_as_float(s[c]), mul, bias[c])) : 0xff800000u;
+                tmem_st16(tS + col0 + 16 * q, s);
+              }
+              tmem_st_wait();
+            }
+            uint32_t sr[NC / 16][16];
+#pragma unroll
+            for (int q = 0; q < NC / 16; ++q) tmem_ld16(tS + col0 + 16 * q, sr[q]);
+#pragma unroll
+            for (int q = 0; q < NC / 16; ++q) tmem_ld16_wait(sr[q]);
+            float* const xs = reinterpret_cast<float*>(&sr[0][0]);
+            float addc = 0.f, mul = 1.f;
+            if (!whole) {
+              mul = scale;
+              addc = far;
+              if (p.mode == RELPOS_ALIBI) {  // slope (key - position): a constant and the column's part
+                addc = slope * static_cast<float>(key0 + col0 - base - depth);
+#pragma unroll
+                for (int c = 0; c < NC; c += 2) {
+                  const float2 a = __ffma2_rn(make_float2(static_cast<float>(c), static_cast<float>(c + 1)),
+                                              make_float2(slope_raw, slope_raw), make_float2(xs[c], xs[c + 1]));
+                  xs[c] = a.x;
+                  xs[c + 1] = a.y;
                 }
               }
-              tmem_ld16_wait(s);
-#pragma unroll
-              for (int c = 0; c < 16; ++c)
-                s[c] = vis >> c & 1 ? __float_as_uint(fmaf(__uint_as_float(s[c]), mul, bias[c])) : 0xff800000u;
-              tmem_st16(tS + col0 + 16 * q, s);
             }
+            float m0 = -INFINITY, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < NC; c += 8) {
+              m0 = max3f(m0, xs[c], xs[c + 1]);
+              m1 = max3f(m1, xs[c + 2], xs[c + 3]);
+              m2 = max3f(m2, xs[c + 4], xs[c + 5]);
+              m3 = max3f(m3, xs[c + 6], xs[c + 7]);
+            }
+            const float top = fmaf(fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)), mul, addc);
+            const float m_new = fmaxf(m_run, top);
+            const bool moves = m_new > m_run + kRescale;
+            const bool any_moves = __any_sync(0xffffffffu, moves);
+            if (any_moves) {
+              const float alpha = moves ? ex2_approx(m_run - m_new) : 1.f;
+              if (moves) m_run = m_new;
+              if (j > j0 || y > 0) {  // O so far: its last product has to be done; the next waits for these weights
+                ok = __all_sync(0xffffffffu, mbar_wait(bar(W::kODone + 2 * x + 1 - y), ((mine - 1) >> 1) & 1));
+                if (!ok) break;
+                tc_fence_after();
+                l_run *= alpha;
+#pragma unroll 1
+                for (int q = 0; q < D / 16; ++q) {
+                  uint32_t o[16];
+                  tmem_ld16(tO + D * x + 16 * q, o);
+                  tmem_ld16_wait(o);
+#pragma unroll
+                  for (int c = 0; c < 16; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
+                  tmem_st16(tO + D * x + 16 * q, o);
+                }
+              }
+            }
+            float off = addc - (m_run == -INFINITY ? 0.f : m_run);
+            if (FP8 && f16) off += kF16Shift;
+            // weights: P's columns are pairs of keys; other copies' keys are zeros
+            const float2 mul2 = make_float2(mul, mul), off2 = make_float2(off, off);
+            float2 sum0 = make_float2(0.f, 0.f), sum1 = make_float2(0.f, 0.f);
+            auto weights = [&](auto half_type) {
+              constexpr bool F16 = decltype(half_type)::value;
+#pragma unroll
+              for (int q = 0; q < NC / 16; ++q) {
+                uint32_t hi[8];
+                [[maybe_unused]] uint32_t lo[8];
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                  const float2 z = __ffma2_rn(make_float2(xs[16 * q + 2 * c], xs[16 * q + 2 * c + 1]), mul2, off2);
+                  float a = ex2_approx(z.x), b = ex2_approx(z.y);
+                  if (c & 1)
+                    sum1 = __fadd2_rn(sum1, make_float2(a, b));
+                  else
+                    sum0 = __fadd2_rn(sum0, make_float2(a, b));
+                  if (FP8 && (v_rests & both)) {
+                    const float v_rest = info.rest[4 + 2 * y + ((col0 + 16 * q) >> 5)];
+                    a *= v_rest, b *= v_rest;
+                  }
+                  if constexpr (F16) {
+                    hi[c] = pack_half2(a, b);
+                  } else {
+                    hi[c] = pack_bf16x2(a, b);
+                    lo[c] = pack_bf16x2(a - __uint_as_float(hi[c] << 16), b - __uint_as_float(hi[c] & 0xffff0000u));
+                  }
+                }
+                tmem_st8(tS + col0 / 2 + 8 * q, hi);
+                if constexpr (!F16) tmem_st8(tS + 32 + col0 / 2 + 8 * q, lo);
+              }
+              if constexpr (W::kCopies > 1) {
+                const uint32_t zero[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                  if (16 * q / NC == copy) continue;
+                  tmem_st8(tS + 8 * q, zero);
+                  if constexpr (!F16) tmem_st8(tS + 32 + 8 * q, zero);
+                }
+              }
+            };
+            if (FP8 && f16)
+              weights(std::true_type{});
+            else
+              weights(std::false_type{});
+            l_run += (sum0.x + sum0.y) + (sum1.x + sum1.y);
             tmem_st_wait();
           }
-          uint32_t sr[NC / 32][32];
-#pragma unroll
-          for (int q = 0; q < NC / 32; ++q) tmem_ld32(tS + col0 + 32 * q, sr[q]);
-#pragma unroll
-          for (int q = 0; q < NC / 32; ++q) tmem_ld_wait(sr[q]);
-          float* const xs = reinterpret_cast<float*>(&sr[0][0]);
-          float addc = 0.f, mul = 1.f;
-          if (!whole) {
-            mul = scale;
-            addc = far;
-            if (p.mode == RELPOS_ALIBI) {  // slope (key - position): a constant and the column's part
-              addc = slope * static_cast<float>(key0 + col0 - base - depth);
-#pragma unroll
-              for (int c = 0; c < NC; c += 2) {
-                const float2 a = __ffma2_rn(make_float2(static_cast<float>(c), static_cast<float>(c + 1)),
-                                            make_float2(slope_raw, slope_raw), make_float2(xs[c], xs[c + 1]));
-                xs[c] = a.x;
-                xs[c + 1] = a.y;
-              }
-            }
-          }
-          float m0 = -INFINITY, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
-#pragma unroll
-          for (int c = 0; c < NC; c += 8) {
-            m0 = max3f(m0, xs[c], xs[c + 1]);
-            m1 = max3f(m1, xs[c + 2], xs[c + 3]);
-            m2 = max3f(m2, xs[c + 4], xs[c + 5]);
-            m3 = max3f(m3, xs[c + 6], xs[c + 7]);
-          }
-          const float top = fmaf(fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)), mul, addc);
-          const float m_new = fmaxf(m_run, top);
-          const bool moves = m_new > m_run + kRescale;
-          const float alpha = moves ? ex2_approx(m_run - m_new) : 1.f;
-          if (moves) m_run = m_new;
-          float off = addc - (m_run == -INFINITY ? 0.f : m_run);
-          if (FP8 && f16) off += kF16Shift;
-          // O's last product is done (S came behind it), and the next waits for P
-          if (j >= kStep && __any_sync(0xffffffffu, moves)) {
-            l_run *= alpha;
-#pragma unroll 1
-            for (int q = 0; q < D / 16; ++q) {
-              uint32_t o[16];
-              tmem_ld16(tO + D * x + 16 * q, o);
-              tmem_ld16_wait(o);
-#pragma unroll
-              for (int c = 0; c < 16; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
-              tmem_st16(tO + D * x + 16 * q, o);
-            }
-          }
-          // weights: P's columns are pairs of keys; other copies' keys are zeros
-          const float2 mul2 = make_float2(mul, mul), off2 = make_float2(off, off);
-          float2 sum0 = make_float2(0.f, 0.f), sum1 = make_float2(0.f, 0.f);
-          const uint32_t tP = tS + col0 / 2;
-          auto weights = [&](auto half_type) {
-            constexpr bool F16 = decltype(half_type)::value;
-#pragma unroll
-            for (int q = 0; q < NC / 32; ++q) {
-              uint32_t hi[16];
-              [[maybe_unused]] uint32_t lo[16];
-              [[maybe_unused]] const float v_rest = FP8 ? __shfl_sync(0xffffffffu, rest, 4 + (col0 >> 5) + q) : 1.f;
-#pragma unroll
-              for (int c = 0; c < 16; ++c) {
-                const float2 z = __ffma2_rn(make_float2(xs[32 * q + 2 * c], xs[32 * q + 2 * c + 1]), mul2, off2);
-                float a = ex2_approx(z.x), b = ex2_approx(z.y);
-                if (c & 1)
-                  sum1 = __fadd2_rn(sum1, make_float2(a, b));
-                else
-                  sum0 = __fadd2_rn(sum0, make_float2(a, b));
-                if constexpr (FP8) a *= v_rest, b *= v_rest;
-                if constexpr (F16) {
-                  hi[c] = pack_half2(a, b);
-                } else {
-                  hi[c] = pack_bf16x2(a, b);
-                  lo[c] = pack_bf16x2(a - __uint_as_float(hi[c] << 16), b - __uint_as_float(hi[c] & 0xffff0000u));
-                }
-              }
-              tmem_st16(tP + 16 * q, hi);
-              if constexpr (!F16) tmem_st16(tP + 64 + 16 * q, lo);
-            }
-            if constexpr (W::kCopies > 1) {
-              uint32_t zero[16];
-#pragma unroll
-              for (int c = 0; c < 16; ++c) zero[c] = 0u;
-#pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                if (q * 32 / NC == copy) continue;
-                tmem_st16(tS + 16 * q, zero);
-                if constexpr (!F16) tmem_st16(tS + 64 + 16 * q, zero);
-              }
-            }
-          };
-          if (FP8 && f16)
-            weights(std::true_type{});
-          else
-            weights(std::false_type{});
-          l_run += (sum0.x + sum0.y) + (sum1.x + sum1.y);
-          tmem_st_wait();
+          tc_fence_before();
+          mbar_arrive(bar(W::kPFull + 2 * x + y));
         }
-        tc_fence_before();
-        mbar_arrive(bar(W::kPFull + x));
       }
+      seq += n;
       // ---- the unit's parts joined. After a wait that ran out a warp goes on without
       // waiting, so that all meet at the barriers.
-      if (ok && n > j0) ok = __all_sync(0xffffffffu, mbar_wait(bar(W::kODone + x), (mine - 1) & 1));
+      if (ok && n > j0) ok = __all_sync(0xffffffffu, mbar_wait(bar(W::kODone + 2 * x + 1), ((mine - 1) >> 1) & 1));
       if (f16 && m_run != -INFINITY) m_run -= kF16Shift;  // what O and the sum are relative to
       ml[128 * x + t] = make_float2(m_run, l_run);
       // the exponent of O goes with the other warpgroup's too
@@ -708,7 +751,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         m = -INFINITY;
 #pragma unroll
         for (int i = 0; i < kParts; ++i) {
-          parts[i] = ml[i * NC + ri];
+          parts[i] = ml[i * W::kLanes + ri];
           m = fmaxf(m, parts[i].x);
         }
         sum = 0.f;
@@ -722,23 +765,23 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         const float inv = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
         float* const join = reinterpret_cast<float*>(smem + W::kOffJoin);
 #pragma unroll 1
-        for (int col = 0; col < D; col += 32) {
-          uint32_t o[32];
-          tmem_ld32(tO + D * x + col, o);
-          tmem_ld_wait(o);
-          float* const mine_at = join + (threadIdx.x - 128) * 33;
+        for (int col = 0; col < D; col += 16) {
+          uint32_t o[16];
+          tmem_ld16(tO + D * x + col, o);
+          tmem_ld16_wait(o);
+          float* const mine_at = join + (threadIdx.x - 128) * 17;
 #pragma unroll
-          for (int c = 0; c < 32; ++c)
+          for (int c = 0; c < 16; ++c)
             mine_at[c] = active && n > x ? __uint_as_float(o[c]) * mine_by * inv * unit_v : 0.f;
           named_bar_sync(1, 256);
           // 4 columns of a row a thread
-          for (int i = threadIdx.x - 128; i < rows * 8; i += 256) {
-            const int row = i >> 3, c = 4 * (i & 7);
+          for (int i = threadIdx.x - 128; i < rows * 4; i += 256) {
+            const int row = i >> 2, c = 4 * (i & 3);
             float v[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int k = 0; k < kParts; ++k)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) v[e] += join[(k * NC + row) * 33 + c + e];
+              for (int e = 0; e < 4; ++e) v[e] += join[(k * W::kLanes + row) * 17 + c + e];
             const int rr = row0 + row, nd = rr / p.G;
             if (!whole) {
               *reinterpret_cast<float4*>(p.part_o + (static_cast<size_t>(slot) * p.rows + row) * D + col + c) =
@@ -795,7 +838,19 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       ++unit;
     } while (w.next(p));
   } else {
-    setmaxnreg_dec<88>();
+    setmaxnreg_dec<104>();
+    Share share(p, lane);
+    Walk& w = share.w;
+    const bool some = w.tiles > 0;
+    if (p.direct && !some) {  // no key is seen: zero rows
+      if (threadIdx.x == 384) report_length(p, w.c.b);
+      const int row0 = (w.c.u - w.c.h * p.rt) * p.rows;
+      for (int i = threadIdx.x - 384; i < min(p.G * p.Lq - row0, p.rows) * D; i += 128) {
+        const int r = row0 + i / D, qi = r / p.G;
+        p.out[w.c.b * p.o_batch + (w.c.h * p.G + r - qi * p.G) * p.o_head + qi * p.o_row + i % D] =
+            __float2bfloat16_rn(0.f);
+      }
+    }
     // -------------------------------------------------------------- query rows, values
     const int t = threadIdx.x & 127, wq = warp & 3;
     uint32_t unit = 0, seq = 0;
@@ -888,19 +943,33 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       }
       fence_async_smem();
       mbar_arrive(bar(W::kQFull));
+      // pages and scales of this warp's 32 keys of a tile, which are one page's: pages
+      // two tiles ahead, scales one
+      auto page_of = [&](int j) {
+        const int key = w.key0(j) + 32 * wq;
+        const int page = FP8 && j < n && key < len ? __ldg(w.c.pages + (key >> p.log_page)) : -1;
+        return page < p.num_pages ? page : -1;
+      };
+      auto scales_of = [&](int page) {
+        if (!FP8 || page < 0) return make_float2(0.f, 0.f);
+        const size_t ph = static_cast<size_t>(page) * p.Hkv + h;
+        return make_float2(__ldg(p.k_scale + ph), __ldg(p.v_scale + ph));
+      };
+      int page = page_of(0), page_next = page_of(1);
+      float2 scales = scales_of(page);
       for (int j = 0; ok && j < n; ++j) {
         const int key0 = w.key0(j);
         const bool special = w.special(j);
         if constexpr (FP8) {
-          // this warp's 32 keys: one page
-          const int key = key0 + 32 * wq;
-          int page = key < len ? __ldg(w.c.pages + (key >> p.log_page)) : -1;
-          if (page >= p.num_pages) page = -1;
-          float s2[2] = {0.f, 0.f}, unused;
-          if (page >= 0) {
-            const size_t ph = static_cast<size_t>(page) * p.Hkv + h;
-            split_scale(__ldg(p.k_scale + ph), s2[0], unused);
-            split_scale(__ldg(p.v_scale + ph), s2[1], unused);
+          const float2 scales_next = scales_of(page_next);
+          const int page_after = page_of(j + 2);
+          float s2[2], rest[2];
+          split_scale(scales.x, s2[0], rest[0]);
+          split_scale(scales.y, s2[1], rest[1]);
+          if (lane == 0) {
+            TileInfo& info = tile_infos[(seq + j) % kTileInfos];
+            info.rest[wq] = rest[0], info.rest[4 + wq] = rest[1];
+            info.flags[wq] = page >= 0 ? 1 | (rest[0] != 1.f) << 1 | (rest[1] != 1.f) << 2 : 0;
           }
           for (int kv = 0; kv < 2; ++kv) {
             const uint32_t pos = 2 * (seq + j) + kv, rs = pos % W::kRawSlots, cs = pos % W::kSlots;
@@ -962,10 +1031,13 @@ __global__ void __launch_bounds__(kWideThreads, 1)
               }
             }
             fence_async_smem();
-            mbar_arrive(bar(W::kFull + cs));
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar(W::kRawEmpty + rs));
+            if (lane == 0) {
+              mbar_arrive(bar(W::kFull + cs));
+              mbar_arrive(bar(W::kRawEmpty + rs));
+            }
           }
+          page = page_next, page_next = page_after, scales = scales_next;
         } else {
           const uint32_t pos = 2 * (seq + j) + 1, vs = pos % W::kSlots;
           ok = __all_sync(0xffffffffu, mbar_wait(bar(W::kFull + vs), (pos / W::kSlots) & 1));
