@@ -134,6 +134,16 @@ struct UnitInfo {
   int ek, ev;  // fp16: exponents that keys and values are in units of
 };
 
+// Waits of this kernel: a few instructions each (its roles' loops share an instruction
+// cache that they would not fit with the waits on a clock of ptx.cuh), limited by a
+// number of tries, tens of milliseconds at the least.
+RP_DEVI bool wait_on(uint32_t bar, uint32_t parity) {
+#pragma unroll 1
+  for (int i = 0; i < 1 << 21; ++i)
+    if (mbar_try_wait(bar, parity)) return true;
+  return false;
+}
+
 // A block's units, as each role walks them
 struct Walk {
   Cursor c;
@@ -331,7 +341,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           const uint32_t n = __popc(__ballot_sync(0xffffffffu, there));
           for (int kv = 0; ok && kv < 2; ++kv, ++pos) {
             const uint32_t slot = pos % kRing;
-            if (pos >= kRing) ok = mbar_wait_warp(bar(empty0 + slot), (pos / kRing - 1) & 1);
+            if (pos >= kRing) ok = __all_sync(0xffffffffu, wait_on(bar(empty0 + slot), (pos / kRing - 1) & 1));
             if (!ok) break;
             const uint32_t dst = ring + slot * kSlotBytes;
             if (lane == 0)
@@ -353,8 +363,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       } while (ok && w.next(p));
       // never leave with copies in flight
       for (uint32_t k = pos > kRing ? pos - kRing : 0; k < pos; ++k)
-        mbar_wait_warp(bar(full0 + k % kRing), (k / kRing) & 1, 100000000ull);
-    } else if ((warp == 1 || warp == 3) && some) {
+        wait_on(bar(full0 + k % kRing), (k / kRing) & 1);
+    } else if ((warp == 1 || warp == 3) && lane == 0 && some) {
       // ------------------------------------------------------------ issuers
       const uint32_t x = warp == 1 ? 0u : 1u;
       const uint32_t s_col = tmem + kColS + 128 * x, o_col = tmem + kColO + D * x;
@@ -362,66 +372,66 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       uint32_t seq = 0, mine = 0, unit = 0;  // tiles before the unit, own halves, units
       do {
         const int n = w.xe - w.x;
-        ok = mbar_wait_warp(bar(W::kQFull), unit & 1);
+        ok = wait_on(bar(W::kQFull), unit & 1);
         const bool f16 = FP8 && infos[unit & 1].f16;
         // the operands' type: bf16 (1) or fp16 (0)
-        const uint32_t types = f16 ? 0u : (1u << 7) | (1u << 10);
         constexpr uint32_t kTypes = (1u << 7) | (1u << 10);
+        const uint32_t types = f16 ? 0u : kTypes;
         const uint32_t idesc_s = (idesc_bf16_f32(128, kHalf, 0, 0) & ~kTypes) | types;
         const uint32_t idesc_o = (idesc_bf16_f32(128, D, 0, 1) & ~kTypes) | types;
         const int j0 = kPair ? 0 : x;
         const int halves = j0 < n ? 2 * ((n - j0 + kStep - 1) / kStep) : 0;  // of the own tiles
-        auto tile_of = [&](int i) { return seq + j0 + (i >> 1) * kStep; };
-        // scores of half i
-        auto scores = [&](int i) {
-          const uint32_t kp = 2 * tile_of(i), ks = kp % W::kSlots, c = mine + i, y = i & 1;
-          if (y == 0) ok = ok && mbar_wait_warp(bar(W::kFull + ks), (kp / W::kSlots) & 1);
+        // half i's scores two halves ahead of its weights' product
+#pragma unroll 1
+        for (int i = -2; ok && i < halves; ++i) {
+          if (i >= 0) {
+            const uint32_t vp = 2 * (seq + j0 + (i >> 1) * kStep) + 1, vs = vp % W::kSlots, c = mine + i, y = i & 1;
+            ok = wait_on(bar(W::kPFull + 2 * x + y), (c >> 1) & 1);
+            if (ok && i == 0 && unit > 0) ok = wait_on(bar(W::kOFree + x), (unit - 1) & 1);
+            if (ok && y == 0) ok = wait_on(bar(W::kFull + vs), (vp / W::kSlots) & 1);
+            if (!FP8 && ok && y == 0) ok = wait_on(bar(W::kClean + vs), (vp / W::kValueTurn) & 1);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t dv = smem_desc_sw128(sbase + W::kOffTile + vs * W::kTile + y * 8192, 16384, 1024);
+            const uint32_t p_col = s_col + kHalf * y;
+#pragma unroll
+            for (int kk = 0; kk < kHalf / 16; ++kk)
+              umma_bf16_ts(o_col, p_col + 8 * kk, dv + 128 * kk, idesc_o, i > 0 || kk > 0);
+            if (!f16) {
+#pragma unroll
+              for (int kk = 0; kk < kHalf / 16; ++kk)
+                umma_bf16_ts(o_col, p_col + 32 + 8 * kk, dv + 128 * kk, idesc_o, 1u);
+            }
+            tc_commit(bar(W::kODone + 2 * x + y));
+            if (y) tc_commit(bar(W::kEmpty + vs));
+          }
+          const int a = i + 2;
+          if (a >= halves) continue;
+          const uint32_t kp = 2 * (seq + j0 + (a >> 1) * kStep), ks = kp % W::kSlots, c = mine + a, y = a & 1;
+          if (y == 0) ok = wait_on(bar(W::kFull + ks), (kp / W::kSlots) & 1);
           // the weights of the last half but one lie in its columns
-          if (ok && c >= 2) ok = mbar_wait_warp(bar(W::kODone + 2 * x + y), ((c - 2) >> 1) & 1);
-          if (!ok) return;
+          if (ok && c >= 2) ok = wait_on(bar(W::kODone + 2 * x + y), ((c - 2) >> 1) & 1);
+          if (!ok) break;
           tc_fence_after();
           const uint64_t dk = smem_desc_sw128(sbase + W::kOffTile + ks * W::kTile + y * 8192, 16, 1024);
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint64_t off = (kk >> 2) * 1024 + 2 * (kk & 3);
-            umma_bf16_ss_elect(s_col + kHalf * y, dq + off, dk + off, idesc_s, kk > 0);
+            umma_bf16_ss(s_col + kHalf * y, dq + off, dk + off, idesc_s, kk > 0);
           }
-          tc_commit_elect(bar(W::kSFull + 2 * x + y));
-          if (y) tc_commit_elect(bar(W::kEmpty + ks));
-          if (i == halves - 1) tc_commit_elect(bar(W::kQEmpty));
-        };
-        if (halves) scores(0);
-        if (halves && ok) scores(1);
-        for (int i = 0; ok && i < halves; ++i) {
-          const uint32_t vp = 2 * tile_of(i) + 1, vs = vp % W::kSlots, c = mine + i, y = i & 1;
-          ok = mbar_wait_warp(bar(W::kPFull + 2 * x + y), (c >> 1) & 1);
-          if (ok && i == 0 && unit > 0) ok = mbar_wait_warp(bar(W::kOFree + x), (unit - 1) & 1);
-          if (ok && y == 0) ok = mbar_wait_warp(bar(W::kFull + vs), (vp / W::kSlots) & 1);
-          if (!FP8 && ok && y == 0) ok = mbar_wait_warp(bar(W::kClean + vs), (vp / W::kValueTurn) & 1);
-          if (!ok) break;
-          tc_fence_after();
-          const uint64_t dv = smem_desc_sw128(sbase + W::kOffTile + vs * W::kTile + y * 8192, 16384, 1024);
-          const uint32_t p_col = s_col + kHalf * y;
-#pragma unroll
-          for (int kk = 0; kk < kHalf / 16; ++kk)
-            umma_bf16_ts_elect(o_col, p_col + 8 * kk, dv + 128 * kk, idesc_o, i > 0 || kk > 0);
-          if (!f16) {
-#pragma unroll
-            for (int kk = 0; kk < kHalf / 16; ++kk)
-              umma_bf16_ts_elect(o_col, p_col + 32 + 8 * kk, dv + 128 * kk, idesc_o, 1u);
-          }
-          tc_commit_elect(bar(W::kODone + 2 * x + y));
-          if (y) tc_commit_elect(bar(W::kEmpty + vs));
-          if (i + 2 < halves) scores(i + 2);
+          tc_commit(bar(W::kSFull + 2 * x + y));
+          if (y) tc_commit(bar(W::kEmpty + ks));
+          if (a == halves - 1) tc_commit(bar(W::kQEmpty));
         }
-        if (halves == 0) tc_commit_elect(bar(W::kQEmpty));  // no tile of the unit
+        if (halves == 0) tc_commit(bar(W::kQEmpty));  // no tile of the unit
         mine += halves;
         seq += n;
         ++unit;
       } while (ok && w.next(p));
-      tc_commit_elect(bar(W::kFinal + x));
-      mbar_wait_warp(bar(W::kFinal + x), 0, 100000000ull);
+      tc_commit(bar(W::kFinal + x));
+      wait_on(bar(W::kFinal + x), 0);
     }
+    __syncwarp();
   } else if (warp < 12) {
     setmaxnreg_inc<168>();
     Share share(p, lane);
@@ -503,7 +513,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
 #pragma unroll 1
         for (int y = 0; y < 2; ++y, ++mine) {
           const int key0 = w.key0(j) + kHalf * y;
-          ok = ok && __all_sync(0xffffffffu, mbar_wait(bar(W::kSFull + 2 * x + y), (mine >> 1) & 1));
+          ok = ok && __all_sync(0xffffffffu, wait_on(bar(W::kSFull + 2 * x + y), (mine >> 1) & 1));
           if (!ok) break;
           tc_fence_after();
           if (FP8 && y == 0) {
@@ -612,7 +622,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
               const float alpha = moves ? ex2_approx(m_run - m_new) : 1.f;
               if (moves) m_run = m_new;
               if (j > j0 || y > 0) {  // O so far: its last product has to be done; the next waits for these weights
-                ok = __all_sync(0xffffffffu, mbar_wait(bar(W::kODone + 2 * x + 1 - y), ((mine - 1) >> 1) & 1));
+                ok = __all_sync(0xffffffffu, wait_on(bar(W::kODone + 2 * x + 1 - y), ((mine - 1) >> 1) & 1));
                 if (!ok) break;
                 tc_fence_after();
                 l_run *= alpha;
@@ -632,8 +642,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             // weights: P's columns are pairs of keys; other copies' keys are zeros
             const float2 mul2 = make_float2(mul, mul), off2 = make_float2(off, off);
             float2 sum0 = make_float2(0.f, 0.f), sum1 = make_float2(0.f, 0.f);
-            auto weights = [&](auto half_type) {
-              constexpr bool F16 = decltype(half_type)::value;
+            auto weights = [&](auto half_type, auto with_rests) {
+              constexpr bool F16 = decltype(half_type)::value, kRests = decltype(with_rests)::value;
 #pragma unroll
               for (int q = 0; q < NC / 16; ++q) {
                 uint32_t hi[8];
@@ -646,7 +656,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                     sum1 = __fadd2_rn(sum1, make_float2(a, b));
                   else
                     sum0 = __fadd2_rn(sum0, make_float2(a, b));
-                  if (FP8 && (v_rests & both)) {
+                  if constexpr (kRests) {
                     const float v_rest = info.rest[4 + 2 * y + ((col0 + 16 * q) >> 5)];
                     a *= v_rest, b *= v_rest;
                   }
@@ -670,10 +680,16 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                 }
               }
             };
-            if (FP8 && f16)
-              weights(std::true_type{});
-            else
-              weights(std::false_type{});
+            if (FP8 && (v_rests & both)) {
+              if (f16)
+                weights(std::true_type{}, std::true_type{});
+              else
+                weights(std::false_type{}, std::true_type{});
+            } else if (FP8 && f16) {
+              weights(std::true_type{}, std::false_type{});
+            } else {
+              weights(std::false_type{}, std::false_type{});
+            }
             l_run += (sum0.x + sum0.y) + (sum1.x + sum1.y);
             tmem_st_wait();
           }
@@ -684,7 +700,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       seq += n;
       // ---- the unit's parts joined. After a wait that ran out a warp goes on without
       // waiting, so that all meet at the barriers.
-      if (ok && n > j0) ok = __all_sync(0xffffffffu, mbar_wait(bar(W::kODone + 2 * x + 1), ((mine - 1) >> 1) & 1));
+      if (ok && n > j0) ok = __all_sync(0xffffffffu, wait_on(bar(W::kODone + 2 * x + 1), ((mine - 1) >> 1) & 1));
       if (f16 && m_run != -INFINITY) m_run -= kF16Shift;  // what O and the sum are relative to
       ml[128 * x + t] = make_float2(m_run, l_run);
       // the exponent of O goes with the other warpgroup's too
@@ -858,7 +874,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     if (some) do {
       const int n = w.xe - w.x, len = w.c.len, base = w.base, h = w.c.h;
       const int row0 = (w.c.u - h * p.rt) * p.rows, rows = min(p.G * p.Lq - row0, p.rows);
-      if (ok && unit > 0) ok = __all_sync(0xffffffffu, mbar_wait(bar(W::kQEmpty), (unit - 1) & 1));
+      if (ok && unit > 0) ok = __all_sync(0xffffffffu, wait_on(bar(W::kQEmpty), (unit - 1) & 1));
       bool f16 = false;
       int ek = 0, ev = 0;
       if constexpr (FP8) {
@@ -973,62 +989,63 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           }
           for (int kv = 0; kv < 2; ++kv) {
             const uint32_t pos = 2 * (seq + j) + kv, rs = pos % W::kRawSlots, cs = pos % W::kSlots;
-            ok = mbar_wait(bar(W::kRawFull + rs), (pos / W::kRawSlots) & 1);
-            if (pos >= W::kSlots) ok = ok && mbar_wait(bar(W::kEmpty + cs), (pos / W::kSlots - 1) & 1);
+            ok = wait_on(bar(W::kRawFull + rs), (pos / W::kRawSlots) & 1);
+            if (pos >= W::kSlots) ok = ok && wait_on(bar(W::kEmpty + cs), (pos / W::kSlots - 1) & 1);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             const uint32_t raw = sbase + W::kOffRaw + rs * W::kRaw, to = sbase + W::kOffTile + cs * W::kTile;
-            // fp16: in units of the largest scale's power of two
-            const float s = kv ? s2[1] : s2[0];
-            const float s16 = times_pow2(s, -(kv ? ev : ek));
-            const uint32_t by = pack_half2(s16, s16);
-            const bool clean = kv && special && key0 + 32 * wq + 31 >= base;
             // 8 rows a step, 4 lanes a row (of half a row at d = 128, odd rows the other
             // half, so that reads and writes meet all banks); 4 steps' loads at a time
-            auto row_of = [&](int it) { return 32 * wq + 8 * (D == 64 ? it : it >> 1) + (lane >> 2); };
-            auto half_of = [&](int it) { return D == 64 ? 0 : (it ^ row_of(it)) & 1; };
-            const int g = lane & 3;
+            auto convert = [&](auto code_pairs, auto special_rows) {
+              constexpr bool kSpecial = decltype(special_rows)::value;
+              const int g = lane & 3, r0 = 32 * wq + (lane >> 2);
+#pragma unroll 1
+              for (int it0 = 0; it0 < 4 * W::kHalves; it0 += 4) {
+                // (row, half) of step e: rows go on by 8 with each step, at d = 128 with
+                // every other
+                const int r1 = r0 + 8 * (D == 64 ? it0 : it0 / 2), odd = D == 64 ? 0 : r0 & 1;
+                auto row_of = [&](int e) { return r1 + 8 * (D == 64 ? e : e / 2); };
+                auto half_of = [&](int e) { return D == 64 ? 0 : (e & 1) ^ odd; };
+                uint4 u[4];
 #pragma unroll
-            for (int it0 = 0; it0 < 4 * W::kHalves; it0 += 4) {
-              uint4 u[4];
+                for (int e = 0; e < 4; ++e) u[e] = lds128(raw + row_of(e) * D + half_of(e) * 64 + g * 16);
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int r = row_of(it0 + e);
-                u[e] = lds128(raw + r * D + half_of(it0 + e) * 64 + g * 16);
-                if (page < 0 || key0 + r >= len) u[e] = make_uint4(0u, 0u, 0u, 0u);
-              }
+                for (int e = 0; e < 4; ++e) {
+                  const int r = row_of(e);
+                  if constexpr (kSpecial)
+                    if (page < 0 || key0 + r >= len) u[e] = make_uint4(0u, 0u, 0u, 0u);
+                  const uint32_t c4[4] = {u[e].x, u[e].y, u[e].z, u[e].w};
+                  uint32_t o[8];
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int r = row_of(it0 + e);
-                const uint32_t c4[4] = {u[e].x, u[e].y, u[e].z, u[e].w};
-                uint32_t o[8];
-                if (f16) {
+                  for (int k = 0; k < 4; ++k) o[2 * k] = code_pairs(half2_lo(c4[k])), o[2 * k + 1] = code_pairs(half2_hi(c4[k]));
+                  if constexpr (kSpecial) {
+                    if (kv && key0 + r >= base) {
+                      const uint32_t ones = f16 ? 0x7c007c00u : 0x7f807f80u;  // exponents of what is not finite
+                      const uint32_t gone = key0 + r >= len ? ~0u : 0u;
 #pragma unroll
-                  for (int k = 0; k < 4; ++k) {
-                    o[2 * k] = mul_half2(half2_lo(c4[k]), by);
-                    o[2 * k + 1] = mul_half2(half2_hi(c4[k]), by);
+                      for (int k = 0; k < 8; ++k) {
+                        const uint32_t no = __vcmpeq2(o[k] & ones, ones);
+                        if (no & ~gone) *foul = 1;
+                        o[k] &= ~(no | gone);
+                      }
+                    }
                   }
-                } else {
-#pragma unroll
-                  for (int k = 0; k < 4; ++k) {
-                    o[2 * k] = bf16_of(half2_lo(c4[k]), s);
-                    o[2 * k + 1] = bf16_of(half2_hi(c4[k]), s);
-                  }
+                  const uint32_t to_row = to + half_of(e) * 16384 + r * 128;
+                  sts128(to_row + (((2 * g) ^ (r & 7)) << 4), o[0], o[1], o[2], o[3]);
+                  sts128(to_row + (((2 * g + 1) ^ (r & 7)) << 4), o[4], o[5], o[6], o[7]);
                 }
-                if (clean && key0 + r >= base) {
-                  const uint32_t ones = f16 ? 0x7c007c00u : 0x7f807f80u;  // exponents of what is not finite
-                  uint32_t bad = key0 + r >= len ? ~0u : 0u;
-#pragma unroll
-                  for (int k = 0; k < 8; ++k) {
-                    const uint32_t no = __vcmpeq2(o[k] & ones, ones);
-                    if (no && key0 + r < len) *foul = 1;
-                    o[k] &= ~(no | bad);
-                  }
-                }
-                const uint32_t to_row = to + half_of(it0 + e) * 16384 + r * 128;
-                sts128(to_row + (((2 * g) ^ (r & 7)) << 4), o[0], o[1], o[2], o[3]);
-                sts128(to_row + (((2 * g + 1) ^ (r & 7)) << 4), o[4], o[5], o[6], o[7]);
               }
+            };
+            const bool odd_rows = page < 0 || key0 + 32 * wq + 31 >= base;  // drafted ones, or none
+            const float s = kv ? s2[1] : s2[0];
+            if (f16) {  // in units of the largest scale's power of two
+              const float s16 = times_pow2(s, -(kv ? ev : ek));
+              const uint32_t by = pack_half2(s16, s16);
+              auto f = [&](uint32_t h2) { return mul_half2(h2, by); };
+              if (odd_rows) convert(f, std::true_type{}); else convert(f, std::false_type{});
+            } else {
+              auto f = [&](uint32_t h2) { return bf16_of(h2, s); };
+              if (odd_rows) convert(f, std::true_type{}); else convert(f, std::false_type{});
             }
             fence_async_smem();
             __syncwarp();
@@ -1040,7 +1057,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           page = page_next, page_next = page_after, scales = scales_next;
         } else {
           const uint32_t pos = 2 * (seq + j) + 1, vs = pos % W::kSlots;
-          ok = __all_sync(0xffffffffu, mbar_wait(bar(W::kFull + vs), (pos / W::kSlots) & 1));
+          ok = __all_sync(0xffffffffu, wait_on(bar(W::kFull + vs), (pos / W::kSlots) & 1));
           if (!ok) break;
           const uint32_t to = sbase + W::kOffTile + vs * W::kTile;
           // rows from the first drafted slot on
