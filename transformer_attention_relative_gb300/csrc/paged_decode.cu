@@ -291,6 +291,7 @@ int decode_call(const RelposPagedCache* cache, const void* Q, const RelposRowStr
   if (!split.wide) ok = cudaLaunchKernelEx(&cfg, v.decode, p) == cudaSuccess;
   if (!p.direct) {
     cfg.dynamicSmemBytes = 0;
+    if (split.wide) cfg.blockDim = dim3(kWideCombineThreads);
     ok = ok && cudaLaunchKernelEx(&cfg, v.combine, p) == cudaSuccess;
     ok = cudaFreeAsync(scratch, s) == cudaSuccess && ok;
   }

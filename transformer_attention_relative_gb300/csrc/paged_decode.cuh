@@ -130,6 +130,7 @@ PagedTreeVariant paged_tree_bf16_128(int rows8);
 // Units of up to 256 rows on the tensor cores' 128-row products (paged_wide.cuh)
 constexpr int kWideRows = 256, kWideTile = 128;
 constexpr int kWideLut = 2048;  // T5 biases of near distances that it keeps, of all heads of a group
+constexpr int kWideCombineThreads = 1024;
 using PagedWideLaunch = int(const RelposPagedCache& cache, const PagedTreeParams& p, int blocks,
                             void (**combine)(PagedTreeParams), cudaStream_t stream);
 PagedWideLaunch paged_wide_bf16_64, paged_wide_bf16_128, paged_wide_e4m3_64, paged_wide_e4m3_128;
@@ -1255,18 +1256,18 @@ __global__ void __launch_bounds__(kPdThreads, NQ * D <= 64 ? 4 : NQ * D <= 128 ?
 // its threads for each end. What a slot holds the decode kernel has noted, so
 // that nothing is searched for here: these blocks mostly start when that
 // kernel's leave their SM.
-template <int D, class P>
-__global__ void __launch_bounds__(kPdThreads) relpos_paged_combine_kernel(const __grid_constant__ P p) {
+template <int D, class P, int THREADS = kPdThreads>
+__global__ void __launch_bounds__(THREADS) relpos_paged_combine_kernel(const __grid_constant__ P p) {
   griddep_launch_dependents();
   griddep_wait();
-  constexpr int kHalf = kPdThreads / 2;
+  constexpr int kHalf = THREADS / 2;
   const int end = threadIdx.x / kHalf, tid = threadIdx.x % kHalf;
   const int4 what = __ldcg(p.ends + 2 * blockIdx.x + end);
   const int c0 = what.x, k = what.y, b = what.z, u = what.w;
   for (int i = blockIdx.x; i < p.B; i += gridDim.x) {
     if (seq_len(p, i) > 0) continue;
     if (threadIdx.x == 0) report_length(p, i);
-    for (int r = threadIdx.x / 32; r < p.Hq * p.Lq; r += kPdWarps)
+    for (int r = threadIdx.x / 32; r < p.Hq * p.Lq; r += THREADS / 32)
       for (int j = threadIdx.x % 32; j < D; j += 32)
         p.out[i * p.o_batch + r / p.Lq * p.o_head + r % p.Lq * p.o_row + j] = __float2bfloat16_rn(0.f);
   }

@@ -144,6 +144,36 @@ RP_DEVI bool wait_on(uint32_t bar, uint32_t parity) {
   return false;
 }
 
+RP_DEVI bool wait_warp(uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, wait_on(bar, parity)); }
+
+// One lane of a converged warp, and what it alone issues
+RP_DEVI uint32_t elect_one() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+  return e;
+}
+RP_DEVI void umma_ss_if(uint32_t on, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 e, %5, 0;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(on)
+      : "memory");
+}
+RP_DEVI void umma_ts_if(uint32_t on, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 e, %5, 0;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(on)
+      : "memory");
+}
+RP_DEVI void commit_if(uint32_t on, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %1, 0;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+      "r"(on)
+      : "memory");
+}
+
 // A block's units, as each role walks them
 struct Walk {
   Cursor c;
@@ -161,8 +191,12 @@ struct Walk {
     load(p);
     return true;
   }
-  // tile j of the unit's in this block; whether it needs masks
-  RP_DEVI int key0(int j) const { return (c.t + j) * kWideTile; }
+  // first key of the unit's j-th tile in this block, from the last one on: a decaying
+  // bias (ALiBi) then has its largest logits first, and no maximum moves after those
+  RP_DEVI int key0(int j) const { return (c.t + xe - x - 1 - j) * kWideTile; }
+  RP_DEVI int first_key() const { return c.t * kWideTile; }
+  RP_DEVI int end_key() const { return min((c.t + xe - x) * kWideTile, c.len); }
+  // whether a tile needs masks
   RP_DEVI bool special(int j) const { return key0(j) + kWideTile > base; }
 };
 
@@ -364,15 +398,19 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       // never leave with copies in flight
       for (uint32_t k = pos > kRing ? pos - kRing : 0; k < pos; ++k)
         wait_on(bar(full0 + k % kRing), (k / kRing) & 1);
-    } else if ((warp == 1 || warp == 3) && lane == 0 && some) {
+    } else if ((warp == 1 || warp == 3) && some) {
       // ------------------------------------------------------------ issuers
+      // The whole warp goes the same way (operands stay uniform), one thread issues.
+      // Rolled loops: straight-line code for these few instructions a tile is
+      // fetched anew each time (950 cycles for the 4 products of a half's weights).
+      const uint32_t leader = elect_one();
       const uint32_t x = warp == 1 ? 0u : 1u;
       const uint32_t s_col = tmem + kColS + 128 * x, o_col = tmem + kColO + D * x;
       const uint64_t dq = smem_desc_sw128(sbase + W::kOffQ + (kPair ? x * W::kQTile : 0u), 16, 1024);
       uint32_t seq = 0, mine = 0, unit = 0;  // tiles before the unit, own halves, units
       do {
         const int n = w.xe - w.x;
-        ok = wait_on(bar(W::kQFull), unit & 1);
+        ok = wait_warp(bar(W::kQFull), unit & 1);
         const bool f16 = FP8 && infos[unit & 1].f16;
         // the operands' type: bf16 (1) or fp16 (0)
         constexpr uint32_t kTypes = (1u << 7) | (1u << 10);
@@ -386,52 +424,47 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         for (int i = -2; ok && i < halves; ++i) {
           if (i >= 0) {
             const uint32_t vp = 2 * (seq + j0 + (i >> 1) * kStep) + 1, vs = vp % W::kSlots, c = mine + i, y = i & 1;
-            ok = wait_on(bar(W::kPFull + 2 * x + y), (c >> 1) & 1);
-            if (ok && i == 0 && unit > 0) ok = wait_on(bar(W::kOFree + x), (unit - 1) & 1);
-            if (ok && y == 0) ok = wait_on(bar(W::kFull + vs), (vp / W::kSlots) & 1);
-            if (!FP8 && ok && y == 0) ok = wait_on(bar(W::kClean + vs), (vp / W::kValueTurn) & 1);
+            ok = wait_warp(bar(W::kPFull + 2 * x + y), (c >> 1) & 1);
+            if (ok && i == 0 && unit > 0) ok = wait_warp(bar(W::kOFree + x), (unit - 1) & 1);
+            if (ok && y == 0) ok = wait_warp(bar(W::kFull + vs), (vp / W::kSlots) & 1);
+            if (!FP8 && ok && y == 0) ok = wait_warp(bar(W::kClean + vs), (vp / W::kValueTurn) & 1);
             if (!ok) break;
             tc_fence_after();
             const uint64_t dv = smem_desc_sw128(sbase + W::kOffTile + vs * W::kTile + y * 8192, 16384, 1024);
             const uint32_t p_col = s_col + kHalf * y;
-#pragma unroll
-            for (int kk = 0; kk < kHalf / 16; ++kk)
-              umma_bf16_ts(o_col, p_col + 8 * kk, dv + 128 * kk, idesc_o, i > 0 || kk > 0);
-            if (!f16) {
-#pragma unroll
-              for (int kk = 0; kk < kHalf / 16; ++kk)
-                umma_bf16_ts(o_col, p_col + 32 + 8 * kk, dv + 128 * kk, idesc_o, 1u);
-            }
-            tc_commit(bar(W::kODone + 2 * x + y));
-            if (y) tc_commit(bar(W::kEmpty + vs));
+            // (bf16: the second parts of the weights behind the first)
+#pragma unroll 1
+            for (int kk = 0; kk < (f16 ? 1 : 2) * kHalf / 16; ++kk)
+              umma_ts_if(leader, o_col, p_col + 8 * kk, dv + 128 * (kk & (kHalf / 16 - 1)), idesc_o, i > 0 || kk > 0);
+            commit_if(leader, bar(W::kODone + 2 * x + y));
+            if (y) commit_if(leader, bar(W::kEmpty + vs));
           }
           const int a = i + 2;
           if (a >= halves) continue;
           const uint32_t kp = 2 * (seq + j0 + (a >> 1) * kStep), ks = kp % W::kSlots, c = mine + a, y = a & 1;
-          if (y == 0) ok = wait_on(bar(W::kFull + ks), (kp / W::kSlots) & 1);
+          if (y == 0) ok = wait_warp(bar(W::kFull + ks), (kp / W::kSlots) & 1);
           // the weights of the last half but one lie in its columns
-          if (ok && c >= 2) ok = wait_on(bar(W::kODone + 2 * x + y), ((c - 2) >> 1) & 1);
+          if (ok && c >= 2) ok = wait_warp(bar(W::kODone + 2 * x + y), ((c - 2) >> 1) & 1);
           if (!ok) break;
           tc_fence_after();
           const uint64_t dk = smem_desc_sw128(sbase + W::kOffTile + ks * W::kTile + y * 8192, 16, 1024);
-#pragma unroll
+#pragma unroll 1
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint64_t off = (kk >> 2) * 1024 + 2 * (kk & 3);
-            umma_bf16_ss(s_col + kHalf * y, dq + off, dk + off, idesc_s, kk > 0);
+            umma_ss_if(leader, s_col + kHalf * y, dq + off, dk + off, idesc_s, kk > 0);
           }
-          tc_commit(bar(W::kSFull + 2 * x + y));
-          if (y) tc_commit(bar(W::kEmpty + ks));
-          if (a == halves - 1) tc_commit(bar(W::kQEmpty));
+          commit_if(leader, bar(W::kSFull + 2 * x + y));
+          if (y) commit_if(leader, bar(W::kEmpty + ks));
+          if (a == halves - 1) commit_if(leader, bar(W::kQEmpty));
         }
-        if (halves == 0) tc_commit(bar(W::kQEmpty));  // no tile of the unit
+        if (halves == 0) commit_if(leader, bar(W::kQEmpty));  // no tile of the unit
         mine += halves;
         seq += n;
         ++unit;
       } while (ok && w.next(p));
-      tc_commit(bar(W::kFinal + x));
-      wait_on(bar(W::kFinal + x), 0);
+      commit_if(leader, bar(W::kFinal + x));
+      wait_warp(bar(W::kFinal + x), 0);
     }
-    __syncwarp();
   } else if (warp < 12) {
     setmaxnreg_inc<168>();
     Share share(p, lane);
@@ -819,7 +852,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       if (*foul && active && copy == 0) {
         // drafted values of this block's tiles that are not finite, for the rows that
         // see them: infinities and NaN as their sum
-        const int lo = max(w.key0(0) - base, 0), hi = min(w.key0(n), len) - base;
+        const int lo = max(w.first_key() - base, 0), hi = w.end_key() - base;
         const int from = kPair ? 0 : x * (D / 2), upto = kPair ? D : from + D / 2;
 #pragma unroll 1
         for (int c = from; c < upto; ++c) {
@@ -881,7 +914,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         // exponents of the pages' scales: the largest, and how far below it the
         // smallest may be (one that has none is as far as can be)
         int top_k = -200, low_k = 200, top_v = -200, low_v = 200;
-        const int first = w.key0(0) >> p.log_page, last = (min(w.key0(n), len) - 1) >> p.log_page;
+        const int first = w.first_key() >> p.log_page, last = (w.end_key() - 1) >> p.log_page;
 #pragma unroll 4
         for (int i = first + t; i <= last; i += 128) {
           const int page = __ldg(w.c.pages + i);
@@ -1129,7 +1162,7 @@ int launch_wide(const RelposPagedCache& cache, const PagedTreeParams& p, int blo
   std::memset(&k, 0, sizeof(k));
   std::memset(&v, 0, sizeof(v));
   if (!FP8 && (!page_map(&k, cache.k, cache) || !page_map(&v, cache.v, cache))) return RELPOS_ERR_CUDA;
-  *combine = relpos_paged_combine_kernel<D, PagedTreeParams>;
+  *combine = relpos_paged_combine_kernel<D, PagedTreeParams, kWideCombineThreads>;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
