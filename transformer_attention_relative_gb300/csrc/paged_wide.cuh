@@ -8,20 +8,21 @@
 //
 // A unit is a sequence, key/value head and some of its rows (query heads of the
 // group times nodes). Two softmax warpgroups share its key tiles in one of three ways:
-//   up to 256 rows (PAIR): each takes half the rows and every tile;
+//   more than 128 rows (a pair): each takes half the rows and every tile;
 //   up to 128 rows: each takes all rows and every other tile;
-//   up to 64 or 32 rows (REP = 2, 4): the same, and the rows stand 2 or 4 times in the
-//     128 of a product, each copy with a half or quarter of the keys: as many products,
-//     but a thread has a half or quarter of the exponentials, and the chain from scores
-//     to weights, which few rows cannot hide, is as much shorter.
+//   units of up to 64 or 32 rows (COPIES = 2, 4): the same, and the rows stand 2 or 4
+//     times in the 128 of a product, each copy with a half or quarter of the keys: as
+//     many products, but a thread has a half or quarter of the exponentials, and the
+//     chain from scores to weights, which few rows cannot hide, is as much shorter.
 // A warpgroup goes through its tiles by halves of 64 keys, with a buffer of scores for
 // either half: the scores of the next half are there when a half's weights are done.
+// Keys and values come by halves too, in the order in which the products need them.
 // What the warpgroups and copies hold apart (maximum, sum, O) is joined at the unit's
 // end. Blocks take equal shares of all units' tiles, as in paged_decode.cuh, one block
 // an SM.
 //
-//   warp 0        producer: a tile's pages, K and V in turn, into a ring of shared
-//                 memory (bf16: tensor copies, swizzled; e4m3: bulk copies).
+//   warp 0        producer: halves of keys and values from their pages into a ring of
+//                 shared memory (bf16: tensor copies, swizzled; e4m3: bulk copies).
 //   warps 1, 3    issuers of the products, one for each softmax warpgroup.
 //   warps 4-11    the softmax warpgroups; thread t holds row t of a product.
 //   warps 12-15   a unit's query rows into shared memory; e4m3: codes to 16-bit tiles;
@@ -68,60 +69,52 @@ constexpr uint32_t kTmemCols = 512, kColS = 0, kColO = 256;
 constexpr int kHalf = 64;  // keys of a half
 constexpr float kRescale = 8.f;  // the running maximum moves when a row's grows by this (log2)
 constexpr float kF16Shift = 5.f;  // fp16 weights are 2^5 times those of bf16: up to 2^13 (2^14 with a scale's rest)
+constexpr uint32_t kNoPage = 0xffffffffu;  // in place of a scale
 constexpr int kF16Window = 15;    // exponents of page scales below the largest
 
-// What the converters know of a tile's 32-key groups, for the softmax; as many as
-// they can be ahead and more
-struct TileInfo {
-  float rest[8];    // of the keys' and the values' scales
-  uint8_t flags[4]; // 1: the page is there; 2, 4: the rest of the keys' (values') scale is not 1
+// What the producer knows of a half's two 32-key groups, for the softmax; a ring for
+// either warpgroup's halves, longer than the producer can be ahead
+struct HalfInfo {
+  float k_rest[2], v_rest[2];  // of the scales
+  uint8_t flags[2];            // 1: the page is there; 2, 4: the rest of the keys' (values') scale is not 1
 };
-constexpr int kTileInfos = 8;
+constexpr int kInfos = 32;
 
-// REP: copies of the rows in a product; 0: PAIR
-template <int D, bool FP8, int REP>
+template <int D, bool FP8, int COPIES>
 struct Wide {
-  static constexpr bool kPair = REP == 0;
-  static constexpr int kCopies = kPair ? 1 : REP;
-  static constexpr int kLanes = 128 / kCopies;                        // rows of a copy
-  static constexpr int kCols = kHalf / kCopies;                       // and keys of a half in it
-  static constexpr int kRows = kPair ? 256 : kLanes;                  // of a unit at most
-  static constexpr int kHalves = D / 64;
+  static constexpr int kLanes = 128 / COPIES;                         // rows of a copy
+  static constexpr int kCols = kHalf / COPIES;                        // and keys of a half in it
+  static constexpr int kQTiles = COPIES == 1 ? 2 : 1;
   static constexpr uint32_t kQTile = 128 * D * 2;
-  static constexpr uint32_t kTile = 128 * D * 2;                      // a 16-bit tile of keys or values
-  static constexpr uint32_t kRaw = 128 * D;                           // and of codes
-  // 16-bit tiles: an issuer holds a tile's values while it waits for the keys of its
-  // next tile, which lie 3 positions on (PAIR: 1)
-  static constexpr int kSlots = FP8 ? (D == 64 ? 6 : kPair ? 3 : 4) : (D == 64 ? 8 : 4);
-  static_assert(kSlots >= (kPair ? 3 : 4), "ring of tiles");
-  // positions between two values in one slot: with an odd number of slots keys and
-  // values take turns there
-  static constexpr int kValueTurn = kSlots % 2 ? 2 * kSlots : kSlots;
-  static constexpr int kRawSlots = FP8 ? (D == 64 ? 6 : kCopies > 1 ? 2 : 3) : 0;
+  static constexpr uint32_t kSlot = kHalf * D * 2;                    // a half's keys or values, 16 bits
+  static constexpr uint32_t kRaw = kHalf * D;                         // and as codes
+  static constexpr int kSlots = D == 64 ? (FP8 ? 12 : 16) : FP8 ? (COPIES == 1 ? 6 : 8) : COPIES == 1 ? 8 : 10;
+  static constexpr int kRawSlots = !FP8 ? 0 : D == 64 ? 12 : COPIES == 1 ? 6 : 4;
   static constexpr uint32_t kOffQ = 0;
-  static constexpr uint32_t kOffTile = kOffQ + (kPair ? 2 : 1) * kQTile;
-  static constexpr uint32_t kOffRaw = kOffTile + kSlots * kTile;
-  static constexpr uint32_t kOffJoin = kOffRaw + kRawSlots * kRaw;    // REP > 1: 16 columns of 256 rows to be joined
-  static constexpr uint32_t kOffLut = kOffJoin + (kCopies > 1 ? 256 * 17 * 4 : 0);
+  static constexpr uint32_t kOffTile = kOffQ + kQTiles * kQTile;
+  static constexpr uint32_t kOffRaw = kOffTile + kSlots * kSlot;
+  static constexpr uint32_t kOffJoin = kOffRaw + kRawSlots * kRaw;    // copies: 16 columns of 256 rows to be joined
+  static constexpr uint32_t kOffLut = kOffJoin + (COPIES > 1 ? 256 * 17 * 4 : 0);
   static constexpr uint32_t kOffLine = kOffLut + kWideLut * 4;        // ancestors' words
   static constexpr uint32_t kOffDeep = kOffLine + kMaxNodes * 8;      // depths
   static constexpr uint32_t kOffMl = kOffDeep + kMaxNodes * 4;        // [2][128] maximum and sum
   static constexpr uint32_t kOffQx = kOffMl + 2 * 128 * 8;            // [2][256] exponents of query rows
   static constexpr uint32_t kOffInfo = kOffQx + 2 * 256 * 4;          // [2] UnitInfo
-  static constexpr uint32_t kOffTiles = kOffInfo + 64;                // [kTileInfos] TileInfo
-  static constexpr uint32_t kOffBar = kOffTiles + kTileInfos * 48;
+  static constexpr uint32_t kOffHalves = kOffInfo + 64;               // [2][kInfos] HalfInfo
+  static constexpr uint32_t kOffScales = kOffHalves + 2 * kInfos * 24;  // [kRawSlots][2] scales, NaN bits kNone: no page
+  static constexpr uint32_t kOffBar = kOffScales + kRawSlots * 8;
   // barriers
-  static constexpr uint32_t kFull = 0;                                // tile slots: written
+  static constexpr uint32_t kFull = 0;                                // slots: written
   static constexpr uint32_t kEmpty = kFull + kSlots;                  // and read
   static constexpr uint32_t kRawFull = kEmpty + kSlots;
   static constexpr uint32_t kRawEmpty = kRawFull + kRawSlots;
   static constexpr uint32_t kQFull = kRawEmpty + kRawSlots;
   static constexpr uint32_t kQEmpty = kQFull + 1;
-  static constexpr uint32_t kSFull = kQEmpty + 1;                     // + 2 warpgroup + half
+  static constexpr uint32_t kSFull = kQEmpty + 1;                     // + 2 warpgroup + parity of the half
   static constexpr uint32_t kPFull = kSFull + 4;
   static constexpr uint32_t kODone = kPFull + 4;
   static constexpr uint32_t kOFree = kODone + 4;                      // + warpgroup
-  static constexpr uint32_t kClean = kOFree + 2;                      // bf16: a slot's values looked through
+  static constexpr uint32_t kClean = kOFree + 2;                      // bf16: slots looked through
   static constexpr uint32_t kFinal = kClean + (FP8 ? 0 : kSlots);
   static constexpr uint32_t kBars = kFinal + 2;
   static constexpr uint32_t kOffMisc = kOffBar + kBars * 8;           // TMEM address, foul flag, 8 ints of the converters
@@ -174,15 +167,25 @@ RP_DEVI void commit_if(uint32_t on, uint32_t bar) {
       : "memory");
 }
 
-// A block's units, as each role walks them
+// A block's units, as each role walks them. COPIES as in Wide.
+template <int COPIES>
 struct Walk {
   Cursor c;
   int tiles, x, xe;  // tiles of the block; those of the present unit [x, xe)
   int base, live;    // first drafted slot, nodes
+  int row0, rows;    // first row of the unit in its key/value head, rows that have a node
+  bool pair;         // both warpgroups take every tile, with half the rows each
+  int h0, h1;        // halves of the first and the second warpgroup (a pair: of both, and 0)
   RP_DEVI void load(const PagedTreeParams& p) {
     xe = min(tiles, x + c.nt - c.t);
     live = row_count(p, c.b);
     base = c.len - live;
+    row0 = (c.u - c.h * p.rt) * p.rows;
+    rows = max(0, min(p.rows, live * p.G - row0));
+    pair = COPIES == 1 && rows > 128;
+    const int n = rows > 0 ? xe - x : 0;
+    h0 = pair ? 2 * n : 2 * ((n + 1) >> 1);
+    h1 = pair ? 0 : 2 * (n >> 1);
   }
   RP_DEVI bool next(const PagedTreeParams& p) {
     c.template forward<kWideTile>(p, xe - x);
@@ -191,19 +194,38 @@ struct Walk {
     load(p);
     return true;
   }
-  // first key of the unit's j-th tile in this block, from the last one on: a decaying
-  // bias (ALiBi) then has its largest logits first, and no maximum moves after those
-  RP_DEVI int key0(int j) const { return (c.t + xe - x - 1 - j) * kWideTile; }
+  // First key of a warpgroup's h-th half, from the last one of the block's tiles on: a
+  // decaying bias (ALiBi) then has its largest logits first, and no maximum moves
+  // after those.
+  RP_DEVI int place_of(int of, int h) const { return pair ? h : 2 * (of + (h & ~1)) + (h & 1); }  // from the last one on
+  RP_DEVI int end_tiles() const { return (c.t + xe - x) * kWideTile; }
+  RP_DEVI int key_of(int of, int h) const { return end_tiles() - kHalf * (place_of(of, h) + 1); }
   RP_DEVI int first_key() const { return c.t * kWideTile; }
   RP_DEVI int end_key() const { return min((c.t + xe - x) * kWideTile, c.len); }
-  // whether a tile needs masks
-  RP_DEVI bool special(int j) const { return key0(j) + kWideTile > base; }
+};
+
+// The order in which a unit's halves of keys and values pass through shared memory:
+// the keys of either warpgroup's first two halves, then for i = 0, 1, .. the values
+// of half i and the keys of half i + 2 of the one and of the other.
+struct Items {
+  int h0, h1, i, x;
+  bool value;
+  RP_DEVI Items(int a, int b) : h0(a), h1(b), i(-2), x(0), value(false) {}
+  RP_DEVI bool valid() const { return h0 > 0 && i < h0; }
+  RP_DEVI int half() const { return value ? i : i + 2; }
+  RP_DEVI void next() {
+    do {
+      value = !value;
+      if (value && (x ^= 1) == 0) ++i;
+    } while (i < h0 && (half() < 0 || half() >= (x ? h1 : h0)));
+  }
 };
 
 // A block's share. Each role calls this for itself, behind its register limit: what is
 // live across the roles' branch is kept to the lowest of them (and was spilled).
+template <int COPIES>
 struct Share {
-  Walk w;
+  Walk<COPIES> w;
   int size, at;  // cost of a block's share, and that at which the present unit starts
   RP_DEVI Share(const PagedTreeParams& p, int lane) : size(0), at(0) {
     constexpr int KT = kWideTile;
@@ -302,21 +324,21 @@ RP_DEVI float times_pow2(float x, int e) {
 // two codes times a scale as bf16
 RP_DEVI uint32_t bf16_of(uint32_t h2, float s) { return pack_bf16x2(half_lo(h2) * s, half_hi(h2) * s); }
 
-template <int D, bool FP8, int REP>
+template <int D, bool FP8, int COPIES>
 __global__ void __launch_bounds__(kWideThreads, 1)
     relpos_paged_wide_kernel(const __grid_constant__ PagedTreeParams p, const __grid_constant__ CUtensorMap tm_k,
                              const __grid_constant__ CUtensorMap tm_v) {
-  using W = Wide<D, FP8, REP>;
+  using W = Wide<D, FP8, COPIES>;
   constexpr int KT = kWideTile;
-  constexpr bool kPair = W::kPair;
-  constexpr int kStep = kPair ? 1 : 2;  // a warpgroup's tiles: x, x + 2, .. or all
+  // a slot is read by both warpgroups' products, or by one's, which then counts twice
+  constexpr int kReaders = COPIES == 1 ? 2 : 1;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* const smem = smem_raw + (sbase - smem_u32(smem_raw));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   auto bar = [&](uint32_t i) { return sbase + W::kOffBar + 8 * i; };
   volatile int* const foul = reinterpret_cast<volatile int*>(smem + W::kOffMisc + 4);
-  TileInfo* const tile_infos = reinterpret_cast<TileInfo*>(smem + W::kOffTiles);
+  HalfInfo* const half_infos = reinterpret_cast<HalfInfo*>(smem + W::kOffHalves);
   UnitInfo* const infos = reinterpret_cast<UnitInfo*>(smem + W::kOffInfo);
   int* const q_exp = reinterpret_cast<int*>(smem + W::kOffQx);
 
@@ -324,7 +346,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     for (uint32_t i = 0; i < W::kBars; ++i) {
       uint32_t n = 1;
       if (FP8 && i < W::kEmpty) n = 4;                          // converted by four warps
-      if (i >= W::kEmpty && i < W::kRawFull) n = kPair ? 2 : 1; // read by both issuers' products
+      if (i >= W::kEmpty && i < W::kRawFull) n = kReaders;
       if (i >= W::kRawEmpty && i < W::kQFull) n = 4;            // a warp each
       if (i == W::kQFull) n = 128;
       if (i == W::kQEmpty) n = 2;                               // both issuers
@@ -349,51 +371,92 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   bool ok = true;
   if (warp < 4) {
     setmaxnreg_dec<72>();
-    Share share(p, lane);
-    Walk& w = share.w;
+    Share<COPIES> share(p, lane);
+    Walk<COPIES>& w = share.w;
     const bool some = w.tiles > 0;
     if (warp == 0 && some) {
       // ------------------------------------------------------------ producer
-      uint32_t pos = 0;  // of the ring: K of tile i at 2 i, V behind it
-      const int per_tile = KT >> p.log_page;  // pages of a tile
+      uint32_t pos = 0, seq0 = 0, seq1 = 0;  // of the ring; either warpgroup's halves before
+      const int per_page = min(kHalf, 1 << p.log_page), boxes = kHalf / per_page;  // keys of a copy, copies
       constexpr int kRing = FP8 ? W::kRawSlots : W::kSlots;
-      constexpr uint32_t kSlotBytes = FP8 ? W::kRaw : W::kTile;
+      constexpr uint32_t kSlotBytes = FP8 ? W::kRaw : W::kSlot;
       const uint32_t full0 = FP8 ? W::kRawFull : W::kFull, empty0 = FP8 ? W::kRawEmpty : W::kEmpty;
       const uint32_t ring = sbase + (FP8 ? W::kOffRaw : W::kOffTile);
       const uint32_t none = static_cast<uint32_t>(p.num_pages) * p.Hkv;  // beyond the pool: zeros
       do {
-        for (int j = 0; ok && j < w.xe - w.x; ++j) {
-          const int key = w.key0(j) + (lane << p.log_page);
-          int page = -1;
-          bool there = false;
-          if (lane < per_tile && key < w.c.len) {
-            page = __ldg(w.c.pages + (key >> p.log_page));
-            there = page >= 0 && page < p.num_pages;
-            if (!there) atomicCAS(p.status, 0, RELPOS_ERR_PAGE);
+        // Pages (and scales) of 16 halves at a time, a 32-key group a lane: a lookup each
+        // would put its latency into every copy. Items go back to the last 16 but one.
+        int page_now = -1, page_last = -1, batch = -1;
+        [[maybe_unused]] float2 scale_now = make_float2(0.f, 0.f), scale_last = scale_now;
+        auto look = [&](int to) {
+          page_last = page_now, scale_last = scale_now;
+          batch = to;
+          const int key = w.end_tiles() - kHalf * (16 * to + (lane >> 1) + 1) + 32 * (lane & 1);
+          const int page = key >= w.first_key() && key < w.c.len ? __ldg(w.c.pages + (key >> p.log_page)) : -2;
+          if (page != -2 && (page < 0 || page >= p.num_pages)) atomicCAS(p.status, 0, RELPOS_ERR_PAGE);
+          page_now = page >= 0 && page < p.num_pages ? page : -1;
+          if constexpr (FP8) {
+            const size_t ph = static_cast<size_t>(max(page_now, 0)) * p.Hkv + w.c.h;
+            scale_now = make_float2(__ldg(p.k_scale + ph), __ldg(p.v_scale + ph));
           }
-          const uint32_t ph = there ? static_cast<uint32_t>(page) * p.Hkv + w.c.h : none;
-          const uint32_t n = __popc(__ballot_sync(0xffffffffu, there));
-          for (int kv = 0; ok && kv < 2; ++kv, ++pos) {
+        };
+#pragma unroll 1
+        for (Items it(w.h0, w.h1); ok && it.valid(); it.next(), ++pos) {
+          const int g = w.place_of(it.x, it.half());
+          if (g >> 4 > batch) look(g >> 4);
+          // lanes 0 and 1: the half's groups
+          const int from = 2 * (g & 15) + (lane & 1);
+          const bool recent = g >> 4 == batch;
+          const int page = __shfl_sync(0xffffffffu, recent ? page_now : page_last, from);
+          const bool there = page >= 0;
+          if constexpr (FP8) {
+            const float sk = __shfl_sync(0xffffffffu, recent ? scale_now.x : scale_last.x, from);
+            const float sv = __shfl_sync(0xffffffffu, recent ? scale_now.y : scale_last.y, from);
             const uint32_t slot = pos % kRing;
-            if (pos >= kRing) ok = __all_sync(0xffffffffu, wait_on(bar(empty0 + slot), (pos / kRing - 1) & 1));
+            if (pos >= kRing) ok = wait_warp(bar(empty0 + slot), (pos / kRing - 1) & 1);
             if (!ok) break;
-            const uint32_t dst = ring + slot * kSlotBytes;
-            if (lane == 0)
-              mbar_arrive_expect_tx(bar(full0 + slot), FP8 ? (n * W::kRaw) >> (7 - p.log_page) : W::kTile);
-            __syncwarp();
-            if (lane < per_tile) {
-              if constexpr (FP8) {
-                const uint32_t bytes = static_cast<uint32_t>(D) << p.log_page;
-                if (there) bulk_load(dst + lane * bytes, (kv ? p.v : p.k) + static_cast<size_t>(ph) * bytes, bytes, bar(full0 + slot));
-              } else {
-                for (int hf = 0; hf < W::kHalves; ++hf)
-                  tma_load_3d(dst + hf * 16384 + ((lane << p.log_page) * 128), kv ? &tm_v : &tm_k, bar(full0 + slot), 64 * hf,
-                              0, static_cast<int>(ph));
+            if (lane < 2) {
+              float* const of_slot = reinterpret_cast<float*>(smem + W::kOffScales) + 2 * slot;
+              float k2, v2, kr, vr;
+              split_scale(sk, k2, kr);
+              split_scale(sv, v2, vr);
+              const float of_kind = it.value ? v2 : k2;
+              of_slot[lane] = !there ? __uint_as_float(kNoPage) : of_kind == of_kind ? of_kind : NAN;
+              if (!it.value) {
+                HalfInfo& info = half_infos[it.x * kInfos + ((it.x ? seq1 : seq0) + it.half()) % kInfos];
+                info.k_rest[lane] = kr, info.v_rest[lane] = vr;
+                info.flags[lane] = there ? 1 | (kr != 1.f) << 1 | (vr != 1.f) << 2 : 0;
               }
             }
-            __syncwarp();
+          } else {
+            const uint32_t slot = pos % kRing;
+            if (pos >= kRing) ok = wait_warp(bar(empty0 + slot), (pos / kRing - 1) & 1);
+            if (!ok) break;
+            if (lane < 2 && !it.value)
+              half_infos[it.x * kInfos + ((it.x ? seq1 : seq0) + it.half()) % kInfos].flags[lane] = there;
           }
+          const uint32_t slot = pos % kRing, dst = ring + slot * kSlotBytes;
+          const bool copies = lane < boxes;
+          const uint32_t n = __popc(__ballot_sync(0xffffffffu, copies && there));
+          if (lane == 0) mbar_arrive_expect_tx(bar(full0 + slot), FP8 ? n * per_page * D : W::kSlot);
+          __syncwarp();
+          if (copies) {
+            const int in_page = (w.end_tiles() - kHalf * (g + 1) + lane * per_page) & ((1 << p.log_page) - 1);
+            const uint32_t ph = there ? static_cast<uint32_t>(page) * p.Hkv + w.c.h : none;
+            if constexpr (FP8) {
+              if (there)
+                bulk_load(dst + lane * per_page * D,
+                          (it.value ? p.v : p.k) + ((static_cast<size_t>(ph) << p.log_page) + in_page) * D, per_page * D,
+                          bar(full0 + slot));
+            } else {
+              for (int hf = 0; hf < D / 64; ++hf)
+                tma_load_3d(dst + hf * 8192 + lane * per_page * 128, it.value ? &tm_v : &tm_k, bar(full0 + slot), 64 * hf,
+                            in_page, static_cast<int>(ph));
+            }
+          }
+          __syncwarp();
         }
+        seq0 += w.h0, seq1 += w.h1;
       } while (ok && w.next(p));
       // never leave with copies in flight
       for (uint32_t k = pos > kRing ? pos - kRing : 0; k < pos; ++k)
@@ -406,10 +469,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       const uint32_t leader = elect_one();
       const uint32_t x = warp == 1 ? 0u : 1u;
       const uint32_t s_col = tmem + kColS + 128 * x, o_col = tmem + kColO + D * x;
-      const uint64_t dq = smem_desc_sw128(sbase + W::kOffQ + (kPair ? x * W::kQTile : 0u), 16, 1024);
-      uint32_t seq = 0, mine = 0, unit = 0;  // tiles before the unit, own halves, units
+      uint32_t pos = 0, mine = 0, unit = 0;  // of the ring, own halves before, units
       do {
-        const int n = w.xe - w.x;
         ok = wait_warp(bar(W::kQFull), unit & 1);
         const bool f16 = FP8 && infos[unit & 1].f16;
         // the operands' type: bf16 (1) or fp16 (0)
@@ -417,49 +478,54 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         const uint32_t types = f16 ? 0u : kTypes;
         const uint32_t idesc_s = (idesc_bf16_f32(128, kHalf, 0, 0) & ~kTypes) | types;
         const uint32_t idesc_o = (idesc_bf16_f32(128, D, 0, 1) & ~kTypes) | types;
-        const int j0 = kPair ? 0 : x;
-        const int halves = j0 < n ? 2 * ((n - j0 + kStep - 1) / kStep) : 0;  // of the own tiles
+        const uint64_t dq = smem_desc_sw128(sbase + W::kOffQ + (w.pair ? x * W::kQTile : 0u), 16, 1024);
+        const int halves = w.pair || x == 0 ? w.h0 : w.h1;
+        const bool twice = kReaders == 2 && !w.pair;
         // half i's scores two halves ahead of its weights' product
 #pragma unroll 1
-        for (int i = -2; ok && i < halves; ++i) {
-          if (i >= 0) {
-            const uint32_t vp = 2 * (seq + j0 + (i >> 1) * kStep) + 1, vs = vp % W::kSlots, c = mine + i, y = i & 1;
+        for (int i = -2; ok && i < w.h0; ++i) {
+          // positions as in Items
+          const int before = (i >= 0) + (i + 2 < w.h0), behind = (i >= 0 && i < w.h1) + (i + 2 < w.h1);
+          const uint32_t vp = pos + (w.pair || x == 0 ? 0 : before), kp = vp + (i >= 0 && i < halves);
+          pos += before + behind;
+          if (i >= 0 && i < halves) {
+            const uint32_t vs = vp % W::kSlots, c = mine + i, y = i & 1;
             ok = wait_warp(bar(W::kPFull + 2 * x + y), (c >> 1) & 1);
             if (ok && i == 0 && unit > 0) ok = wait_warp(bar(W::kOFree + x), (unit - 1) & 1);
-            if (ok && y == 0) ok = wait_warp(bar(W::kFull + vs), (vp / W::kSlots) & 1);
-            if (!FP8 && ok && y == 0) ok = wait_warp(bar(W::kClean + vs), (vp / W::kValueTurn) & 1);
+            if (ok) ok = wait_warp(bar(W::kFull + vs), (vp / W::kSlots) & 1);
+            if (!FP8 && ok) ok = wait_warp(bar(W::kClean + vs), (vp / W::kSlots) & 1);
             if (!ok) break;
             tc_fence_after();
-            const uint64_t dv = smem_desc_sw128(sbase + W::kOffTile + vs * W::kTile + y * 8192, 16384, 1024);
+            const uint64_t dv = smem_desc_sw128(sbase + W::kOffTile + vs * W::kSlot, 8192, 1024);
             const uint32_t p_col = s_col + kHalf * y;
             // (bf16: the second parts of the weights behind the first)
 #pragma unroll 1
             for (int kk = 0; kk < (f16 ? 1 : 2) * kHalf / 16; ++kk)
               umma_ts_if(leader, o_col, p_col + 8 * kk, dv + 128 * (kk & (kHalf / 16 - 1)), idesc_o, i > 0 || kk > 0);
             commit_if(leader, bar(W::kODone + 2 * x + y));
-            if (y) commit_if(leader, bar(W::kEmpty + vs));
+            commit_if(leader, bar(W::kEmpty + vs));
+            if (twice) commit_if(leader, bar(W::kEmpty + vs));
           }
           const int a = i + 2;
           if (a >= halves) continue;
-          const uint32_t kp = 2 * (seq + j0 + (a >> 1) * kStep), ks = kp % W::kSlots, c = mine + a, y = a & 1;
-          if (y == 0) ok = wait_warp(bar(W::kFull + ks), (kp / W::kSlots) & 1);
+          const uint32_t ks = kp % W::kSlots, c = mine + a, y = a & 1;
+          ok = wait_warp(bar(W::kFull + ks), (kp / W::kSlots) & 1);
           // the weights of the last half but one lie in its columns
           if (ok && c >= 2) ok = wait_warp(bar(W::kODone + 2 * x + y), ((c - 2) >> 1) & 1);
           if (!ok) break;
           tc_fence_after();
-          const uint64_t dk = smem_desc_sw128(sbase + W::kOffTile + ks * W::kTile + y * 8192, 16, 1024);
+          const uint64_t dk = smem_desc_sw128(sbase + W::kOffTile + ks * W::kSlot, 16, 1024);
 #pragma unroll 1
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint64_t off = (kk >> 2) * 1024 + 2 * (kk & 3);
-            umma_ss_if(leader, s_col + kHalf * y, dq + off, dk + off, idesc_s, kk > 0);
-          }
+          for (int kk = 0; kk < D / 16; ++kk)
+            umma_ss_if(leader, s_col + kHalf * y, dq + (kk >> 2) * 1024 + 2 * (kk & 3), dk + (kk >> 2) * 512 + 2 * (kk & 3),
+                       idesc_s, kk > 0);
           commit_if(leader, bar(W::kSFull + 2 * x + y));
-          if (y) commit_if(leader, bar(W::kEmpty + ks));
+          commit_if(leader, bar(W::kEmpty + ks));
+          if (twice) commit_if(leader, bar(W::kEmpty + ks));
           if (a == halves - 1) commit_if(leader, bar(W::kQEmpty));
         }
-        if (halves == 0) commit_if(leader, bar(W::kQEmpty));  // no tile of the unit
+        if (halves == 0) commit_if(leader, bar(W::kQEmpty));  // no half of the unit
         mine += halves;
-        seq += n;
         ++unit;
       } while (ok && w.next(p));
       commit_if(leader, bar(W::kFinal + x));
@@ -467,8 +533,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     }
   } else if (warp < 12) {
     setmaxnreg_inc<168>();
-    Share share(p, lane);
-    Walk& w = share.w;
+    Share<COPIES> share(p, lane);
+    Walk<COPIES>& w = share.w;
     int& at = share.at;
     const int size = share.size;
     if (!p.direct && threadIdx.x == 128) p.ends[2 * blockIdx.x] = p.ends[2 * blockIdx.x + 1] = make_int4(0, 0, 0, 0);
@@ -484,11 +550,12 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     int* const deep = reinterpret_cast<int*>(smem + W::kOffDeep);
     float2* const ml = reinterpret_cast<float2*>(smem + W::kOffMl);
     const int lut_len = p.t5_R + 1;
-    uint32_t mine = 0, unit = 0, seq = 0;  // halves, units, tiles before
+    uint32_t mine = 0, unit = 0, seq0 = 0, seq1 = 0;  // own halves, units, either warpgroup's halves before
     int tree_of = -1, lut_of = -1;
     if (some) do {
-      const int n = w.xe - w.x, len = w.c.len, base = w.base, live = w.live, h = w.c.h;
-      const int row0 = (w.c.u - h * p.rt) * p.rows, rows = min(p.G * p.Lq - row0, p.rows);
+      const int n = w.xe - w.x, len = w.c.len, base = w.base, live = w.live, h = w.c.h, row0 = w.row0;
+      const bool pair = w.pair;
+      const int own = pair || x == 0 ? w.h0 : w.h1;  // halves
       // the tree, and the biases of the distances below the last bucket's
       if (tree_of != w.c.b && warp == 4) {
         tree_lines(p, w.c.b, live, lane, line);
@@ -506,11 +573,10 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       }
       named_bar_sync(1, 256);
       // this thread's row of the unit
-      const int half = (rows + 1) >> 1;
-      const int ri = kPair ? x * half + t : t % W::kLanes;
-      const bool real = kPair ? t < half && ri < rows : ri < rows;
+      const int half = (w.rows + 1) >> 1;
+      const int ri = pair ? x * half + t : t % W::kLanes;
+      const bool active = ri < w.rows && (!pair || t < half);
       const int r = row0 + ri, node = r / p.G, hq = h * p.G + r - node * p.G;
-      const bool active = real && node < live;
       const bool any = __any_sync(0xffffffffu, active);
       const unsigned long long sees = active ? line[node] : 0ull;
       const float* const my_lut = lut + (active ? (r - node * p.G) * lut_len : 0);
@@ -528,42 +594,31 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       int ev = 0;
 
       float m_run = -INFINITY, l_run = 0.f;
-      // bf16: pages of a tile's 32-key groups in lanes 0 .. 3, a tile ahead
-      int page_ahead = -1;
-      auto look = [&](int j) {
-        const int key = w.key0(j) + 32 * lane;
-        page_ahead = !FP8 && lane < 4 && j < n && key < len ? __ldg(w.c.pages + (key >> p.log_page)) : -1;
-      };
-      const int j0 = kPair ? 0 : x;
-      look(j0);
-      for (int j = j0; ok && j < n; j += kStep) {
-        unsigned there = 0xfu, k_rests = 0u, v_rests = 0u;
-        if constexpr (!FP8) {
-          there = __ballot_sync(0xffffffffu, page_ahead >= 0 && page_ahead < p.num_pages) & 0xfu;
-          look(j + kStep);
-        }
-        const TileInfo& info = tile_infos[(seq + j) % kTileInfos];
 #pragma unroll 1
-        for (int y = 0; y < 2; ++y, ++mine) {
-          const int key0 = w.key0(j) + kHalf * y;
-          ok = ok && __all_sync(0xffffffffu, wait_on(bar(W::kSFull + 2 * x + y), (mine >> 1) & 1));
+      for (int i = 0; ok && i < own; ++i, ++mine) {
+        {
+          const int y = i & 1, key0 = w.key_of(x, i);
+          // bits of the two groups: page there, rest of the keys' scale, of the values'
+          unsigned there = 3u, k_rests = 0u, v_rests = 0u;
+          const HalfInfo& info = half_infos[pair || x == 0 ? (seq0 + i) % kInfos : kInfos + (seq1 + i) % kInfos];
+          ok = __all_sync(0xffffffffu, wait_on(bar(W::kSFull + 2 * x + y), (mine >> 1) & 1));
           if (!ok) break;
           tc_fence_after();
-          if (FP8 && y == 0) {
-            const uint32_t flags = *reinterpret_cast<const uint32_t*>(info.flags);
-            auto bits = [&](int of) {
-              const uint32_t f = flags >> of & 0x01010101u;
-              return (f | f >> 7 | f >> 14 | f >> 21) & 0xfu;
-            };
-            there = bits(0), k_rests = bits(1), v_rests = bits(2);
+          {
+            const uint32_t f = *reinterpret_cast<const uint16_t*>(info.flags);
+            if (f != 0x0101u) {
+              there = (f & 1u) | (f >> 7 & 2u);
+              k_rests = (f >> 1 & 1u) | (f >> 8 & 2u);
+              v_rests = (f >> 2 & 1u) | (f >> 9 & 2u);
+            }
           }
-          if (j == j0 && y == 0) {
+          if (i == 0) {
             if constexpr (FP8) {
               const UnitInfo u = infos[unit & 1];
               f16 = u.f16;
               if (f16) {
                 ev = u.ev;
-                scale = times_pow2(p.scale_log2, u.ek + q_exp[(unit & 1) * 256 + (kPair ? 128 * x + t : ri)]);
+                scale = times_pow2(p.scale_log2, u.ek + q_exp[(unit & 1) * 256 + (pair ? 128 * x + t : ri)]);
               }
             }
             if (p.mode == RELPOS_ALIBI) slope_raw = slope / scale;
@@ -573,15 +628,14 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           if (any) {
             const uint32_t tS = tS0 + kHalf * y;
             const bool near = p.mode == RELPOS_T5 && base - (key0 + kHalf) < p.t5_R;
-            const unsigned both = 3u << 2 * y;  // this half's groups
-            const bool whole = key0 + kHalf > base || (there & both) != both || near || odd || !plain || (k_rests & both);
+            const bool whole = key0 + kHalf > base || there != 3u || near || odd || !plain || k_rests;
             if (whole) {  // the scores become logits
 #pragma unroll 1
               for (int q = 0; q < NC / 16; ++q) {
                 uint32_t s[16];
                 tmem_ld16(tS + col0 + 16 * q, s);
-                const int group = 2 * y + ((col0 + 16 * q) >> 5);
-                const float mul = FP8 ? scale * info.rest[group] : scale;
+                const int group = (col0 + 16 * q) >> 5;
+                const float mul = FP8 ? scale * info.k_rest[group] : scale;
                 const int o0 = key0 + col0 + 16 * q - base;  // among the drafted slots
                 unsigned vis = 0xffffu;
                 if (o0 >= 0)
@@ -654,7 +708,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             if (any_moves) {
               const float alpha = moves ? ex2_approx(m_run - m_new) : 1.f;
               if (moves) m_run = m_new;
-              if (j > j0 || y > 0) {  // O so far: its last product has to be done; the next waits for these weights
+              if (i > 0) {  // O so far: its last product has to be done; the next waits for these weights
                 ok = __all_sync(0xffffffffu, wait_on(bar(W::kODone + 2 * x + 1 - y), ((mine - 1) >> 1) & 1));
                 if (!ok) break;
                 tc_fence_after();
@@ -690,7 +744,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                   else
                     sum0 = __fadd2_rn(sum0, make_float2(a, b));
                   if constexpr (kRests) {
-                    const float v_rest = info.rest[4 + 2 * y + ((col0 + 16 * q) >> 5)];
+                    const float v_rest = info.v_rest[(col0 + 16 * q) >> 5];
                     a *= v_rest, b *= v_rest;
                   }
                   if constexpr (F16) {
@@ -703,7 +757,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                 tmem_st8(tS + col0 / 2 + 8 * q, hi);
                 if constexpr (!F16) tmem_st8(tS + 32 + col0 / 2 + 8 * q, lo);
               }
-              if constexpr (W::kCopies > 1) {
+              if constexpr (COPIES > 1) {
                 const uint32_t zero[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
@@ -713,7 +767,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                 }
               }
             };
-            if (FP8 && (v_rests & both)) {
+            if (FP8 && v_rests) {
               if (f16)
                 weights(std::true_type{}, std::true_type{});
               else
@@ -730,10 +784,10 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           mbar_arrive(bar(W::kPFull + 2 * x + y));
         }
       }
-      seq += n;
+      seq0 += w.h0, seq1 += w.h1;
       // ---- the unit's parts joined. After a wait that ran out a warp goes on without
       // waiting, so that all meet at the barriers.
-      if (ok && n > j0) ok = __all_sync(0xffffffffu, wait_on(bar(W::kODone + 2 * x + 1), ((mine - 1) >> 1) & 1));
+      if (ok && own > 0) ok = __all_sync(0xffffffffu, wait_on(bar(W::kODone + 2 * x + 1), ((mine - 1) >> 1) & 1));
       if (f16 && m_run != -INFINITY) m_run -= kF16Shift;  // what O and the sum are relative to
       ml[128 * x + t] = make_float2(m_run, l_run);
       // the exponent of O goes with the other warpgroup's too
@@ -755,47 +809,50 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       float* const part = p.part_o + (static_cast<size_t>(slot) * p.rows + ri) * D;
       __nv_bfloat16* const to = p.out + w.c.b * p.o_batch + hq * p.o_head + node * p.o_row;
       float m = m_run, sum = l_run;
-      if constexpr (W::kCopies == 1) {
+      if constexpr (COPIES == 1) {
         float by0 = 1.f, by1 = 0.f;
-        if constexpr (!kPair) {
+        if (!pair) {
           const float2 p0 = ml[t], p1 = ml[128 + t];
           m = fmaxf(p0.x, p1.x);
           by0 = part_of(p0, m), by1 = part_of(p1, m);
           sum = sum_of(p0, by0) + sum_of(p1, by1);
         }
         const float inv = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
-        const uint32_t tO0 = tO + (kPair ? D * x : 0);
-        const int from = kPair ? 0 : x * (D / 2), upto = kPair ? D : from + D / 2;
+        const bool second = !pair && w.h1 > 0;
+        const uint32_t tO0 = tO + (pair ? D * x : 0);
+        const int from = pair ? 0 : x * (D / 2), upto = pair ? D : from + D / 2;
+        if (any) {
 #pragma unroll 1
-        for (int col = from; col < upto; col += 8) {
-          uint32_t o0[8], o1[8];
-          tmem_ld8(tO0 + col, o0);
-          if (!kPair) tmem_ld8(tO0 + D + col, o1);
-          tmem_ld8_wait(o0);
-          if (!kPair) tmem_ld8_wait(o1);
-          if (!real) continue;
-          float v[8];
+          for (int col = from; col < upto; col += 8) {
+            uint32_t o0[8], o1[8];
+            tmem_ld8(tO0 + col, o0);
+            if (second) tmem_ld8(tO0 + D + col, o1);
+            tmem_ld8_wait(o0);
+            if (second) tmem_ld8_wait(o1);
+            if (!active) continue;
+            float v[8];
 #pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            v[c] = __uint_as_float(o0[c]) * by0;
-            if (!kPair && n > 1) v[c] += __uint_as_float(o1[c]) * by1;
-            v[c] = active ? v[c] * inv * unit_v : 0.f;
-          }
-          if (!whole) {
-            float4* const to4 = reinterpret_cast<float4*>(part + col);
-            to4[0] = make_float4(v[0], v[1], v[2], v[3]);
-            to4[1] = make_float4(v[4], v[5], v[6], v[7]);
-          } else if (p.o_vec) {
-            *reinterpret_cast<uint4*>(to + col) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                                             pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
-          } else {
+            for (int c = 0; c < 8; ++c) {
+              v[c] = __uint_as_float(o0[c]) * by0;
+              if (second) v[c] += __uint_as_float(o1[c]) * by1;
+              v[c] = v[c] * inv * unit_v;
+            }
+            if (!whole) {
+              float4* const to4 = reinterpret_cast<float4*>(part + col);
+              to4[0] = make_float4(v[0], v[1], v[2], v[3]);
+              to4[1] = make_float4(v[4], v[5], v[6], v[7]);
+            } else if (p.o_vec) {
+              *reinterpret_cast<uint4*>(to + col) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                                               pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+            } else {
 #pragma unroll
-            for (int c = 0; c < 8; ++c) to[col + c] = __float2bfloat16_rn(v[c]);
+              for (int c = 0; c < 8; ++c) to[col + c] = __float2bfloat16_rn(v[c]);
+            }
           }
         }
       } else {
         // all copies of both warpgroups, in order, through shared memory
-        constexpr int kParts = 2 * W::kCopies;
+        constexpr int kParts = 2 * COPIES;
         float2 parts[kParts];
         m = -INFINITY;
 #pragma unroll
@@ -809,7 +866,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         for (int i = 0; i < kParts; ++i) {
           const float by = part_of(parts[i], m);
           sum += sum_of(parts[i], by);
-          if (i == x * W::kCopies + copy) mine_by = by;
+          if (i == x * COPIES + copy) mine_by = by;
         }
         const float inv = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
         float* const join = reinterpret_cast<float*>(smem + W::kOffJoin);
@@ -821,10 +878,10 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           float* const mine_at = join + (threadIdx.x - 128) * 17;
 #pragma unroll
           for (int c = 0; c < 16; ++c)
-            mine_at[c] = active && n > x ? __uint_as_float(o[c]) * mine_by * inv * unit_v : 0.f;
+            mine_at[c] = active && own > 0 ? __uint_as_float(o[c]) * mine_by * inv * unit_v : 0.f;
           named_bar_sync(1, 256);
           // 4 columns of a row a thread
-          for (int i = threadIdx.x - 128; i < rows * 4; i += 256) {
+          for (int i = threadIdx.x - 128; i < w.rows * 4; i += 256) {
             const int row = i >> 2, c = 4 * (i & 3);
             float v[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -849,11 +906,18 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           named_bar_sync(1, 256);
         }
       }
+      if (whole) {  // rows without a node
+        const int all = min(p.G * p.Lq - row0, p.rows);
+        for (int i = w.rows * D + static_cast<int>(threadIdx.x) - 128; i < all * D; i += 256) {
+          const int rr = row0 + i / D, nd = rr / p.G;
+          p.out[w.c.b * p.o_batch + (h * p.G + rr - nd * p.G) * p.o_head + nd * p.o_row + i % D] = __float2bfloat16_rn(0.f);
+        }
+      }
       if (*foul && active && copy == 0) {
         // drafted values of this block's tiles that are not finite, for the rows that
         // see them: infinities and NaN as their sum
         const int lo = max(w.first_key() - base, 0), hi = w.end_key() - base;
-        const int from = kPair ? 0 : x * (D / 2), upto = kPair ? D : from + D / 2;
+        const int from = pair ? 0 : x * (D / 2), upto = pair ? D : from + D / 2;
 #pragma unroll 1
         for (int c = from; c < upto; ++c) {
           float y = 0.f;
@@ -877,7 +941,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             part[c] = y;
         }
       }
-      if (!whole && (kPair || x == 0) && copy == 0 && real)
+      if (!whole && (pair || x == 0) && copy == 0 && active)
         *reinterpret_cast<float2*>(p.part_ml + 2 * (static_cast<size_t>(slot) * p.rows + ri)) =
             make_float2(m == -INFINITY ? -FLT_MAX : m, sum);
       tc_fence_before();
@@ -888,8 +952,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     } while (w.next(p));
   } else {
     setmaxnreg_dec<104>();
-    Share share(p, lane);
-    Walk& w = share.w;
+    Share<COPIES> share(p, lane);
+    Walk<COPIES>& w = share.w;
     const bool some = w.tiles > 0;
     if (p.direct && !some) {  // no key is seen: zero rows
       if (threadIdx.x == 384) report_length(p, w.c.b);
@@ -902,11 +966,10 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     }
     // -------------------------------------------------------------- query rows, values
     const int t = threadIdx.x & 127, wq = warp & 3;
-    uint32_t unit = 0, seq = 0;
+    uint32_t unit = 0, pos = 0;  // units, items
     int* const range = reinterpret_cast<int*>(smem + W::kOffMisc + 16);  // [4][2] of the warps
     if (some) do {
-      const int n = w.xe - w.x, len = w.c.len, base = w.base, h = w.c.h;
-      const int row0 = (w.c.u - h * p.rt) * p.rows, rows = min(p.G * p.Lq - row0, p.rows);
+      const int len = w.c.len, base = w.base, h = w.c.h;
       if (ok && unit > 0) ok = __all_sync(0xffffffffu, wait_on(bar(W::kQEmpty), (unit - 1) & 1));
       bool f16 = false;
       int ek = 0, ev = 0;
@@ -943,19 +1006,19 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       }
       // query rows: 8 values a lane, D / 8 lanes a row, 4 rows' loads at a time
       constexpr int kQLanes = D / 8, kQStep = 128 / kQLanes;  // rows of a step
-      constexpr int kQRows = kPair ? 256 : 128;               // of the tiles
-      const int half = (rows + 1) >> 1;
+      const int q_rows = w.pair ? 256 : 128;                  // of the tiles
+      const int half = (w.rows + 1) >> 1;
 #pragma unroll 1
-      for (int i0 = 0; i0 < kQRows; i0 += 4 * kQStep) {
+      for (int i0 = 0; i0 < q_rows; i0 += 4 * kQStep) {
         uint4 u[4];
         const int c = t % kQLanes;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int line_of = i0 + e * kQStep + t / kQLanes;  // row of the tiles
-          const int ri = kPair ? (line_of >> 7) * half + (line_of & 127) : line_of % W::kLanes;
-          const int r = row0 + ri, node = r / p.G, hq = h * p.G + r - node * p.G;
+          const int ri = w.pair ? (line_of >> 7) * half + (line_of & 127) : line_of % W::kLanes;
+          const int r = w.row0 + ri, node = r / p.G, hq = h * p.G + r - node * p.G;
           u[e] = make_uint4(0u, 0u, 0u, 0u);
-          if (ri < rows && (!kPair || (line_of & 127) < half) && node < w.live) {
+          if (ri < w.rows && (!w.pair || (line_of & 127) < half)) {
             const __nv_bfloat16* q = p.Q + w.c.b * p.q_batch + hq * p.q_head + node * p.q_row + 8 * c;
             if (p.q_vec) {
               u[e] = __ldg(reinterpret_cast<const uint4*>(q));
@@ -992,129 +1055,102 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       }
       fence_async_smem();
       mbar_arrive(bar(W::kQFull));
-      // pages and scales of this warp's 32 keys of a tile, which are one page's: pages
-      // two tiles ahead, scales one
-      auto page_of = [&](int j) {
-        const int key = w.key0(j) + 32 * wq;
-        const int page = FP8 && j < n && key < len ? __ldg(w.c.pages + (key >> p.log_page)) : -1;
-        return page < p.num_pages ? page : -1;
-      };
-      auto scales_of = [&](int page) {
-        if (!FP8 || page < 0) return make_float2(0.f, 0.f);
-        const size_t ph = static_cast<size_t>(page) * p.Hkv + h;
-        return make_float2(__ldg(p.k_scale + ph), __ldg(p.v_scale + ph));
-      };
-      int page = page_of(0), page_next = page_of(1);
-      float2 scales = scales_of(page);
-      for (int j = 0; ok && j < n; ++j) {
-        const int key0 = w.key0(j);
-        const bool special = w.special(j);
-        if constexpr (FP8) {
-          const float2 scales_next = scales_of(page_next);
-          const int page_after = page_of(j + 2);
-          float s2[2], rest[2];
-          split_scale(scales.x, s2[0], rest[0]);
-          split_scale(scales.y, s2[1], rest[1]);
-          if (lane == 0) {
-            TileInfo& info = tile_infos[(seq + j) % kTileInfos];
-            info.rest[wq] = rest[0], info.rest[4 + wq] = rest[1];
-            info.flags[wq] = page >= 0 ? 1 | (rest[0] != 1.f) << 1 | (rest[1] != 1.f) << 2 : 0;
-          }
-          for (int kv = 0; kv < 2; ++kv) {
-            const uint32_t pos = 2 * (seq + j) + kv, rs = pos % W::kRawSlots, cs = pos % W::kSlots;
-            ok = wait_on(bar(W::kRawFull + rs), (pos / W::kRawSlots) & 1);
-            if (pos >= W::kSlots) ok = ok && wait_on(bar(W::kEmpty + cs), (pos / W::kSlots - 1) & 1);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            const uint32_t raw = sbase + W::kOffRaw + rs * W::kRaw, to = sbase + W::kOffTile + cs * W::kTile;
-            // 8 rows a step, 4 lanes a row (of half a row at d = 128, odd rows the other
-            // half, so that reads and writes meet all banks); 4 steps' loads at a time
-            auto convert = [&](auto code_pairs, auto special_rows) {
-              constexpr bool kSpecial = decltype(special_rows)::value;
-              const int g = lane & 3, r0 = 32 * wq + (lane >> 2);
 #pragma unroll 1
-              for (int it0 = 0; it0 < 4 * W::kHalves; it0 += 4) {
-                // (row, half) of step e: rows go on by 8 with each step, at d = 128 with
-                // every other
-                const int r1 = r0 + 8 * (D == 64 ? it0 : it0 / 2), odd = D == 64 ? 0 : r0 & 1;
-                auto row_of = [&](int e) { return r1 + 8 * (D == 64 ? e : e / 2); };
-                auto half_of = [&](int e) { return D == 64 ? 0 : (e & 1) ^ odd; };
-                uint4 u[4];
+      for (Items now(w.h0, w.h1); ok && now.valid(); now.next(), ++pos) {
+        const int key0 = w.key_of(now.x, now.half());
+        if constexpr (FP8) {
+          const uint32_t rs = pos % W::kRawSlots, cs = pos % W::kSlots;
+          ok = wait_on(bar(W::kRawFull + rs), (pos / W::kRawSlots) & 1);
+          if (pos >= W::kSlots) ok = ok && wait_on(bar(W::kEmpty + cs), (pos / W::kSlots - 1) & 1);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          // of this warp's 16 keys, which are one page's
+          const float given = reinterpret_cast<const float*>(smem + W::kOffScales)[2 * rs + (wq >> 1)];
+          const bool there = __float_as_uint(given) != kNoPage;
+          const float s = there ? given : 0.f;
+          const uint32_t raw = sbase + W::kOffRaw + rs * W::kRaw, to = sbase + W::kOffTile + cs * W::kSlot;
+          // 8 rows a step, 4 lanes a row (of half a row at d = 128, odd rows the other
+          // half, so that reads and writes meet all banks)
+          auto convert = [&](auto code_pairs, auto special_rows) {
+            constexpr bool kSpecial = decltype(special_rows)::value;
+            constexpr int kSteps = D / 32;
+            const int g = lane & 3, r0 = 16 * wq + (lane >> 2), odd = D == 64 ? 0 : r0 & 1;
+            auto row_of = [&](int e) { return r0 + 8 * (D == 64 ? e : e / 2); };
+            auto half_of = [&](int e) { return D == 64 ? 0 : (e & 1) ^ odd; };
+            uint4 u[kSteps];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) u[e] = lds128(raw + row_of(e) * D + half_of(e) * 64 + g * 16);
+            for (int e = 0; e < kSteps; ++e) u[e] = lds128(raw + row_of(e) * D + half_of(e) * 64 + g * 16);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  const int r = row_of(e);
-                  if constexpr (kSpecial)
-                    if (page < 0 || key0 + r >= len) u[e] = make_uint4(0u, 0u, 0u, 0u);
-                  const uint32_t c4[4] = {u[e].x, u[e].y, u[e].z, u[e].w};
-                  uint32_t o[8];
+            for (int e = 0; e < kSteps; ++e) {
+              const int r = row_of(e);
+              if constexpr (kSpecial)
+                if (!there || key0 + r >= len) u[e] = make_uint4(0u, 0u, 0u, 0u);
+              const uint32_t c4[4] = {u[e].x, u[e].y, u[e].z, u[e].w};
+              uint32_t o[8];
 #pragma unroll
-                  for (int k = 0; k < 4; ++k) o[2 * k] = code_pairs(half2_lo(c4[k])), o[2 * k + 1] = code_pairs(half2_hi(c4[k]));
-                  if constexpr (kSpecial) {
-                    if (kv && key0 + r >= base) {
-                      const uint32_t ones = f16 ? 0x7c007c00u : 0x7f807f80u;  // exponents of what is not finite
-                      const uint32_t gone = key0 + r >= len ? ~0u : 0u;
+              for (int k = 0; k < 4; ++k) o[2 * k] = code_pairs(half2_lo(c4[k])), o[2 * k + 1] = code_pairs(half2_hi(c4[k]));
+              if constexpr (kSpecial) {
+                if (now.value && key0 + r >= base) {
+                  const uint32_t ones = f16 ? 0x7c007c00u : 0x7f807f80u;  // exponents of what is not finite
+                  const uint32_t gone = key0 + r >= len ? ~0u : 0u;
 #pragma unroll
-                      for (int k = 0; k < 8; ++k) {
-                        const uint32_t no = __vcmpeq2(o[k] & ones, ones);
-                        if (no & ~gone) *foul = 1;
-                        o[k] &= ~(no | gone);
-                      }
-                    }
+                  for (int k = 0; k < 8; ++k) {
+                    const uint32_t no = __vcmpeq2(o[k] & ones, ones);
+                    if (no & ~gone) *foul = 1;
+                    o[k] &= ~(no | gone);
                   }
-                  const uint32_t to_row = to + half_of(e) * 16384 + r * 128;
-                  sts128(to_row + (((2 * g) ^ (r & 7)) << 4), o[0], o[1], o[2], o[3]);
-                  sts128(to_row + (((2 * g + 1) ^ (r & 7)) << 4), o[4], o[5], o[6], o[7]);
                 }
               }
-            };
-            const bool odd_rows = page < 0 || key0 + 32 * wq + 31 >= base;  // drafted ones, or none
-            const float s = kv ? s2[1] : s2[0];
-            if (f16) {  // in units of the largest scale's power of two
-              const float s16 = times_pow2(s, -(kv ? ev : ek));
-              const uint32_t by = pack_half2(s16, s16);
-              auto f = [&](uint32_t h2) { return mul_half2(h2, by); };
-              if (odd_rows) convert(f, std::true_type{}); else convert(f, std::false_type{});
-            } else {
-              auto f = [&](uint32_t h2) { return bf16_of(h2, s); };
-              if (odd_rows) convert(f, std::true_type{}); else convert(f, std::false_type{});
+              const uint32_t to_row = to + half_of(e) * 8192 + r * 128;
+              sts128(to_row + (((2 * g) ^ (r & 7)) << 4), o[0], o[1], o[2], o[3]);
+              sts128(to_row + (((2 * g + 1) ^ (r & 7)) << 4), o[4], o[5], o[6], o[7]);
             }
-            fence_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              mbar_arrive(bar(W::kFull + cs));
-              mbar_arrive(bar(W::kRawEmpty + rs));
-            }
-          }
-          page = page_next, page_next = page_after, scales = scales_next;
-        } else {
-          const uint32_t pos = 2 * (seq + j) + 1, vs = pos % W::kSlots;
-          ok = __all_sync(0xffffffffu, wait_on(bar(W::kFull + vs), (pos / W::kSlots) & 1));
-          if (!ok) break;
-          const uint32_t to = sbase + W::kOffTile + vs * W::kTile;
-          // rows from the first drafted slot on
-          for (int i = special ? t : 128 * W::kHalves * 8; i < 128 * W::kHalves * 8; i += 128) {
-            const int r = (i >> 3) & 127, key = key0 + r;
-            if (key < base) continue;
-            const uint32_t a = to + (i >> 10) * 16384 + r * 128 + (i & 7) * 16;
-            if (key >= len) {
-              sts128(a, 0u, 0u, 0u, 0u);
-              continue;
-            }
-            const uint4 u = lds128(a);
-            if (foul_bf16(u.x) || foul_bf16(u.y) || foul_bf16(u.z) || foul_bf16(u.w)) {
-              *foul = 1;
-              auto finite = [](uint32_t y) { return y & ~__vcmpeq2(y & 0x7f807f80u, 0x7f807f80u); };
-              sts128(a, finite(u.x), finite(u.y), finite(u.z), finite(u.w));
-            }
+          };
+          const bool odd_rows = !there || key0 + 16 * wq + 15 >= base;  // drafted ones, or none
+          if (f16) {  // in units of the largest scale's power of two
+            const float s16 = times_pow2(s, -(now.value ? ev : ek));
+            const uint32_t by = pack_half2(s16, s16);
+            auto f = [&](uint32_t h2) { return mul_half2(h2, by); };
+            if (odd_rows) convert(f, std::true_type{}); else convert(f, std::false_type{});
+          } else {
+            auto f = [&](uint32_t h2) { return bf16_of(h2, s); };
+            if (odd_rows) convert(f, std::true_type{}); else convert(f, std::false_type{});
           }
           fence_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(bar(W::kFull + cs));
+            mbar_arrive(bar(W::kRawEmpty + rs));
+          }
+        } else {
+          const uint32_t vs = pos % W::kSlots;
+          ok = __all_sync(0xffffffffu, wait_on(bar(W::kFull + vs), (pos / W::kSlots) & 1));
+          if (!ok) break;
+          if (now.value && key0 + kHalf > base) {
+            // rows from the first drafted slot on
+            const uint32_t to = sbase + W::kOffTile + vs * W::kSlot;
+#pragma unroll 1
+            for (int i = t; i < kHalf * (D / 64) * 8; i += 128) {
+              const int r = (i >> 3) & (kHalf - 1), key = key0 + r;
+              if (key < base) continue;
+              const uint32_t a = to + (i >> 9) * 8192 + r * 128 + (i & 7) * 16;
+              if (key >= len) {
+                sts128(a, 0u, 0u, 0u, 0u);
+                continue;
+              }
+              const uint4 u = lds128(a);
+              if (foul_bf16(u.x) || foul_bf16(u.y) || foul_bf16(u.z) || foul_bf16(u.w)) {
+                *foul = 1;
+                auto finite = [](uint32_t y) { return y & ~__vcmpeq2(y & 0x7f807f80u, 0x7f807f80u); };
+                sts128(a, finite(u.x), finite(u.y), finite(u.z), finite(u.w));
+              }
+            }
+            fence_async_smem();
+          }
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(W::kClean + vs));
         }
       }
-      seq += n;
       ++unit;
     } while (w.next(p));  // (after a wait that ran out too, for the barriers' sake)
   }
@@ -1136,26 +1172,27 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
   return fn;
 }
 
-// A pool's pages as [page and head, slot, dim], in boxes of one page's 64 columns
+// A pool's pages as [page and head, slot, dim], in boxes of 64 columns and up to a half's
+// slots
 bool page_map(CUtensorMap* m, const void* pool, const RelposPagedCache& c) {
   auto fn = encoder();
   if (!fn) return false;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(c.d), static_cast<cuuint64_t>(c.page),
                               static_cast<cuuint64_t>(c.num_pages) * c.H};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(c.d) * 2, static_cast<cuuint64_t>(c.d) * 2 * c.page};
-  const cuuint32_t box[3] = {64u, static_cast<cuuint32_t>(c.page), 1u};
+  const cuuint32_t box[3] = {64u, static_cast<cuuint32_t>(std::min(c.page, kHalf)), 1u};
   const cuuint32_t step[3] = {1u, 1u, 1u};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(pool), dims, strides, box, step,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, bool FP8, int REP>
+template <int D, bool FP8, int COPIES>
 int launch_wide(const RelposPagedCache& cache, const PagedTreeParams& p, int blocks, void (**combine)(PagedTreeParams),
                 cudaStream_t stream) {
-  using W = Wide<D, FP8, REP>;
+  using W = Wide<D, FP8, COPIES>;
   static_assert(W::kSmem <= 232448, "shared memory of a block");
-  if (cudaFuncSetAttribute(relpos_paged_wide_kernel<D, FP8, REP>, cudaFuncAttributeMaxDynamicSharedMemorySize, W::kSmem) !=
+  if (cudaFuncSetAttribute(relpos_paged_wide_kernel<D, FP8, COPIES>, cudaFuncAttributeMaxDynamicSharedMemorySize, W::kSmem) !=
       cudaSuccess)
     return RELPOS_ERR_CUDA;
   CUtensorMap k, v;
@@ -1173,13 +1210,12 @@ int launch_wide(const RelposPagedCache& cache, const PagedTreeParams& p, int blo
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, relpos_paged_wide_kernel<D, FP8, REP>, p, k, v) == cudaSuccess ? RELPOS_OK : RELPOS_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, relpos_paged_wide_kernel<D, FP8, COPIES>, p, k, v) == cudaSuccess ? RELPOS_OK : RELPOS_ERR_CUDA;
 }
 
 template <int D, bool FP8>
 int launch_wide(const RelposPagedCache& cache, const PagedTreeParams& p, int blocks, void (**combine)(PagedTreeParams),
                 cudaStream_t stream) {
-  if (p.rows > 128) return launch_wide<D, FP8, 0>(cache, p, blocks, combine, stream);
   if (p.rows > 64) return launch_wide<D, FP8, 1>(cache, p, blocks, combine, stream);
   if (p.rows > 32) return launch_wide<D, FP8, 2>(cache, p, blocks, combine, stream);
   return launch_wide<D, FP8, 4>(cache, p, blocks, combine, stream);
