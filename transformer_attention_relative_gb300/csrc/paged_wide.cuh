@@ -14,14 +14,13 @@
 //     times in the 128 of a product, each copy with a half or quarter of the keys: as
 //     many products, but a thread has a half or quarter of the exponentials, and the
 //     chain from scores to weights, which few rows cannot hide, is as much shorter.
-// A warpgroup goes through its tiles by halves of 64 keys, with a buffer of scores for
-// either half: the scores of the next half are there when a half's weights are done.
-// Keys and values come by halves too, in the order in which the products need them.
+// Keys and values of the tiles come in the order in which the products need them. While
+// a warpgroup turns its scores into weights, the other's products run.
 // What the warpgroups and copies hold apart (maximum, sum, O) is joined at the unit's
 // end. Blocks take equal shares of all units' tiles, as in paged_decode.cuh, one block
 // an SM.
 //
-//   warp 0        producer: halves of keys and values from their pages into a ring of
+//   warp 0        producer: tiles of keys and values from their pages into a ring of
 //                 shared memory (bf16: tensor copies, swizzled; e4m3: bulk copies).
 //   warps 1, 3    issuers of the products, one for each softmax warpgroup.
 //   warps 4-11    the softmax warpgroups; thread t holds row t of a product.
@@ -64,32 +63,31 @@ namespace relpos {
 namespace {
 
 constexpr int kWideThreads = 512;
-// S (then P) of warpgroup x and half y of a tile at 128 x + 64 y, O at 256 + x D
-constexpr uint32_t kTmemCols = 512, kColS = 0, kColO = 256;
-constexpr int kHalf = 64;  // keys of a half
+constexpr uint32_t kTmemCols = 512, kColS = 0, kColO = 256;  // S (then P) of warpgroup x at 128 x, O at 256 + x D
+constexpr int kGroups = 4;  // 32-key groups of a tile, each of one page
 constexpr float kRescale = 8.f;  // the running maximum moves when a row's grows by this (log2)
 constexpr float kF16Shift = 5.f;  // fp16 weights are 2^5 times those of bf16: up to 2^13 (2^14 with a scale's rest)
 constexpr uint32_t kNoPage = 0xffffffffu;  // in place of a scale
 constexpr int kF16Window = 15;    // exponents of page scales below the largest
 
-// What the producer knows of a half's two 32-key groups, for the softmax; a ring for
-// either warpgroup's halves, longer than the producer can be ahead
-struct HalfInfo {
-  float k_rest[2], v_rest[2];  // of the scales
-  uint8_t flags[2];            // 1: the page is there; 2, 4: the rest of the keys' (values') scale is not 1
+// What the producer knows of a tile's 32-key groups, for the softmax; a ring for
+// either warpgroup's tiles, longer than the producer can be ahead
+struct TileInfo {
+  float k_rest[kGroups], v_rest[kGroups];  // of the scales
+  uint8_t flags[kGroups];  // 1: the page is there; 2, 4: the rest of the keys' (values') scale is not 1
 };
-constexpr int kInfos = 32;
+constexpr int kInfos = 16;
 
 template <int D, bool FP8, int COPIES>
 struct Wide {
   static constexpr int kLanes = 128 / COPIES;                         // rows of a copy
-  static constexpr int kCols = kHalf / COPIES;                        // and keys of a half in it
+  static constexpr int kCols = kWideTile / COPIES;                    // and keys of a tile in it
   static constexpr int kQTiles = COPIES == 1 ? 2 : 1;
   static constexpr uint32_t kQTile = 128 * D * 2;
-  static constexpr uint32_t kSlot = kHalf * D * 2;                    // a half's keys or values, 16 bits
-  static constexpr uint32_t kRaw = kHalf * D;                         // and as codes
-  static constexpr int kSlots = D == 64 ? (FP8 ? 12 : 16) : FP8 ? (COPIES == 1 ? 6 : 8) : COPIES == 1 ? 8 : 10;
-  static constexpr int kRawSlots = !FP8 ? 0 : D == 64 ? 12 : COPIES == 1 ? 6 : 4;
+  static constexpr uint32_t kSlot = kWideTile * D * 2;                // a tile's keys or values, 16 bits
+  static constexpr uint32_t kRaw = kWideTile * D;                     // and as codes
+  static constexpr int kSlots = D == 64 ? (FP8 ? 6 : 8) : FP8 ? (COPIES == 1 ? 3 : 4) : COPIES == 1 ? 4 : 5;
+  static constexpr int kRawSlots = !FP8 ? 0 : D == 64 ? 6 : COPIES == 1 ? 3 : 2;
   static constexpr uint32_t kOffQ = 0;
   static constexpr uint32_t kOffTile = kOffQ + kQTiles * kQTile;
   static constexpr uint32_t kOffRaw = kOffTile + kSlots * kSlot;
@@ -100,9 +98,9 @@ struct Wide {
   static constexpr uint32_t kOffMl = kOffDeep + kMaxNodes * 4;        // [2][128] maximum and sum
   static constexpr uint32_t kOffQx = kOffMl + 2 * 128 * 8;            // [2][256] exponents of query rows
   static constexpr uint32_t kOffInfo = kOffQx + 2 * 256 * 4;          // [2] UnitInfo
-  static constexpr uint32_t kOffHalves = kOffInfo + 64;               // [2][kInfos] HalfInfo
-  static constexpr uint32_t kOffScales = kOffHalves + 2 * kInfos * 24;  // [kRawSlots][2] scales, NaN bits kNone: no page
-  static constexpr uint32_t kOffBar = kOffScales + kRawSlots * 8;
+  static constexpr uint32_t kOffTiles = kOffInfo + 64;                // [2][kInfos] TileInfo
+  static constexpr uint32_t kOffScales = kOffTiles + 2 * kInfos * sizeof(TileInfo);  // [kRawSlots][kGroups], kNoPage: none
+  static constexpr uint32_t kOffBar = (kOffScales + kRawSlots * kGroups * 4 + 7) / 8 * 8;
   // barriers
   static constexpr uint32_t kFull = 0;                                // slots: written
   static constexpr uint32_t kEmpty = kFull + kSlots;                  // and read
@@ -110,10 +108,10 @@ struct Wide {
   static constexpr uint32_t kRawEmpty = kRawFull + kRawSlots;
   static constexpr uint32_t kQFull = kRawEmpty + kRawSlots;
   static constexpr uint32_t kQEmpty = kQFull + 1;
-  static constexpr uint32_t kSFull = kQEmpty + 1;                     // + 2 warpgroup + parity of the half
-  static constexpr uint32_t kPFull = kSFull + 4;
-  static constexpr uint32_t kODone = kPFull + 4;
-  static constexpr uint32_t kOFree = kODone + 4;                      // + warpgroup
+  static constexpr uint32_t kSFull = kQEmpty + 1;                     // + warpgroup
+  static constexpr uint32_t kPFull = kSFull + 2;
+  static constexpr uint32_t kODone = kPFull + 2;
+  static constexpr uint32_t kOFree = kODone + 2;
   static constexpr uint32_t kClean = kOFree + 2;                      // bf16: slots looked through
   static constexpr uint32_t kFinal = kClean + (FP8 ? 0 : kSlots);
   static constexpr uint32_t kBars = kFinal + 2;
@@ -175,7 +173,7 @@ struct Walk {
   int base, live;    // first drafted slot, nodes
   int row0, rows;    // first row of the unit in its key/value head, rows that have a node
   bool pair;         // both warpgroups take every tile, with half the rows each
-  int h0, h1;        // halves of the first and the second warpgroup (a pair: of both, and 0)
+  int h0, h1;        // tiles of the first and the second warpgroup (a pair: of both, and 0)
   RP_DEVI void load(const PagedTreeParams& p) {
     xe = min(tiles, x + c.nt - c.t);
     live = row_count(p, c.b);
@@ -184,8 +182,8 @@ struct Walk {
     rows = max(0, min(p.rows, live * p.G - row0));
     pair = COPIES == 1 && rows > 128;
     const int n = rows > 0 ? xe - x : 0;
-    h0 = pair ? 2 * n : 2 * ((n + 1) >> 1);
-    h1 = pair ? 0 : 2 * (n >> 1);
+    h0 = pair ? n : (n + 1) >> 1;
+    h1 = pair ? 0 : n >> 1;
   }
   RP_DEVI bool next(const PagedTreeParams& p) {
     c.template forward<kWideTile>(p, xe - x);
@@ -194,30 +192,30 @@ struct Walk {
     load(p);
     return true;
   }
-  // First key of a warpgroup's h-th half, from the last one of the block's tiles on: a
+  // First key of a warpgroup's h-th tile, from the last one of the block's tiles on: a
   // decaying bias (ALiBi) then has its largest logits first, and no maximum moves
   // after those.
-  RP_DEVI int place_of(int of, int h) const { return pair ? h : 2 * (of + (h & ~1)) + (h & 1); }  // from the last one on
+  RP_DEVI int place_of(int of, int h) const { return pair ? h : of + 2 * h; }  // from the last one on
   RP_DEVI int end_tiles() const { return (c.t + xe - x) * kWideTile; }
-  RP_DEVI int key_of(int of, int h) const { return end_tiles() - kHalf * (place_of(of, h) + 1); }
+  RP_DEVI int key_of(int of, int h) const { return end_tiles() - kWideTile * (place_of(of, h) + 1); }
   RP_DEVI int first_key() const { return c.t * kWideTile; }
   RP_DEVI int end_key() const { return min((c.t + xe - x) * kWideTile, c.len); }
 };
 
-// The order in which a unit's halves of keys and values pass through shared memory:
-// the keys of either warpgroup's first two halves, then for i = 0, 1, .. the values
-// of half i and the keys of half i + 2 of the one and of the other.
+// The order in which a unit's tiles of keys and values pass through shared memory:
+// the keys of either warpgroup's first tile, then for i = 0, 1, .. the values of tile
+// i and the keys of tile i + 1 of the one and of the other.
 struct Items {
   int h0, h1, i, x;
   bool value;
-  RP_DEVI Items(int a, int b) : h0(a), h1(b), i(-2), x(0), value(false) {}
+  RP_DEVI Items(int a, int b) : h0(a), h1(b), i(-1), x(0), value(false) {}
   RP_DEVI bool valid() const { return h0 > 0 && i < h0; }
-  RP_DEVI int half() const { return value ? i : i + 2; }
+  RP_DEVI int tile() const { return value ? i : i + 1; }
   RP_DEVI void next() {
     do {
       value = !value;
       if (value && (x ^= 1) == 0) ++i;
-    } while (i < h0 && (half() < 0 || half() >= (x ? h1 : h0)));
+    } while (i < h0 && (tile() < 0 || tile() >= (x ? h1 : h0)));
   }
 };
 
@@ -338,7 +336,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   auto bar = [&](uint32_t i) { return sbase + W::kOffBar + 8 * i; };
   volatile int* const foul = reinterpret_cast<volatile int*>(smem + W::kOffMisc + 4);
-  HalfInfo* const half_infos = reinterpret_cast<HalfInfo*>(smem + W::kOffHalves);
+  TileInfo* const tile_infos = reinterpret_cast<TileInfo*>(smem + W::kOffTiles);
   UnitInfo* const infos = reinterpret_cast<UnitInfo*>(smem + W::kOffInfo);
   int* const q_exp = reinterpret_cast<int*>(smem + W::kOffQx);
 
@@ -376,22 +374,22 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     const bool some = w.tiles > 0;
     if (warp == 0 && some) {
       // ------------------------------------------------------------ producer
-      uint32_t pos = 0, seq0 = 0, seq1 = 0;  // of the ring; either warpgroup's halves before
-      const int per_page = min(kHalf, 1 << p.log_page), boxes = kHalf / per_page;  // keys of a copy, copies
+      uint32_t pos = 0, seq0 = 0, seq1 = 0;  // of the ring; either warpgroup's tiles before
+      const int per_page = 1 << p.log_page, boxes = KT >> p.log_page;  // keys of a copy, copies
       constexpr int kRing = FP8 ? W::kRawSlots : W::kSlots;
       constexpr uint32_t kSlotBytes = FP8 ? W::kRaw : W::kSlot;
       const uint32_t full0 = FP8 ? W::kRawFull : W::kFull, empty0 = FP8 ? W::kRawEmpty : W::kEmpty;
       const uint32_t ring = sbase + (FP8 ? W::kOffRaw : W::kOffTile);
       const uint32_t none = static_cast<uint32_t>(p.num_pages) * p.Hkv;  // beyond the pool: zeros
       do {
-        // Pages (and scales) of 16 halves at a time, a 32-key group a lane: a lookup each
-        // would put its latency into every copy. Items go back to the last 16 but one.
+        // Pages (and scales) of 8 tiles at a time, a 32-key group a lane: a lookup each
+        // would put its latency into every copy. Items go back to the last 8 but one.
         int page_now = -1, page_last = -1, batch = -1;
         [[maybe_unused]] float2 scale_now = make_float2(0.f, 0.f), scale_last = scale_now;
         auto look = [&](int to) {
           page_last = page_now, scale_last = scale_now;
           batch = to;
-          const int key = w.end_tiles() - kHalf * (16 * to + (lane >> 1) + 1) + 32 * (lane & 1);
+          const int key = w.end_tiles() - KT * (8 * to + (lane >> 2) + 1) + 32 * (lane & 3);
           const int page = key >= w.first_key() && key < w.c.len ? __ldg(w.c.pages + (key >> p.log_page)) : -2;
           if (page != -2 && (page < 0 || page >= p.num_pages)) atomicCAS(p.status, 0, RELPOS_ERR_PAGE);
           page_now = page >= 0 && page < p.num_pages ? page : -1;
@@ -402,11 +400,11 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         };
 #pragma unroll 1
         for (Items it(w.h0, w.h1); ok && it.valid(); it.next(), ++pos) {
-          const int g = w.place_of(it.x, it.half());
-          if (g >> 4 > batch) look(g >> 4);
-          // lanes 0 and 1: the half's groups
-          const int from = 2 * (g & 15) + (lane & 1);
-          const bool recent = g >> 4 == batch;
+          const int g = w.place_of(it.x, it.tile());
+          if (g >> 3 > batch) look(g >> 3);
+          // lanes 0 .. 3: the tile's groups; lanes 4 .. 7: the groups where pages start
+          const int from = 4 * (g & 7) + (lane < 4 ? lane : ((lane & 3) << p.log_page >> 5) & 3);
+          const bool recent = g >> 3 == batch;
           const int page = __shfl_sync(0xffffffffu, recent ? page_now : page_last, from);
           const bool there = page >= 0;
           if constexpr (FP8) {
@@ -415,15 +413,15 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             const uint32_t slot = pos % kRing;
             if (pos >= kRing) ok = wait_warp(bar(empty0 + slot), (pos / kRing - 1) & 1);
             if (!ok) break;
-            if (lane < 2) {
-              float* const of_slot = reinterpret_cast<float*>(smem + W::kOffScales) + 2 * slot;
+            if (lane < kGroups) {
+              float* const of_slot = reinterpret_cast<float*>(smem + W::kOffScales) + kGroups * slot;
               float k2, v2, kr, vr;
               split_scale(sk, k2, kr);
               split_scale(sv, v2, vr);
               const float of_kind = it.value ? v2 : k2;
               of_slot[lane] = !there ? __uint_as_float(kNoPage) : of_kind == of_kind ? of_kind : NAN;
               if (!it.value) {
-                HalfInfo& info = half_infos[it.x * kInfos + ((it.x ? seq1 : seq0) + it.half()) % kInfos];
+                TileInfo& info = tile_infos[it.x * kInfos + ((it.x ? seq1 : seq0) + it.tile()) % kInfos];
                 info.k_rest[lane] = kr, info.v_rest[lane] = vr;
                 info.flags[lane] = there ? 1 | (kr != 1.f) << 1 | (vr != 1.f) << 2 : 0;
               }
@@ -432,26 +430,25 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             const uint32_t slot = pos % kRing;
             if (pos >= kRing) ok = wait_warp(bar(empty0 + slot), (pos / kRing - 1) & 1);
             if (!ok) break;
-            if (lane < 2 && !it.value)
-              half_infos[it.x * kInfos + ((it.x ? seq1 : seq0) + it.half()) % kInfos].flags[lane] = there;
+            if (lane < kGroups && !it.value)
+              tile_infos[it.x * kInfos + ((it.x ? seq1 : seq0) + it.tile()) % kInfos].flags[lane] = there;
           }
           const uint32_t slot = pos % kRing, dst = ring + slot * kSlotBytes;
-          const bool copies = lane < boxes;
+          const int copy = lane - kGroups;  // a page's, by lanes 4 ..
+          const bool copies = copy >= 0 && copy < boxes;
           const uint32_t n = __popc(__ballot_sync(0xffffffffu, copies && there));
           if (lane == 0) mbar_arrive_expect_tx(bar(full0 + slot), FP8 ? n * per_page * D : W::kSlot);
           __syncwarp();
           if (copies) {
-            const int in_page = (w.end_tiles() - kHalf * (g + 1) + lane * per_page) & ((1 << p.log_page) - 1);
             const uint32_t ph = there ? static_cast<uint32_t>(page) * p.Hkv + w.c.h : none;
             if constexpr (FP8) {
               if (there)
-                bulk_load(dst + lane * per_page * D,
-                          (it.value ? p.v : p.k) + ((static_cast<size_t>(ph) << p.log_page) + in_page) * D, per_page * D,
-                          bar(full0 + slot));
+                bulk_load(dst + copy * per_page * D, (it.value ? p.v : p.k) + (static_cast<size_t>(ph) << p.log_page) * D,
+                          per_page * D, bar(full0 + slot));
             } else {
               for (int hf = 0; hf < D / 64; ++hf)
-                tma_load_3d(dst + hf * 8192 + lane * per_page * 128, it.value ? &tm_v : &tm_k, bar(full0 + slot), 64 * hf,
-                            in_page, static_cast<int>(ph));
+                tma_load_3d(dst + hf * 16384 + copy * per_page * 128, it.value ? &tm_v : &tm_k, bar(full0 + slot), 64 * hf, 0,
+                            static_cast<int>(ph));
             }
           }
           __syncwarp();
@@ -469,63 +466,64 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       const uint32_t leader = elect_one();
       const uint32_t x = warp == 1 ? 0u : 1u;
       const uint32_t s_col = tmem + kColS + 128 * x, o_col = tmem + kColO + D * x;
-      uint32_t pos = 0, mine = 0, unit = 0;  // of the ring, own halves before, units
+      uint32_t pos = 0, mine = 0, unit = 0;  // of the ring, own tiles before, units
       do {
         ok = wait_warp(bar(W::kQFull), unit & 1);
         const bool f16 = FP8 && infos[unit & 1].f16;
         // the operands' type: bf16 (1) or fp16 (0)
         constexpr uint32_t kTypes = (1u << 7) | (1u << 10);
         const uint32_t types = f16 ? 0u : kTypes;
-        const uint32_t idesc_s = (idesc_bf16_f32(128, kHalf, 0, 0) & ~kTypes) | types;
+        const uint32_t idesc_s = (idesc_bf16_f32(128, KT, 0, 0) & ~kTypes) | types;
         const uint32_t idesc_o = (idesc_bf16_f32(128, D, 0, 1) & ~kTypes) | types;
         const uint64_t dq = smem_desc_sw128(sbase + W::kOffQ + (w.pair ? x * W::kQTile : 0u), 16, 1024);
-        const int halves = w.pair || x == 0 ? w.h0 : w.h1;
+        const int own = w.pair || x == 0 ? w.h0 : w.h1;
         const bool twice = kReaders == 2 && !w.pair;
-        // half i's scores two halves ahead of its weights' product
+        // weights' product of tile i, then scores of tile i + 1
 #pragma unroll 1
-        for (int i = -2; ok && i < w.h0; ++i) {
+        for (int i = -1; ok && i < w.h0; ++i) {
           // positions as in Items
-          const int before = (i >= 0) + (i + 2 < w.h0), behind = (i >= 0 && i < w.h1) + (i + 2 < w.h1);
-          const uint32_t vp = pos + (w.pair || x == 0 ? 0 : before), kp = vp + (i >= 0 && i < halves);
+          const int before = (i >= 0) + (i + 1 < w.h0), behind = (i >= 0 && i < w.h1) + (i + 1 < w.h1);
+          const uint32_t vp = pos + (w.pair || x == 0 ? 0 : before), kp = vp + (i >= 0 && i < own);
           pos += before + behind;
-          if (i >= 0 && i < halves) {
-            const uint32_t vs = vp % W::kSlots, c = mine + i, y = i & 1;
-            ok = wait_warp(bar(W::kPFull + 2 * x + y), (c >> 1) & 1);
-            if (ok && i == 0 && unit > 0) ok = wait_warp(bar(W::kOFree + x), (unit - 1) & 1);
-            if (ok) ok = wait_warp(bar(W::kFull + vs), (vp / W::kSlots) & 1);
+          if (i >= 0 && i < own) {
+            const uint32_t vs = vp % W::kSlots, c = mine + i;
+            ok = wait_warp(bar(W::kFull + vs), (vp / W::kSlots) & 1);
             if (!FP8 && ok) ok = wait_warp(bar(W::kClean + vs), (vp / W::kSlots) & 1);
+            if (ok && i == 0 && unit > 0) ok = wait_warp(bar(W::kOFree + x), (unit - 1) & 1);
+            if (ok) ok = wait_warp(bar(W::kPFull + x), c & 1);
             if (!ok) break;
             tc_fence_after();
-            const uint64_t dv = smem_desc_sw128(sbase + W::kOffTile + vs * W::kSlot, 8192, 1024);
-            const uint32_t p_col = s_col + kHalf * y;
+            const uint64_t dv = smem_desc_sw128(sbase + W::kOffTile + vs * W::kSlot, 16384, 1024);
             // (bf16: the second parts of the weights behind the first)
 #pragma unroll 1
-            for (int kk = 0; kk < (f16 ? 1 : 2) * kHalf / 16; ++kk)
-              umma_ts_if(leader, o_col, p_col + 8 * kk, dv + 128 * (kk & (kHalf / 16 - 1)), idesc_o, i > 0 || kk > 0);
-            commit_if(leader, bar(W::kODone + 2 * x + y));
+            for (int kk = 0; kk < (f16 ? 1 : 2) * KT / 16; ++kk)
+              umma_ts_if(leader, o_col, s_col + 64 * (kk >> 2 & 1) + 32 * (kk >> 3) + 8 * (kk & 3), dv + 128 * (kk & 7), idesc_o,
+                         i > 0 || kk > 0);
+            commit_if(leader, bar(W::kODone + x));
             commit_if(leader, bar(W::kEmpty + vs));
             if (twice) commit_if(leader, bar(W::kEmpty + vs));
           }
-          const int a = i + 2;
-          if (a >= halves) continue;
-          const uint32_t ks = kp % W::kSlots, c = mine + a, y = a & 1;
+          const int a = i + 1;
+          if (a >= own) continue;
+          const uint32_t ks = kp % W::kSlots, c = mine + a;
           ok = wait_warp(bar(W::kFull + ks), (kp / W::kSlots) & 1);
-          // the weights of the last half but one lie in its columns
-          if (ok && c >= 2) ok = wait_warp(bar(W::kODone + 2 * x + y), ((c - 2) >> 1) & 1);
+          // the weights of the tile before lie in its columns
+          if (ok && c > 0) ok = wait_warp(bar(W::kODone + x), (c - 1) & 1);
           if (!ok) break;
           tc_fence_after();
           const uint64_t dk = smem_desc_sw128(sbase + W::kOffTile + ks * W::kSlot, 16, 1024);
 #pragma unroll 1
-          for (int kk = 0; kk < D / 16; ++kk)
-            umma_ss_if(leader, s_col + kHalf * y, dq + (kk >> 2) * 1024 + 2 * (kk & 3), dk + (kk >> 2) * 512 + 2 * (kk & 3),
-                       idesc_s, kk > 0);
-          commit_if(leader, bar(W::kSFull + 2 * x + y));
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint64_t off = (kk >> 2) * 1024 + 2 * (kk & 3);
+            umma_ss_if(leader, s_col, dq + off, dk + off, idesc_s, kk > 0);
+          }
+          commit_if(leader, bar(W::kSFull + x));
           commit_if(leader, bar(W::kEmpty + ks));
           if (twice) commit_if(leader, bar(W::kEmpty + ks));
-          if (a == halves - 1) commit_if(leader, bar(W::kQEmpty));
+          if (a == own - 1) commit_if(leader, bar(W::kQEmpty));
         }
-        if (halves == 0) commit_if(leader, bar(W::kQEmpty));  // no half of the unit
-        mine += halves;
+        if (own == 0) commit_if(leader, bar(W::kQEmpty));  // no tile of the unit
+        mine += own;
         ++unit;
       } while (ok && w.next(p));
       commit_if(leader, bar(W::kFinal + x));
@@ -541,21 +539,21 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     const bool some = w.tiles > 0;
     // -------------------------------------------------------------- softmax
     const int x = (warp - 4) >> 2, t = threadIdx.x & 127;
-    constexpr int NC = W::kCols;                     // columns of a thread, of a half's
+    constexpr int NC = W::kCols;                     // columns of a thread, of a tile's
     const int copy = t / W::kLanes, col0 = copy * NC;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t tS0 = tmem + lanes + kColS + 128 * x, tO = tmem + lanes + kColO;
+    const uint32_t tS = tmem + lanes + kColS + 128 * x, tO = tmem + lanes + kColO;
     float* const lut = reinterpret_cast<float*>(smem + W::kOffLut);
     unsigned long long* const line = reinterpret_cast<unsigned long long*>(smem + W::kOffLine);
     int* const deep = reinterpret_cast<int*>(smem + W::kOffDeep);
     float2* const ml = reinterpret_cast<float2*>(smem + W::kOffMl);
     const int lut_len = p.t5_R + 1;
-    uint32_t mine = 0, unit = 0, seq0 = 0, seq1 = 0;  // own halves, units, either warpgroup's halves before
+    uint32_t mine = 0, unit = 0, seq0 = 0, seq1 = 0;  // own tiles, units, either warpgroup's tiles before
     int tree_of = -1, lut_of = -1;
     if (some) do {
       const int n = w.xe - w.x, len = w.c.len, base = w.base, live = w.live, h = w.c.h, row0 = w.row0;
       const bool pair = w.pair;
-      const int own = pair || x == 0 ? w.h0 : w.h1;  // halves
+      const int own = pair || x == 0 ? w.h0 : w.h1;  // tiles
       // the tree, and the biases of the distances below the last bucket's
       if (tree_of != w.c.b && warp == 4) {
         tree_lines(p, w.c.b, live, lane, line);
@@ -597,20 +595,20 @@ __global__ void __launch_bounds__(kWideThreads, 1)
 #pragma unroll 1
       for (int i = 0; ok && i < own; ++i, ++mine) {
         {
-          const int y = i & 1, key0 = w.key_of(x, i);
-          // bits of the two groups: page there, rest of the keys' scale, of the values'
-          unsigned there = 3u, k_rests = 0u, v_rests = 0u;
-          const HalfInfo& info = half_infos[pair || x == 0 ? (seq0 + i) % kInfos : kInfos + (seq1 + i) % kInfos];
-          ok = __all_sync(0xffffffffu, wait_on(bar(W::kSFull + 2 * x + y), (mine >> 1) & 1));
+          const int key0 = w.key_of(x, i);
+          // bits of the groups: page there, rest of the keys' scale, of the values'
+          unsigned there = 0xfu, k_rests = 0u, v_rests = 0u;
+          const TileInfo& info = tile_infos[pair || x == 0 ? (seq0 + i) % kInfos : kInfos + (seq1 + i) % kInfos];
+          ok = __all_sync(0xffffffffu, wait_on(bar(W::kSFull + x), mine & 1));
           if (!ok) break;
           tc_fence_after();
-          {
-            const uint32_t f = *reinterpret_cast<const uint16_t*>(info.flags);
-            if (f != 0x0101u) {
-              there = (f & 1u) | (f >> 7 & 2u);
-              k_rests = (f >> 1 & 1u) | (f >> 8 & 2u);
-              v_rests = (f >> 2 & 1u) | (f >> 9 & 2u);
-            }
+          const uint32_t flags = *reinterpret_cast<const uint32_t*>(info.flags);
+          if (flags != 0x01010101u) {
+            auto bits = [&](int of) {
+              const uint32_t f = flags >> of & 0x01010101u;
+              return (f | f >> 7 | f >> 14 | f >> 21) & 0xfu;
+            };
+            there = bits(0), k_rests = bits(1), v_rests = bits(2);
           }
           if (i == 0) {
             if constexpr (FP8) {
@@ -626,9 +624,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             plain = __all_sync(0xffffffffu, !active || (scale > 0.f && fabsf(slope_raw) <= 0x1p60f));
           }
           if (any) {
-            const uint32_t tS = tS0 + kHalf * y;
-            const bool near = p.mode == RELPOS_T5 && base - (key0 + kHalf) < p.t5_R;
-            const bool whole = key0 + kHalf > base || there != 3u || near || odd || !plain || k_rests;
+            const bool near = p.mode == RELPOS_T5 && base - (key0 + KT) < p.t5_R;
+            const bool whole = key0 + KT > base || there != 0xfu || near || odd || !plain || k_rests;
             if (whole) {  // the scores become logits
 #pragma unroll 1
               for (int q = 0; q < NC / 16; ++q) {
@@ -672,46 +669,57 @@ __global__ void __launch_bounds__(kWideThreads, 1)
               }
               tmem_st_wait();
             }
-            uint32_t sr[NC / 16][16];
-#pragma unroll
-            for (int q = 0; q < NC / 16; ++q) tmem_ld16(tS + col0 + 16 * q, sr[q]);
-#pragma unroll
-            for (int q = 0; q < NC / 16; ++q) tmem_ld16_wait(sr[q]);
+            // 64 columns at a time; where there are more, they are read again for the
+            // weights (held, they do not fit the registers)
+            constexpr int CH = NC < 64 ? NC : 64;
+            uint32_t sr[CH / 16][16];
             float* const xs = reinterpret_cast<float*>(&sr[0][0]);
             float addc = 0.f, mul = 1.f;
             if (!whole) {
               mul = scale;
               addc = far;
-              if (p.mode == RELPOS_ALIBI) {  // slope (key - position): a constant and the column's part
-                addc = slope * static_cast<float>(key0 + col0 - base - depth);
+              // slope (key - position): a constant and the column's part
+              if (p.mode == RELPOS_ALIBI) addc = slope * static_cast<float>(key0 + col0 - base - depth);
+            }
+            const float col_slope = whole ? 0.f : slope_raw;
+            auto read = [&](int from) {
 #pragma unroll
-                for (int c = 0; c < NC; c += 2) {
+              for (int q = 0; q < CH / 16; ++q) tmem_ld16(tS + col0 + from + 16 * q, sr[q]);
+#pragma unroll
+              for (int q = 0; q < CH / 16; ++q) tmem_ld16_wait(sr[q]);
+              if (p.mode == RELPOS_ALIBI) {
+#pragma unroll
+                for (int c = 0; c < CH; c += 2) {
                   const float2 a = __ffma2_rn(make_float2(static_cast<float>(c), static_cast<float>(c + 1)),
-                                              make_float2(slope_raw, slope_raw), make_float2(xs[c], xs[c + 1]));
+                                              make_float2(col_slope, col_slope), make_float2(xs[c], xs[c + 1]));
                   xs[c] = a.x;
                   xs[c + 1] = a.y;
                 }
               }
-            }
-            float m0 = -INFINITY, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
+            };
+            // (the columns before these 64 as a constant: of a chunk's maximum, and of its weights)
+            const float chunk_slope = whole ? 0.f : 64.f * slope;
+            float top = -INFINITY;
+#pragma unroll 1
+            for (int q = 0; q < NC / CH; ++q) {
+              read(CH * q);
+              float m0 = -INFINITY, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
 #pragma unroll
-            for (int c = 0; c < NC; c += 8) {
-              m0 = max3f(m0, xs[c], xs[c + 1]);
-              m1 = max3f(m1, xs[c + 2], xs[c + 3]);
-              m2 = max3f(m2, xs[c + 4], xs[c + 5]);
-              m3 = max3f(m3, xs[c + 6], xs[c + 7]);
+              for (int c = 0; c < CH; c += 8) {
+                m0 = max3f(m0, xs[c], xs[c + 1]);
+                m1 = max3f(m1, xs[c + 2], xs[c + 3]);
+                m2 = max3f(m2, xs[c + 4], xs[c + 5]);
+                m3 = max3f(m3, xs[c + 6], xs[c + 7]);
+              }
+              top = fmaxf(top, fmaf(fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)), mul, fmaf(chunk_slope, q, addc)));
             }
-            const float top = fmaf(fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)), mul, addc);
             const float m_new = fmaxf(m_run, top);
             const bool moves = m_new > m_run + kRescale;
             const bool any_moves = __any_sync(0xffffffffu, moves);
             if (any_moves) {
               const float alpha = moves ? ex2_approx(m_run - m_new) : 1.f;
               if (moves) m_run = m_new;
-              if (i > 0) {  // O so far: its last product has to be done; the next waits for these weights
-                ok = __all_sync(0xffffffffu, wait_on(bar(W::kODone + 2 * x + 1 - y), ((mine - 1) >> 1) & 1));
-                if (!ok) break;
-                tc_fence_after();
+              if (i > 0) {  // O so far: its last product is done (the scores came behind it), the next waits for P
                 l_run *= alpha;
 #pragma unroll 1
                 for (int q = 0; q < D / 16; ++q) {
@@ -726,44 +734,54 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             }
             float off = addc - (m_run == -INFINITY ? 0.f : m_run);
             if (FP8 && f16) off += kF16Shift;
-            // weights: P's columns are pairs of keys; other copies' keys are zeros
-            const float2 mul2 = make_float2(mul, mul), off2 = make_float2(off, off);
+            // weights: P's columns are pairs of keys; other copies' keys are zeros. The weights
+            // of 64 keys lie in their scores' columns, the second parts behind the first.
+            auto place = [&](int col) { return tS + (col & 64) + (col & 63) / 2; };
+            const float2 mul2 = make_float2(mul, mul);
             float2 sum0 = make_float2(0.f, 0.f), sum1 = make_float2(0.f, 0.f);
             auto weights = [&](auto half_type, auto with_rests) {
               constexpr bool F16 = decltype(half_type)::value, kRests = decltype(with_rests)::value;
+#pragma unroll 1
+              for (int ch = 0; ch < NC / CH; ++ch) {
+                // the last chunk read is still there: it goes first
+                const int from = CH * (NC / CH - 1 - ch);
+                if (ch > 0) read(from);
+                const float off_ch = fmaf(chunk_slope, static_cast<float>(from / 64), off);
+                const float2 off2 = make_float2(off_ch, off_ch);
 #pragma unroll
-              for (int q = 0; q < NC / 16; ++q) {
-                uint32_t hi[8];
-                [[maybe_unused]] uint32_t lo[8];
+                for (int q = 0; q < CH / 16; ++q) {
+                  uint32_t hi[8];
+                  [[maybe_unused]] uint32_t lo[8];
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                  const float2 z = __ffma2_rn(make_float2(xs[16 * q + 2 * c], xs[16 * q + 2 * c + 1]), mul2, off2);
-                  float a = ex2_approx(z.x), b = ex2_approx(z.y);
-                  if (c & 1)
-                    sum1 = __fadd2_rn(sum1, make_float2(a, b));
-                  else
-                    sum0 = __fadd2_rn(sum0, make_float2(a, b));
-                  if constexpr (kRests) {
-                    const float v_rest = info.v_rest[(col0 + 16 * q) >> 5];
-                    a *= v_rest, b *= v_rest;
+                  for (int c = 0; c < 8; ++c) {
+                    const float2 z = __ffma2_rn(make_float2(xs[16 * q + 2 * c], xs[16 * q + 2 * c + 1]), mul2, off2);
+                    float a = ex2_approx(z.x), b = ex2_approx(z.y);
+                    if (c & 1)
+                      sum1 = __fadd2_rn(sum1, make_float2(a, b));
+                    else
+                      sum0 = __fadd2_rn(sum0, make_float2(a, b));
+                    if constexpr (kRests) {
+                      const float v_rest = info.v_rest[(col0 + from + 16 * q) >> 5];
+                      a *= v_rest, b *= v_rest;
+                    }
+                    if constexpr (F16) {
+                      hi[c] = pack_half2(a, b);
+                    } else {
+                      hi[c] = pack_bf16x2(a, b);
+                      lo[c] = pack_bf16x2(a - __uint_as_float(hi[c] << 16), b - __uint_as_float(hi[c] & 0xffff0000u));
+                    }
                   }
-                  if constexpr (F16) {
-                    hi[c] = pack_half2(a, b);
-                  } else {
-                    hi[c] = pack_bf16x2(a, b);
-                    lo[c] = pack_bf16x2(a - __uint_as_float(hi[c] << 16), b - __uint_as_float(hi[c] & 0xffff0000u));
-                  }
+                  tmem_st8(place(col0 + from + 16 * q), hi);
+                  if constexpr (!F16) tmem_st8(place(col0 + from + 16 * q) + 32, lo);
                 }
-                tmem_st8(tS + col0 / 2 + 8 * q, hi);
-                if constexpr (!F16) tmem_st8(tS + 32 + col0 / 2 + 8 * q, lo);
               }
               if constexpr (COPIES > 1) {
                 const uint32_t zero[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
+                for (int q = 0; q < 8; ++q) {
                   if (16 * q / NC == copy) continue;
-                  tmem_st8(tS + 8 * q, zero);
-                  if constexpr (!F16) tmem_st8(tS + 32 + 8 * q, zero);
+                  tmem_st8(place(16 * q), zero);
+                  if constexpr (!F16) tmem_st8(place(16 * q) + 32, zero);
                 }
               }
             };
@@ -781,13 +799,13 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             tmem_st_wait();
           }
           tc_fence_before();
-          mbar_arrive(bar(W::kPFull + 2 * x + y));
+          mbar_arrive(bar(W::kPFull + x));
         }
       }
       seq0 += w.h0, seq1 += w.h1;
       // ---- the unit's parts joined. After a wait that ran out a warp goes on without
       // waiting, so that all meet at the barriers.
-      if (ok && own > 0) ok = __all_sync(0xffffffffu, wait_on(bar(W::kODone + 2 * x + 1), ((mine - 1) >> 1) & 1));
+      if (ok && own > 0) ok = __all_sync(0xffffffffu, wait_on(bar(W::kODone + x), (mine - 1) & 1));
       if (f16 && m_run != -INFINITY) m_run -= kF16Shift;  // what O and the sum are relative to
       ml[128 * x + t] = make_float2(m_run, l_run);
       // the exponent of O goes with the other warpgroup's too
@@ -1057,15 +1075,15 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       mbar_arrive(bar(W::kQFull));
 #pragma unroll 1
       for (Items now(w.h0, w.h1); ok && now.valid(); now.next(), ++pos) {
-        const int key0 = w.key_of(now.x, now.half());
+        const int key0 = w.key_of(now.x, now.tile());
         if constexpr (FP8) {
           const uint32_t rs = pos % W::kRawSlots, cs = pos % W::kSlots;
           ok = wait_on(bar(W::kRawFull + rs), (pos / W::kRawSlots) & 1);
           if (pos >= W::kSlots) ok = ok && wait_on(bar(W::kEmpty + cs), (pos / W::kSlots - 1) & 1);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
-          // of this warp's 16 keys, which are one page's
-          const float given = reinterpret_cast<const float*>(smem + W::kOffScales)[2 * rs + (wq >> 1)];
+          // of this warp's 32 keys, which are one page's
+          const float given = reinterpret_cast<const float*>(smem + W::kOffScales)[kGroups * rs + wq];
           const bool there = __float_as_uint(given) != kNoPage;
           const float s = there ? given : 0.f;
           const uint32_t raw = sbase + W::kOffRaw + rs * W::kRaw, to = sbase + W::kOffTile + cs * W::kSlot;
@@ -1073,40 +1091,42 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           // half, so that reads and writes meet all banks)
           auto convert = [&](auto code_pairs, auto special_rows) {
             constexpr bool kSpecial = decltype(special_rows)::value;
-            constexpr int kSteps = D / 32;
-            const int g = lane & 3, r0 = 16 * wq + (lane >> 2), odd = D == 64 ? 0 : r0 & 1;
-            auto row_of = [&](int e) { return r0 + 8 * (D == 64 ? e : e / 2); };
-            auto half_of = [&](int e) { return D == 64 ? 0 : (e & 1) ^ odd; };
-            uint4 u[kSteps];
+            const int g = lane & 3, odd = D == 64 ? 0 : lane >> 2 & 1;
+#pragma unroll 1
+            for (int r0 = 32 * wq + (lane >> 2); r0 < 32 * wq + 32; r0 += 4 * 512 / D) {
+              auto row_of = [&](int e) { return r0 + 8 * (D == 64 ? e : e / 2); };
+              auto half_of = [&](int e) { return D == 64 ? 0 : (e & 1) ^ odd; };
+              uint4 u[4];
 #pragma unroll
-            for (int e = 0; e < kSteps; ++e) u[e] = lds128(raw + row_of(e) * D + half_of(e) * 64 + g * 16);
+              for (int e = 0; e < 4; ++e) u[e] = lds128(raw + row_of(e) * D + half_of(e) * 64 + g * 16);
 #pragma unroll
-            for (int e = 0; e < kSteps; ++e) {
-              const int r = row_of(e);
-              if constexpr (kSpecial)
-                if (!there || key0 + r >= len) u[e] = make_uint4(0u, 0u, 0u, 0u);
-              const uint32_t c4[4] = {u[e].x, u[e].y, u[e].z, u[e].w};
-              uint32_t o[8];
+              for (int e = 0; e < 4; ++e) {
+                const int r = row_of(e);
+                if constexpr (kSpecial)
+                  if (!there || key0 + r >= len) u[e] = make_uint4(0u, 0u, 0u, 0u);
+                const uint32_t c4[4] = {u[e].x, u[e].y, u[e].z, u[e].w};
+                uint32_t o[8];
 #pragma unroll
-              for (int k = 0; k < 4; ++k) o[2 * k] = code_pairs(half2_lo(c4[k])), o[2 * k + 1] = code_pairs(half2_hi(c4[k]));
-              if constexpr (kSpecial) {
-                if (now.value && key0 + r >= base) {
-                  const uint32_t ones = f16 ? 0x7c007c00u : 0x7f807f80u;  // exponents of what is not finite
-                  const uint32_t gone = key0 + r >= len ? ~0u : 0u;
+                for (int k = 0; k < 4; ++k) o[2 * k] = code_pairs(half2_lo(c4[k])), o[2 * k + 1] = code_pairs(half2_hi(c4[k]));
+                if constexpr (kSpecial) {
+                  if (now.value && key0 + r >= base) {
+                    const uint32_t ones = f16 ? 0x7c007c00u : 0x7f807f80u;  // exponents of what is not finite
+                    const uint32_t gone = key0 + r >= len ? ~0u : 0u;
 #pragma unroll
-                  for (int k = 0; k < 8; ++k) {
-                    const uint32_t no = __vcmpeq2(o[k] & ones, ones);
-                    if (no & ~gone) *foul = 1;
-                    o[k] &= ~(no | gone);
+                    for (int k = 0; k < 8; ++k) {
+                      const uint32_t no = __vcmpeq2(o[k] & ones, ones);
+                      if (no & ~gone) *foul = 1;
+                      o[k] &= ~(no | gone);
+                    }
                   }
                 }
+                const uint32_t to_row = to + half_of(e) * 16384 + r * 128;
+                sts128(to_row + (((2 * g) ^ (r & 7)) << 4), o[0], o[1], o[2], o[3]);
+                sts128(to_row + (((2 * g + 1) ^ (r & 7)) << 4), o[4], o[5], o[6], o[7]);
               }
-              const uint32_t to_row = to + half_of(e) * 8192 + r * 128;
-              sts128(to_row + (((2 * g) ^ (r & 7)) << 4), o[0], o[1], o[2], o[3]);
-              sts128(to_row + (((2 * g + 1) ^ (r & 7)) << 4), o[4], o[5], o[6], o[7]);
             }
           };
-          const bool odd_rows = !there || key0 + 16 * wq + 15 >= base;  // drafted ones, or none
+          const bool odd_rows = !there || key0 + 32 * wq + 31 >= base;  // drafted ones, or none
           if (f16) {  // in units of the largest scale's power of two
             const float s16 = times_pow2(s, -(now.value ? ev : ek));
             const uint32_t by = pack_half2(s16, s16);
@@ -1126,14 +1146,14 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           const uint32_t vs = pos % W::kSlots;
           ok = __all_sync(0xffffffffu, wait_on(bar(W::kFull + vs), (pos / W::kSlots) & 1));
           if (!ok) break;
-          if (now.value && key0 + kHalf > base) {
+          if (now.value && key0 + KT > base) {
             // rows from the first drafted slot on
             const uint32_t to = sbase + W::kOffTile + vs * W::kSlot;
 #pragma unroll 1
-            for (int i = t; i < kHalf * (D / 64) * 8; i += 128) {
-              const int r = (i >> 3) & (kHalf - 1), key = key0 + r;
+            for (int i = t; i < KT * (D / 64) * 8; i += 128) {
+              const int r = (i >> 3) & (KT - 1), key = key0 + r;
               if (key < base) continue;
-              const uint32_t a = to + (i >> 9) * 8192 + r * 128 + (i & 7) * 16;
+              const uint32_t a = to + (i >> 10) * 16384 + r * 128 + (i & 7) * 16;
               if (key >= len) {
                 sts128(a, 0u, 0u, 0u, 0u);
                 continue;
@@ -1172,15 +1192,14 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
   return fn;
 }
 
-// A pool's pages as [page and head, slot, dim], in boxes of 64 columns and up to a half's
-// slots
+// A pool's pages as [page and head, slot, dim], in boxes of one page's 64 columns
 bool page_map(CUtensorMap* m, const void* pool, const RelposPagedCache& c) {
   auto fn = encoder();
   if (!fn) return false;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(c.d), static_cast<cuuint64_t>(c.page),
                               static_cast<cuuint64_t>(c.num_pages) * c.H};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(c.d) * 2, static_cast<cuuint64_t>(c.d) * 2 * c.page};
-  const cuuint32_t box[3] = {64u, static_cast<cuuint32_t>(std::min(c.page, kHalf)), 1u};
+  const cuuint32_t box[3] = {64u, static_cast<cuuint32_t>(c.page), 1u};
   const cuuint32_t step[3] = {1u, 1u, 1u};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(pool), dims, strides, box, step,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
