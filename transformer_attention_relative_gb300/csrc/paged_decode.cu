@@ -152,7 +152,7 @@ int split_of(const RelposPagedCache* cache, int B, int Hq, int Lq, int max_pages
     out->rows = (G * Lq + out->rt - 1) / out->rt;
     const long long units = static_cast<long long>(B) * cache->H * out->rt;
     const long long tiles = (capacity + kWideTile - 1) / kWideTile;
-    if (units > (1 << 30) || units * (tiles + kWideUnitCost) > (1 << 30)) return RELPOS_ERR_UNSUPPORTED;
+    if (units > (1 << 30) || units * (tiles + 4) > (1 << 28)) return RELPOS_ERR_UNSUPPORTED;
     if (static_cast<long long>(cache->num_pages) * cache->H > 0x7fffffffll) return RELPOS_ERR_UNSUPPORTED;
     const int sms = device_sms();
     if (sms <= 0) return RELPOS_ERR_CUDA;

@@ -39,9 +39,6 @@ constexpr int kPdWarps = 4;
 constexpr int kPdThreads = 32 * kPdWarps;
 constexpr int kPdMinTiles = 4;  // fewest tiles of a block's share: one for each warp
 constexpr int kPdUnitCost = 12;  // what a unit costs a block beside its tiles, in tiles
-constexpr int kWideUnitCost = 3;  // the same in tiles of 128 keys (paged_wide.cuh)
-template <int KT>
-inline constexpr int unit_extra = KT == 128 ? kWideUnitCost : kPdUnitCost;
 constexpr int kPdBuckets = 256;
 
 // The weights p are kept as 2^(logit - off) for a row offset `off` that starts
@@ -247,7 +244,7 @@ struct Cursor {
 // Cost of a sequence's unit
 template <int KT>
 RP_DEVI int unit_cost(int len) {
-  return len > 0 ? (len + KT - 1) / KT + unit_extra<KT> : 0;
+  return len > 0 ? (len + KT - 1) / KT + kPdUnitCost : 0;
 }
 
 template <int KT, class P>
@@ -284,20 +281,20 @@ RP_DEVI Cursor locate(const P& p, int lane, int len0, int x, int& unit_at, int& 
       seqs += __popc(some & ((1u << l) - 1));
       c.b = b0 + l;
       c.len = __shfl_sync(0xffffffffu, len, l);
-      c.nt = unit - unit_extra<KT>;
+      c.nt = unit - kPdUnitCost;
       c.pages = p.table + c.b * p.table_stride;
       c.u = (x - cost * per) / unit;
       unit_at = cost * per + c.u * unit;
-      c.t = max(x - unit_at - unit_extra<KT>, 0);
+      c.t = max(x - unit_at - kPdUnitCost, 0);
       c.h = c.u / p.rt;
-      before = (cost - seqs * unit_extra<KT>) * per + c.u * c.nt + c.t;
+      before = (cost - seqs * kPdUnitCost) * per + c.u * c.nt + c.t;
       return c;
     }
     cost += __shfl_sync(0xffffffffu, upto, 31);
     seqs += __popc(some);
   }
   unit_at = cost * per;
-  before = (cost - seqs * unit_extra<KT>) * per;
+  before = (cost - seqs * kPdUnitCost) * per;
   return c;
 }
 

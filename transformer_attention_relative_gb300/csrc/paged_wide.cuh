@@ -112,7 +112,8 @@ struct Wide {
   static constexpr uint32_t kPFull = kSFull + 2;
   static constexpr uint32_t kODone = kPFull + 2;
   static constexpr uint32_t kOFree = kODone + 2;
-  static constexpr uint32_t kClean = kOFree + 2;                      // bf16: slots looked through
+  static constexpr uint32_t kStagger = kOFree + 2;                    // a pair's first warpgroup has its first maximum
+  static constexpr uint32_t kClean = kStagger + 1;                      // bf16: slots looked through
   static constexpr uint32_t kFinal = kClean + (FP8 ? 0 : kSlots);
   static constexpr uint32_t kBars = kFinal + 2;
   static constexpr uint32_t kOffMisc = kOffBar + kBars * 8;           // TMEM address, foul flag, 8 ints of the converters
@@ -219,35 +220,101 @@ struct Items {
   }
 };
 
-// A block's share. Each role calls this for itself, behind its register limit: what is
-// live across the roles' branch is kept to the lowest of them (and was spilled).
+// Costs that shares are equal in: a unit's tiles, more for a pair (2 x 131075 tokens
+// of 256 rows took 5.2 thousand cycles a tile, of 128 rows 3.5), and what a unit costs beside.
+constexpr int kPairCost = 3, kTileCost = 2, kUnitCost = 6;
+
+struct UnitCost {
+  int nt, tile, all;  // tiles, cost of one, of the unit
+  RP_DEVI UnitCost(const PagedTreeParams& p, int b, int copies) {
+    const int len = seq_len(p, b);
+    nt = (len + kWideTile - 1) / kWideTile;
+    tile = copies == 1 && nt > 0 && min(p.rows, row_count(p, b) * p.G) > 128 ? kPairCost : kTileCost;
+    all = nt > 0 ? nt * tile + kUnitCost : 0;
+  }
+};
+
+// A block's share: the tiles that begin within it. Each role calls this for itself,
+// behind its register limit: what is live across the roles' branch is kept to the
+// lowest of them (and was spilled).
 template <int COPIES>
 struct Share {
   Walk<COPIES> w;
   int size, at;  // cost of a block's share, and that at which the present unit starts
   RP_DEVI Share(const PagedTreeParams& p, int lane) : size(0), at(0) {
-    constexpr int KT = kWideTile;
     const int per = p.Hkv * p.rt;
-    if (p.direct) {
-      w.c.b = blockIdx.x / per;
-      w.c.u = blockIdx.x - w.c.b * per;
-      w.c.t = 0;
-      w.c.len = seq_len(p, w.c.b);
-      w.c.nt = w.tiles = (w.c.len + KT - 1) / KT;
-      w.c.h = w.c.u / p.rt;
-      w.c.pages = p.table + w.c.b * p.table_stride;
-    } else {
-      const int len0 = seq_len(p, lane);
-      const int total = total_cost<KT>(p, lane, len0);
-      size = max((total + p.blocks - 1) / p.blocks, 1 + unit_extra<KT>);
-      const int begin = min(static_cast<int>(blockIdx.x) * size, total);
-      int first, last, unused;
-      locate<KT>(p, lane, len0, min(begin + size, total), unused, last);
-      w.c = locate<KT>(p, lane, len0, begin, at, first);
-      w.tiles = begin == total ? 0 : last - first;
-    }
     w.x = 0;
+    if (p.direct) {
+      enter(p, blockIdx.x / per, blockIdx.x % per, 0);
+      w.tiles = w.c.nt;
+    } else {
+      int total = 0;
+      for (int b = lane; b < p.B; b += 32) total += UnitCost(p, b, COPIES).all;
+      total = __reduce_add_sync(0xffffffffu, total) * per;
+      size = max((total + p.blocks - 1) / p.blocks, kTileCost + kUnitCost);
+      const int begin = min(static_cast<int>(blockIdx.x) * size, total), end = min(begin + size, total);
+      // the first tiles at or behind begin and end, and the tiles before either
+      int b0 = p.B, u0 = 0, t0 = 0, at0 = 0, tiles0 = 0, tiles1 = 0;
+      int cost = 0, tiles = 0;  // of the sequences looked at, a unit each
+      for (int first = 0; first < p.B; first += 32) {
+        const int b = first + lane;
+        int mine = 0, nt = 0, tile = 1;
+        if (b < p.B) {
+          const UnitCost c(p, b, COPIES);
+          mine = c.all, nt = c.nt, tile = c.tile;
+        }
+        int upto = mine, nt_upto = nt;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, upto, o), z = __shfl_up_sync(0xffffffffu, nt_upto, o);
+          if (lane >= o) upto += y, nt_upto += z;
+        }
+        const int from = (cost + upto - mine) * per, to = (cost + upto) * per;  // of all its units
+        auto place = [&](int x, int& u, int& t) {  // in this lane's sequence, or behind it
+          u = min((x - from) / max(mine, 1), per - 1);
+          t = max(0, (x - from - u * mine - kUnitCost + tile - 1) / tile);
+          if (x - from - u * mine < kUnitCost) t = 0;
+          if (t >= nt) ++u, t = 0;  // the next unit's first
+        };
+        int u = 0, t = 0;
+        const bool has0 = mine > 0 && begin >= from && begin < to, has1 = mine > 0 && end > from && end <= to;
+        if (has0) place(begin, u, t);
+        const unsigned m0 = __ballot_sync(0xffffffffu, has0);
+        if (m0) {
+          const int l = __ffs(m0) - 1;
+          b0 = first + l;
+          u0 = __shfl_sync(0xffffffffu, u, l), t0 = __shfl_sync(0xffffffffu, t, l);
+          at0 = __shfl_sync(0xffffffffu, from + u * mine, l);
+          tiles0 = __shfl_sync(0xffffffffu, (tiles + nt_upto - nt) * per + u * nt + t, l);
+        }
+        if (has1) place(end, u, t);
+        const unsigned m1 = __ballot_sync(0xffffffffu, has1);
+        if (m1) tiles1 = __shfl_sync(0xffffffffu, (tiles + nt_upto - nt) * per + u * nt + t, __ffs(m1) - 1);
+        cost += __shfl_sync(0xffffffffu, upto, 31);
+        tiles += __shfl_sync(0xffffffffu, nt_upto, 31);
+      }
+      at = at0;
+      enter(p, b0, u0, t0);
+      w.tiles = begin == total ? 0 : tiles1 - tiles0;
+      if (w.tiles > 0 && u0 == per) {  // behind a sequence's last unit: the next one's first
+        ++w.c.b;
+        w.c.u = w.c.t = 0;
+        w.c.template enter<kWideTile>(p);
+        w.c.h = 0;
+      }
+    }
     if (w.tiles > 0) w.load(p);
+  }
+  RP_DEVI void enter(const PagedTreeParams& p, int b, int u, int t) {
+    w.c.b = b, w.c.u = u, w.c.t = t;
+    w.c.len = seq_len(p, b);
+    w.c.nt = (w.c.len + kWideTile - 1) / kWideTile;
+    w.c.h = u / p.rt;
+    w.c.pages = p.table + b * p.table_stride;
+  }
+  // cost of the present unit, and of its tiles
+  RP_DEVI int tile_cost(const PagedTreeParams& p) const {
+    return COPIES == 1 && min(p.rows, w.live * p.G) > 128 ? kPairCost : kTileCost;
   }
 };
 
@@ -466,7 +533,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       const uint32_t leader = elect_one();
       const uint32_t x = warp == 1 ? 0u : 1u;
       const uint32_t s_col = tmem + kColS + 128 * x, o_col = tmem + kColO + D * x;
-      uint32_t pos = 0, mine = 0, unit = 0;  // of the ring, own tiles before, units
+      uint32_t pos = 0, mine = 0, unit = 0, pairs = 0;  // of the ring, own tiles before, units, pairs among them
       do {
         ok = wait_warp(bar(W::kQFull), unit & 1);
         const bool f16 = FP8 && infos[unit & 1].f16;
@@ -506,7 +573,10 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           const int a = i + 1;
           if (a >= own) continue;
           const uint32_t ks = kp % W::kSlots, c = mine + a;
-          ok = wait_warp(bar(W::kFull + ks), (kp / W::kSlots) & 1);
+          // a pair's second warpgroup starts behind the first, so that the one's products
+          // run while the other has its scores
+          if (w.pair && x == 1 && a == 0) ok = wait_warp(bar(W::kStagger), pairs & 1);
+          if (ok) ok = wait_warp(bar(W::kFull + ks), (kp / W::kSlots) & 1);
           // the weights of the tile before lie in its columns
           if (ok && c > 0) ok = wait_warp(bar(W::kODone + x), (c - 1) & 1);
           if (!ok) break;
@@ -524,6 +594,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         }
         if (own == 0) commit_if(leader, bar(W::kQEmpty));  // no tile of the unit
         mine += own;
+        pairs += w.pair && w.h0 > 0;
         ++unit;
       } while (ok && w.next(p));
       commit_if(leader, bar(W::kFinal + x));
@@ -713,6 +784,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
               }
               top = fmaxf(top, fmaf(fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)), mul, fmaf(chunk_slope, q, addc)));
             }
+            if (COPIES == 1 && pair && i == 0 && threadIdx.x == 128) mbar_arrive(bar(W::kStagger));
             const float m_new = fmaxf(m_run, top);
             const bool moves = m_new > m_run + kRescale;
             const bool any_moves = __any_sync(0xffffffffu, moves);
@@ -816,8 +888,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       const bool whole = w.c.t == 0 && n == w.c.nt;
       const int slot = 2 * blockIdx.x + (w.c.t == 0 ? 1 : 0);
       if (!whole && threadIdx.x == 128) {  // the same thread wrote the zeros before
-        const int c0 = (at + unit_extra<KT>) / size;
-        p.ends[slot] = make_int4(c0, (at + unit_extra<KT> + w.c.nt - 1) / size - c0 + 1, w.c.b, w.c.u);
+        const int c0 = (at + kUnitCost) / size;
+        p.ends[slot] = make_int4(c0, (at + kUnitCost + (w.c.nt - 1) * share.tile_cost(p)) / size - c0 + 1, w.c.b, w.c.u);
       }
       // a weight of 0 would make NaN of what is nothing
       auto part_of = [](float2 part, float m) { return part.x == -INFINITY ? 0.f : ex2_approx(part.x - m); };
@@ -965,7 +1037,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       tc_fence_before();
       mbar_arrive(bar(W::kOFree));
       mbar_arrive(bar(W::kOFree + 1));
-      at += unit_extra<KT> + w.c.nt;
+      at += kUnitCost + w.c.nt * share.tile_cost(p);
       ++unit;
     } while (w.next(p));
   } else {
