@@ -22,7 +22,7 @@
 //
 //   warp 0        producer: tiles of keys and values from their pages into a ring of
 //                 shared memory (bf16: tensor copies, swizzled; e4m3: bulk copies).
-//   warps 1, 3    issuers of the products, one for each softmax warpgroup.
+//   warps 1 - 3   issuers of the products: scores; either warpgroup's weights by values.
 //   warps 4-11    the softmax warpgroups; thread t holds row t of a product.
 //   warps 12-15   a unit's query rows into shared memory; e4m3: codes to 16-bit tiles;
 //                 both: values that some row must not see.
@@ -115,7 +115,7 @@ struct Wide {
   static constexpr uint32_t kStagger = kOFree + 2;                    // a pair's first warpgroup has its first maximum
   static constexpr uint32_t kClean = kStagger + 1;                      // bf16: slots looked through
   static constexpr uint32_t kFinal = kClean + (FP8 ? 0 : kSlots);
-  static constexpr uint32_t kBars = kFinal + 2;
+  static constexpr uint32_t kBars = kFinal + 3;
   static constexpr uint32_t kOffMisc = kOffBar + kBars * 8;           // TMEM address, foul flag, 8 ints of the converters
   static constexpr uint32_t kSmem = kOffMisc + 64 + 1024;             // and room to align
 };
@@ -414,7 +414,6 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       if (i >= W::kEmpty && i < W::kRawFull) n = kReaders;
       if (i >= W::kRawEmpty && i < W::kQFull) n = 4;            // a warp each
       if (i == W::kQFull) n = 128;
-      if (i == W::kQEmpty) n = 2;                               // both issuers
       if (i >= W::kClean && i < W::kFinal) n = 4;
       if (i >= W::kPFull && i < W::kODone) n = 128;
       if (i == W::kOFree || i == W::kOFree + 1) n = 256;
@@ -525,80 +524,99 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       // never leave with copies in flight
       for (uint32_t k = pos > kRing ? pos - kRing : 0; k < pos; ++k)
         wait_on(bar(full0 + k % kRing), (k / kRing) & 1);
-    } else if ((warp == 1 || warp == 3) && some) {
+    } else if (some) {
       // ------------------------------------------------------------ issuers
-      // The whole warp goes the same way (operands stay uniform), one thread issues.
-      // Rolled loops: straight-line code for these few instructions a tile is
-      // fetched anew each time (950 cycles for the 4 products of a half's weights).
+      // Warp 1: scores, of the one warpgroup and the other; warps 2 and 3: the weights'
+      // products of either. The whole warp goes the same way (operands stay uniform),
+      // one thread issues. Each goes through all items, in their order.
       const uint32_t leader = elect_one();
-      const uint32_t x = warp == 1 ? 0u : 1u;
-      const uint32_t s_col = tmem + kColS + 128 * x, o_col = tmem + kColO + D * x;
-      uint32_t pos = 0, mine = 0, unit = 0, pairs = 0;  // of the ring, own tiles before, units, pairs among them
-      do {
-        ok = wait_warp(bar(W::kQFull), unit & 1);
-        const bool f16 = FP8 && infos[unit & 1].f16;
-        // the operands' type: bf16 (1) or fp16 (0)
-        constexpr uint32_t kTypes = (1u << 7) | (1u << 10);
-        const uint32_t types = f16 ? 0u : kTypes;
-        const uint32_t idesc_s = (idesc_bf16_f32(128, KT, 0, 0) & ~kTypes) | types;
-        const uint32_t idesc_o = (idesc_bf16_f32(128, D, 0, 1) & ~kTypes) | types;
-        const uint64_t dq = smem_desc_sw128(sbase + W::kOffQ + (w.pair ? x * W::kQTile : 0u), 16, 1024);
-        const int own = w.pair || x == 0 ? w.h0 : w.h1;
-        const bool twice = kReaders == 2 && !w.pair;
-        // weights' product of tile i, then scores of tile i + 1
+      constexpr uint32_t kTypes = (1u << 7) | (1u << 10);  // the operands' type: bf16 (1) or fp16 (0)
+      uint32_t slot = 0, turn = 0, unit = 0, mine0 = 0, mine1 = 0;  // place in the ring; units, either's tiles before
+      auto pass = [&] {
+        if (++slot == W::kSlots) slot = 0, turn ^= 1;
+      };
+      if (warp == 1) {
+        uint32_t pairs = 0;  // among the units before
+        do {
+          ok = wait_warp(bar(W::kQFull), unit & 1);
+          const uint32_t idesc = (idesc_bf16_f32(128, KT, 0, 0) & ~kTypes) | (FP8 && infos[unit & 1].f16 ? 0u : kTypes);
 #pragma unroll 1
-        for (int i = -1; ok && i < w.h0; ++i) {
-          // positions as in Items
-          const int before = (i >= 0) + (i + 1 < w.h0), behind = (i >= 0 && i < w.h1) + (i + 1 < w.h1);
-          const uint32_t vp = pos + (w.pair || x == 0 ? 0 : before), kp = vp + (i >= 0 && i < own);
-          pos += before + behind;
-          if (i >= 0 && i < own) {
-            const uint32_t vs = vp % W::kSlots, c = mine + i;
-            ok = wait_warp(bar(W::kFull + vs), (vp / W::kSlots) & 1);
-            if (!FP8 && ok) ok = wait_warp(bar(W::kClean + vs), (vp / W::kSlots) & 1);
-            if (ok && i == 0 && unit > 0) ok = wait_warp(bar(W::kOFree + x), (unit - 1) & 1);
-            if (ok) ok = wait_warp(bar(W::kPFull + x), c & 1);
+          for (Items it(w.h0, w.h1); ok && it.valid(); it.next(), pass()) {
+            if (it.value) continue;
+            const int i = it.tile();
+            const uint32_t first = w.pair ? 0u : it.x, last = w.pair ? 1u : it.x;
+            ok = wait_warp(bar(W::kFull + slot), turn);
+            // (copies end in any order; what was looked through was so in order)
+            if (!FP8 && ok) ok = wait_warp(bar(W::kClean + slot), turn);
+#pragma unroll 1
+            for (uint32_t x = first; ok && x <= last; ++x) {
+              // the weights of the tile before lie in its columns
+              const uint32_t c = (x ? mine1 : mine0) + i;
+              if (c > 0) ok = wait_warp(bar(W::kODone + x), (c - 1) & 1);
+              // a pair's second warpgroup starts behind the first, so that the one's
+              // products run while the other has its scores
+              if (ok && w.pair && x == 1 && i == 0) ok = wait_warp(bar(W::kStagger), pairs & 1);
+              if (!ok) break;
+              tc_fence_after();
+              uint64_t a = smem_desc_sw128(sbase + W::kOffQ + (w.pair ? x * W::kQTile : 0u), 16, 1024);
+              uint64_t b = smem_desc_sw128(sbase + W::kOffTile + slot * W::kSlot, 16, 1024);
+#pragma unroll 1
+              for (int hf = 0; hf < D / 64; ++hf, a += 1024, b += 1024)
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                  umma_ss_if(leader, tmem + kColS + 128 * x, a + 2 * kk, b + 2 * kk, idesc, hf > 0 || kk > 0);
+              commit_if(leader, bar(W::kSFull + x));
+              commit_if(leader, bar(W::kEmpty + slot));
+              if (kReaders == 2 && !w.pair) commit_if(leader, bar(W::kEmpty + slot));
+            }
+          }
+          commit_if(leader, bar(W::kQEmpty));
+          mine0 += w.h0, mine1 += w.pair ? w.h0 : w.h1;
+          pairs += w.pair && w.h0 > 0;
+          ++unit;
+        } while (ok && w.next(p));
+      } else {
+        const uint32_t x = warp - 2;
+        do {
+#pragma unroll 1
+          for (Items it(w.h0, w.h1); ok && it.valid(); it.next(), pass()) {
+            if (!it.value || !(w.pair || it.x == static_cast<int>(x))) continue;
+            const int i = it.tile();
+            // The weights first: a wait for a phase also passes while the barrier is two
+            // phases back, and this warp skips the other warpgroup's items. That the keys
+            // of these weights were ready, at most three items before, says that the item
+            // before in this slot was (slots become ready in order).
+            ok = wait_warp(bar(W::kPFull + x), (mine0 + i) & 1);
+            if (i == 0 && unit > 0 && ok) ok = wait_warp(bar(W::kOFree + x), (unit - 1) & 1);
+            if (ok) ok = wait_warp(bar(W::kFull + slot), turn);
+            if (!FP8 && ok) ok = wait_warp(bar(W::kClean + slot), turn);
             if (!ok) break;
             tc_fence_after();
-            const uint64_t dv = smem_desc_sw128(sbase + W::kOffTile + vs * W::kSlot, 16384, 1024);
-            // (bf16: the second parts of the weights behind the first)
+            const bool f16 = FP8 && infos[unit & 1].f16;
+            const uint32_t idesc = (idesc_bf16_f32(128, D, 0, 1) & ~kTypes) | (f16 ? 0u : kTypes);
+            uint64_t b = smem_desc_sw128(sbase + W::kOffTile + slot * W::kSlot, 16384, 1024);
+            // 64 keys at a time (bf16: the second parts of their weights behind the first)
+            uint32_t a = tmem + kColS + 128 * x;
 #pragma unroll 1
-            for (int kk = 0; kk < (f16 ? 1 : 2) * KT / 16; ++kk)
-              umma_ts_if(leader, o_col, s_col + 64 * (kk >> 2 & 1) + 32 * (kk >> 3) + 8 * (kk & 3), dv + 128 * (kk & 7), idesc_o,
-                         i > 0 || kk > 0);
+            for (int ch = 0; ch < 2; ++ch, a += 64, b += 512) {
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                umma_ts_if(leader, tmem + kColO + D * x, a + 8 * kk, b + 128 * kk, idesc, i > 0 || ch > 0 || kk > 0);
+              if (f16) continue;
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                umma_ts_if(leader, tmem + kColO + D * x, a + 32 + 8 * kk, b + 128 * kk, idesc, 1u);
+            }
             commit_if(leader, bar(W::kODone + x));
-            commit_if(leader, bar(W::kEmpty + vs));
-            if (twice) commit_if(leader, bar(W::kEmpty + vs));
+            commit_if(leader, bar(W::kEmpty + slot));
+            if (kReaders == 2 && !w.pair) commit_if(leader, bar(W::kEmpty + slot));
           }
-          const int a = i + 1;
-          if (a >= own) continue;
-          const uint32_t ks = kp % W::kSlots, c = mine + a;
-          // a pair's second warpgroup starts behind the first, so that the one's products
-          // run while the other has its scores
-          if (w.pair && x == 1 && a == 0) ok = wait_warp(bar(W::kStagger), pairs & 1);
-          if (ok) ok = wait_warp(bar(W::kFull + ks), (kp / W::kSlots) & 1);
-          // the weights of the tile before lie in its columns
-          if (ok && c > 0) ok = wait_warp(bar(W::kODone + x), (c - 1) & 1);
-          if (!ok) break;
-          tc_fence_after();
-          const uint64_t dk = smem_desc_sw128(sbase + W::kOffTile + ks * W::kSlot, 16, 1024);
-#pragma unroll 1
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint64_t off = (kk >> 2) * 1024 + 2 * (kk & 3);
-            umma_ss_if(leader, s_col, dq + off, dk + off, idesc_s, kk > 0);
-          }
-          commit_if(leader, bar(W::kSFull + x));
-          commit_if(leader, bar(W::kEmpty + ks));
-          if (twice) commit_if(leader, bar(W::kEmpty + ks));
-          if (a == own - 1) commit_if(leader, bar(W::kQEmpty));
-        }
-        if (own == 0) commit_if(leader, bar(W::kQEmpty));  // no tile of the unit
-        mine += own;
-        pairs += w.pair && w.h0 > 0;
-        ++unit;
-      } while (ok && w.next(p));
-      commit_if(leader, bar(W::kFinal + x));
-      wait_warp(bar(W::kFinal + x), 0);
+          mine0 += w.pair || x == 0 ? w.h0 : w.h1;
+          ++unit;
+        } while (ok && w.next(p));
+      }
+      commit_if(leader, bar(W::kFinal + warp - 1));
+      wait_warp(bar(W::kFinal + warp - 1), 0);
     }
   } else if (warp < 12) {
     setmaxnreg_inc<168>();
