@@ -639,9 +639,14 @@ int relpos_paged_decode(const RelposPagedCache* cache, const void* Q, const Relp
  */
 int relpos_selftest_paged_decode_split(const RelposPagedCache* cache, int B, int Hq, int Lq, int max_pages, int* rows,
                                        int* launches);
-/* the same for a relpos_paged_tree_decode of n nodes (rows 8, 16, or up to 128 on the tensor cores' wide products) */
-int relpos_selftest_paged_tree_split(const RelposPagedCache* cache, int B, int Hq, int n, int max_pages, int* rows,
-                                     int* launches);
+/*
+ * The same for a relpos_paged_tree_decode of n nodes; wide is 1 where it runs on products
+ * of 128 rows, with units of up to 256 (but for a T5 bias whose nearest distances, R of
+ * them that have buckets of their own, fill a table of more than 2048 entries
+ * (R + 1) Hq / H: that runs on the others).
+ */
+int relpos_selftest_paged_tree_split(const RelposPagedCache* cache, int B, int Hq, int n, int max_pages, int bias_mode,
+                                     int* rows, int* launches, int* wide);
 
 /*
  * ---------------------------------------------------------------------------

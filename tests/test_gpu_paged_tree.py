@@ -20,6 +20,23 @@ def _built():
     G.ensure_built()
 
 
+@pytest.fixture(autouse=True, params=["short table", "long table"])
+def _tables(request):
+    """Each case with its own table, and with one of so many columns that the library counts on long sequences and takes
+    the wide products where there are rows enough for them."""
+    global _columns
+    _columns = 0 if request.param == "short table" else 160 * 128
+    yield
+
+
+_columns = 0
+
+
+def _table(table, page):
+    more = max(0, _columns // page - table.shape[1])
+    return torch.nn.functional.pad(table, (0, more), value=-1).cuda()
+
+
 def _tree(kind, B, n, seed=0):
     if kind == "chain":
         return torch.arange(-1, n - 1, dtype=torch.int32).expand(B, n).contiguous()
@@ -32,7 +49,7 @@ def _tree(kind, B, n, seed=0):
 
 
 def _gpu(cache, q, table, lens, parents, bias, mode, nodes=None, **kw):
-    o = rp.paged_tree_decode(q.cuda(), cache, table.cuda(), lens.cuda(), parents.cuda(),
+    o = rp.paged_tree_decode(q.cuda(), cache, _table(table, cache.page_size), lens.cuda(), parents.cuda(),
                              nodes=None if nodes is None else torch.tensor(nodes, dtype=torch.int32).cuda(),
                              bias=None if bias is None else bias.cuda(), mode=MODES[mode], **kw)
     torch.cuda.synchronize()
@@ -248,7 +265,7 @@ def test_strides_alignment_and_a_shared_tree(dtype, Hq):
     wide = torch.zeros(2, n, Hq, 2 * 64 + 1, dtype=BF)
     wide[..., 1:65] = q.transpose(1, 2)
     out = torch.full((2, n, Hq, 2 * 64 + 1), 7.0, dtype=BF, device="cuda")
-    x = rp.paged_tree_decode(wide.cuda()[..., 1:65].transpose(1, 2), cache, table.cuda(), lens.cuda(), parents.cuda(),
+    x = rp.paged_tree_decode(wide.cuda()[..., 1:65].transpose(1, 2), cache, _table(table, 32), lens.cuda(), parents.cuda(),
                              bias=bias.cuda(), mode=rp.MODE_T5, out=out[..., 65:].transpose(1, 2))
     _check(x, ref, size, dtype == E4)
     assert (out[..., :65] == 7.0).all()

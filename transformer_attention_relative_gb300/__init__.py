@@ -118,7 +118,7 @@ def load_library(path: str = LIB_PATH):
     lib.relpos_paged_decode.restype = i
     lib.relpos_selftest_paged_decode_split.argtypes = [p(_PagedCache), i, i, i, i, p(i), p(i)]
     lib.relpos_selftest_paged_decode_split.restype = i
-    lib.relpos_selftest_paged_tree_split.argtypes = [p(_PagedCache), i, i, i, i, p(i), p(i)]
+    lib.relpos_selftest_paged_tree_split.argtypes = [p(_PagedCache), i, i, i, i, i, p(i), p(i), p(i)]
     lib.relpos_selftest_paged_tree_split.restype = i
     lib.relpos_paged_tree_decode.argtypes = [p(_PagedCache), vp, p(_RowStrides), i, i, i, vp, ll, i, vp, vp, vp, ll, i, vp,
                                              i, i, f, vp, p(_RowStrides), vp]
@@ -251,9 +251,9 @@ def relpos_selftest_paged_decode_split(cache, B, Hq, Lq, max_pages, rows, launch
     return load_library().relpos_selftest_paged_decode_split(cache, B, Hq, Lq, max_pages, rows, launches)
 
 
-def relpos_selftest_paged_tree_split(cache, B, Hq, n, max_pages, rows, launches) -> int:
-    """Rows of a unit and launches of a tree decode of these sizes, on the current device."""
-    return load_library().relpos_selftest_paged_tree_split(cache, B, Hq, n, max_pages, rows, launches)
+def relpos_selftest_paged_tree_split(cache, B, Hq, n, max_pages, bias_mode, rows, launches, wide) -> int:
+    """Rows of a unit, launches and kind of products of a tree decode of these sizes, on the current device."""
+    return load_library().relpos_selftest_paged_tree_split(cache, B, Hq, n, max_pages, bias_mode, rows, launches, wide)
 
 
 def relpos_paged_tree_decode(cache, Q, q_strides, B, Hq, n, block_table, table_stride, max_pages, lens, nodes, parents,

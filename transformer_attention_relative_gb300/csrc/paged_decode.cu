@@ -138,16 +138,32 @@ struct Split {
   bool wide;  // the kernel of paged_wide.cuh in place of v.decode
 };
 
-constexpr int kWideFrom = 17;  // rows of a key/value head
+// Rows of a key/value head from which trees take the kernel of paged_wide.cuh. Its time
+// hardly depends on the rows up to 64, here the keys are read and multiplied again for
+// every 16 rows. us here / there for 16 sequences x 8 heads x 8192 tokens:
+//   rows                          8        16        24        48        64
+//   bf16  d =  64, no bias    71 /  71 100 /  72 168 /  72 236 /  74 288 /  75
+//   bf16  d = 128, no bias   116 / 112 122 / 114 199 / 114 288 / 121 367 / 122
+//   e4m3  d =  64, no bias    46 /  87  57 /  87  86 /  88 117 /  85 149 /  87
+//   e4m3  d = 128, no bias    73 / 106  82 / 108 116 / 108 164 / 108 209 / 109
+//   e4m3  d =  64, ALiBi      51 /  87  86 /  88 147 /  89 214 /  89 268 /  90
+//   e4m3  d = 128, ALiBi      78 / 114 112 / 117 189 / 119 277 / 125 359 / 127
+// (there a column's distance costs nothing beside the products, and codes have to
+// become 16-bit tiles first).
+int wide_from(const RelposPagedCache* cache, int mode) {
+  if (cache->dtype == RELPOS_BF16) return 9;
+  return mode == RELPOS_ALIBI ? 17 : 33;
+}
 
 template <class P>
-int split_of(const RelposPagedCache* cache, int B, int Hq, int Lq, int max_pages, int near, Split<P>* out) {
+int split_of(const RelposPagedCache* cache, int B, int Hq, int Lq, int max_pages, int mode, int near,
+             Split<P>* out) {
   const int G = Hq / cache->H;
   if (G > 65535) return RELPOS_ERR_UNSUPPORTED;
   const long long capacity = static_cast<long long>(max_pages) * cache->page;
   if (capacity > (1 << 28)) return RELPOS_ERR_UNSUPPORTED;
-  out->wide = std::is_same_v<P, PagedTreeParams> && G * Lq >= kWideFrom && static_cast<long long>(G) * near <= kWideLut;
-  if (out->wide) {
+  out->wide = false;
+  if (std::is_same_v<P, PagedTreeParams> && G * Lq >= wide_from(cache, mode) && static_cast<long long>(G) * near <= kWideLut) {
     out->rt = (G * Lq + kWideRows - 1) / kWideRows;
     out->rows = (G * Lq + out->rt - 1) / out->rt;
     const long long units = static_cast<long long>(B) * cache->H * out->rt;
@@ -157,8 +173,14 @@ int split_of(const RelposPagedCache* cache, int B, int Hq, int Lq, int max_pages
     const int sms = device_sms();
     if (sms <= 0) return RELPOS_ERR_CUDA;
     out->direct = tiles <= 2;
-    out->blocks = static_cast<int>(out->direct ? units : std::min<long long>(sms, units * tiles));
-    return RELPOS_OK;
+    out->blocks = static_cast<int>(out->direct ? units : sms);
+    // Where there are no more tiles than SMs, more and smaller blocks are ahead: here / there
+    // for 8 heads of 1024 tokens (64 tiles), 64 rows: bf16 22 / 22 and 24 / 29 us (d = 64,
+    // 128), e4m3 21 / 27 and 25 / 34, 256 rows: 27 / 33, 34 / 47, 24 / 40 and 31 / 55;
+    // 4 sequences of them (256 tiles), 64 rows: 27 / 23, 35 / 31, 25 / 28 and 31 / 35,
+    // 256 rows: 60 / 35, 67 / 51, 44 / 41 and 64 / 57.
+    out->wide = units * tiles > sms;
+    if (out->wide) return RELPOS_OK;
   }
   out->v = variant_of<P>(cache->d, cache->dtype, 1);
   out->rt = (G * Lq + 7) / 8;
@@ -230,7 +252,7 @@ int decode_call(const RelposPagedCache* cache, const void* Q, const RelposRowStr
     if (rc != RELPOS_OK) return rc;
   }
   Split<P> split;
-  rc = split_of(cache, B, Hq, Lq, max_pages, bias_mode == RELPOS_T5 ? p.t5_R + 1 : 0, &split);
+  rc = split_of(cache, B, Hq, Lq, max_pages, bias_mode, bias_mode == RELPOS_T5 ? p.t5_R + 1 : 0, &split);
   if (rc != RELPOS_OK) return rc;
   PagedVariant<P> v = split.v;
 
@@ -308,30 +330,32 @@ int decode_call(const RelposPagedCache* cache, const void* Q, const RelposRowStr
 using namespace relpos;
 
 template <class P>
-static int selftest_split(const RelposPagedCache* cache, int B, int Hq, int Lq, int most_rows, int max_pages, int* rows,
-                          int* launches) {
+static int selftest_split(const RelposPagedCache* cache, int B, int Hq, int Lq, int most_rows, int max_pages, int mode,
+                          int* rows, int* launches, int* wide) {
   const int rc = check_paged_cache(cache);
   if (rc != RELPOS_OK) return rc;
-  if (!rows || !launches || cache->H < 1 || cache->num_pages < 1 || B < 1 || Hq < 1 || Hq % cache->H || Lq < 1 ||
+  if (!rows || !launches || !wide || cache->H < 1 || cache->num_pages < 1 || B < 1 || Hq < 1 || Hq % cache->H || Lq < 1 ||
       max_pages < 1)
     return RELPOS_ERR_INVALID_ARG;
   if (Lq > most_rows) return RELPOS_ERR_UNSUPPORTED;
   Split<P> split;
-  const int err = split_of(cache, B, Hq, Lq, max_pages, 0, &split);
+  const int err = split_of(cache, B, Hq, Lq, max_pages, mode, 0, &split);
   if (err != RELPOS_OK) return err;
   *rows = split.rows;
   *launches = split.direct ? 1 : 2;
+  *wide = split.wide;
   return RELPOS_OK;
 }
 
 extern "C" int relpos_selftest_paged_decode_split(const RelposPagedCache* cache, int B, int Hq, int Lq, int max_pages,
                                                   int* rows, int* launches) {
-  return selftest_split<PagedDecodeParams>(cache, B, Hq, Lq, 8, max_pages, rows, launches);
+  int wide;
+  return selftest_split<PagedDecodeParams>(cache, B, Hq, Lq, 8, max_pages, RELPOS_NO_BIAS, rows, launches, &wide);
 }
 
 extern "C" int relpos_selftest_paged_tree_split(const RelposPagedCache* cache, int B, int Hq, int n, int max_pages,
-                                                int* rows, int* launches) {
-  return selftest_split<PagedTreeParams>(cache, B, Hq, n, kMaxNodes, max_pages, rows, launches);
+                                                int bias_mode, int* rows, int* launches, int* wide) {
+  return selftest_split<PagedTreeParams>(cache, B, Hq, n, kMaxNodes, max_pages, bias_mode, rows, launches, wide);
 }
 
 extern "C" int relpos_paged_decode(const RelposPagedCache* cache, const void* Q, const RelposRowStrides* qs, int B,

@@ -70,13 +70,13 @@ constexpr float kF16Shift = 5.f;  // fp16 weights are 2^5 times those of bf16: u
 constexpr uint32_t kNoPage = 0xffffffffu;  // in place of a scale
 constexpr int kF16Window = 15;    // exponents of page scales below the largest
 
-// What the producer knows of a tile's 32-key groups, for the softmax; a ring for
-// either warpgroup's tiles, longer than the producer can be ahead
+// What the producer knows of a tile's 32-key groups, for the softmax; a ring longer than
+// the producer can be ahead
 struct TileInfo {
   float k_rest[kGroups], v_rest[kGroups];  // of the scales
   uint8_t flags[kGroups];  // 1: the page is there; 2, 4: the rest of the keys' (values') scale is not 1
 };
-constexpr int kInfos = 16;
+constexpr int kInfos = 32;
 
 template <int D, bool FP8, int COPIES>
 struct Wide {
@@ -86,8 +86,8 @@ struct Wide {
   static constexpr uint32_t kQTile = 128 * D * 2;
   static constexpr uint32_t kSlot = kWideTile * D * 2;                // a tile's keys or values, 16 bits
   static constexpr uint32_t kRaw = kWideTile * D;                     // and as codes
-  static constexpr int kSlots = D == 64 ? (FP8 ? 6 : 8) : FP8 ? (COPIES == 1 ? 3 : 4) : COPIES == 1 ? 4 : 5;
-  static constexpr int kRawSlots = !FP8 ? 0 : D == 64 ? 6 : COPIES == 1 ? 3 : 2;
+  static constexpr int kSlots = D == 64 ? (FP8 ? 6 : 8) : FP8 ? 3 : COPIES == 1 ? 4 : 5;
+  static constexpr int kRawSlots = !FP8 ? 0 : D == 64 ? 6 : COPIES == 1 ? 3 : 4;
   static constexpr uint32_t kOffQ = 0;
   static constexpr uint32_t kOffTile = kOffQ + kQTiles * kQTile;
   static constexpr uint32_t kOffRaw = kOffTile + kSlots * kSlot;
@@ -98,8 +98,8 @@ struct Wide {
   static constexpr uint32_t kOffMl = kOffDeep + kMaxNodes * 4;        // [2][128] maximum and sum
   static constexpr uint32_t kOffQx = kOffMl + 2 * 128 * 8;            // [2][256] exponents of query rows
   static constexpr uint32_t kOffInfo = kOffQx + 2 * 256 * 4;          // [2] UnitInfo
-  static constexpr uint32_t kOffTiles = kOffInfo + 64;                // [2][kInfos] TileInfo
-  static constexpr uint32_t kOffScales = kOffTiles + 2 * kInfos * sizeof(TileInfo);  // [kRawSlots][kGroups], kNoPage: none
+  static constexpr uint32_t kOffTiles = kOffInfo + 64;                // [kInfos] TileInfo
+  static constexpr uint32_t kOffScales = kOffTiles + kInfos * sizeof(TileInfo);  // [kRawSlots][kGroups], kNoPage: none
   static constexpr uint32_t kOffBar = (kOffScales + kRawSlots * kGroups * 4 + 7) / 8 * 8;
   // barriers
   static constexpr uint32_t kFull = 0;                                // slots: written
@@ -174,7 +174,7 @@ struct Walk {
   int base, live;    // first drafted slot, nodes
   int row0, rows;    // first row of the unit in its key/value head, rows that have a node
   bool pair;         // both warpgroups take every tile, with half the rows each
-  int h0, h1;        // tiles of the first and the second warpgroup (a pair: of both, and 0)
+  int n;             // tiles of the unit to work on
   RP_DEVI void load(const PagedTreeParams& p) {
     xe = min(tiles, x + c.nt - c.t);
     live = row_count(p, c.b);
@@ -182,9 +182,7 @@ struct Walk {
     row0 = (c.u - c.h * p.rt) * p.rows;
     rows = max(0, min(p.rows, live * p.G - row0));
     pair = COPIES == 1 && rows > 128;
-    const int n = rows > 0 ? xe - x : 0;
-    h0 = pair ? n : (n + 1) >> 1;
-    h1 = pair ? 0 : n >> 1;
+    n = rows > 0 ? xe - x : 0;
   }
   RP_DEVI bool next(const PagedTreeParams& p) {
     c.template forward<kWideTile>(p, xe - x);
@@ -193,30 +191,45 @@ struct Walk {
     load(p);
     return true;
   }
-  // First key of a warpgroup's h-th tile, from the last one of the block's tiles on: a
-  // decaying bias (ALiBi) then has its largest logits first, and no maximum moves
-  // after those.
-  RP_DEVI int place_of(int of, int h) const { return pair ? h : of + 2 * h; }  // from the last one on
+  // Tile j is the j-th from the last one of the block's: a decaying bias (ALiBi) then has
+  // its largest logits first, and no maximum moves after those. A warpgroup's i-th tile,
+  // and how many it has:
+  RP_DEVI int tile_of(int of, int i) const { return pair ? i : of + 2 * i; }
+  RP_DEVI int own(int of) const { return pair ? n : (n + 1 - of) >> 1; }
   RP_DEVI int end_tiles() const { return (c.t + xe - x) * kWideTile; }
-  RP_DEVI int key_of(int of, int h) const { return end_tiles() - kWideTile * (place_of(of, h) + 1); }
+  RP_DEVI int key_of(int j) const { return end_tiles() - kWideTile * (j + 1); }
   RP_DEVI int first_key() const { return c.t * kWideTile; }
   RP_DEVI int end_key() const { return min((c.t + xe - x) * kWideTile, c.len); }
 };
 
-// The order in which a unit's tiles of keys and values pass through shared memory:
-// the keys of either warpgroup's first tile, then for i = 0, 1, .. the values of tile
-// i and the keys of tile i + 1 of the one and of the other.
+// The order in which a unit's tiles pass through shared memory: the keys of the first
+// tile, or first two (either warpgroup's), then each tile's values and the keys of the
+// one that the same warpgroup has next.
 struct Items {
-  int h0, h1, i, x;
+  int n, ahead, j;  // tiles, how far the keys are ahead of the values; tile
   bool value;
-  RP_DEVI Items(int a, int b) : h0(a), h1(b), i(-1), x(0), value(false) {}
-  RP_DEVI bool valid() const { return h0 > 0 && i < h0; }
-  RP_DEVI int tile() const { return value ? i : i + 1; }
+  template <class W>
+  RP_DEVI explicit Items(const W& w) : n(w.n), ahead(w.pair ? 1 : 2), j(0), value(false) {}
+  RP_DEVI bool valid() const { return j < n; }
   RP_DEVI void next() {
-    do {
-      value = !value;
-      if (value && (x ^= 1) == 0) ++i;
-    } while (i < h0 && (tile() < 0 || tile() >= (x ? h1 : h0)));
+    if (value) {
+      value = j + ahead >= n;
+      j += value ? 1 : ahead;
+    } else if (j + 1 < min(ahead, n)) {
+      ++j;
+    } else {
+      value = true;
+      j = max(j + 1 - ahead, 0);
+    }
+  }
+  // Places of a tile's keys and values in that order
+  template <class W>
+  RP_DEVI static uint32_t keys_at(const W& w, int j) {
+    return w.pair ? 2 * j : max(2 * j - 1, 0);
+  }
+  template <class W>
+  RP_DEVI static uint32_t values_at(const W& w, int j) {
+    return w.pair ? 2 * j + 1 : min(2 * j + 2, 2 * w.n - 1);
   }
 };
 
@@ -414,6 +427,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       if (i >= W::kEmpty && i < W::kRawFull) n = kReaders;
       if (i >= W::kRawEmpty && i < W::kQFull) n = 4;            // a warp each
       if (i == W::kQFull) n = 128;
+      if (i == W::kQEmpty) n = 3;                               // the issuers
       if (i >= W::kClean && i < W::kFinal) n = 4;
       if (i >= W::kPFull && i < W::kODone) n = 128;
       if (i == W::kOFree || i == W::kOFree + 1) n = 256;
@@ -440,7 +454,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     const bool some = w.tiles > 0;
     if (warp == 0 && some) {
       // ------------------------------------------------------------ producer
-      uint32_t pos = 0, seq0 = 0, seq1 = 0;  // of the ring; either warpgroup's tiles before
+      uint32_t pos = 0, slot = 0, turn = 1, seq = 0;  // items, place in the ring; tiles before
       const int per_page = 1 << p.log_page, boxes = KT >> p.log_page;  // keys of a copy, copies
       constexpr int kRing = FP8 ? W::kRawSlots : W::kSlots;
       constexpr uint32_t kSlotBytes = FP8 ? W::kRaw : W::kSlot;
@@ -465,8 +479,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           }
         };
 #pragma unroll 1
-        for (Items it(w.h0, w.h1); ok && it.valid(); it.next(), ++pos) {
-          const int g = w.place_of(it.x, it.tile());
+        for (Items it(w); it.valid(); it.next(), ++pos) {
+          const int g = it.j;
           if (g >> 3 > batch) look(g >> 3);
           // lanes 0 .. 3: the tile's groups; lanes 4 .. 7: the groups where pages start
           const int from = 4 * (g & 7) + (lane < 4 ? lane : ((lane & 3) << p.log_page >> 5) & 3);
@@ -476,8 +490,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           if constexpr (FP8) {
             const float sk = __shfl_sync(0xffffffffu, recent ? scale_now.x : scale_last.x, from);
             const float sv = __shfl_sync(0xffffffffu, recent ? scale_now.y : scale_last.y, from);
-            const uint32_t slot = pos % kRing;
-            if (pos >= kRing) ok = wait_warp(bar(empty0 + slot), (pos / kRing - 1) & 1);
+            ok = wait_warp(bar(empty0 + slot), turn);
             if (!ok) break;
             if (lane < kGroups) {
               float* const of_slot = reinterpret_cast<float*>(smem + W::kOffScales) + kGroups * slot;
@@ -487,19 +500,17 @@ __global__ void __launch_bounds__(kWideThreads, 1)
               const float of_kind = it.value ? v2 : k2;
               of_slot[lane] = !there ? __uint_as_float(kNoPage) : of_kind == of_kind ? of_kind : NAN;
               if (!it.value) {
-                TileInfo& info = tile_infos[it.x * kInfos + ((it.x ? seq1 : seq0) + it.tile()) % kInfos];
+                TileInfo& info = tile_infos[(seq + g) % kInfos];
                 info.k_rest[lane] = kr, info.v_rest[lane] = vr;
                 info.flags[lane] = there ? 1 | (kr != 1.f) << 1 | (vr != 1.f) << 2 : 0;
               }
             }
           } else {
-            const uint32_t slot = pos % kRing;
-            if (pos >= kRing) ok = wait_warp(bar(empty0 + slot), (pos / kRing - 1) & 1);
+            ok = wait_warp(bar(empty0 + slot), turn);
             if (!ok) break;
-            if (lane < kGroups && !it.value)
-              tile_infos[it.x * kInfos + ((it.x ? seq1 : seq0) + it.tile()) % kInfos].flags[lane] = there;
+            if (lane < kGroups && !it.value) tile_infos[(seq + g) % kInfos].flags[lane] = there;
           }
-          const uint32_t slot = pos % kRing, dst = ring + slot * kSlotBytes;
+          const uint32_t dst = ring + slot * kSlotBytes;
           const int copy = lane - kGroups;  // a page's, by lanes 4 ..
           const bool copies = copy >= 0 && copy < boxes;
           const uint32_t n = __popc(__ballot_sync(0xffffffffu, copies && there));
@@ -518,8 +529,9 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             }
           }
           __syncwarp();
+          if (++slot == kRing) slot = 0, turn ^= 1;
         }
-        seq0 += w.h0, seq1 += w.h1;
+        seq += w.n;
       } while (ok && w.next(p));
       // never leave with copies in flight
       for (uint32_t k = pos > kRing ? pos - kRing : 0; k < pos; ++k)
@@ -528,34 +540,30 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       // ------------------------------------------------------------ issuers
       // Warp 1: scores, of the one warpgroup and the other; warps 2 and 3: the weights'
       // products of either. The whole warp goes the same way (operands stay uniform),
-      // one thread issues. Each goes through all items, in their order.
+      // one thread issues.
       const uint32_t leader = elect_one();
       constexpr uint32_t kTypes = (1u << 7) | (1u << 10);  // the operands' type: bf16 (1) or fp16 (0)
-      uint32_t slot = 0, turn = 0, unit = 0, mine0 = 0, mine1 = 0;  // place in the ring; units, either's tiles before
-      auto pass = [&] {
-        if (++slot == W::kSlots) slot = 0, turn ^= 1;
-      };
+      uint32_t pos = 0, unit = 0, mine0 = 0, mine1 = 0;  // items before, units, either warpgroup's tiles before
       if (warp == 1) {
         uint32_t pairs = 0;  // among the units before
         do {
           ok = wait_warp(bar(W::kQFull), unit & 1);
           const uint32_t idesc = (idesc_bf16_f32(128, KT, 0, 0) & ~kTypes) | (FP8 && infos[unit & 1].f16 ? 0u : kTypes);
 #pragma unroll 1
-          for (Items it(w.h0, w.h1); ok && it.valid(); it.next(), pass()) {
-            if (it.value) continue;
-            const int i = it.tile();
-            const uint32_t first = w.pair ? 0u : it.x, last = w.pair ? 1u : it.x;
+          for (int j = 0; ok && j < w.n; ++j) {
+            const uint32_t at = pos + Items::keys_at(w, j), slot = at % W::kSlots, turn = at / W::kSlots & 1;
             ok = wait_warp(bar(W::kFull + slot), turn);
             // (copies end in any order; what was looked through was so in order)
             if (!FP8 && ok) ok = wait_warp(bar(W::kClean + slot), turn);
+            const uint32_t last = w.pair ? 1u : j & 1;
 #pragma unroll 1
-            for (uint32_t x = first; ok && x <= last; ++x) {
+            for (uint32_t x = w.pair ? 0u : last; ok && x <= last; ++x) {
               // the weights of the tile before lie in its columns
-              const uint32_t c = (x ? mine1 : mine0) + i;
+              const uint32_t c = w.pair ? (x ? mine1 : mine0) + j : (x ? mine1 : mine0) + (j >> 1);
               if (c > 0) ok = wait_warp(bar(W::kODone + x), (c - 1) & 1);
               // a pair's second warpgroup starts behind the first, so that the one's
               // products run while the other has its scores
-              if (ok && w.pair && x == 1 && i == 0) ok = wait_warp(bar(W::kStagger), pairs & 1);
+              if (ok && w.pair && x == 1 && j == 0) ok = wait_warp(bar(W::kStagger), pairs & 1);
               if (!ok) break;
               tc_fence_after();
               uint64_t a = smem_desc_sw128(sbase + W::kOffQ + (w.pair ? x * W::kQTile : 0u), 16, 1024);
@@ -571,37 +579,41 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             }
           }
           commit_if(leader, bar(W::kQEmpty));
-          mine0 += w.h0, mine1 += w.pair ? w.h0 : w.h1;
-          pairs += w.pair && w.h0 > 0;
+          mine0 += w.own(0), mine1 += w.own(1), pos += 2 * w.n;
+          pairs += w.pair && w.n > 0;
           ++unit;
         } while (ok && w.next(p));
       } else {
         const uint32_t x = warp - 2;
         do {
+          ok = wait_warp(bar(W::kQFull), unit & 1);
+          const bool f16 = FP8 && infos[unit & 1].f16;
+          // the units before are done with, and what the converters left of the last but one
+          if (lane == 0) mbar_arrive(bar(W::kQEmpty));
+          const uint32_t idesc = (idesc_bf16_f32(128, D, 0, 1) & ~kTypes) | (f16 ? 0u : kTypes);
+          const int step = w.pair ? 1 : 2;
+          bool first = true;
 #pragma unroll 1
-          for (Items it(w.h0, w.h1); ok && it.valid(); it.next(), pass()) {
-            if (!it.value || !(w.pair || it.x == static_cast<int>(x))) continue;
-            const int i = it.tile();
+          for (int j = w.pair ? 0 : x; ok && j < w.n; j += step, ++mine0) {
+            const uint32_t at = pos + Items::values_at(w, j), slot = at % W::kSlots, turn = at / W::kSlots & 1;
             // The weights first: a wait for a phase also passes while the barrier is two
             // phases back, and this warp skips the other warpgroup's items. That the keys
             // of these weights were ready, at most three items before, says that the item
             // before in this slot was (slots become ready in order).
-            ok = wait_warp(bar(W::kPFull + x), (mine0 + i) & 1);
-            if (i == 0 && unit > 0 && ok) ok = wait_warp(bar(W::kOFree + x), (unit - 1) & 1);
+            ok = wait_warp(bar(W::kPFull + x), mine0 & 1);
+            if (first && unit > 0 && ok) ok = wait_warp(bar(W::kOFree + x), (unit - 1) & 1);
             if (ok) ok = wait_warp(bar(W::kFull + slot), turn);
             if (!FP8 && ok) ok = wait_warp(bar(W::kClean + slot), turn);
             if (!ok) break;
             tc_fence_after();
-            const bool f16 = FP8 && infos[unit & 1].f16;
-            const uint32_t idesc = (idesc_bf16_f32(128, D, 0, 1) & ~kTypes) | (f16 ? 0u : kTypes);
             uint64_t b = smem_desc_sw128(sbase + W::kOffTile + slot * W::kSlot, 16384, 1024);
             // 64 keys at a time (bf16: the second parts of their weights behind the first)
-            uint32_t a = tmem + kColS + 128 * x;
+            uint32_t a = tmem + kColS + 128 * x, add = !first;
 #pragma unroll 1
             for (int ch = 0; ch < 2; ++ch, a += 64, b += 512) {
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                umma_ts_if(leader, tmem + kColO + D * x, a + 8 * kk, b + 128 * kk, idesc, i > 0 || ch > 0 || kk > 0);
+              for (int kk = 0; kk < 4; ++kk, add = 1u)
+                umma_ts_if(leader, tmem + kColO + D * x, a + 8 * kk, b + 128 * kk, idesc, add);
               if (f16) continue;
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk)
@@ -610,8 +622,9 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             commit_if(leader, bar(W::kODone + x));
             commit_if(leader, bar(W::kEmpty + slot));
             if (kReaders == 2 && !w.pair) commit_if(leader, bar(W::kEmpty + slot));
+            first = false;
           }
-          mine0 += w.pair || x == 0 ? w.h0 : w.h1;
+          pos += 2 * w.n;
           ++unit;
         } while (ok && w.next(p));
       }
@@ -637,12 +650,12 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     int* const deep = reinterpret_cast<int*>(smem + W::kOffDeep);
     float2* const ml = reinterpret_cast<float2*>(smem + W::kOffMl);
     const int lut_len = p.t5_R + 1;
-    uint32_t mine = 0, unit = 0, seq0 = 0, seq1 = 0;  // own tiles, units, either warpgroup's tiles before
+    uint32_t mine = 0, unit = 0, seq = 0;  // own tiles, units, all tiles before
     int tree_of = -1, lut_of = -1;
     if (some) do {
       const int n = w.xe - w.x, len = w.c.len, base = w.base, live = w.live, h = w.c.h, row0 = w.row0;
       const bool pair = w.pair;
-      const int own = pair || x == 0 ? w.h0 : w.h1;  // tiles
+      const int own = w.own(x);  // tiles
       // the tree, and the biases of the distances below the last bucket's
       if (tree_of != w.c.b && warp == 4) {
         tree_lines(p, w.c.b, live, lane, line);
@@ -684,10 +697,10 @@ __global__ void __launch_bounds__(kWideThreads, 1)
 #pragma unroll 1
       for (int i = 0; ok && i < own; ++i, ++mine) {
         {
-          const int key0 = w.key_of(x, i);
+          const int j = w.tile_of(x, i), key0 = w.key_of(j);
           // bits of the groups: page there, rest of the keys' scale, of the values'
           unsigned there = 0xfu, k_rests = 0u, v_rests = 0u;
-          const TileInfo& info = tile_infos[pair || x == 0 ? (seq0 + i) % kInfos : kInfos + (seq1 + i) % kInfos];
+          const TileInfo& info = tile_infos[(seq + j) % kInfos];
           ok = __all_sync(0xffffffffu, wait_on(bar(W::kSFull + x), mine & 1));
           if (!ok) break;
           tc_fence_after();
@@ -892,7 +905,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           mbar_arrive(bar(W::kPFull + x));
         }
       }
-      seq0 += w.h0, seq1 += w.h1;
+      seq += w.n;
       // ---- the unit's parts joined. After a wait that ran out a warp goes on without
       // waiting, so that all meet at the barriers.
       if (ok && own > 0) ok = __all_sync(0xffffffffu, wait_on(bar(W::kODone + x), (mine - 1) & 1));
@@ -926,7 +939,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           sum = sum_of(p0, by0) + sum_of(p1, by1);
         }
         const float inv = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
-        const bool second = !pair && w.h1 > 0;
+        const bool second = !pair && w.n > 1;
         const uint32_t tO0 = tO + (pair ? D * x : 0);
         const int from = pair ? 0 : x * (D / 2), upto = pair ? D : from + D / 2;
         if (any) {
@@ -1074,7 +1087,9 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     }
     // -------------------------------------------------------------- query rows, values
     const int t = threadIdx.x & 127, wq = warp & 3;
-    uint32_t unit = 0, pos = 0;  // units, items
+    uint32_t unit = 0;
+    // places in the rings of codes (turn to wait for) and tiles (the other turn is waited for)
+    uint32_t rs = 0, rturn = 0, cs = 0, cturn = 0;
     int* const range = reinterpret_cast<int*>(smem + W::kOffMisc + 16);  // [4][2] of the warps
     if (some) do {
       const int len = w.c.len, base = w.base, h = w.c.h;
@@ -1163,13 +1178,14 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       }
       fence_async_smem();
       mbar_arrive(bar(W::kQFull));
+      // 2^-e, subnormal at the largest
+      [[maybe_unused]] const float down_k = times_pow2(1.f, -ek), down_v = times_pow2(1.f, -ev);
 #pragma unroll 1
-      for (Items now(w.h0, w.h1); ok && now.valid(); now.next(), ++pos) {
-        const int key0 = w.key_of(now.x, now.tile());
+      for (Items now(w); now.valid(); now.next()) {
+        const int key0 = w.key_of(now.j);
         if constexpr (FP8) {
-          const uint32_t rs = pos % W::kRawSlots, cs = pos % W::kSlots;
-          ok = wait_on(bar(W::kRawFull + rs), (pos / W::kRawSlots) & 1);
-          if (pos >= W::kSlots) ok = ok && wait_on(bar(W::kEmpty + cs), (pos / W::kSlots - 1) & 1);
+          ok = ok && wait_on(bar(W::kRawFull + rs), rturn);
+          ok = ok && wait_on(bar(W::kEmpty + cs), cturn ^ 1);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           // of this warp's 32 keys, which are one page's
@@ -1218,7 +1234,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           };
           const bool odd_rows = !there || key0 + 32 * wq + 31 >= base;  // drafted ones, or none
           if (f16) {  // in units of the largest scale's power of two
-            const float s16 = times_pow2(s, -(now.value ? ev : ek));
+            const float s16 = s * (now.value ? down_v : down_k);
             const uint32_t by = pack_half2(s16, s16);
             auto f = [&](uint32_t h2) { return mul_half2(h2, by); };
             if (odd_rows) convert(f, std::true_type{}); else convert(f, std::false_type{});
@@ -1232,13 +1248,13 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             mbar_arrive(bar(W::kFull + cs));
             mbar_arrive(bar(W::kRawEmpty + rs));
           }
+          if (++rs == W::kRawSlots) rs = 0, rturn ^= 1;
         } else {
-          const uint32_t vs = pos % W::kSlots;
-          ok = __all_sync(0xffffffffu, wait_on(bar(W::kFull + vs), (pos / W::kSlots) & 1));
+          ok = ok && __all_sync(0xffffffffu, wait_on(bar(W::kFull + cs), cturn));
           if (!ok) break;
           if (now.value && key0 + KT > base) {
             // rows from the first drafted slot on
-            const uint32_t to = sbase + W::kOffTile + vs * W::kSlot;
+            const uint32_t to = sbase + W::kOffTile + cs * W::kSlot;
 #pragma unroll 1
             for (int i = t; i < KT * (D / 64) * 8; i += 128) {
               const int r = (i >> 3) & (KT - 1), key = key0 + r;
@@ -1258,8 +1274,9 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             fence_async_smem();
           }
           __syncwarp();
-          if (lane == 0) mbar_arrive(bar(W::kClean + vs));
+          if (lane == 0) mbar_arrive(bar(W::kClean + cs));
         }
+        if (++cs == W::kSlots) cs = 0, cturn ^= 1;
       }
       ++unit;
     } while (w.next(p));  // (after a wait that ran out too, for the barriers' sake)
