@@ -10,6 +10,7 @@
 #include <climits>
 #include <cstdint>
 #include <cstring>
+#include <mutex>
 
 #include "../../include/relpos_attn.h"
 #include "paged.cuh"
@@ -123,6 +124,10 @@ RP_DEVI float larger(float a, float b) { return !(fabsf(b) <= fabsf(a)) && b == 
 // A block takes one head's keys or values of one sequence: it holds every kept
 // token's row in registers before it writes the first, so that rows may be taken
 // in any order.
+// HELD: 16-byte pieces of a thread; with 4 of them (512 of a block: 32 kept tokens of
+// 256 bytes) twice as many blocks fit an SM as with 16, and 256 sequences x 8 heads of up to
+// 17 kept tokens take 9.0 us instead of 11.9.
+template <int HELD>
 __global__ void __launch_bounds__(kCompactThreads) relpos_paged_compact_kernel(const __grid_constant__ CompactParams p) {
   __shared__ int from[kMaxKept], to[kMaxKept];  // row of the pool (page * slots + slot), -1: none
   __shared__ float had[kMaxKept];
@@ -131,10 +136,12 @@ __global__ void __launch_bounds__(kCompactThreads) relpos_paged_compact_kernel(c
   griddep_wait();
   const int b = blockIdx.y, h = blockIdx.x >> 1, val = blockIdx.x & 1, tid = threadIdx.x;
   const bool first = blockIdx.x == 0;  // the one that reports
-  const int len = __ldg(p.lens + b);
+  // (all that depends on nothing else at once: a chain of loads is what bounds this)
+  const int len = __ldg(p.lens + b), n = p.nodes ? __ldg(p.nodes + b) : p.n;
+  const int counts = p.counts ? __ldg(p.counts + b) : INT_MAX;
+  const int j = tid < p.m ? __ldg(p.kept + b * p.kept_stride + tid) : -1;
   if (len <= 0) return;
-  const int n = p.nodes ? __ldg(p.nodes + b) : p.n;
-  const int count = p.counts ? __ldg(p.counts + b) : min(p.m, n);
+  const int count = p.counts ? counts : min(p.m, n);
   if (len > static_cast<long long>(p.max_pages) << p.log_page || n < 0 || n > len || count < 0 || count > min(p.m, n)) {
     if (first && tid == 0)
       report(p.status, len > static_cast<long long>(p.max_pages) << p.log_page ? RELPOS_ERR_PAGE : RELPOS_ERR_TREE);
@@ -145,6 +152,7 @@ __global__ void __launch_bounds__(kCompactThreads) relpos_paged_compact_kernel(c
   const int base = len - n, page0 = base >> p.log_page, slots = 1 << p.log_page;
   const int* row = p.table + b * p.table_stride;
   float* const scale = val ? p.cache.v_scale : p.cache.k_scale;
+  const int j_page = tid < count && j >= 0 && j < n ? __ldg(row + ((base + j) >> p.log_page)) : -1;
   if (tid < kSpan) {
     const int last = (base + count - 1) >> p.log_page;
     int page = page0 + tid <= last ? __ldg(row + page0 + tid) : -1;
@@ -157,16 +165,14 @@ __global__ void __launch_bounds__(kCompactThreads) relpos_paged_compact_kernel(c
   }
   __syncthreads();
   if (tid < count) {
-    const int j = __ldg(p.kept + b * p.kept_stride + tid);
     int src = -1;
     if (j < 0 || j >= n) {
       if (first) report(p.status, RELPOS_ERR_TREE);
     } else {
-      const int page = __ldg(row + ((base + j) >> p.log_page));
-      if (page < 0 || page >= p.cache.num_pages) {
+      if (j_page < 0 || j_page >= p.cache.num_pages) {
         if (first) report(p.status, RELPOS_ERR_PAGE);
       } else {
-        src = page;
+        src = j_page;
       }
     }
     const int own = page_no[((base + tid) >> p.log_page) - page0];
@@ -190,10 +196,9 @@ __global__ void __launch_bounds__(kCompactThreads) relpos_paged_compact_kernel(c
     const long long page = r >> p.log_page;
     return reinterpret_cast<uint4*>(pool + (((page * p.cache.H + h) << p.log_page) + (r & (slots - 1))) * p.row_bytes) + chunk;
   };
-  constexpr int kHeld = kMaxKept * 16 / kCompactThreads;  // chunks of a thread at most
-  uint4 held[kHeld];
+  uint4 held[HELD];
 #pragma unroll
-  for (int i = 0; i < kHeld; ++i) {
+  for (int i = 0; i < HELD; ++i) {
     const int x = tid + i * kCompactThreads, t = x / chunks;
     if (t < count && from[t] >= 0) held[i] = *at(from[t], x - t * chunks);
   }
@@ -212,7 +217,7 @@ __global__ void __launch_bounds__(kCompactThreads) relpos_paged_compact_kernel(c
     __syncthreads();
   }
 #pragma unroll
-  for (int i = 0; i < kHeld; ++i) {
+  for (int i = 0; i < HELD; ++i) {
     const int x = tid + i * kCompactThreads, t = x / chunks;
     if (t < count && from[t] >= 0) {
       const uint4 u = eight ? rescaled16(held[i], had[t], want[((base + t) >> p.log_page) - page0]) : held[i];
@@ -242,8 +247,14 @@ struct AssignParams {
   int* status;
 };
 
-constexpr int kAssignThreads = 1024, kAssignBlocks = 8, kMaxRows = 8192;
-constexpr int kAssignWarps = kAssignThreads / 32;
+// Threads of a block and blocks of the cluster: as many as there may be, but 512
+// threads, whose barriers are quicker, up to 65536 entries of pool and tables. us
+// with 8 x 1024, 16 x 512 and 16 x 1024 threads, caches cold: 64 sequences of 1000 tokens 16.9,
+// 14.8, 16.9; of 7000 27.1, 23.0, 25.1; 512 of 16384 (524 thousand entries) 66, 60, 44.
+// One block: 12 to 13 us instead of 13 to 15 for one short sequence, 19 to 21 for 64.
+constexpr int kAssignThreads = 1024, kAssignFewThreads = 512, kAssignFew = 65536;
+constexpr int kAssignBlocks = 16, kPortableBlocks = 8;  // (more than 8 where the device says so)
+constexpr int kAssignWarps = kAssignThreads / 32, kMaxRows = 8192;
 constexpr int kIsCopy = 1 << 30;
 
 // What a new row is made of
@@ -252,7 +263,20 @@ struct NewRow {
   int part;   // tokens in the page after them, which it continues
   int tail;   // that page, -1: none
   int pages;  // that it has in the end
-  const int* from;
+  int source;
+};
+
+// What every block keeps of all new rows, in shared memory
+struct Rows {
+  int* fresh;     // [B2 + 1] pages that it needs, then those that the rows before need
+  int* at;        // [B2] full, then the entry of its first fresh page (and kIsCopy)
+  int* tail;      // [B2]
+  int* source;    // [B2]
+  uint8_t* part;  // [B2]
+  static constexpr size_t bytes(int rows) { return 17 * static_cast<size_t>(rows) + 4; }
+  RP_DEVI Rows(int* s, int rows)
+      : fresh(s), at(s + rows + 1), tail(at + rows), source(tail + rows),
+        part(reinterpret_cast<uint8_t*>(source + rows)) {}
 };
 
 RP_DEVI int pages_of(int len, int log_page) { return static_cast<int>((static_cast<unsigned>(len) + (1u << log_page) - 1) >> log_page); }
@@ -280,47 +304,60 @@ RP_DEVI NewRow new_row(const AssignParams& p, int i, bool tell) {
   }
   const int keep = s < 0 ? 0 : min(old_len(p, s, false), want);
   NewRow r;
-  r.from = p.table + (s < 0 ? 0 : s * p.table_stride);
+  r.source = s;
   r.full = keep >> p.log_page;
   r.part = keep & ((1 << p.log_page) - 1);
-  r.tail = r.part ? __ldg(r.from + r.full) : -1;
+  r.tail = r.part ? __ldg(p.table + s * p.table_stride + r.full) : -1;
   if (!is_page(p, r.tail)) r.tail = -1;
   r.pages = pages_of(want, p.log_page);
   return r;
 }
 
 // One cluster does it all: its barriers (under a microsecond) stand between the
-// passes over the rows and the pages, which take little time themselves.
-__global__ void __cluster_dims__(kAssignBlocks, 1, 1) __launch_bounds__(kAssignThreads)
-    relpos_paged_assign_kernel(const __grid_constant__ AssignParams p) {
+// passes over the rows and the pages, which take little time themselves. Loads of
+// independent entries go out four or eight at a time: what bounds the passes is
+// their latency.
+__global__ void __launch_bounds__(kAssignThreads) relpos_paged_assign_kernel(const __grid_constant__ AssignParams p) {
   extern __shared__ int rows_s[];
-  int* const first = rows_s;           // [B2 + 1] fresh pages of the rows before
-  int* const at = rows_s + p.B2 + 1;   // [B2] entry of a row's first fresh page (and kIsCopy)
+  const Rows rows(rows_s, p.B2);
   __shared__ int sums[kAssignWarps + 1];
   __shared__ int free_of[kAssignBlocks];  // free pages of each block's share
   cg::cluster_group cluster = cg::this_cluster();
-  const int rank = cluster.block_rank();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int all = rank * kAssignThreads + tid, warps = kAssignBlocks * kAssignWarps;
+  const int rank = cluster.block_rank(), blocks = cluster.num_blocks();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, width = blockDim.x;
+  const int all = rank * width + tid, threads = blocks * width, of_warps = width >> 5, warps = blocks * of_warps;
   griddep_wait();
 
-  for (int i = all; i < p.num_pages; i += kAssignBlocks * kAssignThreads) {
+#pragma unroll 8
+  for (int i = all; i < p.num_pages; i += threads) {
     const int r = __ldg(p.refs + i);
     if (r < 0) report(p.status, RELPOS_ERR_PAGE);
     p.new_refs[i] = max(r, 0);
   }
+  for (int i = tid; i < p.B2; i += width) {
+    const NewRow r = new_row(p, i, rank == 0);
+    rows.fresh[i] = r.pages - r.full;
+    rows.at[i] = r.full;
+    rows.tail[i] = r.tail;
+    rows.source[i] = r.source;
+    rows.part[i] = static_cast<uint8_t>(r.part);
+  }
   cluster.sync();
 
   // the old rows' references go; more of them than a page has are an error
-  for (int b = rank * kAssignWarps + warp; b < p.B; b += warps) {
+  for (int b = rank * of_warps + warp; b < p.B; b += warps) {
     const int* row = p.table + b * p.table_stride;
     const int n = pages_of(old_len(p, b, lane == 0), p.log_page);
-    for (int j = lane; j < n; j += 32) {
-      const int page = __ldg(row + j);
-      if (!is_page(p, page)) {
-        report(p.status, RELPOS_ERR_PAGE);
-      } else if (atomicSub(p.new_refs + page, 1) <= 0) {
-        atomicAdd(p.new_refs + page, 1);
+    for (int j = lane; j < n; j += 128) {
+      int page[4], had[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) page[e] = j + 32 * e < n ? __ldg(row + j + 32 * e) : -1;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) had[e] = is_page(p, page[e]) ? atomicSub(p.new_refs + page[e], 1) : 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (j + 32 * e >= n || had[e] > 0) continue;
+        if (is_page(p, page[e])) atomicAdd(p.new_refs + page[e], 1);
         report(p.status, RELPOS_ERR_PAGE);
       }
     }
@@ -328,19 +365,20 @@ __global__ void __cluster_dims__(kAssignBlocks, 1, 1) __launch_bounds__(kAssignT
   cluster.sync();
 
   // the pages that new rows share
-  for (int i = rank * kAssignWarps + warp; i < p.B2; i += warps) {
-    const NewRow r = new_row(p, i, lane == 0);
+  for (int i = rank * of_warps + warp; i < p.B2; i += warps) {
+    const int full = rows.at[i], source = rows.source[i];
+    const int* from = p.table + (source < 0 ? 0 : source * p.table_stride);
     int* out = p.new_table + i * p.new_stride;
-    for (int j = lane; j < p.new_max; j += 32) {
-      int page = -1;
-      if (j < r.full) {
-        page = __ldg(r.from + j);
-        if (is_page(p, page))
-          atomicAdd(p.new_refs + page, 1);
-        else
-          page = -1;
+    for (int j = lane; j < p.new_max; j += 128) {
+      int page[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) page[e] = j + 32 * e < full ? __ldg(from + j + 32 * e) : -1;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (!is_page(p, page[e])) page[e] = -1;
+        if (page[e] >= 0) atomicAdd(p.new_refs + page[e], 1);
+        if (j + 32 * e < p.new_max) out[j + 32 * e] = page[e];
       }
-      out[j] = page;
     }
     if (lane < 3) p.copies[3 * i + lane] = -1;
   }
@@ -348,24 +386,24 @@ __global__ void __cluster_dims__(kAssignBlocks, 1, 1) __launch_bounds__(kAssignT
 
   // A last page that is filled in part and that nobody else holds goes to the
   // lowest row that continues it: the count, which is 0, takes that row.
-  for (int i = all; i < p.B2; i += kAssignBlocks * kAssignThreads) {
-    const NewRow r = new_row(p, i, false);
-    if (r.tail >= 0 && __ldcg(p.new_refs + r.tail) <= 0) atomicMin(p.new_refs + r.tail, INT_MIN + i);
+  for (int i = all; i < p.B2; i += threads) {
+    const int tail = rows.tail[i];
+    if (tail >= 0 && __ldcg(p.new_refs + tail) <= 0) atomicMin(p.new_refs + tail, INT_MIN + i);
   }
   cluster.sync();
 
   // Fresh pages that each row needs, and their sums, in every block; the free
   // pages of this block's share.
   int before = 0;
-  for (int i0 = 0; i0 < p.B2; i0 += kAssignThreads) {
+  for (int i0 = 0; i0 < p.B2; i0 += width) {
     const int i = i0 + tid;
     int need = 0;
     if (i < p.B2) {
-      const NewRow r = new_row(p, i, false);
-      const bool stays = r.tail >= 0 && __ldcg(p.new_refs + r.tail) == INT_MIN + i;
-      need = r.pages - r.full - stays;
-      at[i] = (r.full + stays) | (r.tail >= 0 && !stays ? kIsCopy : 0);
-      if (stays && rank == 0) p.new_table[i * p.new_stride + r.full] = r.tail;
+      const int tail = rows.tail[i], full = rows.at[i];
+      const bool stays = tail >= 0 && __ldcg(p.new_refs + tail) == INT_MIN + i;
+      need = rows.fresh[i] - stays;
+      rows.at[i] = (full + stays) | (tail >= 0 && !stays ? kIsCopy : 0);
+      if (stays && rank == 0) p.new_table[i * p.new_stride + full] = tail;
     }
     int upto = need;
 #pragma unroll
@@ -377,61 +415,72 @@ __global__ void __cluster_dims__(kAssignBlocks, 1, 1) __launch_bounds__(kAssignT
     if (lane == 31) sums[warp] = upto;
     __syncthreads();
     int base = before;
-    for (int w = 0; w < kAssignWarps; ++w) {
+    for (int w = 0; w < of_warps; ++w) {
       if (w < warp) base += sums[w];
       before += sums[w];
     }
-    if (i < p.B2) first[i] = base + upto - need;
+    if (i < p.B2) rows.fresh[i] = base + upto - need;
   }
   const int total = before;
   // a warp's pages: a run of whole 32s
   const int run = (p.num_pages + 32 * warps - 1) / (32 * warps) * 32;
-  const int page0 = min((rank * kAssignWarps + warp) * run, p.num_pages), page1 = min(page0 + run, p.num_pages);
+  const int page0 = min((rank * of_warps + warp) * run, p.num_pages), page1 = min(page0 + run, p.num_pages);
+  auto look = [&](int from, unsigned (&some)[8]) {  // which of the next 8 times 32 pages are free
+    int refs[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) refs[e] = from + 32 * e + lane < page1 ? __ldcg(p.new_refs + from + 32 * e + lane) : 1;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) some[e] = __ballot_sync(0xffffffffu, refs[e] == 0);
+  };
   int mine = 0;
-  for (int i = page0 + lane; i - lane < page1; i += 32)
-    mine += __popc(__ballot_sync(0xffffffffu, i < page1 && __ldcg(p.new_refs + i) == 0));
+  for (int i = page0; i < page1; i += 256) {
+    unsigned some[8];
+    look(i, some);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) mine += __popc(some[e]);
+  }
   __syncthreads();
   if (lane == 0) sums[warp] = mine;
   __syncthreads();
   int rest = 0, of_block = 0;
-  for (int w = 0; w < kAssignWarps; ++w) {
+  for (int w = 0; w < of_warps; ++w) {
     if (w < warp) rest += sums[w];
     of_block += sums[w];
   }
-  if (tid < kAssignBlocks) *cluster.map_shared_rank(free_of + rank, tid) = of_block;
-  if (tid == 0) first[p.B2] = total;
+  if (tid < blocks) *cluster.map_shared_rank(free_of + rank, tid) = of_block;
+  if (tid == 0) rows.fresh[p.B2] = total;
   cluster.sync();
 
   // the rows that keep a last page, and the k-th free page to the k-th request
-  for (int i = all; i < p.B2; i += kAssignBlocks * kAssignThreads) {
-    const NewRow r = new_row(p, i, false);
-    if (r.tail >= 0 && !(at[i] & kIsCopy)) p.new_refs[r.tail] = 1;
-  }
+  for (int i = all; i < p.B2; i += threads)
+    if (rows.tail[i] >= 0 && !(rows.at[i] & kIsCopy)) p.new_refs[rows.tail[i]] = 1;
   int free_all = 0;
-  for (int w = 0; w < kAssignBlocks; ++w) {
+  for (int w = 0; w < blocks; ++w) {
     if (w < rank) rest += free_of[w];
     free_all += free_of[w];
   }
   if (all == 0 && total > free_all) report(p.status, RELPOS_ERR_PAGE);
-  for (int i = page0 + lane; i - lane < page1 && rest < total; i += 32) {
-    const bool is_free = i < page1 && __ldcg(p.new_refs + i) == 0;
-    const unsigned some = __ballot_sync(0xffffffffu, is_free);
-    const int k = rest + __popc(some & ((1u << lane) - 1));
-    rest += __popc(some);
-    if (!is_free || k >= total) continue;
-    int lo = 0, hi = p.B2;  // the last row with first[row] <= k has a request there
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (first[mid] <= k) lo = mid; else hi = mid;
-    }
-    const int j = (at[lo] & ~kIsCopy) + k - first[lo];
-    p.new_table[lo * p.new_stride + j] = i;
-    p.new_refs[i] = 1;
-    if (k == first[lo] && (at[lo] & kIsCopy)) {
-      const NewRow r = new_row(p, lo, false);
-      p.copies[3 * lo] = r.tail;
-      p.copies[3 * lo + 1] = i;
-      p.copies[3 * lo + 2] = r.part;
+  for (int i0 = page0; i0 < page1 && rest < total; i0 += 256) {
+    unsigned some[8];
+    look(i0, some);
+#pragma unroll 1
+    for (int e = 0; e < 8; ++e) {
+      const int i = i0 + 32 * e + lane, k = rest + __popc(some[e] & ((1u << lane) - 1));
+      rest += __popc(some[e]);
+      if (!(some[e] >> lane & 1) || k >= total) continue;
+      int lo = 0, hi = p.B2;  // the last row with fresh[row] <= k has a request there
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (rows.fresh[mid] <= k) lo = mid; else hi = mid;
+      }
+      const int at = rows.at[lo];
+      p.new_table[lo * p.new_stride + (at & ~kIsCopy) + k - rows.fresh[lo]] = i;
+      p.new_refs[i] = 1;
+      if (k == rows.fresh[lo] && (at & kIsCopy)) {
+        p.copies[3 * lo] = rows.tail[lo];
+        p.copies[3 * lo + 1] = i;
+        p.copies[3 * lo + 2] = rows.part[lo];
+      }
     }
   }
 }
@@ -440,20 +489,57 @@ int log_of(int page) { return page == 32 ? 5 : page == 64 ? 6 : page == 128 ? 7 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 template <class P>
-cudaError_t launch(void (*kernel)(P), dim3 grid, int threads, size_t smem, void* stream, const P& p) {
-  cudaLaunchAttribute attr[1];
+cudaError_t launch(void (*kernel)(P), dim3 grid, int threads, size_t smem, void* stream, const P& p, int cluster = 1) {
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = static_cast<cudaStream_t>(stream);
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p);
   if (e != cudaSuccess) cudaGetLastError();
   return e;
+}
+
+// Blocks of the cluster on the current device (asked once for each), with the
+// kernel's launches of them allowed; 0 on failure
+int assign_blocks() {
+  constexpr int kDevices = 64;
+  static std::mutex mu;
+  static int known[kDevices];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) return 0;
+  std::lock_guard<std::mutex> lk(mu);
+  if (known[dev]) return known[dev];
+  const int smem = static_cast<int>(Rows::bytes(kMaxRows));
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = kAssignBlocks;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kAssignBlocks);
+  cfg.blockDim = dim3(kAssignThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;  // this may come up first under capture
+  cudaThreadExchangeStreamCaptureMode(&mode);
+  int n = 0;
+  const bool ok = cudaFuncSetAttribute(relpos_paged_assign_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) == cudaSuccess;
+  const bool many = ok &&
+                    cudaFuncSetAttribute(relpos_paged_assign_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+                    cudaOccupancyMaxActiveClusters(&n, relpos_paged_assign_kernel, &cfg) == cudaSuccess && n > 0;
+  cudaThreadExchangeStreamCaptureMode(&mode);
+  cudaGetLastError();
+  if (!ok) return 0;
+  return known[dev] = many ? kAssignBlocks : kPortableBlocks;
 }
 
 }  // namespace
@@ -516,7 +602,10 @@ extern "C" int relpos_paged_compact(const RelposPagedCache* cache, int B, const 
   p.counts = counts;
   p.status = device_status();
   if (!p.status) return RELPOS_ERR_CUDA;
-  return launch(relpos_paged_compact_kernel, dim3(2 * cache->H, B), kCompactThreads, 0, stream, p) == cudaSuccess
+  constexpr int kFew = 4, kAll = kMaxKept * 16 / kCompactThreads;
+  const bool few = m * (p.row_bytes / 16) <= kFew * kCompactThreads;
+  return launch(few ? relpos_paged_compact_kernel<kFew> : relpos_paged_compact_kernel<kAll>, dim3(2 * cache->H, B),
+                kCompactThreads, 0, stream, p) == cudaSuccess
              ? RELPOS_OK
              : RELPOS_ERR_CUDA;
 }
@@ -559,14 +648,11 @@ extern "C" int relpos_paged_assign(const int* refs, int num_pages, int page, con
   p.copies = copies;
   p.status = device_status();
   if (!p.status) return RELPOS_ERR_CUDA;
-  const size_t smem = (2 * static_cast<size_t>(B2) + 1) * sizeof(int);
-  if (smem > 40 * 1024 &&
-      cudaFuncSetAttribute(relpos_paged_assign_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (2 * kMaxRows + 1) * sizeof(int)) != cudaSuccess) {
-    cudaGetLastError();
-    return RELPOS_ERR_CUDA;
-  }
-  return launch(relpos_paged_assign_kernel, dim3(kAssignBlocks), kAssignThreads, smem, stream, p) == cudaSuccess
+  const int blocks = assign_blocks();
+  if (blocks == 0) return RELPOS_ERR_CUDA;
+  const long long entries = num_pages + static_cast<long long>(B) * max_pages + static_cast<long long>(B2) * new_max_pages;
+  return launch(relpos_paged_assign_kernel, dim3(blocks), entries > kAssignFew ? kAssignThreads : kAssignFewThreads,
+                Rows::bytes(B2), stream, p, blocks) == cudaSuccess
              ? RELPOS_OK
              : RELPOS_ERR_CUDA;
 }
