@@ -113,7 +113,8 @@ struct Wide {
   static constexpr uint32_t kODone = kPFull + 2;
   static constexpr uint32_t kOFree = kODone + 2;
   static constexpr uint32_t kStagger = kOFree + 2;                    // a pair's first warpgroup has its first maximum
-  static constexpr uint32_t kClean = kStagger + 1;                      // bf16: slots looked through
+  static constexpr uint32_t kPHalf = kStagger + 1;                    // no copies: weights of a tile's second 64 keys
+  static constexpr uint32_t kClean = kPHalf + 2;                      // bf16: slots looked through
   static constexpr uint32_t kFinal = kClean + (FP8 ? 0 : kSlots);
   static constexpr uint32_t kBars = kFinal + 3;
   static constexpr uint32_t kOffMisc = kOffBar + kBars * 8;           // TMEM address, foul flag, 8 ints of the converters
@@ -429,7 +430,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       if (i == W::kQFull) n = 128;
       if (i == W::kQEmpty) n = 3;                               // the issuers
       if (i >= W::kClean && i < W::kFinal) n = 4;
-      if (i >= W::kPFull && i < W::kODone) n = 128;
+      if ((i >= W::kPFull && i < W::kODone) || (i >= W::kPHalf && i < W::kPHalf + 2)) n = 128;
       if (i == W::kOFree || i == W::kOFree + 1) n = 256;
       mbar_init(bar(i), n);
     }
@@ -600,25 +601,34 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             // phases back, and this warp skips the other warpgroup's items. That the keys
             // of these weights were ready, at most three items before, says that the item
             // before in this slot was (slots become ready in order).
-            ok = wait_warp(bar(W::kPFull + x), mine0 & 1);
+            ok = wait_warp(bar((COPIES == 1 ? W::kPHalf : W::kPFull) + x), mine0 & 1);
             if (first && unit > 0 && ok) ok = wait_warp(bar(W::kOFree + x), (unit - 1) & 1);
             if (ok) ok = wait_warp(bar(W::kFull + slot), turn);
             if (!FP8 && ok) ok = wait_warp(bar(W::kClean + slot), turn);
             if (!ok) break;
             tc_fence_after();
-            uint64_t b = smem_desc_sw128(sbase + W::kOffTile + slot * W::kSlot, 16384, 1024);
-            // 64 keys at a time (bf16: the second parts of their weights behind the first)
-            uint32_t a = tmem + kColS + 128 * x, add = !first;
+            const uint64_t b0 = smem_desc_sw128(sbase + W::kOffTile + slot * W::kSlot, 16384, 1024);
+            // 64 keys at a time, the second ones first (bf16: the second parts of their
+            // weights behind the first)
+            uint32_t add = !first;
 #pragma unroll 1
-            for (int ch = 0; ch < 2; ++ch, a += 64, b += 512) {
+            for (int ch = 1; ok && ch >= 0; --ch) {
+              const uint64_t b = b0 + 512 * ch;
+              const uint32_t a = tmem + kColS + 128 * x + 64 * ch;
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk, add = 1u)
                 umma_ts_if(leader, tmem + kColO + D * x, a + 8 * kk, b + 128 * kk, idesc, add);
-              if (f16) continue;
+              if (!f16) {
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                umma_ts_if(leader, tmem + kColO + D * x, a + 32 + 8 * kk, b + 128 * kk, idesc, 1u);
+                for (int kk = 0; kk < 4; ++kk)
+                  umma_ts_if(leader, tmem + kColO + D * x, a + 32 + 8 * kk, b + 128 * kk, idesc, 1u);
+              }
+              if (COPIES == 1 && ch == 1) {
+                ok = wait_warp(bar(W::kPFull + x), mine0 & 1);
+                tc_fence_after();
+              }
             }
+            if (!ok) break;
             commit_if(leader, bar(W::kODone + x));
             commit_if(leader, bar(W::kEmpty + slot));
             if (kReaders == 2 && !w.pair) commit_if(leader, bar(W::kEmpty + slot));
@@ -877,6 +887,11 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                   tmem_st8(place(col0 + from + 16 * q), hi);
                   if constexpr (!F16) tmem_st8(place(col0 + from + 16 * q) + 32, lo);
                 }
+                if (COPIES == 1 && ch == 0) {  // their product starts while the others are at it
+                  tmem_st_wait();
+                  tc_fence_before();
+                  mbar_arrive(bar(W::kPHalf + x));
+                }
               }
               if constexpr (COPIES > 1) {
                 const uint32_t zero[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
@@ -900,6 +915,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             }
             l_run += (sum0.x + sum0.y) + (sum1.x + sum1.y);
             tmem_st_wait();
+          } else if (COPIES == 1) {
+            mbar_arrive(bar(W::kPHalf + x));
           }
           tc_fence_before();
           mbar_arrive(bar(W::kPFull + x));
