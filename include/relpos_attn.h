@@ -198,7 +198,8 @@ int relpos_index_ids(int mode, int n, int rel_first, int num_buckets, int rel_pa
  * of this library hit a bounded-wait limit since the last check
  * (RELPOS_ERR_DEVICE_TIMEOUT), met a page number or length outside its paged
  * cache (RELPOS_ERR_PAGE) or something outside a tree of drafted tokens
- * (RELPOS_ERR_TREE), whichever came first, or a CUDA error (RELPOS_ERR_CUDA). Clears the recorded device status. Blocking.
+ * (RELPOS_ERR_TREE), whichever came first, or a CUDA error (RELPOS_ERR_CUDA).
+ * Clears the recorded device status. Blocking.
  */
 int relpos_check_status(void* stream);
 
@@ -673,8 +674,15 @@ int relpos_selftest_paged_tree_split(const RelposPagedCache* cache, int B, int H
  *   nodes       device, int32 [B]: n_b, 0 .. n; null: n each.
  *   parents     device, int32, node i of sequence b at parents[b * parent_stride +
  *               i] (parent_stride 0: one tree for the whole batch).
- * All other arguments, scratch and the way in which pages that do not exist are
- * left out as for relpos_paged_decode. A parent that is neither -1 nor an earlier
+ * All other arguments, the rounding of weights and the way in which pages that do
+ * not exist are left out as for relpos_paged_decode. The cache is read once for up
+ * to 16 rows (query heads of a group times n), or once for up to 256 where there are
+ * many (from 9 rows on in BF16 caches, 17 or 33 in E4M3 ones) and the block table has
+ * room for more tiles of 128 tokens, over all sequences and heads, than the device
+ * has SMs. Scratch from the library's pool, as for relpos_paged_decode: up to about
+ * 8 MB, or 40 MB (d = 64: 20) for up to 256 rows; none where the block table holds
+ * few tiles (there, up to 256 tokens). Values of drafted tokens that are not finite reach
+ * the rows that see them and no others. A parent that is neither -1 nor an earlier
  * node counts as -1, and a sequence with n_b outside 0 .. n or above its length
  * has zero rows; relpos_check_status() reports both as RELPOS_ERR_TREE.
  */
@@ -699,8 +707,8 @@ int relpos_paged_tree_decode(const RelposPagedCache* cache, const void* Q, const
  * E4M3 caches: where a token changes its page, that page's scale for a head becomes
  * the larger of its own and the pages' that its new tokens come from, and the codes
  * in it are rounded to it; a token that stays in its page, or comes from one of
- * the same scale, keeps its code. Rows of Kept with an entry outside the tree keep
- * that slot as it was, a sequence with a count outside its range all of them
+ * the same scale, keeps its code. A slot whose entry of kept lies outside the tree
+ * stays as it was, and in a sequence with a count outside its range all of them do
  * (RELPOS_ERR_TREE); pages that do not exist as in relpos_paged_append. Slots behind
  * the kept tokens hold what they held, at their page's new scale. Pages written must
  * not be shared by two sequences of the call. Asynchronous on `stream`, no scratch.

@@ -1270,8 +1270,9 @@ __global__ void __launch_bounds__(THREADS) relpos_paged_combine_kernel(const __g
   }
   if (k == 0) return;
   const int h = u / p.rt, row0 = (u - h * p.rt) * p.rows, rows = min(p.G * p.Lq - row0, p.rows);
-  // this block's columns (4 dims of a row) of the unit's rows * D / 4
-  const int me = blockIdx.x - c0, cols = rows * (D / 4);
+  // this block's columns (4 dims of a row) of the unit's, those of rows with a node
+  const int live = max(0, min(row_count(p, b) * p.G - row0, rows));
+  const int me = blockIdx.x - c0, cols = live * (D / 4);
   const int first = cols * me / k, count = cols * (me + 1) / k - first;
   int lanes = 1;  // that share a column, a power of two
   while (lanes < 32 && lanes < k && 2 * lanes * count <= kHalf) lanes *= 2;
@@ -1305,7 +1306,6 @@ __global__ void __launch_bounds__(THREADS) relpos_paged_combine_kernel(const __g
     }
     if (i < count && part == 0) {
       const int qi = (row0 + r) / p.G, hq = h * p.G + (row0 + r) - qi * p.G;
-      if (qi >= row_count(p, b)) acc = make_float4(0.f, 0.f, 0.f, 0.f), l = 0.f;  // no node
       const float inv = l == 0.f ? 0.f : 1.f / l;
       __nv_bfloat16* op = p.out + b * p.o_batch + hq * p.o_head + qi * p.o_row + 4 * d4;
       const uint32_t w[2] = {pack_bf2(acc.x * inv, acc.y * inv), pack_bf2(acc.z * inv, acc.w * inv)};
@@ -1319,6 +1319,10 @@ __global__ void __launch_bounds__(THREADS) relpos_paged_combine_kernel(const __g
         }
       }
     }
+  }
+  for (int i = live * D + me * kHalf + tid; i < rows * D; i += k * kHalf) {  // the others
+    const int r = row0 + i / D, qi = r / p.G;
+    p.out[b * p.o_batch + (h * p.G + r - qi * p.G) * p.o_head + qi * p.o_row + i % D] = __float2bfloat16_rn(0.f);
   }
 }
 

@@ -15,10 +15,22 @@
 //     many products, but a thread has a half or quarter of the exponentials, and the
 //     chain from scores to weights, which few rows cannot hide, is as much shorter.
 // Keys and values of the tiles come in the order in which the products need them. While
-// a warpgroup turns its scores into weights, the other's products run.
+// a warpgroup turns its scores into weights, the other's products run; the product of a
+// tile's second 64 keys starts while the weights of the first 64 are formed.
 // What the warpgroups and copies hold apart (maximum, sum, O) is joined at the unit's
-// end. Blocks take equal shares of all units' tiles, as in paged_decode.cuh, one block
-// an SM.
+// end. Blocks take shares of equal cost of all units' tiles, as in paged_decode.cuh, one
+// block an SM.
+//
+// What bounds it: for few rows the pages' way through shared memory (16 x 8 heads x 8192
+// tokens: bf16, d = 128, 114 us, 69 % of the HBM rate; e4m3 106, conversion of the codes);
+// for many rows a warpgroup's chain from scores to weights and back, of about 7000 cycles
+// a tile for a pair: scores into registers twice (128 of them do not fit) 1300, exponentials
+// and weights 2000, the two products, their issue and the barriers between 2500, with the
+// tensor pipe a third busy (2 x 131075 tokens, 64 nodes, 16 query and 4 key heads, d = 128, e4m3:
+// 203 us; the products alone take 73).
+// All roles' loops together have to fit the instruction cache: rolled loops and waits of a
+// few instructions took the same work from 338 to 193 us, and reading scores 32 columns
+// ahead (larger code) cost 10 %.
 //
 //   warp 0        producer: tiles of keys and values from their pages into a ring of
 //                 shared memory (bf16: tensor copies, swizzled; e4m3: bulk copies).
@@ -234,8 +246,10 @@ struct Items {
   }
 };
 
-// Costs that shares are equal in: a unit's tiles, more for a pair (2 x 131075 tokens
-// of 256 rows took 5.2 thousand cycles a tile, of 128 rows 3.5), and what a unit costs beside.
+// Costs that shares are equal in: a unit's tiles, more for a pair (12 sequences of 8191
+// tokens, 8 heads, d = 128, e4m3: 7.0 thousand cycles a tile with 132 rows, 4.4 with 96), and
+// what a unit costs beside. With 3 : 2, 24 ragged sequences of up to 132 rows take 137 us, with
+// equal costs 183, with 4 : 3 151.
 constexpr int kPairCost = 3, kTileCost = 2, kUnitCost = 6;
 
 struct UnitCost {
