@@ -222,3 +222,35 @@ def test_a_long_context_of_many_rows(dtype):
     got = _run(cache, q, table, lens, parents, bias, "t5", [64, 64])
     _check(got, *_ref(cache, q, table, lens, parents, bias, "t5", [64, 64]), dtype == E4)
     np.testing.assert_array_equal(got.isfinite().cpu(), True)
+
+
+@pytest.mark.parametrize("dtype", [E4, BF])
+@pytest.mark.parametrize("n", [3, 40])
+def test_pages_past_4_gb(dtype, n):
+    """The same pages at the end of a pool whose keys take more than 4 GB: the same bits, whichever products run."""
+    size = 1 if dtype == E4 else 2
+    pages = (1 << 32) // (2 * 128 * 128 * size) + 40
+    cache, q, table, lens, bias = _case([900, 300], 4, 2, n, 128, 128, dtype, "alibi", 44)
+    parents = _tree("random", 2, n, 44)
+    far = rp.PagedCache.empty(pages, 2, 128, page_size=128, dtype=dtype)
+    at = pages - cache.num_pages
+    for name in ("k", "v"):
+        getattr(far, name).view(torch.uint8)[at:] = getattr(cache, name).view(torch.uint8)
+        if dtype == E4:
+            getattr(far, name + "_scale")[at:] = getattr(cache, name + "_scale")
+    outs = [rp.paged_tree_decode(q.cuda(), c, _long(t, 128).cuda(), lens.cuda(), parents.cuda(), bias=bias.cuda(),
+                                 mode=rp.MODE_ALIBI)
+            for c, t in ((cache, table), (far, torch.where(table >= 0, table + at, table)))]
+    assert rp.check_status() == 0 and torch.equal(*outs)
+    _check(outs[1], *_ref(cache, q, table, lens, parents, bias, "alibi"), dtype == E4)
+
+
+@pytest.mark.parametrize("dtype", [E4, BF])
+def test_sequences_that_share_pages_and_a_shared_query(dtype):
+    """One context under several trees, and one query row for all of them (strides of 0)."""
+    cache, q, table, lens, bias = _case([500], 8, 2, 40, 64, 64, dtype, "t5", 45)
+    B = 5
+    parents = _tree("random", B, 40, 45)
+    got = _run(cache, q.cuda().expand(B, -1, -1, -1), table.expand(B, -1), lens.expand(B).contiguous(), parents, bias, "t5")
+    for b in range(B):
+        _check(got[b:b + 1], *_ref(cache, q, table, lens, parents[b:b + 1], bias, "t5"), dtype == E4)
