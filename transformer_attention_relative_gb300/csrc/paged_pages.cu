@@ -37,7 +37,8 @@ struct CopyParams {
 constexpr int kCopyThreads = 256;
 
 // A block copies one head's keys or values of one entry: `tokens` rows that lie
-// one after another.
+// one after another. Bound by HBM: 1024 pages of 64 tokens, 8 heads, d = 128, bf16 take 83 us,
+// 95 % of the rate of a plain copy.
 __global__ void __launch_bounds__(kCopyThreads) relpos_paged_copy_kernel(const __grid_constant__ CopyParams p) {
   griddep_wait();
   const int parts = 2 * p.cache.H;
@@ -123,7 +124,8 @@ RP_DEVI float larger(float a, float b) { return !(fabsf(b) <= fabsf(a)) && b == 
 
 // A block takes one head's keys or values of one sequence: it holds every kept
 // token's row in registers before it writes the first, so that rows may be taken
-// in any order.
+// in any order. Bound by its chain of loads (lengths and kept nodes, pages, scales, rows):
+// 4.6 us for 32 sequences, 16 heads, 5 kept tokens of e4m3.
 // HELD: 16-byte pieces of a thread; with 4 of them (512 of a block: 32 kept tokens of
 // 256 bytes) twice as many blocks fit an SM as with 16, and 256 sequences x 8 heads of up to
 // 17 kept tokens take 9.0 us instead of 11.9.
@@ -313,10 +315,11 @@ RP_DEVI NewRow new_row(const AssignParams& p, int i, bool tell) {
   return r;
 }
 
-// One cluster does it all: its barriers (under a microsecond) stand between the
-// passes over the rows and the pages, which take little time themselves. Loads of
-// independent entries go out four or eight at a time: what bounds the passes is
-// their latency.
+// One cluster does it all: five of its barriers (under a microsecond each) stand between
+// the passes over the rows and the pages. What bounds it are those and the latency of the
+// passes' loads, which therefore go out four or eight at a time where they are
+// independent (64 sequences over 4096 pages 9.9 us; 512 sequences of 16384 tokens over 262144
+// pages 33 us, 64 with eight blocks and a load at a time).
 __global__ void __launch_bounds__(kAssignThreads) relpos_paged_assign_kernel(const __grid_constant__ AssignParams p) {
   extern __shared__ int rows_s[];
   const Rows rows(rows_s, p.B2);
