@@ -141,10 +141,11 @@ struct UnitInfo {
 
 // Waits of this kernel: a few instructions each (its roles' loops share an instruction
 // cache that they would not fit with the waits on a clock of ptx.cuh), limited by a
-// number of tries, tens of milliseconds at the least.
+// number of tries: ten milliseconds at the least (what is waited for is microseconds of
+// the same block's work), and seconds where a try is suspended for long.
 RP_DEVI bool wait_on(uint32_t bar, uint32_t parity) {
 #pragma unroll 1
-  for (int i = 0; i < 1 << 21; ++i)
+  for (int i = 0; i < 1 << 18; ++i)
     if (mbar_try_wait(bar, parity)) return true;
   return false;
 }
